@@ -18,6 +18,9 @@ Entry points (the C ABI in include/entq.h, same names):
   count_symbols_device, encode_device, pack_device, region_bytes
                                       on-device encoder (same regions)
   encode_batch_device(...) -> DeviceBatch  the device path of encode_batch
+  int8 (module)                       products of quantised activations with
+                                      decoded Int8 codes, the gated
+                                      feed-forward kernel, their gradients
 """
 from __future__ import annotations
 
@@ -124,6 +127,16 @@ def lib():
             "entq_decode_gemm_tiles": (c.c_int, [vp, vp, vp, vp, c.c_int, vp, u64, vp, vp]),
             "entq_decode_gemm_tiles_bf16_split": (c.c_int, [vp, vp, vp, vp, c.c_int, vp, u64, vp,
                                                             vp]),
+            "entq_quantize_rows": (c.c_int, [vp, vp, u64, vp, vp]),
+            "entq_int8_gemm_workspace_bytes": (u64, [vp, vp]),
+            "entq_int8_gemm": (c.c_int, [vp, vp, vp, c.c_int, u64, vp, u64, vp]),
+            "entq_int8_gated_workspace_bytes": (u64, [vp, vp, vp]),
+            "entq_int8_gated": (c.c_int, [vp, vp, vp, c.c_int, vp, c.c_int, u64, vp, u64, vp]),
+            "entq_int8_gemm_backward_workspace_bytes": (u64, [vp, vp, vp]),
+            "entq_int8_gemm_backward": (c.c_int, [vp, vp, vp, vp, u64, vp, vp, u64, vp]),
+            "entq_int8_gated_backward_workspace_bytes": (u64, [vp, vp, vp, vp]),
+            "entq_int8_gated_backward": (c.c_int, [vp, vp, vp, vp, c.c_int, vp, u64, vp, vp, vp,
+                                                   u64, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -147,7 +160,10 @@ EXPORTED = ["entq_plan_workspace_bytes", "entq_plan", "entq_decode", "entq_decod
             "entq_build_freq_device", "entq_decode_gemm_workspace_bytes",
             "entq_decode_gemm_static", "entq_tile_order", "entq_decode_gemm_tiles_workspace_bytes",
             "entq_decode_gemm_tiles", "entq_decode_gemm_tiles_bf16_split",
-            "entq_tile_order_device"]
+            "entq_tile_order_device", "entq_quantize_rows", "entq_int8_gemm_workspace_bytes",
+            "entq_int8_gemm", "entq_int8_gated_workspace_bytes", "entq_int8_gated",
+            "entq_int8_gemm_backward_workspace_bytes", "entq_int8_gemm_backward",
+            "entq_int8_gated_backward_workspace_bytes", "entq_int8_gated_backward"]
 
 
 def _str(status: int) -> str:

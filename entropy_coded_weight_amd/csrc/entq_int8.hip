@@ -1,0 +1,404 @@
+// entq_int8.hip -- the int8 calls of entq.h: argument checks, workspace
+// layout, the quantiser of activation rows and the small kernels around the
+// products.
+#include <algorithm>
+
+#include "entq_int8.h"
+
+namespace entq {
+namespace {
+
+// ---------------------------------------------------------------------------
+// quantiser
+// ---------------------------------------------------------------------------
+
+constexpr float kMinScale = 0x1p-100f;  // its inverse is finite
+constexpr int kQuantThreads = 256;
+
+template <int TYPE>
+__device__ __forceinline__ float load_act(const void *x, uint64_t at) {
+    if (TYPE == ENTQ_F32) return ((const float *)x)[at];
+    return from16(((const uint16_t *)x)[at], TYPE == ENTQ_F16);
+}
+
+// One workgroup per row. The largest magnitude is found on the bits of |x|
+// as integers, where infinities and NaNs come out on top.
+template <int TYPE>
+__global__ __launch_bounds__(kQuantThreads) void quantize_rows(const void *x, uint64_t ldx, uint32_t K,
+                                                               int8_t *codes, uint64_t ldc, uint32_t pad,
+                                                               float *scales) {
+    __shared__ uint32_t top[kQuantThreads / 64];
+    const uint64_t row = blockIdx.x;
+    uint32_t big = 0;
+    for (uint32_t c = threadIdx.x; c < K; c += kQuantThreads)
+        big = max(big, __float_as_uint(load_act<TYPE>(x, row * ldx + c)) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 32; o; o /= 2) big = max(big, (uint32_t)__shfl_xor((int)big, o));
+    if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQuantThreads / 64; ++i) big = max(big, top[i]);
+    const bool finite = big < 0x7F800000u;
+    const float scale = fmaxf(__uint_as_float(big) * (float)(1.0 / 127), kMinScale);
+    const float inv = 1.0f / scale;
+    if (threadIdx.x == 0) scales[row] = finite ? scale : __uint_as_float(0x7FC00000u);
+    for (uint32_t c = threadIdx.x; c < pad; c += kQuantThreads) {
+        float q = 0.0f;
+        if (finite && c < K) q = rintf(load_act<TYPE>(x, row * ldx + c) * inv);
+        codes[row * ldc + c] = (int8_t)fminf(fmaxf(q, -127.0f), 127.0f);
+    }
+}
+
+int launch_quantize(const entq_rows &x, int8_t *codes, uint64_t ldc, uint32_t pad, float *scales,
+                    hipStream_t s) {
+    if (x.rows == 0) return ENTQ_OK;
+    const dim3 grid(x.rows);
+    if (x.type == ENTQ_BF16)
+        quantize_rows<ENTQ_BF16><<<grid, kQuantThreads, 0, s>>>(x.d_data, x.ld, x.cols, codes, ldc, pad, scales);
+    else if (x.type == ENTQ_F16)
+        quantize_rows<ENTQ_F16><<<grid, kQuantThreads, 0, s>>>(x.d_data, x.ld, x.cols, codes, ldc, pad, scales);
+    else
+        quantize_rows<ENTQ_F32><<<grid, kQuantThreads, 0, s>>>(x.d_data, x.ld, x.cols, codes, ldc, pad, scales);
+    return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
+}
+
+// ---------------------------------------------------------------------------
+// backward helpers
+// ---------------------------------------------------------------------------
+
+// norm[0]: a power of two that brings the largest |scale| into [1, 2), and
+// norm[1] its inverse: dy sw then spans the range dy itself has, which F16
+// holds by the caller's choice. 1 where all scales are 0 or one is not finite.
+__global__ __launch_bounds__(1024) void scale_norm(const float *a, const float *b, uint32_t n, float *norm) {
+    __shared__ uint32_t top[16];
+    uint32_t big = 0;
+    for (uint32_t i = threadIdx.x; i < n; i += 1024) {
+        big = max(big, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+        if (b) big = max(big, __float_as_uint(b[i]) & 0x7FFFFFFFu);
+    }
+#pragma unroll
+    for (int o = 32; o; o /= 2) big = max(big, (uint32_t)__shfl_xor((int)big, o));
+    if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 16; ++i) big = max(big, top[i]);
+        int e = (int)(big >> 23) - 127;
+        if (big == 0 || big >= 0x7F800000u) e = 0;
+        e = max(-126, min(126, e));
+        norm[0] = __uint_as_float((uint32_t)(127 - e) << 23);
+        norm[1] = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+}
+
+// Column sums of the token blocks' partial sums, in block order.
+__global__ __launch_bounds__(256) void sum_parts(const float *p0, const float *p1, uint32_t blocks, uint32_t n,
+                                                 float *out0, float *out1) {
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+    const float *p = blockIdx.y ? p1 : p0;
+    float *out = blockIdx.y ? out1 : out0;
+    if (i >= n || !out) return;
+    float s = 0.0f;
+    for (uint32_t b = 0; b < blocks; ++b) s += p[(uint64_t)b * n + i];
+    out[i] = s;
+}
+
+__global__ __launch_bounds__(256) void fill_zero(uint8_t *p, uint64_t ld, uint32_t bytes) {
+    for (uint32_t c = blockIdx.x * 256 + threadIdx.x; c < bytes; c += gridDim.x * 256)
+        p[blockIdx.y * ld + c] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// checks and layout
+// ---------------------------------------------------------------------------
+
+uint32_t type_bytes(int t) { return t == ENTQ_F32 ? 4 : t == ENTQ_I8 ? 1 : 2; }
+
+entq_status check_rows(const entq_rows *r, bool acts, bool codes) {
+    if (!r || r->reserved) return ENTQ_EINVAL;
+    if (r->type < ENTQ_BF16 || r->type > ENTQ_I8) return ENTQ_EINVAL;
+    if (r->type == ENTQ_I8 ? !codes : !acts) return ENTQ_EINVAL;
+    if (r->cols > ENTQ_INT8_MAX_COLS || r->rows > 0x7FFFFFFFu || r->ld < r->cols) return ENTQ_EINVAL;
+    if (r->ld > (1ull << 40)) return ENTQ_EINVAL;
+    if (r->rows && r->cols && !r->d_data) return ENTQ_EINVAL;
+    if (r->type == ENTQ_I8 && r->rows && !r->d_scales) return ENTQ_EINVAL;
+    if (r->type != ENTQ_I8 && r->d_scales) return ENTQ_EINVAL;
+    if ((uintptr_t)r->d_data % type_bytes(r->type) || (uintptr_t)r->d_scales % 4) return ENTQ_EALIGN;
+    return ENTQ_OK;
+}
+
+entq_status check_out(const void *p, int type, uint64_t ld, uint32_t rows, uint32_t cols) {
+    if (type != ENTQ_BF16 && type != ENTQ_F16 && type != ENTQ_F32) return ENTQ_EINVAL;
+    if (ld < cols || ld > (1ull << 40)) return ENTQ_EINVAL;
+    if (rows && cols && !p) return ENTQ_EINVAL;
+    if ((uintptr_t)p % type_bytes(type)) return ENTQ_EALIGN;
+    return ENTQ_OK;
+}
+
+bool vec4(const void *p, uint64_t ld, int type) {
+    return (uintptr_t)p % (4 * type_bytes(type)) == 0 && ld % 4 == 0;
+}
+
+// Takes pieces of the workspace in order; with base null it only counts.
+struct Pieces {
+    uint8_t *base;
+    uint64_t used = 0;
+    explicit Pieces(void *b) : base((uint8_t *)b) {}
+    template <class T>
+    T *take(uint64_t n) {
+        const uint64_t at = used;
+        used += (n * sizeof(T) + 255) / 256 * 256;
+        return base ? (T *)(base + at) : nullptr;
+    }
+};
+
+struct Call {
+    Int8Mode mode;
+    const entq_rows *x, *w[2], *dy;
+    int n_w;
+    entq_status bad;
+};
+
+Call describe(Int8Mode mode, const entq_rows *x, const entq_rows *w0, const entq_rows *w1, const entq_rows *dy) {
+    Call c{mode, x, {w0, w1}, dy, mode == kGated || mode == kGatedBwd ? 2 : 1, ENTQ_OK};
+    const bool back = mode == kBwd || mode == kGatedBwd;
+    if ((c.bad = check_rows(x, !back, true)) != ENTQ_OK) return c;
+    for (int i = 0; i < c.n_w; ++i) {
+        if ((c.bad = check_rows(c.w[i], false, true)) != ENTQ_OK) return c;
+        if (c.w[i]->cols != x->cols || c.w[i]->rows != w0->rows) {
+            c.bad = ENTQ_EINVAL;
+            return c;
+        }
+    }
+    if (back) {
+        // (the gradient's columns are channels: not bounded by the sums' limit)
+        if (!dy || dy->reserved || (dy->type != ENTQ_BF16 && dy->type != ENTQ_F16) || dy->d_scales ||
+            dy->rows != x->rows || dy->cols != w0->rows || dy->ld < dy->cols || dy->ld > (1ull << 40) ||
+            (dy->rows && dy->cols && !dy->d_data))
+            c.bad = ENTQ_EINVAL;
+        else if ((uintptr_t)dy->d_data % 2)
+            c.bad = ENTQ_EALIGN;
+    }
+    return c;
+}
+
+// What a call keeps in the workspace.
+struct Layout {
+    int8_t *codes;      // quantised activations, or null
+    float *scales;
+    uint64_t ldc;
+    uint16_t *d[2];     // scaled gradients
+    uint64_t ldd;
+    float *part[2];
+    float *norm;
+    uint64_t bytes;
+};
+
+Layout lay_out(const Call &c, void *ws) {
+    Layout l{};
+    Pieces p(ws);
+    const uint64_t M = c.x->rows, N = c.w[0]->rows;
+    l.ldc = (c.x->cols + 127ull) / 128 * 128;
+    l.ldd = (N + 63) / 64 * 64;
+    if (c.x->type != ENTQ_I8) {
+        l.codes = p.take<int8_t>(M * l.ldc);
+        l.scales = p.take<float>(M);
+    }
+    if (c.mode == kBwd || c.mode == kGatedBwd) {
+        for (int i = 0; i < c.n_w; ++i) {
+            l.d[i] = p.take<uint16_t>(M * l.ldd);
+            l.part[i] = p.take<float>((uint64_t)int8_token_blocks((uint32_t)M) * N);
+        }
+        l.norm = p.take<float>(2);
+    }
+    l.bytes = p.used;
+    return l;
+}
+
+uint64_t workspace_bytes_of(const Call &c) { return c.bad == ENTQ_OK ? lay_out(c, nullptr).bytes : 0; }
+
+entq_status zero_rows(void *p, int type, uint64_t ld, uint32_t rows, uint32_t cols, hipStream_t s) {
+    if (!p || !rows || !cols) return ENTQ_OK;
+    const uint32_t b = type_bytes(type);
+    for (uint32_t r = 0; r < rows; r += 65535) {
+        const uint32_t n = std::min(rows - r, 65535u);
+        fill_zero<<<dim3(std::min(64u, cols * b / 256 + 1), n), 256, 0, s>>>((uint8_t *)p + (uint64_t)r * ld * b,
+                                                                             ld * b, cols * b);
+    }
+    return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
+}
+
+Int8Args arguments(const Call &c) {
+    Int8Args a{};
+    a.x = (const int8_t *)c.x->d_data;
+    a.sx = c.x->d_scales;
+    a.ldx = c.x->ld;
+    for (int i = 0; i < c.n_w; ++i) {
+        a.w[i] = (const int8_t *)c.w[i]->d_data;
+        a.sw[i] = c.w[i]->d_scales;
+        a.ldw[i] = c.w[i]->ld;
+    }
+    a.M = c.x->rows;
+    a.N = c.w[0]->rows;
+    a.K = c.x->cols;
+    return a;
+}
+
+entq_status check_workspace(const void *ws, uint64_t bytes, uint64_t need) {
+    if (!need) return ENTQ_OK;
+    if (!ws || bytes < need) return ENTQ_EWORKSPACE;
+    return (uintptr_t)ws % 256 ? ENTQ_EALIGN : ENTQ_OK;
+}
+
+entq_status forward(const Call &c, int act, void *y, int type, uint64_t ldy, void *ws, uint64_t ws_bytes,
+                    hipStream_t s) {
+    if (c.bad != ENTQ_OK) return c.bad;
+    entq_status st = check_out(y, type, ldy, c.x->rows, c.w[0]->rows);
+    if (st != ENTQ_OK) return st;
+    if ((st = check_workspace(ws, ws_bytes, workspace_bytes_of(c))) != ENTQ_OK) return st;
+    if (c.x->rows == 0 || c.w[0]->rows == 0) return ENTQ_OK;
+    if (c.x->cols == 0) return zero_rows(y, type, ldy, c.x->rows, c.w[0]->rows, s);
+    const Layout l = lay_out(c, ws);
+    Int8Args a = arguments(c);
+    if (c.x->type != ENTQ_I8) {
+        const int q = launch_quantize(*c.x, l.codes, l.ldc, (uint32_t)l.ldc, l.scales, s);
+        if (q != ENTQ_OK) return (entq_status)q;
+        a.x = l.codes;
+        a.sx = l.scales;
+        a.ldx = l.ldc;
+    }
+    a.act = act;
+    a.y = y;
+    a.type = type;
+    a.ldy = ldy;
+    a.vec = vec4(y, ldy, type);
+    return (entq_status)launch_int8_product(c.mode, a, s);
+}
+
+entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0, float *ds1, void *ws,
+                     uint64_t ws_bytes, hipStream_t s) {
+    if (c.bad != ENTQ_OK) return c.bad;
+    const uint32_t M = c.x->rows, N = c.w[0]->rows, K = c.x->cols;
+    if (dx) {
+        const entq_status st = check_out(dx, c.dy->type, lddx, M, K);
+        if (st != ENTQ_OK) return st;
+    }
+    if ((uintptr_t)ds0 % 4 || (uintptr_t)ds1 % 4) return ENTQ_EALIGN;
+    const entq_status st = check_workspace(ws, ws_bytes, workspace_bytes_of(c));
+    if (st != ENTQ_OK) return st;
+    if (M == 0 || N == 0 || K == 0) {
+        if (zero_rows(dx, c.dy->type, lddx, M, K, s) != ENTQ_OK) return ENTQ_EHIP;
+        if (zero_rows(ds0, ENTQ_F32, N, 1, N, s) != ENTQ_OK) return ENTQ_EHIP;
+        return zero_rows(ds1, ENTQ_F32, N, 1, N, s);
+    }
+    if (!dx && !ds0 && !ds1) return ENTQ_OK;
+    const Layout l = lay_out(c, ws);
+    Int8Args a = arguments(c);
+    const bool f16 = c.dy->type == ENTQ_F16;
+    if (f16 && dx) {
+        scale_norm<<<1, 1024, 0, s>>>(a.sw[0], a.sw[1], N, l.norm);
+        a.norm = l.norm;
+    }
+    a.act = act;
+    a.y = const_cast<void *>(c.dy->d_data);
+    a.type = c.dy->type;
+    a.ldy = c.dy->ld;
+    a.vec = vec4(a.y, a.ldy, a.type);
+    a.ldd = l.ldd;
+    for (int i = 0; i < c.n_w; ++i) {
+        a.d[i] = dx ? l.d[i] : nullptr;
+        a.part[i] = (i ? ds1 : ds0) ? l.part[i] : nullptr;
+    }
+    int r = launch_int8_product(c.mode, a, s);
+    if (r != ENTQ_OK) return (entq_status)r;
+    if (ds0 || ds1) {
+        sum_parts<<<dim3((N + 255) / 256, c.n_w), 256, 0, s>>>(l.part[0], l.part[1], int8_token_blocks(M), N, ds0,
+                                                               ds1);
+        if (hipGetLastError() != hipSuccess) return ENTQ_EHIP;
+    }
+    if (!dx) return ENTQ_OK;
+    GradArgs g{};
+    for (int i = 0; i < c.n_w; ++i) {
+        g.d[i] = l.d[i];
+        g.w[i] = a.w[i];
+        g.ldw[i] = a.ldw[i];
+    }
+    g.ldd = l.ldd;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.n_w = c.n_w;
+    g.f16 = f16;
+    g.dx = dx;
+    g.lddx = lddx;
+    g.vec = vec4(dx, lddx, c.dy->type);
+    g.norm = a.norm;
+    return (entq_status)launch_grad_product(g, s);
+}
+
+bool bad_act(int act) { return act < ENTQ_ACT_SILU || act > ENTQ_ACT_RELU; }
+
+}  // namespace
+}  // namespace entq
+
+using entq::describe;
+
+extern "C" {
+
+entq_status entq_quantize_rows(const entq_rows *x, int8_t *d_codes, uint64_t ldc, float *d_scales,
+                               void *stream) {
+    const entq_status st = entq::check_rows(x, true, false);
+    if (st != ENTQ_OK) return st;
+    if (ldc < x->cols || ldc > (1ull << 40)) return ENTQ_EINVAL;
+    if (x->rows && ((x->cols && !d_codes) || !d_scales)) return ENTQ_EINVAL;
+    if ((uintptr_t)d_scales % 4) return ENTQ_EALIGN;
+    return (entq_status)entq::launch_quantize(*x, d_codes, ldc, x->cols, d_scales, (hipStream_t)stream);
+}
+
+uint64_t entq_int8_gemm_workspace_bytes(const entq_rows *x, const entq_rows *w) {
+    return entq::workspace_bytes_of(describe(entq::kFwd, x, w, nullptr, nullptr));
+}
+
+entq_status entq_int8_gemm(const entq_rows *x, const entq_rows *w, void *d_y, int y_type, uint64_t ldy,
+                           void *d_workspace, uint64_t workspace_bytes, void *stream) {
+    return entq::forward(describe(entq::kFwd, x, w, nullptr, nullptr), 0, d_y, y_type, ldy, d_workspace,
+                         workspace_bytes, (hipStream_t)stream);
+}
+
+uint64_t entq_int8_gated_workspace_bytes(const entq_rows *x, const entq_rows *gate, const entq_rows *up) {
+    return entq::workspace_bytes_of(describe(entq::kGated, x, gate, up, nullptr));
+}
+
+entq_status entq_int8_gated(const entq_rows *x, const entq_rows *gate, const entq_rows *up, int activation,
+                            void *d_h, int h_type, uint64_t ldh, void *d_workspace, uint64_t workspace_bytes,
+                            void *stream) {
+    if (entq::bad_act(activation)) return ENTQ_EINVAL;
+    return entq::forward(describe(entq::kGated, x, gate, up, nullptr), activation, d_h, h_type, ldh, d_workspace,
+                         workspace_bytes, (hipStream_t)stream);
+}
+
+uint64_t entq_int8_gemm_backward_workspace_bytes(const entq_rows *dy, const entq_rows *x, const entq_rows *w) {
+    return entq::workspace_bytes_of(describe(entq::kBwd, x, w, nullptr, dy));
+}
+
+entq_status entq_int8_gemm_backward(const entq_rows *dy, const entq_rows *x, const entq_rows *w, void *d_dx,
+                                    uint64_t lddx, float *d_dw_scales, void *d_workspace,
+                                    uint64_t workspace_bytes, void *stream) {
+    return entq::backward(describe(entq::kBwd, x, w, nullptr, dy), 0, d_dx, lddx, d_dw_scales, nullptr,
+                          d_workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+uint64_t entq_int8_gated_backward_workspace_bytes(const entq_rows *dh, const entq_rows *x, const entq_rows *gate,
+                                                  const entq_rows *up) {
+    return entq::workspace_bytes_of(describe(entq::kGatedBwd, x, gate, up, dh));
+}
+
+entq_status entq_int8_gated_backward(const entq_rows *dh, const entq_rows *x, const entq_rows *gate,
+                                     const entq_rows *up, int activation, void *d_dx, uint64_t lddx,
+                                     float *d_dgate_scales, float *d_dup_scales, void *d_workspace,
+                                     uint64_t workspace_bytes, void *stream) {
+    if (entq::bad_act(activation)) return ENTQ_EINVAL;
+    return entq::backward(describe(entq::kGatedBwd, x, gate, up, dh), activation, d_dx, lddx, d_dgate_scales,
+                          d_dup_scales, d_workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -600,6 +600,108 @@ typedef struct {
 entq_status entq_pack_device_adaptive_batch(const entq_pack_adaptive_job *jobs, int n_jobs,
                                             void *d_blob, void *stream);
 
+/* ---- Products on int8 codes ----
+ *
+ * entq_decode's ENTQ_OUT_CODES leaves a tensor's Int8 codes row-major in
+ * device memory; with the per-row scales they are the weights W[n][k] =
+ * sw[n] w[n][k]. The calls below take such codes as they are, quantise the
+ * activations to int8 with one scale per row (token) and multiply on the
+ * int8 matrix cores, whose sums are exact in int32. All are enqueued on
+ * stream, allocate nothing, and are deterministic: the same inputs give the
+ * same bits. Results never overlap inputs or each other. */
+
+typedef enum { ENTQ_BF16 = 0, ENTQ_F16 = 1, ENTQ_F32 = 2, ENTQ_I8 = 3 } entq_eltype;
+
+typedef enum {
+    ENTQ_ACT_SILU = 0,       /* g / (1 + exp(-g))                                    */
+    ENTQ_ACT_GELU = 1,       /* g (1 + erf(g / sqrt 2)) / 2                          */
+    ENTQ_ACT_GELU_TANH = 2,  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2      */
+    ENTQ_ACT_RELU = 3        /* g for g > 0, else 0 (gradient 0 at 0)                */
+} entq_activation;
+
+/* A row-major matrix in device memory: element (r, c) at index r ld + c of
+ * d_data (ld >= cols, in elements; any alignment of the element's size).
+ * ENTQ_I8: codes with d_scales[rows]; the other types are activations and
+ * d_scales is NULL. cols <= ENTQ_INT8_MAX_COLS, which keeps every sum of
+ * code products inside int32. */
+typedef struct {
+    const void *d_data;
+    uint64_t ld;
+    const float *d_scales;
+    uint32_t rows, cols;
+    int32_t type;            /* entq_eltype */
+    uint32_t reserved;       /* 0 */
+} entq_rows;
+
+#define ENTQ_INT8_MAX_COLS 131071u
+
+/* Codes and scales of activation rows: for row r with a = max_c |x[r][c]|,
+ *   scale[r] = max(fl(a fl(1/127)), 2^-100),
+ *   code[r][c] = rint(fl(x[r][c] fl(1 / scale[r]))) clamped to +-127,
+ * fl() rounding to fp32 and rint() half to even: codes are the same whatever
+ * kernel computes them. A row that holds a NaN or an infinity gets the scale
+ * NaN and codes 0, so every result made from it is NaN. x: BF16, F16 or F32.
+ * d_codes: int8 [rows][ldc >= cols]; d_scales: fp32 [rows]. */
+entq_status entq_quantize_rows(const entq_rows *x, int8_t *d_codes, uint64_t ldc,
+                               float *d_scales, void *stream);
+
+/* Y = X . W^T: y[m][n] = sx[m] sw[n] sum_k x[m][k] w[n][k], the sum exact in
+ * int32, scaled in fp32 as (sum sx) sw and rounded once to y_type (BF16, F16
+ * or F32). x: [M][K] codes with scales, or activations (then quantised as
+ * entq_quantize_rows does, inside the call). w: [N][K], ENTQ_I8. d_y:
+ * [M][ldy >= N]. K = 0 gives zeros. */
+uint64_t entq_int8_gemm_workspace_bytes(const entq_rows *x, const entq_rows *w);
+entq_status entq_int8_gemm(const entq_rows *x, const entq_rows *w, void *d_y, int y_type,
+                           uint64_t ldy, void *d_workspace, uint64_t workspace_bytes,
+                           void *stream);
+
+/* The gated feed-forward products in one kernel: with g = X . gate^T and
+ * u = X . up^T as entq_int8_gemm computes them (before its rounding),
+ * h[m][n] = act(g[m][n]) u[m][n], rounded once to h_type. gate and up have
+ * the same shape. */
+uint64_t entq_int8_gated_workspace_bytes(const entq_rows *x, const entq_rows *gate,
+                                         const entq_rows *up);
+entq_status entq_int8_gated(const entq_rows *x, const entq_rows *gate, const entq_rows *up,
+                            int activation, void *d_h, int h_type, uint64_t ldh,
+                            void *d_workspace, uint64_t workspace_bytes, void *stream);
+
+/* Gradients of entq_int8_gemm for dy = dL/dY, [M][N] of type BF16 or F16.
+ * The weight codes are constants and the quantiser of x is passed straight
+ * through:
+ *   dx[m][k] = sum_n (dy[m][n] sw[n]) w[n][k]      (dy's type, [M][lddx >= K])
+ *   dsw[n] = sum_m dy[m][n] sx[m] sum_k x[m][k] w[n][k]          (fp32, [N])
+ * dy sw is rounded to dy's type (F16: after division by a power of two, the
+ * same for all n, that keeps it in range) for the 16-bit matrix cores, sums
+ * are fp32. x: the codes and scales the forward pass used (ENTQ_I8).
+ * d_dx or d_dw_scales may be NULL: that gradient is not computed. M = 0
+ * leaves dsw = 0; N = 0 leaves dx = 0. */
+uint64_t entq_int8_gemm_backward_workspace_bytes(const entq_rows *dy, const entq_rows *x,
+                                                 const entq_rows *w);
+entq_status entq_int8_gemm_backward(const entq_rows *dy, const entq_rows *x, const entq_rows *w,
+                                    void *d_dx, uint64_t lddx, float *d_dw_scales,
+                                    void *d_workspace, uint64_t workspace_bytes, void *stream);
+
+/* Gradients of entq_int8_gated for dh = dL/dH, [M][N] of type BF16 or F16; g
+ * and u are computed again. With dg = dh u act'(g), du = dh act(g):
+ *   dx[m][k] = sum_n (dg[m][n] sg[n]) gate[n][k] + (du[m][n] su[n]) up[n][k]
+ *   dsg[n] = sum_m dg[m][n] g[m][n] / sg[n], dsu[n] likewise (without the
+ *   division: g / sg is the scaled sum before its channel scale).
+ * Rounding, NULL gradients and empty sizes as entq_int8_gemm_backward. */
+uint64_t entq_int8_gated_backward_workspace_bytes(const entq_rows *dh, const entq_rows *x,
+                                                  const entq_rows *gate, const entq_rows *up);
+entq_status entq_int8_gated_backward(const entq_rows *dh, const entq_rows *x,
+                                     const entq_rows *gate, const entq_rows *up, int activation,
+                                     void *d_dx, uint64_t lddx, float *d_dgate_scales,
+                                     float *d_dup_scales, void *d_workspace,
+                                     uint64_t workspace_bytes, void *stream);
+
+/* The workspace of the four calls: 256-byte aligned (else ENTQ_EALIGN), at
+ * least what the call's _workspace_bytes function returns for the same
+ * matrices (else ENTQ_EWORKSPACE; 0 means NULL is fine, or invalid
+ * arguments), not used by other work while the call runs. It holds quantised
+ * activations, 16-byte aligned copies of matrices whose rows are not, partial
+ * sums, and in a backward call the scaled gradients. */
+
 #ifdef __cplusplus
 }
 #endif
