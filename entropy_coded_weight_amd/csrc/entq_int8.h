@@ -51,6 +51,27 @@ __device__ __forceinline__ float from16(uint16_t b, bool f16) {
     return f16 ? (float)__builtin_bit_cast(_Float16, b) : __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
+// Codes k..k+15 of a row of K codes at any address, zeros past its end. Reads
+// only aligned dwords that hold a byte of the row.
+__device__ __forceinline__ v4i load16_any(const int8_t *row, uint32_t k, uint32_t K) {
+    if (k >= K) return v4i{0, 0, 0, 0};
+    const uintptr_t at = (uintptr_t)row + k, end = (uintptr_t)row + K;
+    const uint32_t shift = at % 4, n = min(16u, K - k);
+    const uint32_t *p = (const uint32_t *)(at - shift);
+    uint32_t d[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) d[i] = (uintptr_t)(p + i) < end ? p[i] : 0;
+    v4i v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t b = __builtin_amdgcn_alignbyte(d[i + 1], d[i], shift);
+        const int left = (int)n - 4 * i;
+        if (left < 4) b = left > 0 ? b & ((1u << (8 * left)) - 1) : 0;
+        v[i] = (int)b;
+    }
+    return v;
+}
+
 // act(v) and, for the backward pass, act'(v). exp is the hardware's 2^x after
 // a product with log2 e (relative error about 1e-7 times the exponent, which
 // is small where the result is not).
@@ -189,9 +210,16 @@ struct GradArgs {
     const float *norm;      // F16: result times norm[1]; or null
 };
 
-// Launchers; each returns an entq_status.
-int launch_int8_product(Int8Mode mode, const Int8Args &a, hipStream_t s);
+// How a product runs.
+struct Int8Plan {
+    int tile;               // tokens of a tile
+    uint32_t part_rows;     // rows of Int8Args::part
+};
+Int8Plan int8_plan(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K);
+
+// Launchers; each returns an entq_status. Rows of x and w must start at
+// multiples of 16 bytes, strides below 2^23, K be a multiple of 16.
+int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s);
 int launch_grad_product(const GradArgs &a, hipStream_t s);
-uint32_t int8_token_blocks(uint32_t M);  // rows of Int8Args::part
 
 }  // namespace entq

@@ -63,6 +63,31 @@ int launch_quantize(const entq_rows &x, int8_t *codes, uint64_t ldc, uint32_t pa
 }
 
 // ---------------------------------------------------------------------------
+// aligned copies
+// ---------------------------------------------------------------------------
+
+// Rows of K codes at any address into rows of ldc (a multiple of 16), zeros
+// after column K.
+__global__ __launch_bounds__(256) void align_rows(const int8_t *src, uint64_t ld, uint32_t rows, uint32_t K,
+                                                  int8_t *dst, uint32_t ldc) {
+    const uint32_t c = 16 * (blockIdx.x * 256 + threadIdx.x);
+    if (c >= ldc) return;
+    for (uint64_t r = blockIdx.y; r < rows; r += gridDim.y)
+        *(v4i *)(dst + r * ldc + c) = load16_any(src + r * ld, c, K);
+}
+
+int launch_align(const entq_rows &m, int8_t *dst, uint32_t ldc, hipStream_t s) {
+    align_rows<<<dim3((ldc / 16 + 255) / 256, std::min(m.rows, 65535u)), 256, 0, s>>>(
+        (const int8_t *)m.d_data, m.ld, m.rows, m.cols, dst, ldc);
+    return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
+}
+
+// Whether the products can read the codes where they are.
+bool direct(const entq_rows &m) {
+    return (uintptr_t)m.d_data % 16 == 0 && m.ld % 16 == 0 && m.cols % 16 == 0 && m.ld < (1u << 23);
+}
+
+// ---------------------------------------------------------------------------
 // backward helpers
 // ---------------------------------------------------------------------------
 
@@ -183,13 +208,16 @@ Call describe(Int8Mode mode, const entq_rows *x, const entq_rows *w0, const entq
 
 // What a call keeps in the workspace.
 struct Layout {
-    int8_t *codes;      // quantised activations, or null
+    int8_t *codes;      // quantised activations or an aligned copy of codes, or null
     float *scales;
     uint64_t ldc;
+    int8_t *w[2];       // aligned copies of weights, or null
+    uint32_t ldw;
     uint16_t *d[2];     // scaled gradients
     uint64_t ldd;
     float *part[2];
     float *norm;
+    Int8Plan plan;
     uint64_t bytes;
 };
 
@@ -199,14 +227,20 @@ Layout lay_out(const Call &c, void *ws) {
     const uint64_t M = c.x->rows, N = c.w[0]->rows;
     l.ldc = (c.x->cols + 127ull) / 128 * 128;
     l.ldd = (N + 63) / 64 * 64;
+    l.ldw = (c.x->cols + 15) / 16 * 16;
+    l.plan = int8_plan(c.mode, (uint32_t)M, (uint32_t)N, l.ldw);
     if (c.x->type != ENTQ_I8) {
         l.codes = p.take<int8_t>(M * l.ldc);
         l.scales = p.take<float>(M);
+    } else if (!direct(*c.x)) {
+        l.codes = p.take<int8_t>(M * l.ldc);
     }
+    for (int i = 0; i < c.n_w; ++i)
+        if (!direct(*c.w[i])) l.w[i] = p.take<int8_t>(N * l.ldw);
     if (c.mode == kBwd || c.mode == kGatedBwd) {
         for (int i = 0; i < c.n_w; ++i) {
             l.d[i] = p.take<uint16_t>(M * l.ldd);
-            l.part[i] = p.take<float>((uint64_t)int8_token_blocks((uint32_t)M) * N);
+            l.part[i] = p.take<float>((uint64_t)l.plan.part_rows * N);
         }
         l.norm = p.take<float>(2);
     }
@@ -227,20 +261,38 @@ entq_status zero_rows(void *p, int type, uint64_t ld, uint32_t rows, uint32_t co
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
-Int8Args arguments(const Call &c) {
-    Int8Args a{};
+// The products' operands: quantised or copied into the workspace where they
+// have to be.
+entq_status operands(const Call &c, const Layout &l, Int8Args &a, hipStream_t s) {
+    a = Int8Args{};
+    a.M = c.x->rows;
+    a.N = c.w[0]->rows;
+    a.K = l.ldw;
     a.x = (const int8_t *)c.x->d_data;
     a.sx = c.x->d_scales;
     a.ldx = c.x->ld;
-    for (int i = 0; i < c.n_w; ++i) {
-        a.w[i] = (const int8_t *)c.w[i]->d_data;
-        a.sw[i] = c.w[i]->d_scales;
-        a.ldw[i] = c.w[i]->ld;
+    int r = ENTQ_OK;
+    if (c.x->type != ENTQ_I8) {
+        r = launch_quantize(*c.x, l.codes, l.ldc, (uint32_t)l.ldc, l.scales, s);
+        a.sx = l.scales;
+    } else if (l.codes) {
+        r = launch_align(*c.x, l.codes, (uint32_t)l.ldc, s);
     }
-    a.M = c.x->rows;
-    a.N = c.w[0]->rows;
-    a.K = c.x->cols;
-    return a;
+    if (l.codes) {
+        a.x = l.codes;
+        a.ldx = l.ldc;
+    }
+    for (int i = 0; i < c.n_w && r == ENTQ_OK; ++i) {
+        a.w[i] = (const int8_t *)c.w[i]->d_data;
+        a.ldw[i] = c.w[i]->ld;
+        a.sw[i] = c.w[i]->d_scales;
+        if (l.w[i]) {
+            r = launch_align(*c.w[i], l.w[i], l.ldw, s);
+            a.w[i] = l.w[i];
+            a.ldw[i] = l.ldw;
+        }
+    }
+    return (entq_status)r;
 }
 
 entq_status check_workspace(const void *ws, uint64_t bytes, uint64_t need) {
@@ -258,20 +310,14 @@ entq_status forward(const Call &c, int act, void *y, int type, uint64_t ldy, voi
     if (c.x->rows == 0 || c.w[0]->rows == 0) return ENTQ_OK;
     if (c.x->cols == 0) return zero_rows(y, type, ldy, c.x->rows, c.w[0]->rows, s);
     const Layout l = lay_out(c, ws);
-    Int8Args a = arguments(c);
-    if (c.x->type != ENTQ_I8) {
-        const int q = launch_quantize(*c.x, l.codes, l.ldc, (uint32_t)l.ldc, l.scales, s);
-        if (q != ENTQ_OK) return (entq_status)q;
-        a.x = l.codes;
-        a.sx = l.scales;
-        a.ldx = l.ldc;
-    }
+    Int8Args a;
+    if ((st = operands(c, l, a, s)) != ENTQ_OK) return st;
     a.act = act;
     a.y = y;
     a.type = type;
     a.ldy = ldy;
     a.vec = vec4(y, ldy, type);
-    return (entq_status)launch_int8_product(c.mode, a, s);
+    return (entq_status)launch_int8_product(c.mode, l.plan, a, s);
 }
 
 entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0, float *ds1, void *ws,
@@ -283,7 +329,7 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
         if (st != ENTQ_OK) return st;
     }
     if ((uintptr_t)ds0 % 4 || (uintptr_t)ds1 % 4) return ENTQ_EALIGN;
-    const entq_status st = check_workspace(ws, ws_bytes, workspace_bytes_of(c));
+    entq_status st = check_workspace(ws, ws_bytes, workspace_bytes_of(c));
     if (st != ENTQ_OK) return st;
     if (M == 0 || N == 0 || K == 0) {
         if (zero_rows(dx, c.dy->type, lddx, M, K, s) != ENTQ_OK) return ENTQ_EHIP;
@@ -292,7 +338,8 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     }
     if (!dx && !ds0 && !ds1) return ENTQ_OK;
     const Layout l = lay_out(c, ws);
-    Int8Args a = arguments(c);
+    Int8Args a;
+    if ((st = operands(c, l, a, s)) != ENTQ_OK) return st;
     const bool f16 = c.dy->type == ENTQ_F16;
     if (f16 && dx) {
         scale_norm<<<1, 1024, 0, s>>>(a.sw[0], a.sw[1], N, l.norm);
@@ -308,10 +355,10 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
         a.d[i] = dx ? l.d[i] : nullptr;
         a.part[i] = (i ? ds1 : ds0) ? l.part[i] : nullptr;
     }
-    int r = launch_int8_product(c.mode, a, s);
+    int r = launch_int8_product(c.mode, l.plan, a, s);
     if (r != ENTQ_OK) return (entq_status)r;
     if (ds0 || ds1) {
-        sum_parts<<<dim3((N + 255) / 256, c.n_w), 256, 0, s>>>(l.part[0], l.part[1], int8_token_blocks(M), N, ds0,
+        sum_parts<<<dim3((N + 255) / 256, c.n_w), 256, 0, s>>>(l.part[0], l.part[1], l.plan.part_rows, N, ds0,
                                                                ds1);
         if (hipGetLastError() != hipSuccess) return ENTQ_EHIP;
     }

@@ -1,83 +1,171 @@
 // entq_int8_gemm.hip -- products of int8 activation codes with int8 weight
 // codes, with the epilogues of the forward and backward calls.
-#include "entq_int8.h"
+#include <algorithm>
+
+#include "entq_int8_tile.h"
 
 namespace entq {
 namespace {
 
-constexpr uint32_t kTile = 64;  // tokens and channels of a workgroup's tile
-
-// 16 codes of row r, columns k..k+15; zeros outside the matrix.
-__device__ __forceinline__ v4i load16(const int8_t *p, uint64_t ld, uint32_t r, uint32_t rows,
-                                      uint32_t k, uint32_t K) {
-    v4i v = {0, 0, 0, 0};
-    if (r >= rows || k >= K) return v;
-    const int8_t *q = p + (uint64_t)r * ld + k;
-    if (k + 16 <= K && (uintptr_t)q % 16 == 0) return *(const v4i *)q;
-    uint32_t b[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (k + i < K) b[i / 4] |= (uint32_t)(uint8_t)q[i] << (8 * (i % 4));
-    return v4i{(int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-
-template <int MODE>
-__global__ __launch_bounds__(256) void int8_product(Int8Args a) {
-    constexpr int kW = MODE == kGated || MODE == kGatedBwd ? 2 : 1;
+// A workgroup of 4 waves (WM x WN) computes BM tokens x BN weight rows; a
+// gated tile's rows alternate 32 of gate and 32 of up, so that a lane's
+// fragments hold both sums of a channel. K goes by in steps of 128 codes in
+// two LDS stages. Weights are the matrix instruction's first operand: a lane's
+// results are 4 consecutive channels of one token.
+template <int MODE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uint32_t nb_n) {
+    constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
     constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
-    __shared__ v4i xs[kTile][5], ws[kW][kTile][5];
-    const uint32_t t = threadIdx.x, lane = t % 64, wave = t / 64;
-    const uint32_t n0 = blockIdx.x * kTile, m0 = blockIdx.y * kTile;
-    const uint32_t row = t / 4, chunk = t % 4;
-    v4i acc[kW][4] = {};
-    for (uint32_t k0 = 0; k0 < a.K; k0 += 64) {
-        xs[row][chunk] = load16(a.x, a.ldx, m0 + row, a.M, k0 + 16 * chunk, a.K);
+    constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
+    constexpr int kLoads = (BM + BN) / 32;  // of a wave and step: 8 rows each
+    constexpr uint32_t kStage = (BM + BN) * kRowBytes;
+    constexpr uint32_t kChannels = kTwo ? BN / 2 : BN;
+    static_assert(WM * WN == 4 && (!kTwo || FN % 2 == 0), "");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+
+    const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t wm = wave % WM, wn = wave / WM;
+    uint32_t tm, tn;
+    tile_of(blockIdx.x, nb_m, nb_n, 8, tm, tn);
+    const uint32_t m0 = tm * BM, n0 = tn * kChannels;
+
+    // This wave's loads: rows 8 (4 i + wave) .. + 7 of the stage, tokens first.
+    // Lane l takes chunk (l % 8) ^ (l / 8) of row l / 8, which belongs at l.
+    const uint32_t kc = 16 * ((lane % 8) ^ (lane / 8));
+    uint32_t off[kLoads];
+    const int8_t *base[kLoads];
 #pragma unroll
-        for (int w = 0; w < kW; ++w)
-            ws[w][row][chunk] = load16(a.w[w], a.ldw[w], n0 + row, a.N, k0 + 16 * chunk, a.K);
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kW; ++w) {
-            const v4i wf = ws[w][wave * 16 + lane % 16][lane / 16];
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-                acc[w][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                    wf, xs[f * 16 + lane % 16][lane / 16], acc[w][f], 0, 0, 0);
+    for (int i = 0; i < kLoads; ++i) {
+        const uint32_t first = 8 * (4 * i + wave);
+        if (4 * i * 8 < BM) {
+            base[i] = a.x + (uint64_t)m0 * a.ldx;
+            off[i] = min(first + lane / 8, a.M - 1 - m0) * (uint32_t)a.ldx + kc;
+        } else {
+            const uint32_t r = first - BM, t = kTwo ? r / 32 % 2 : 0;
+            const uint32_t c = kTwo ? r / 64 * 32 + r % 32 : r;
+            base[i] = a.w[t] + (uint64_t)n0 * a.ldw[t];
+            off[i] = min(c + lane / 8, a.N - 1 - n0) * (uint32_t)a.ldw[t] + kc;
         }
-        __syncthreads();
     }
-    const uint32_t n = n0 + wave * 16 + lane / 16 * 4;
-    float sg[4] = {}, su[4] = {};
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
+    const uint32_t steps = (a.K + 127) / 128;
+    auto load = [&](uint32_t step) {
+        const uint32_t to = lds0 + (step & 1) * kStage + wave * 1024;
+        const uint32_t k0 = step * 128;
+        if (k0 + 128 <= a.K) {
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
-        epilogue4<MODE>(a, m0 + f * 16 + lane % 16, n, acc[0][f], acc[kW - 1][f], sg, su);
-    if constexpr (kBack) {
+            for (int i = 0; i < kLoads; ++i) load_lds16(base[i] + k0, off[i], to + i * 4096);
+        } else {
+            // past the row's end: tokens as zeros, weights as whatever is there
+            const bool in = k0 + kc < a.K;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) {
-            if (!a.part[w]) continue;
+            for (int i = 0; i < kLoads; ++i) {
+                if (in)
+                    load_lds16(base[i] + k0, off[i], to + i * 4096);
+                else if (4 * i * 8 < BM)
+                    *(__attribute__((address_space(3))) v4i *)(uintptr_t)(to + i * 4096 + lane * 16) = v4i{0, 0, 0, 0};
+            }
+        }
+    };
+
+    v16i acc[FN][FM] = {};
+    v4i xf[2][FM], wf[2][FN];
+    const uint32_t xrow = lds0 + (wm * (BM / WM) + lane % 32) * kRowBytes;
+    const uint32_t wrow = lds0 + (BM + wn * (BN / WN) + lane % 32) * kRowBytes;
+    auto fetch = [&](int set, uint32_t stage, int sub) {
+        const uint32_t c = stage * kStage + 16 * ((2 * sub + lane / 32) ^ (lane % 8));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float s = w ? su[i] : sg[i];
+        for (int f = 0; f < FN; ++f) wf[set][f] = read_lds16(wrow + c + f * 32 * kRowBytes);
 #pragma unroll
-                for (int o = 1; o < 16; o *= 2) s += __shfl_xor(s, o);
-                if (lane % 16 == 0 && n + i < a.N)
-                    a.part[w][(uint64_t)blockIdx.y * a.N + n + i] = s;
+        for (int f = 0; f < FM; ++f) xf[set][f] = read_lds16(xrow + c + f * 32 * kRowBytes);
+    };
+    auto multiply = [&](int set) {
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+#pragma unroll
+            for (int g = 0; g < FM; ++g)
+                acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[set][f], xf[set][g], acc[f][g], 0, 0, 0);
+    };
+
+    load(0);
+    wait_loads_and_meet();
+    if (steps > 1) load(1);
+    fetch(0, 0, 0);
+    for (uint32_t step = 0; step < steps; ++step) {
+        const uint32_t stage = step & 1;
+        fetch(1, stage, 1);
+        multiply(0);
+        fetch(0, stage, 2);
+        multiply(1);
+        fetch(1, stage, 3);
+        multiply(0);
+        // the stage is read, the next one has landed
+        wait_loads_and_meet();
+        if (step + 2 < steps) load(step + 2);
+        if (step + 1 < steps) fetch(0, stage ^ 1, 0);
+        multiply(1);
+    }
+
+#pragma unroll
+    for (int f = 0; f < FN; f += kTwo ? 2 : 1) {
+        const uint32_t r = wn * (BN / WN) + f * 32;
+        const uint32_t nf = n0 + (kTwo ? r / 64 * 32 : r) + lane / 32 * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float sg[4] = {}, su[4] = {};
+            const uint32_t n = nf + q * 8;
+#pragma unroll
+            for (int g = 0; g < FM; ++g) {
+                const v16i &p = acc[f][g], &p2 = acc[f + (kTwo ? 1 : 0)][g];
+                epilogue4<MODE>(a, m0 + wm * (BM / WM) + g * 32 + lane % 32, n,
+                                v4i{p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]},
+                                v4i{p2[4 * q], p2[4 * q + 1], p2[4 * q + 2], p2[4 * q + 3]}, sg, su);
+            }
+            if constexpr (kBack) {
+#pragma unroll
+                for (int w = 0; w < (kTwo ? 2 : 1); ++w) {
+                    if (!a.part[w]) continue;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float s = w ? su[i] : sg[i];
+#pragma unroll
+                        for (int o = 1; o < 32; o *= 2) s += __shfl_xor(s, o);
+                        if (lane % 32 == 0 && n + i < a.N)
+                            a.part[w][(uint64_t)(tm * WM + wm) * a.N + n + i] = s;
+                    }
+                }
             }
         }
     }
 }
 
+template <int BM, int BN, int WM, int WN>
+void launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
+    const bool two = mode == kGated || mode == kGatedBwd;
+    const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
+    const uint32_t ch = two ? BN / 2 : BN;
+    const uint32_t nb_m = (a.M + BM - 1) / BM, nb_n = (cols + ch - 1) / ch;
+    const dim3 grid(nb_m * nb_n);
+    if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kGated) int8_tiles<kGated, BM, BN, WM, WN><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kBwd) int8_tiles<kBwd, BM, BN, WM, WN><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kGatedBwd) int8_tiles<kGatedBwd, BM, BN, WM, WN><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+}
+
 }  // namespace
 
-uint32_t int8_token_blocks(uint32_t M) { return (M + kTile - 1) / kTile; }
+Int8Plan int8_plan(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K) {
+    Int8Plan p{};
+    const char *f = getenv("ENTQ_TILE");
+    p.tile = f ? atoi(f) : 256;
+    p.part_rows = (M + p.tile - 1) / p.tile * 2;
+    return p;
+}
 
-int launch_int8_product(Int8Mode mode, const Int8Args &a, hipStream_t s) {
-    const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
-    const dim3 grid((cols + kTile - 1) / kTile, int8_token_blocks(a.M));
-    if (mode == kFwd) int8_product<kFwd><<<grid, 256, 0, s>>>(a);
-    if (mode == kGated) int8_product<kGated><<<grid, 256, 0, s>>>(a);
-    if (mode == kBwd) int8_product<kBwd><<<grid, 256, 0, s>>>(a);
-    if (mode == kGatedBwd) int8_product<kGatedBwd><<<grid, 256, 0, s>>>(a);
+int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s) {
+    if (p.tile == 256) launch_tiles<256, 256, 2, 2>(mode, a, s);
+    if (p.tile == 128) launch_tiles<128, 128, 2, 2>(mode, a, s);
+    if (p.tile == 64) launch_tiles<64, 128, 2, 2>(mode, a, s);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 

@@ -1,0 +1,53 @@
+// entq_int8_tile.h -- what the tiled products share: direct global-to-LDS
+// loads of 128-byte row pieces and the order of a grid's tiles.
+#pragma once
+
+#include "entq_int8.h"
+
+namespace entq {
+
+// LDS rows of the tiles are 128 bytes: 8 chunks of 16. Chunk c of row r lies
+// at position c ^ (r & 7), so that 8 consecutive rows read at one chunk touch
+// all 32 banks once (ds_read_b128 takes 8 lanes at a time).
+constexpr uint32_t kRowBytes = 128;
+
+// One 16-byte load per active lane from base + offset straight into LDS at
+// lds + 16 lane. The compiler does not count this load: wait_loads() does.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_lds16(const void *base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Every load of this wave has landed and every LDS read of it is done; then
+// all waves of the workgroup are here.
+__device__ __forceinline__ void wait_loads_and_meet() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_offset(const void *p) { return (uint32_t)(uintptr_t)p; }
+
+__device__ __forceinline__ v4i read_lds16(uint32_t at) {
+    return *(const __attribute__((address_space(3))) v4i *)(uintptr_t)at;
+}
+
+// Workgroup `id` of a grid of nb_a x nb_b tiles -> its tile. Workgroups go to
+// the 8 XCDs in turn; each XCD takes one contiguous piece of the tiles, ordered
+// so that the tiles it runs together form a block of at most `band` tiles
+// along a, which share their operands in the XCD's L2.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t nb_a, uint32_t nb_b, uint32_t band,
+                                        uint32_t &ta, uint32_t &tb) {
+    const uint32_t total = nb_a * nb_b, xcd = id % 8, i = id / 8;
+    const uint32_t q = total / 8, r = total % 8;
+    const uint32_t t = xcd * q + min(xcd, r) + i;
+    const uint32_t group = t / (band * nb_b), first = group * band;
+    const uint32_t in = min(band, nb_a - first), rest = t - group * band * nb_b;
+    ta = first + rest % in;
+    tb = rest / in;
+}
+
+}  // namespace entq
