@@ -49,22 +49,23 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
     const uint32_t steps = (a.K + 127) / 128;
+    auto load_one = [&](int i, uint32_t step) {
+        load_lds16(base[i] + step * 128, off[i], lds0 + (step & 1) * kStage + wave * 1024 + i * 4096);
+    };
     auto load = [&](uint32_t step) {
-        const uint32_t to = lds0 + (step & 1) * kStage + wave * 1024;
-        const uint32_t k0 = step * 128;
-        if (k0 + 128 <= a.K) {
+        if (step * 128 + 128 <= a.K) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) load_lds16(base[i] + k0, off[i], to + i * 4096);
-        } else {
-            // past the row's end: tokens as zeros, weights as whatever is there
-            const bool in = k0 + kc < a.K;
+            for (int i = 0; i < kLoads; ++i) load_one(i, step);
+            return;
+        }
+        // past the row's end: tokens as zeros, weights as whatever is there
+        const bool in = step * 128 + kc < a.K;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                if (in)
-                    load_lds16(base[i] + k0, off[i], to + i * 4096);
-                else if (4 * i * 8 < BM)
-                    *(__attribute__((address_space(3))) v4i *)(uintptr_t)(to + i * 4096 + lane * 16) = v4i{0, 0, 0, 0};
-            }
+        for (int i = 0; i < kLoads; ++i) {
+            if (in)
+                load_one(i, step);
+            else if (4 * i * 8 < BM)
+                *(v4i *)(lds + (step & 1) * kStage + wave * 1024 + i * 4096 + lane * 16) = v4i{0, 0, 0, 0};
         }
     };
 
@@ -72,68 +73,97 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     v4i xf[2][FM], wf[2][FN];
     const uint32_t xrow = lds0 + (wm * (BM / WM) + lane % 32) * kRowBytes;
     const uint32_t wrow = lds0 + (BM + wn * (BN / WN) + lane % 32) * kRowBytes;
-    auto fetch = [&](int set, uint32_t stage, int sub) {
+    // fragment j of a quarter step: in the order in which they are needed
+    auto fetch_one = [&](int set, uint32_t stage, int sub, int j) {
         const uint32_t c = stage * kStage + 16 * ((2 * sub + lane / 32) ^ (lane % 8));
-#pragma unroll
-        for (int f = 0; f < FN; ++f) wf[set][f] = read_lds16(wrow + c + f * 32 * kRowBytes);
-#pragma unroll
-        for (int f = 0; f < FM; ++f) xf[set][f] = read_lds16(xrow + c + f * 32 * kRowBytes);
+        if (j == 0 || j > FM)
+            wf[set][j ? j - FM : 0] = read_lds16(wrow + c + (j ? j - FM : 0) * 32 * kRowBytes);
+        else
+            xf[set][j - 1] = read_lds16(xrow + c + (j - 1) * 32 * kRowBytes);
     };
-    auto multiply = [&](int set) {
+    // A quarter step: the products of one fragment set, with the next set's
+    // reads and (LOAD) the loads of a later step between them. The order is
+    // fixed: left alone, the compiler reads each fragment right before its
+    // use and waits for it.
+    auto quarter = [&](int set, bool fetch, uint32_t stage, int sub, bool loads, uint32_t step) {
+        constexpr int kMul = FN * FM, kFetch = FN + FM;
 #pragma unroll
-        for (int f = 0; f < FN; ++f)
+        for (int i = 0; i < kMul; ++i) {
 #pragma unroll
-            for (int g = 0; g < FM; ++g)
-                acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[set][f], xf[set][g], acc[f][g], 0, 0, 0);
+            for (int j = i * kFetch / kMul; j < (i + 1) * kFetch / kMul; ++j)
+                if (fetch) fetch_one(set ^ 1, stage, sub, j);
+#pragma unroll
+            for (int j = i * kLoads / kMul; j < (i + 1) * kLoads / kMul; ++j)
+                if (loads) load_one(j, step);
+            acc[i / FM][i % FM] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[set][i / FM], xf[set][i % FM],
+                                                                        acc[i / FM][i % FM], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
 
     load(0);
     wait_loads_and_meet();
     if (steps > 1) load(1);
-    fetch(0, 0, 0);
-    for (uint32_t step = 0; step < steps; ++step) {
+#pragma unroll
+    for (int j = 0; j < FN + FM; ++j) fetch_one(0, 0, 0, j);
+    uint32_t step = 0;
+    for (; step + 3 < steps; ++step) {
         const uint32_t stage = step & 1;
-        fetch(1, stage, 1);
-        multiply(0);
-        fetch(0, stage, 2);
-        multiply(1);
-        fetch(1, stage, 3);
-        multiply(0);
-        // the stage is read, the next one has landed
+        quarter(0, true, stage, 1, false, 0);
+        quarter(1, true, stage, 2, false, 0);
+        quarter(0, true, stage, 3, false, 0);
+        // this stage is read, the next one has landed
+        wait_loads_and_meet();
+        quarter(1, true, stage ^ 1, 0, true, step + 2);
+    }
+#pragma unroll 1
+    for (; step < steps; ++step) {
+        const uint32_t stage = step & 1;
+        quarter(0, true, stage, 1, false, 0);
+        quarter(1, true, stage, 2, false, 0);
+        quarter(0, true, stage, 3, false, 0);
         wait_loads_and_meet();
         if (step + 2 < steps) load(step + 2);
-        if (step + 1 < steps) fetch(0, stage ^ 1, 0);
-        multiply(1);
+        quarter(1, true, stage ^ 1, 0, false, 0);  // (after the last step: read and not used)
     }
 
+    // The sums pass through LDS, 32 tokens of this wave at a time, so that
+    // neighbouring lanes then hold neighbouring channels of one token.
+    constexpr uint32_t kRow = FN * 128 + 16;                  // bytes of a token's sums; 16 spread the banks
+    constexpr uint32_t kQuads = FN * 8 / (kTwo ? 2 : 1);      // groups of 4 channels
+    constexpr uint32_t kTokens = 64 / kQuads;                 // that the wave handles at once
+    static_assert(4 * 32 * kRow <= 2 * kStage, "");
+    __syncthreads();
+    uint8_t *mine = lds + wave * 32 * kRow;
+    const uint32_t quad = lane % kQuads, r = wn * (BN / WN) + (kTwo ? quad / 8 * 64 : 0);
+    const uint32_t n = n0 + (kTwo ? r / 2 + quad % 8 * 4 : r + quad * 4);
+    const uint32_t at = kTwo ? quad / 8 * 256 + quad % 8 * 16 : quad * 16;
+    float sg[4] = {}, su[4] = {};
 #pragma unroll
-    for (int f = 0; f < FN; f += kTwo ? 2 : 1) {
-        const uint32_t r = wn * (BN / WN) + f * 32;
-        const uint32_t nf = n0 + (kTwo ? r / 64 * 32 : r) + lane / 32 * 4;
+    for (int g = 0; g < FM; ++g) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float sg[4] = {}, su[4] = {};
-            const uint32_t n = nf + q * 8;
+        for (int f = 0; f < FN; ++f)
 #pragma unroll
-            for (int g = 0; g < FM; ++g) {
-                const v16i &p = acc[f][g], &p2 = acc[f + (kTwo ? 1 : 0)][g];
-                epilogue4<MODE>(a, m0 + wm * (BM / WM) + g * 32 + lane % 32, n,
-                                v4i{p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]},
-                                v4i{p2[4 * q], p2[4 * q + 1], p2[4 * q + 2], p2[4 * q + 3]}, sg, su);
-            }
-            if constexpr (kBack) {
+            for (int q = 0; q < 4; ++q)
+                *(v4i *)(mine + lane % 32 * kRow + f * 128 + q * 32 + lane / 32 * 16) =
+                    v4i{acc[f][g][4 * q], acc[f][g][4 * q + 1], acc[f][g][4 * q + 2], acc[f][g][4 * q + 3]};
+#pragma unroll 1
+        for (uint32_t t = lane / kQuads; t < 32; t += kTokens) {
+            const uint8_t *p = mine + t * kRow + at;
+            epilogue4<MODE>(a, m0 + wm * (BM / WM) + g * 32 + t, n, *(const v4i *)p,
+                            *(const v4i *)(p + (kTwo ? 128 : 0)), sg, su);
+        }
+    }
+    if constexpr (kBack) {
 #pragma unroll
-                for (int w = 0; w < (kTwo ? 2 : 1); ++w) {
-                    if (!a.part[w]) continue;
+        for (int w = 0; w < (kTwo ? 2 : 1); ++w) {
+            if (!a.part[w]) continue;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float s = w ? su[i] : sg[i];
+            for (int i = 0; i < 4; ++i) {
+                float s = w ? su[i] : sg[i];
 #pragma unroll
-                        for (int o = 1; o < 32; o *= 2) s += __shfl_xor(s, o);
-                        if (lane % 32 == 0 && n + i < a.N)
-                            a.part[w][(uint64_t)(tm * WM + wm) * a.N + n + i] = s;
-                    }
-                }
+                for (uint32_t o = kQuads; o < 64; o *= 2) s += __shfl_xor(s, o);
+                if (lane < kQuads && n + i < a.N) a.part[w][(uint64_t)(tm * WM + wm) * a.N + n + i] = s;
             }
         }
     }
