@@ -51,33 +51,27 @@ __device__ __forceinline__ float from16(uint16_t b, bool f16) {
     return f16 ? (float)__builtin_bit_cast(_Float16, b) : __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
-// Codes k..k+15 of a row of K codes at any address, zeros past its end. Reads
-// only aligned dwords that hold a byte of the row.
+// 16 and 8 bytes at any address: the hardware takes unaligned vector accesses.
+struct __attribute__((packed)) any16 { v4i v; };
+struct __attribute__((packed)) any8 { v2i v; };
+struct __attribute__((packed)) any4 { int v; };
+
+// Codes k..k+15 of a row of K codes at any address, zeros past its end.
 __device__ __forceinline__ v4i load16_any(const int8_t *row, uint32_t k, uint32_t K) {
-    if (k >= K) return v4i{0, 0, 0, 0};
-    const uintptr_t at = (uintptr_t)row + k, end = (uintptr_t)row + K;
-    const uint32_t shift = at % 4, n = min(16u, K - k);
-    const uint32_t *p = (const uint32_t *)(at - shift);
-    uint32_t d[5];
+    if (k + 16 <= K) return ((const any16 *)(row + k))->v;
+    uint32_t b[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 5; ++i) d[i] = (uintptr_t)(p + i) < end ? p[i] : 0;
-    v4i v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t b = __builtin_amdgcn_alignbyte(d[i + 1], d[i], shift);
-        const int left = (int)n - 4 * i;
-        if (left < 4) b = left > 0 ? b & ((1u << (8 * left)) - 1) : 0;
-        v[i] = (int)b;
-    }
-    return v;
+    for (uint32_t i = 0; i < 15; ++i)
+        if (k + i < K) b[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
+    return v4i{(int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
 // act(v) and, for the backward pass, act'(v). exp is the hardware's 2^x after
 // a product with log2 e (relative error about 1e-7 times the exponent, which
-// is small where the result is not).
+// is small where the result is not), 1 / x the hardware's (1 ulp).
 __device__ __forceinline__ float act_and_grad(int act, float v, float &grad) {
     if (act == ENTQ_ACT_SILU) {
-        const float p = 1.0f / (1.0f + __expf(-v));
+        const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-v));
         grad = p * (1.0f + v * (1.0f - p));
         return v * p;
     }
@@ -89,7 +83,7 @@ __device__ __forceinline__ float act_and_grad(int act, float v, float &grad) {
     if (act == ENTQ_ACT_GELU_TANH) {
         // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
         const float z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
-        const float p = 1.0f / (1.0f + __expf(-z2));
+        const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z2));
         grad = p + v * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * v * v);
         return v * p;
     }
@@ -103,26 +97,30 @@ __device__ __forceinline__ float act_only(int act, float v) {
     return act_and_grad(act, v, grad);
 }
 
+// The scales of channels n..n+3, 0 beyond N.
+template <int MODE>
+__device__ __forceinline__ void load_scales(const Int8Args &a, uint32_t n, float (&scale)[2][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool in = n + i < a.N;
+        scale[0][i] = in ? a.sw[0][n + i] : 0.0f;
+        scale[1][i] = in && (MODE == kGated || MODE == kGatedBwd) ? a.sw[1][n + i] : 0.0f;
+    }
+}
+
 // The results for token m and the 4 channels n..n+3 (n a multiple of 4), or
 // the gradients, whose contributions to the channel sums are added to sg, su.
 // Channels of N and beyond are not stored; in a backward pass a token of M
 // and beyond adds nothing.
 template <int MODE>
-__device__ __forceinline__ void epilogue4(const Int8Args &a, uint32_t m, uint32_t n, v4i ag, v4i au,
-                                          float (&sg)[4], float (&su)[4]) {
+__device__ __forceinline__ void epilogue4(const Int8Args &a, const float (&scale)[2][4], float norm, uint32_t m,
+                                          uint32_t n, v4i ag, v4i au, float (&sg)[4], float (&su)[4]) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
     constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
     if (m >= a.M || n >= (kBack ? (uint32_t)a.ldd : a.N)) return;
     const bool whole = n + 4 <= a.N;
     const float sx = a.sx[m];
     const uint64_t at = (uint64_t)m * a.ldy + n;
-    float scale[2][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool in = n + i < a.N;
-        scale[0][i] = in ? a.sw[0][n + i] : 0.0f;
-        if (kTwo) scale[1][i] = in ? a.sw[1][n + i] : 0.0f;
-    }
     if constexpr (!kBack) {
         float v[4];
 #pragma unroll
@@ -163,7 +161,6 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, uint32_t m, uint32_
             for (int i = 0; i < 4; ++i)
                 if (n + i < a.N) b[i] = y[i];
         }
-        const float norm = a.norm ? a.norm[0] : 1.0f;
         uint16_t d[2][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -201,7 +198,10 @@ struct GradArgs {
     const uint16_t *d[2];   // [M][ldd], zero beyond column N
     const int8_t *w[2];     // [N][ldw]
     uint64_t ldd, ldw[2];
-    uint32_t M, N, K;       // N channels, K columns of the result
+    uint32_t M, N, K;       // N channels; K: the weights' columns, a multiple of 16
+    uint32_t cols;          // of the result, K or up to 15 fewer
+    uint32_t splits;        // of the sum; above 1, partial sums go to parts
+    float *parts;           // [splits][M][K]
     int n_w;                // 1 or 2
     bool f16;
     void *dx;               // [M][lddx], bf16 or f16
@@ -220,6 +220,12 @@ Int8Plan int8_plan(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K);
 // Launchers; each returns an entq_status. Rows of x and w must start at
 // multiples of 16 bytes, strides below 2^23, K be a multiple of 16.
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s);
-int launch_grad_product(const GradArgs &a, hipStream_t s);
+
+struct GradPlan {
+    int tile;
+    uint32_t splits;
+};
+GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, int n_w);
+int launch_grad_product(const GradPlan &p, const GradArgs &a, hipStream_t s);
 
 }  // namespace entq

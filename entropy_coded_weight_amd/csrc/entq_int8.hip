@@ -13,7 +13,6 @@ namespace {
 // ---------------------------------------------------------------------------
 
 constexpr float kMinScale = 0x1p-100f;  // its inverse is finite
-constexpr int kQuantThreads = 256;
 
 template <int TYPE>
 __device__ __forceinline__ float load_act(const void *x, uint64_t at) {
@@ -21,44 +20,115 @@ __device__ __forceinline__ float load_act(const void *x, uint64_t at) {
     return from16(((const uint16_t *)x)[at], TYPE == ENTQ_F16);
 }
 
-// One workgroup per row. The largest magnitude is found on the bits of |x|
-// as integers, where infinities and NaNs come out on top.
+// Element i of a 16-byte piece of activations.
 template <int TYPE>
-__global__ __launch_bounds__(kQuantThreads) void quantize_rows(const void *x, uint64_t ldx, uint32_t K,
-                                                               int8_t *codes, uint64_t ldc, uint32_t pad,
-                                                               float *scales) {
-    __shared__ uint32_t top[kQuantThreads / 64];
+__device__ __forceinline__ float act_of(v4i piece, int i) {
+    if (TYPE == ENTQ_F32) return __int_as_float(piece[i]);
+    return from16((uint16_t)((uint32_t)piece[i / 2] >> (16 * (i % 2))), TYPE == ENTQ_F16);
+}
+
+// One workgroup per row, which is read once: VECS pieces of 16 bytes a thread
+// stay in registers between the maximum and the rounding (VECS 0: any length,
+// read twice, the second time out of the L2). Pieces may lie at any address.
+// The largest magnitude is found on the bits of |x| as integers, where
+// infinities and NaNs come out on top. Columns K..pad-1 are written as 0.
+template <int TYPE, int VECS, int THREADS>
+__global__ __launch_bounds__(THREADS) void quantize_rows(const void *x, uint64_t ldx, uint32_t K, int8_t *codes,
+                                                         uint64_t ldc, uint32_t pad, float *scales) {
+    constexpr int kPer = TYPE == ENTQ_F32 ? 4 : 8, kBytes = TYPE == ENTQ_F32 ? 4 : 2;
+    __shared__ uint32_t top[THREADS / 64];
     const uint64_t row = blockIdx.x;
+    const uint8_t *src = (const uint8_t *)x + row * ldx * kBytes;
+    int8_t *dst = codes + row * ldc;
+    const uint32_t full = K / kPer;  // whole pieces
     uint32_t big = 0;
-    for (uint32_t c = threadIdx.x; c < K; c += kQuantThreads)
-        big = max(big, __float_as_uint(load_act<TYPE>(x, row * ldx + c)) & 0x7FFFFFFFu);
+    auto take = [&](float v) { big = max(big, __float_as_uint(v) & 0x7FFFFFFFu); };
+    auto piece = [&](uint32_t p) { return ((const any16 *)(src + (uint64_t)p * 16))->v; };
+    v4i held[VECS ? VECS : 1];
+    if (VECS) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const uint32_t p = i * THREADS + threadIdx.x;
+            held[i] = p < full ? piece(p) : v4i{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) take(act_of<TYPE>(held[i], e));
+    } else {
+        for (uint32_t p = threadIdx.x; p < full; p += THREADS) {
+            const v4i v = piece(p);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) take(act_of<TYPE>(v, e));
+        }
+    }
+    const uint32_t rest = full * kPer + threadIdx.x;  // the last columns, one a thread
+    float last = 0.0f;
+    if (rest < K) take(last = load_act<TYPE>(src, rest));
 #pragma unroll
     for (int o = 32; o; o /= 2) big = max(big, (uint32_t)__shfl_xor((int)big, o));
     if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQuantThreads / 64; ++i) big = max(big, top[i]);
+    for (int i = 0; i < THREADS / 64; ++i) big = max(big, top[i]);
     const bool finite = big < 0x7F800000u;
     const float scale = fmaxf(__uint_as_float(big) * (float)(1.0 / 127), kMinScale);
     const float inv = 1.0f / scale;
     if (threadIdx.x == 0) scales[row] = finite ? scale : __uint_as_float(0x7FC00000u);
-    for (uint32_t c = threadIdx.x; c < pad; c += kQuantThreads) {
-        float q = 0.0f;
-        if (finite && c < K) q = rintf(load_act<TYPE>(x, row * ldx + c) * inv);
-        codes[row * ldc + c] = (int8_t)fminf(fmaxf(q, -127.0f), 127.0f);
+    auto code = [&](float v) {
+        return finite ? (uint32_t)(int)fminf(fmaxf(rintf(v * inv), -127.0f), 127.0f) & 0xFFu : 0u;
+    };
+    auto put = [&](uint32_t p, v4i v) {
+        uint32_t b[2];
+#pragma unroll
+        for (int h = 0; h < kPer / 4; ++h)
+            b[h] = code(act_of<TYPE>(v, 4 * h)) | code(act_of<TYPE>(v, 4 * h + 1)) << 8 |
+                   code(act_of<TYPE>(v, 4 * h + 2)) << 16 | code(act_of<TYPE>(v, 4 * h + 3)) << 24;
+        if (kPer == 8)
+            ((any8 *)(dst + p * 8))->v = v2i{(int)b[0], (int)b[1]};
+        else
+            ((any4 *)(dst + p * 4))->v = (int)b[0];
+    };
+    if (VECS) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const uint32_t p = i * THREADS + threadIdx.x;
+            if (p < full) put(p, held[i]);
+        }
+    } else {
+        for (uint32_t p = threadIdx.x; p < full; p += THREADS) put(p, piece(p));
     }
+    if (rest < K) dst[rest] = (int8_t)code(last);
+    for (uint32_t c = K + threadIdx.x; c < pad; c += THREADS) dst[c] = 0;
+}
+
+template <int TYPE>
+void quantize_typed(const entq_rows &x, uint32_t rows, uint64_t skip, int8_t *codes, uint64_t ldc, uint32_t pad,
+                    float *scales, hipStream_t s) {
+    const void *p = (const uint8_t *)x.d_data + skip * x.ld * (TYPE == ENTQ_F32 ? 4 : 2);
+    int8_t *c = codes + skip * ldc;
+    float *sc = scales + skip;
+    const uint32_t pieces = x.cols / (TYPE == ENTQ_F32 ? 4 : 8);
+    const dim3 grid(rows);
+    if (pieces <= 256)
+        quantize_rows<TYPE, 1, 256><<<grid, 256, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc);
+    else if (pieces <= 1024)
+        quantize_rows<TYPE, 2, 512><<<grid, 512, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc);
+    else if (pieces <= 4096)
+        quantize_rows<TYPE, 4, 1024><<<grid, 1024, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc);
+    else
+        quantize_rows<TYPE, 0, 1024><<<grid, 1024, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc);
 }
 
 int launch_quantize(const entq_rows &x, int8_t *codes, uint64_t ldc, uint32_t pad, float *scales,
                     hipStream_t s) {
-    if (x.rows == 0) return ENTQ_OK;
-    const dim3 grid(x.rows);
-    if (x.type == ENTQ_BF16)
-        quantize_rows<ENTQ_BF16><<<grid, kQuantThreads, 0, s>>>(x.d_data, x.ld, x.cols, codes, ldc, pad, scales);
-    else if (x.type == ENTQ_F16)
-        quantize_rows<ENTQ_F16><<<grid, kQuantThreads, 0, s>>>(x.d_data, x.ld, x.cols, codes, ldc, pad, scales);
-    else
-        quantize_rows<ENTQ_F32><<<grid, kQuantThreads, 0, s>>>(x.d_data, x.ld, x.cols, codes, ldc, pad, scales);
+    constexpr uint32_t kRows = 1u << 20;  // a launch's threads stay below 2^32
+    for (uint64_t r = 0; r < x.rows; r += kRows) {
+        const uint32_t n = (uint32_t)std::min<uint64_t>(kRows, x.rows - r);
+        if (x.type == ENTQ_BF16) quantize_typed<ENTQ_BF16>(x, n, r, codes, ldc, pad, scales, s);
+        if (x.type == ENTQ_F16) quantize_typed<ENTQ_F16>(x, n, r, codes, ldc, pad, scales, s);
+        if (x.type == ENTQ_F32) quantize_typed<ENTQ_F32>(x, n, r, codes, ldc, pad, scales, s);
+    }
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
@@ -136,6 +206,10 @@ __global__ __launch_bounds__(256) void fill_zero(uint8_t *p, uint64_t ld, uint32
 // checks and layout
 // ---------------------------------------------------------------------------
 
+// Channels of a backward call: keeps byte offsets inside a tile of scaled
+// gradients below 2^32.
+constexpr uint32_t kMaxBackChannels = 1u << 22;
+
 uint32_t type_bytes(int t) { return t == ENTQ_F32 ? 4 : t == ENTQ_I8 ? 1 : 2; }
 
 entq_status check_rows(const entq_rows *r, bool acts, bool codes) {
@@ -200,6 +274,8 @@ Call describe(Int8Mode mode, const entq_rows *x, const entq_rows *w0, const entq
             dy->rows != x->rows || dy->cols != w0->rows || dy->ld < dy->cols || dy->ld > (1ull << 40) ||
             (dy->rows && dy->cols && !dy->d_data))
             c.bad = ENTQ_EINVAL;
+        else if (w0->rows > kMaxBackChannels)
+            c.bad = ENTQ_EINVAL;
         else if ((uintptr_t)dy->d_data % 2)
             c.bad = ENTQ_EALIGN;
     }
@@ -218,6 +294,8 @@ struct Layout {
     float *part[2];
     float *norm;
     Int8Plan plan;
+    GradPlan grad;
+    float *parts;       // partial sums of dX, or null
     uint64_t bytes;
 };
 
@@ -243,6 +321,8 @@ Layout lay_out(const Call &c, void *ws) {
             l.part[i] = p.take<float>((uint64_t)l.plan.part_rows * N);
         }
         l.norm = p.take<float>(2);
+        l.grad = grad_plan((uint32_t)M, (uint32_t)N, l.ldw, c.n_w);
+        if (l.grad.splits > 1) l.parts = p.take<float>((uint64_t)l.grad.splits * M * l.ldw);
     }
     l.bytes = p.used;
     return l;
@@ -372,14 +452,17 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     g.ldd = l.ldd;
     g.M = M;
     g.N = N;
-    g.K = K;
+    g.K = l.ldw;
+    g.cols = K;
+    g.splits = l.grad.splits;
+    g.parts = l.parts;
     g.n_w = c.n_w;
     g.f16 = f16;
     g.dx = dx;
     g.lddx = lddx;
     g.vec = vec4(dx, lddx, c.dy->type);
     g.norm = a.norm;
-    return (entq_status)launch_grad_product(g, s);
+    return (entq_status)launch_grad_product(l.grad, g, s);
 }
 
 bool bad_act(int act) { return act < ENTQ_ACT_SILU || act > ENTQ_ACT_RELU; }

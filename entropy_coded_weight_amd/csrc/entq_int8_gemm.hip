@@ -9,19 +9,29 @@ namespace {
 
 // A workgroup of 4 waves (WM x WN) computes BM tokens x BN weight rows; a
 // gated tile's rows alternate 32 of gate and 32 of up, so that a lane's
-// fragments hold both sums of a channel. K goes by in steps of 128 codes in
-// two LDS stages. Weights are the matrix instruction's first operand: a lane's
-// results are 4 consecutive channels of one token.
-template <int MODE, int BM, int BN, int WM, int WN>
+// fragments hold both sums of a channel. K goes by in steps of 128 codes.
+// Weights are the matrix instruction's first operand: a lane's results are 4
+// consecutive channels of one token.
+//
+// SX and SW steps of the two operands are kept in LDS (SX = SW or SW + 1).
+// Once a step is read by every wave its place is loaded again, a quarter of
+// the loads beside each quarter step of products: a CU takes about 24 cycles
+// per load instruction, and loads that wait for their turn hold up the
+// wave's products.
+template <int MODE, int BM, int BN, int WM, int WN, int SX, int SW>
 __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uint32_t nb_n) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
     constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
-    constexpr int kLoads = (BM + BN) / 32;  // of a wave and step: 8 rows each
-    constexpr uint32_t kStage = (BM + BN) * kRowBytes;
+    constexpr int kLoadsX = BM / 32, kLoadsW = BN / 32;  // of a wave and step: 8 rows each
+    constexpr uint32_t kStageX = BM * kRowBytes, kStageW = BN * kRowBytes;
+    constexpr uint32_t kLds = SX * kStageX + SW * kStageW;
     constexpr uint32_t kChannels = kTwo ? BN / 2 : BN;
-    static_assert(WM * WN == 4 && (!kTwo || FN % 2 == 0), "");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+    // loads that may be in flight while the next step is read: those issued
+    // after the last one of that step
+    constexpr int kFlying = (SX - SW) * kLoadsX + (SW - 2) * (kLoadsX + kLoadsW);
+    static_assert(WM * WN == 4 && (!kTwo || FN % 2 == 0) && (SX == SW || SX == SW + 1), "");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
 
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t wm = wave % WM, wn = wave / WM;
@@ -29,116 +39,154 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     tile_of(blockIdx.x, nb_m, nb_n, 8, tm, tn);
     const uint32_t m0 = tm * BM, n0 = tn * kChannels;
 
-    // This wave's loads: rows 8 (4 i + wave) .. + 7 of the stage, tokens first.
-    // Lane l takes chunk (l % 8) ^ (l / 8) of row l / 8, which belongs at l.
-    const uint32_t kc = 16 * ((lane % 8) ^ (lane / 8));
-    uint32_t off[kLoads];
-    const int8_t *base[kLoads];
+    // This wave's loads: rows 8 (4 i + wave) .. + 7 of a tile. Lane l fills
+    // position l % 8 of row l / 8.
+    const uint32_t kc = 16 * ((lane % 8) ^ swizzle(8 * wave + lane / 8));
+    uint32_t xoff[kLoadsX], woff[kLoadsW];
+    const int8_t *xbase = a.x + (uint64_t)m0 * a.ldx;
+    const int8_t *wbase[2] = {a.w[0] + (uint64_t)n0 * a.ldw[0],
+                              kTwo ? a.w[1] + (uint64_t)n0 * a.ldw[1] : nullptr};
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const uint32_t first = 8 * (4 * i + wave);
-        if (4 * i * 8 < BM) {
-            base[i] = a.x + (uint64_t)m0 * a.ldx;
-            off[i] = min(first + lane / 8, a.M - 1 - m0) * (uint32_t)a.ldx + kc;
-        } else {
-            const uint32_t r = first - BM, t = kTwo ? r / 32 % 2 : 0;
-            const uint32_t c = kTwo ? r / 64 * 32 + r % 32 : r;
-            base[i] = a.w[t] + (uint64_t)n0 * a.ldw[t];
-            off[i] = min(c + lane / 8, a.N - 1 - n0) * (uint32_t)a.ldw[t] + kc;
-        }
+    for (int i = 0; i < kLoadsX; ++i)
+        xoff[i] = min(8 * (4 * i + wave) + lane / 8, a.M - 1 - m0) * (uint32_t)a.ldx + kc;
+#pragma unroll
+    for (int i = 0; i < kLoadsW; ++i) {
+        const uint32_t r = 8 * (4 * i + wave), c = kTwo ? r / 64 * 32 + r % 32 : r;
+        woff[i] = min(c + lane / 8, a.N - 1 - n0) * (uint32_t)a.ldw[kTwo ? i % 2 : 0] + kc;
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
+    const uint32_t ldsw = lds0 + SX * kStageX;
     const uint32_t steps = (a.K + 127) / 128;
-    auto load_one = [&](int i, uint32_t step) {
-        load_lds16(base[i] + step * 128, off[i], lds0 + (step & 1) * kStage + wave * 1024 + i * 4096);
+    auto load_x = [&](int i, uint32_t step, uint32_t slot) {
+        load_lds16(xbase + step * 128, xoff[i], lds0 + slot * kStageX + wave * 1024 + i * 4096);
     };
-    auto load = [&](uint32_t step) {
-        if (step * 128 + 128 <= a.K) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) load_one(i, step);
-            return;
-        }
-        // past the row's end: tokens as zeros, weights as whatever is there
+    auto load_w = [&](int i, uint32_t step, uint32_t slot) {
+        load_lds16(wbase[kTwo ? i % 2 : 0] + step * 128, woff[i], ldsw + slot * kStageW + wave * 1024 + i * 4096);
+    };
+    // A whole step's loads; past the rows' end tokens are zeros and weights
+    // whatever is there.
+    auto load_step_x = [&](uint32_t step, uint32_t slot) {
         const bool in = step * 128 + kc < a.K;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
+        for (int i = 0; i < kLoadsX; ++i) {
             if (in)
-                load_one(i, step);
-            else if (4 * i * 8 < BM)
-                *(v4i *)(lds + (step & 1) * kStage + wave * 1024 + i * 4096 + lane * 16) = v4i{0, 0, 0, 0};
+                load_x(i, step, slot);
+            else
+                *(v4i *)(lds + slot * kStageX + wave * 1024 + i * 4096 + lane * 16) = v4i{0, 0, 0, 0};
+        }
+    };
+    auto load_step_w = [&](uint32_t step, uint32_t slot) {
+        if (step * 128 + kc < a.K) {
+#pragma unroll
+            for (int i = 0; i < kLoadsW; ++i) load_w(i, step, slot);
         }
     };
 
     v16i acc[FN][FM] = {};
     v4i xf[2][FM], wf[2][FN];
     const uint32_t xrow = lds0 + (wm * (BM / WM) + lane % 32) * kRowBytes;
-    const uint32_t wrow = lds0 + (BM + wn * (BN / WN) + lane % 32) * kRowBytes;
+    const uint32_t wrow = ldsw + (wn * (BN / WN) + lane % 32) * kRowBytes;
     // fragment j of a quarter step: in the order in which they are needed
-    auto fetch_one = [&](int set, uint32_t stage, int sub, int j) {
-        const uint32_t c = stage * kStage + 16 * ((2 * sub + lane / 32) ^ (lane % 8));
+    auto fetch_one = [&](int set, uint32_t sx, uint32_t sw, int sub, int j) {
+        const uint32_t c = 16 * ((2 * sub + lane / 32) ^ swizzle(lane % 32));
         if (j == 0 || j > FM)
-            wf[set][j ? j - FM : 0] = read_lds16(wrow + c + (j ? j - FM : 0) * 32 * kRowBytes);
+            wf[set][j ? j - FM : 0] = read_lds16(wrow + sw * kStageW + c + (j ? j - FM : 0) * 32 * kRowBytes);
         else
-            xf[set][j - 1] = read_lds16(xrow + c + (j - 1) * 32 * kRowBytes);
+            xf[set][j - 1] = read_lds16(xrow + sx * kStageX + c + (j - 1) * 32 * kRowBytes);
     };
-    // A quarter step: the products of one fragment set, with the next set's
-    // reads and (LOAD) the loads of a later step between them. The order is
-    // fixed: left alone, the compiler reads each fragment right before its
-    // use and waits for it.
-    auto quarter = [&](int set, bool fetch, uint32_t stage, int sub, bool loads, uint32_t step) {
-        constexpr int kMul = FN * FM, kFetch = FN + FM;
+    // A quarter step: the products of one fragment set, between them the
+    // reads of the next set (quarter `sub` of slots sx, sw) and, with part >=
+    // 0, that part of the loads of steps tw and tx into slots lw and lx. The
+    // order is fixed: left alone, the compiler reads each fragment right
+    // before its use and waits for it.
+    auto quarter = [&](int set, uint32_t sx, uint32_t sw, int sub, int part, uint32_t tx, uint32_t tw, uint32_t lx,
+                       uint32_t lw) {
+        constexpr int kMul = FN * FM, kFetch = FN + FM, kLoads = kLoadsX + kLoadsW;
 #pragma unroll
         for (int i = 0; i < kMul; ++i) {
 #pragma unroll
-            for (int j = i * kFetch / kMul; j < (i + 1) * kFetch / kMul; ++j)
-                if (fetch) fetch_one(set ^ 1, stage, sub, j);
+            for (int j = i * kFetch / kMul; j < (i + 1) * kFetch / kMul; ++j) fetch_one(set ^ 1, sx, sw, sub, j);
+            if (part >= 0) {
+                const int f = part * kMul + i;
 #pragma unroll
-            for (int j = i * kLoads / kMul; j < (i + 1) * kLoads / kMul; ++j)
-                if (loads) load_one(j, step);
+                for (int j = f * kLoads / (4 * kMul); j < (f + 1) * kLoads / (4 * kMul); ++j) {
+                    if (j < kLoadsW)
+                        load_w(j, tw, lw);
+                    else
+                        load_x(j - kLoadsW, tx, lx);
+                }
+            }
             acc[i / FM][i % FM] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[set][i / FM], xf[set][i % FM],
                                                                         acc[i / FM][i % FM], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    auto after = [](uint32_t slot, uint32_t slots) { return slot + 1 == slots ? 0 : slot + 1; };
 
-    load(0);
-    wait_loads_and_meet();
-    if (steps > 1) load(1);
+    for (uint32_t i = 0; i < SX; ++i) {
+        if (i < steps) load_step_x(i, i);
+        if (i < SW && i < steps) load_step_w(i, i);
+    }
+    // (the last step's loads may be fewer than kLoads: waits that could meet
+    // them in flight are for all)
+    if (steps > SX)
+        wait_loads_and_meet<(SX - 1) * kLoadsX + (SW - 1) * kLoadsW>();
+    else
+        wait_loads_and_meet<0>();
 #pragma unroll
-    for (int j = 0; j < FN + FM; ++j) fetch_one(0, 0, 0, j);
-    uint32_t step = 0;
-    for (; step + 3 < steps; ++step) {
-        const uint32_t stage = step & 1;
-        quarter(0, true, stage, 1, false, 0);
-        quarter(1, true, stage, 2, false, 0);
-        quarter(0, true, stage, 3, false, 0);
-        // this stage is read, the next one has landed
-        wait_loads_and_meet();
-        quarter(1, true, stage ^ 1, 0, true, step + 2);
+    for (int j = 0; j < FN + FM; ++j) fetch_one(0, 0, 0, 0, j);
+    uint32_t step = 0, sx = 0, sw = 0;
+    quarter(0, 0, 0, 1, -1, 0, 0, 0, 0);
+    quarter(1, 0, 0, 2, -1, 0, 0, 0, 0);
+    quarter(0, 0, 0, 3, -1, 0, 0, 0, 0);
+    if (steps > SX)
+        wait_loads_and_meet<kFlying>();
+    else
+        wait_loads_and_meet<0>();
+    // `step` is read except for its last quarter, which is in registers; the
+    // next step has landed
+    for (; step + SX + 1 < steps; ++step) {
+        const uint32_t nx = after(sx, SX), nw = after(sw, SW), tx = step + SX, tw = step + SW;
+        quarter(1, nx, nw, 0, 0, tx, tw, sx, sw);
+        quarter(0, nx, nw, 1, 1, tx, tw, sx, sw);
+        quarter(1, nx, nw, 2, 2, tx, tw, sx, sw);
+        quarter(0, nx, nw, 3, 3, tx, tw, sx, sw);
+        wait_loads_and_meet<kFlying>();
+        sx = nx;
+        sw = nw;
     }
 #pragma unroll 1
-    for (; step < steps; ++step) {
-        const uint32_t stage = step & 1;
-        quarter(0, true, stage, 1, false, 0);
-        quarter(1, true, stage, 2, false, 0);
-        quarter(0, true, stage, 3, false, 0);
-        wait_loads_and_meet();
-        if (step + 2 < steps) load(step + 2);
-        quarter(1, true, stage ^ 1, 0, false, 0);  // (after the last step: read and not used)
+    for (; step + 1 < steps; ++step) {
+        const uint32_t nx = after(sx, SX), nw = after(sw, SW);
+        if (step + SW < steps) load_step_w(step + SW, sw);
+        if (step + SX < steps) load_step_x(step + SX, sx);
+        quarter(1, nx, nw, 0, -1, 0, 0, 0, 0);
+        quarter(0, nx, nw, 1, -1, 0, 0, 0, 0);
+        quarter(1, nx, nw, 2, -1, 0, 0, 0, 0);
+        quarter(0, nx, nw, 3, -1, 0, 0, 0, 0);
+        wait_loads_and_meet<0>();
+        sx = nx;
+        sw = nw;
     }
+#pragma unroll
+    for (int i = 0; i < FN * FM; ++i)
+        acc[i / FM][i % FM] =
+            __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[1][i / FM], xf[1][i % FM], acc[i / FM][i % FM], 0, 0, 0);
 
     // The sums pass through LDS, 32 tokens of this wave at a time, so that
     // neighbouring lanes then hold neighbouring channels of one token.
     constexpr uint32_t kRow = FN * 128 + 16;                  // bytes of a token's sums; 16 spread the banks
     constexpr uint32_t kQuads = FN * 8 / (kTwo ? 2 : 1);      // groups of 4 channels
     constexpr uint32_t kTokens = 64 / kQuads;                 // that the wave handles at once
-    static_assert(4 * 32 * kRow <= 2 * kStage, "");
+    static_assert(4 * 32 * kRow <= kLds, "");
     __syncthreads();
     uint8_t *mine = lds + wave * 32 * kRow;
     const uint32_t quad = lane % kQuads, r = wn * (BN / WN) + (kTwo ? quad / 8 * 64 : 0);
     const uint32_t n = n0 + (kTwo ? r / 2 + quad % 8 * 4 : r + quad * 4);
     const uint32_t at = kTwo ? quad / 8 * 256 + quad % 8 * 16 : quad * 16;
-    float sg[4] = {}, su[4] = {};
+    float scale[2][4], sg[4] = {}, su[4] = {};
+    load_scales<MODE>(a, n, scale);
+    const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
 #pragma unroll
     for (int g = 0; g < FM; ++g) {
 #pragma unroll
@@ -150,7 +198,7 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
 #pragma unroll 1
         for (uint32_t t = lane / kQuads; t < 32; t += kTokens) {
             const uint8_t *p = mine + t * kRow + at;
-            epilogue4<MODE>(a, m0 + wm * (BM / WM) + g * 32 + t, n, *(const v4i *)p,
+            epilogue4<MODE>(a, scale, norm, m0 + wm * (BM / WM) + g * 32 + t, n, *(const v4i *)p,
                             *(const v4i *)(p + (kTwo ? 128 : 0)), sg, su);
         }
     }
@@ -169,17 +217,17 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int SX, int SW>
 void launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     const bool two = mode == kGated || mode == kGatedBwd;
     const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
     const uint32_t ch = two ? BN / 2 : BN;
     const uint32_t nb_m = (a.M + BM - 1) / BM, nb_n = (cols + ch - 1) / ch;
     const dim3 grid(nb_m * nb_n);
-    if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
-    if (mode == kGated) int8_tiles<kGated, BM, BN, WM, WN><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
-    if (mode == kBwd) int8_tiles<kBwd, BM, BN, WM, WN><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
-    if (mode == kGatedBwd) int8_tiles<kGatedBwd, BM, BN, WM, WN><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kGated) int8_tiles<kGated, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kBwd) int8_tiles<kBwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kGatedBwd) int8_tiles<kGatedBwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
 }
 
 }  // namespace
@@ -193,9 +241,9 @@ Int8Plan int8_plan(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K) {
 }
 
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s) {
-    if (p.tile == 256) launch_tiles<256, 256, 2, 2>(mode, a, s);
-    if (p.tile == 128) launch_tiles<128, 128, 2, 2>(mode, a, s);
-    if (p.tile == 64) launch_tiles<64, 128, 2, 2>(mode, a, s);
+    if (p.tile == 256) launch_tiles<256, 256, 2, 2, 3, 2>(mode, a, s);
+    if (p.tile == 128) launch_tiles<128, 128, 2, 2, 3, 2>(mode, a, s);
+    if (p.tile == 64) launch_tiles<64, 128, 2, 2, 3, 3>(mode, a, s);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 

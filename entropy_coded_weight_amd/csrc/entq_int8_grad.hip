@@ -1,72 +1,260 @@
-// entq_int8_grad.hip -- dX = d . W for 16-bit gradients d [M][N] and int8
-// codes W [N][K]: a product along the weights' rows.
-#include "entq_int8.h"
+// entq_int8_grad.hip -- dX = sum over the weights of d . W for 16-bit
+// gradients d [M][N] and int8 codes W [N][K]: a product along the weights'
+// rows.
+#include <algorithm>
+
+#include "entq_int8_tile.h"
 
 namespace entq {
 namespace {
 
-constexpr uint32_t kTile = 64;
-
+// 8 codes (two dwords) as 8 values of 16 bits; every code is exact in both
+// types.
 template <bool F16>
-__global__ __launch_bounds__(256) void grad_product(GradArgs a) {
-    __shared__ uint16_t ds[kTile][kTile + 8], wt[kTile][kTile + 8];  // wt: column of W, channel
-    const uint32_t t = threadIdx.x, lane = t % 64, wave = t / 64;
-    const uint32_t k0 = blockIdx.x * kTile, m0 = blockIdx.y * kTile;
-    v4f acc[4] = {};
-    for (int w = 0; w < a.n_w; ++w) {
-        for (uint32_t n0 = 0; n0 < a.N; n0 += kTile) {
+__device__ __forceinline__ v2i widen4(int codes) {
+    v2i r;
 #pragma unroll
-            for (uint32_t i = t; i < kTile * kTile / 4; i += 256) {
-                const uint32_t r = i / 16, c = i % 16 * 4;
-                *(uint2 *)&ds[r][c] = m0 + r < a.M
-                                          ? *(const uint2 *)(a.d[w] + (m0 + r) * a.ldd + n0 + c)
-                                          : make_uint2(0, 0);
-            }
-#pragma unroll
-            for (uint32_t i = t; i < kTile * kTile; i += 256) {
-                const uint32_t r = i / 64, c = i % 64;
-                const bool in = n0 + r < a.N && k0 + c < a.K;
-                wt[c][r] = bits16(in ? (float)a.w[w][(n0 + r) * a.ldw[w] + k0 + c] : 0.0f, F16);
-            }
-            __syncthreads();
-#pragma unroll
-            for (uint32_t s = 0; s < kTile; s += 32) {
-                const v4i wf = *(const v4i *)&wt[wave * 16 + lane % 16][s + lane / 16 * 8];
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const v4i df = *(const v4i *)&ds[f * 16 + lane % 16][s + lane / 16 * 8];
-                    if (F16)
-                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            __builtin_bit_cast(f16x8, wf), __builtin_bit_cast(f16x8, df), acc[f], 0,
-                            0, 0);
-                    else
-                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, wf), __builtin_bit_cast(bf16x8, df), acc[f],
-                            0, 0, 0);
-                }
-            }
-            __syncthreads();
+    for (int i = 0; i < 2; ++i) {
+        if (F16) {
+            // 0x6400 | u is 1024 + u for a byte u; u = code + 128
+            const uint32_t u = (uint32_t)codes ^ 0x80808080u;
+            const uint32_t h = __builtin_amdgcn_perm(0x64646464u, u, i ? 0x04030402u : 0x04010400u);
+            typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+            r[i] = __builtin_bit_cast(int, __builtin_bit_cast(f16x2, h) - f16x2{(_Float16)1152.0f, (_Float16)1152.0f});
+        } else {
+            const float lo = (float)(int8_t)(codes >> (16 * i)), hi = (float)(int8_t)(codes >> (16 * i + 8));
+            r[i] = (int)__builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
         }
     }
+    return r;
+}
+
+// A workgroup of 4 waves (WM x WN) computes BM tokens x BK columns. The sum
+// goes by in steps of 64 channels, the first weight's and then the second's;
+// S steps are kept in LDS. The weights stay int8 until they are in registers:
+// a transposing LDS read gives a lane 8 consecutive channels of its column,
+// which it widens to 16 bits (12 vector instructions per 8 codes, beside the
+// products of the fragments before).
+template <bool F16, int BM, int BK, int WM, int WN, int S>
+__global__ __launch_bounds__(256) void grad_tiles(GradArgs a, uint32_t nb_m, uint32_t nb_k) {
+    constexpr int FM = BM / WM / 32, FN = BK / WN / 32;
+    constexpr int kLoadsD = BM / 32, kLoadsW = BK / 64, kLoads = kLoadsD + kLoadsW;
+    constexpr uint32_t kStageD = BM * kRowBytes, kStageW = 64 * BK;
+    constexpr uint32_t kChunks = BK / 16, kRowsW = 64 / kChunks;  // of a weight row; of a wave's load
+    constexpr int kFlying = (S - 2) * kLoads;
+    static_assert(WM * WN == 4 && (BK == 256 || BK == 128), "");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S * (kStageD + kStageW)];
+    // 16-byte chunk c of row r lies at c ^ twist(r): the 16 chunks that 32
+    // lanes read at once (8 rows, 2 neighbouring columns chunks) fill all banks
+    auto twist = [](uint32_t r) { return BK == 256 ? 2 * (r % 8) : 2 * (r / 2 % 4); };
+
+    const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t wm = wave % WM, wn = wave / WM;
+    uint32_t tm, tk;
+    tile_of(blockIdx.x, nb_m, nb_k, 8, tm, tk);
+    const uint32_t m0 = tm * BM, k0 = tk * BK;
+
+    const uint32_t per = (uint32_t)(a.ldd / 64);  // steps of one weight
+    const uint32_t total = a.n_w * per;
+    const uint32_t first = (uint32_t)((uint64_t)total * blockIdx.y / a.splits);
+    const uint32_t steps = (uint32_t)((uint64_t)total * (blockIdx.y + 1) / a.splits) - first;
+
+    uint32_t doff[kLoadsD], wrow[kLoadsW], wcol[kLoadsW];
+#pragma unroll
+    for (int i = 0; i < kLoadsD; ++i)
+        doff[i] = min(8 * (4 * i + wave) + lane / 8, a.M - 1 - m0) * (uint32_t)a.ldd * 2 +
+                  16 * ((lane % 8) ^ swizzle(8 * wave + lane / 8));
+#pragma unroll
+    for (int i = 0; i < kLoadsW; ++i) {
+        wrow[i] = (4 * i + wave) * kRowsW + lane / kChunks;
+        const uint32_t c = 16 * ((lane % kChunks) ^ twist(wrow[i]));
+        wcol[i] = k0 + c < a.K ? k0 + c : 0;  // beyond the columns: results not stored
+    }
+    const uint16_t *dbase[2] = {a.d[0] + (uint64_t)m0 * a.ldd, a.d[1] + (uint64_t)m0 * a.ldd};
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
+    const uint32_t ldsw = lds0 + S * kStageD;
+    // load j of step `step` (of this split) into a slot, weights first
+    auto load_one = [&](int j, uint32_t step, uint32_t slot) {
+        const uint32_t s = first + step, t = s >= per ? 1 : 0, n = (s - t * per);
+        if (j < kLoadsW) {
+            // beyond the channels the last one's codes: d is 0 there
+            const uint32_t off = __umul24(min(wrow[j], a.N - 1 - n * 64), (uint32_t)(t ? a.ldw[1] : a.ldw[0])) + wcol[j];
+            load_lds16((t ? a.w[1] : a.w[0]) + (uint64_t)n * 64 * (t ? a.ldw[1] : a.ldw[0]), off,
+                       ldsw + slot * kStageW + (4 * j + wave) * 1024);
+        } else {
+            load_lds16((t ? dbase[1] : dbase[0]) + n * 64, doff[j - kLoadsW],
+                       lds0 + slot * kStageD + (4 * (j - kLoadsW) + wave) * 1024);
+        }
+    };
+
+    v16f acc[FN][FM] = {};
+    v4i df[2][FM], wf[2][FN];
+    v2i raw[FN];
+    const uint32_t drow = lds0 + (wm * (BM / WM) + lane % 32) * kRowBytes;
+    const uint32_t wr = lane / 32 * 8 + lane % 16 / 2;  // the row whose bytes this lane names
+    uint32_t wat[FN];
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+        wat[f] = ldsw + wr * BK + 16 * ((wn * FN * 2 + f * 2 + lane / 16 % 2) ^ twist(wr)) + lane % 2 * 8;
+    auto fetch_one = [&](int set, uint32_t slot, int sub, int j) {
+        if (j < FN)
+            raw[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (__attribute__((address_space(3))) v2i *)(uintptr_t)(wat[j] + slot * kStageW + sub * 16 * BK));
+        else
+            df[set][j - FN] = read_lds16(drow + slot * kStageD +
+                                         16 * ((2 * sub + lane / 32) ^ swizzle(lane % 32)) +
+                                         (j - FN) * 32 * kRowBytes);
+    };
+    auto widen_one = [&](int set, int j) {  // half a fragment
+        const v2i w = widen4<F16>(raw[j / 2][j % 2]);
+        wf[set][j / 2][2 * (j % 2)] = w[0];
+        wf[set][j / 2][2 * (j % 2) + 1] = w[1];
+    };
+    // 16 channels: the products of one fragment set, beside them the reads
+    // (first half) and the widening (second half) of the next set and, with
+    // part >= 0, that part of a later step's loads.
+    auto quarter = [&](int set, uint32_t slot, int sub, int part, uint32_t step, uint32_t to) {
+        constexpr int kMul = FN * FM, kFetch = FN + FM, kWiden = 2 * FN, kHalf = (kMul + 1) / 2;
+#pragma unroll
+        for (int i = 0; i < kMul; ++i) {
+            if (i < kHalf) {
+#pragma unroll
+                for (int j = i * kFetch / kHalf; j < (i + 1) * kFetch / kHalf; ++j) fetch_one(set ^ 1, slot, sub, j);
+            }
+            if (part >= 0) {
+                const int f = part * kMul + i;
+#pragma unroll
+                for (int j = f * kLoads / (4 * kMul); j < (f + 1) * kLoads / (4 * kMul); ++j) load_one(j, step, to);
+            }
+            if (F16)
+                acc[i / FM][i % FM] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                    __builtin_bit_cast(f16x8, wf[set][i / FM]), __builtin_bit_cast(f16x8, df[set][i % FM]),
+                    acc[i / FM][i % FM], 0, 0, 0);
+            else
+                acc[i / FM][i % FM] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, wf[set][i / FM]), __builtin_bit_cast(bf16x8, df[set][i % FM]),
+                    acc[i / FM][i % FM], 0, 0, 0);
+            if (i >= kMul - kHalf) {
+                const int h = i - (kMul - kHalf);
+#pragma unroll
+                for (int j = h * kWiden / kHalf; j < (h + 1) * kWiden / kHalf; ++j) widen_one(set ^ 1, j);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto after = [](uint32_t slot) { return slot + 1 == S ? 0 : slot + 1; };
+
+    for (uint32_t i = 0; i < (uint32_t)S && i < steps; ++i)
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) load_one(j, i, i);
+    if (steps >= S)
+        wait_loads_and_meet<(S - 1) * kLoads>();
+    else
+        wait_loads_and_meet<0>();
+#pragma unroll
+    for (int j = 0; j < FN + FM; ++j) fetch_one(0, 0, 0, j);
+#pragma unroll
+    for (int j = 0; j < 2 * FN; ++j) widen_one(0, j);
+    uint32_t step = 0, slot = 0;
+    quarter(0, 0, 1, -1, 0, 0);
+    quarter(1, 0, 2, -1, 0, 0);
+    quarter(0, 0, 3, -1, 0, 0);
+    if (steps >= S)
+        wait_loads_and_meet<kFlying>();
+    else
+        wait_loads_and_meet<0>();
+    // `step` is read except for its last quarter, which is in registers; the
+    // next step has landed
+    for (; step + S < steps; ++step) {
+        const uint32_t next = after(slot);
+        quarter(1, next, 0, 0, step + S, slot);
+        quarter(0, next, 1, 1, step + S, slot);
+        quarter(1, next, 2, 2, step + S, slot);
+        quarter(0, next, 3, 3, step + S, slot);
+        wait_loads_and_meet<kFlying>();
+        slot = next;
+    }
+#pragma unroll 1
+    for (; step + 1 < steps; ++step) {
+        slot = after(slot);
+        quarter(1, slot, 0, -1, 0, 0);
+        quarter(0, slot, 1, -1, 0, 0);
+        quarter(1, slot, 2, -1, 0, 0);
+        quarter(0, slot, 3, -1, 0, 0);
+        wait_loads_and_meet<0>();
+    }
+    quarter(1, slot, 0, -1, 0, 0);  // (what it reads is not used)
+
     const float back = a.norm ? a.norm[1] : 1.0f;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        const uint32_t m = m0 + f * 16 + lane % 16, k = k0 + wave * 16 + lane / 16 * 4;
-        if (m >= a.M) continue;
-        uint16_t *to = (uint16_t *)a.dx + m * a.lddx + k;
-        for (int i = 0; i < 4; ++i)
-            if (k + i < a.K) to[i] = bits16(acc[f][i] * back, F16);
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int g = 0; g < FM; ++g) {
+            const uint32_t m = m0 + wm * (BM / WM) + g * 32 + lane % 32;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t k = k0 + wn * (BK / WN) + f * 32 + q * 8 + lane / 32 * 4;
+                const v4f v = {acc[f][g][4 * q], acc[f][g][4 * q + 1], acc[f][g][4 * q + 2], acc[f][g][4 * q + 3]};
+                if (m >= a.M || k >= a.K) continue;
+                if (a.splits > 1) {
+                    *(v4f *)(a.parts + ((uint64_t)blockIdx.y * a.M + m) * a.K + k) = v;
+                    continue;
+                }
+                uint16_t b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = bits16(v[i] * back, F16);
+                uint16_t *to = (uint16_t *)a.dx + (uint64_t)m * a.lddx + k;
+                if (a.vec && k + 4 <= a.cols) {
+                    *(uint2 *)to = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+                } else {
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i)
+                        if (k + i < a.cols) to[i] = b[i];
+                }
+            }
+        }
+}
+
+// dX from the splits' partial sums, added in order.
+__global__ __launch_bounds__(256) void grad_sum(GradArgs a) {
+    const float back = a.norm ? a.norm[1] : 1.0f;
+    const uint32_t k = 4 * (blockIdx.x * 256 + threadIdx.x);
+    if (k >= a.K) return;
+    for (uint64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
+        v4f v = {0, 0, 0, 0};
+        for (uint32_t s = 0; s < a.splits; ++s) v += *(const v4f *)(a.parts + ((uint64_t)s * a.M + m) * a.K + k);
+        for (uint32_t i = 0; i < 4; ++i)
+            if (k + i < a.cols) ((uint16_t *)a.dx)[m * a.lddx + k + i] = bits16(v[i] * back, a.f16);
     }
+}
+
+template <int BM, int BK, int WM, int WN, int S>
+void launch_tiles(const GradArgs &a, hipStream_t s) {
+    const uint32_t nb_m = (a.M + BM - 1) / BM, nb_k = (a.K + BK - 1) / BK;
+    const dim3 grid(nb_m * nb_k, a.splits);
+    if (a.f16)
+        grad_tiles<true, BM, BK, WM, WN, S><<<grid, 256, 0, s>>>(a, nb_m, nb_k);
+    else
+        grad_tiles<false, BM, BK, WM, WN, S><<<grid, 256, 0, s>>>(a, nb_m, nb_k);
 }
 
 }  // namespace
 
-int launch_grad_product(const GradArgs &a, hipStream_t s) {
-    const dim3 grid((a.K + kTile - 1) / kTile, (a.M + kTile - 1) / kTile);
-    if (a.f16)
-        grad_product<true><<<grid, 256, 0, s>>>(a);
-    else
-        grad_product<false><<<grid, 256, 0, s>>>(a);
+GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, int n_w) {
+    GradPlan p{};
+    const char *f = getenv("ENTQ_GTILE");
+    p.tile = f ? atoi(f) : 256;
+    const char *g = getenv("ENTQ_GSPLIT");
+    p.splits = g ? atoi(g) : 1;
+    p.splits = std::min(p.splits, n_w * ((N + 63) / 64));
+    return p;
+}
+
+int launch_grad_product(const GradPlan &p, const GradArgs &a, hipStream_t s) {
+    if (p.tile == 256) launch_tiles<256, 256, 2, 2, 3>(a, s);
+    if (p.tile == 128) launch_tiles<128, 128, 2, 2, 3>(a, s);
+    if (p.tile == 64) launch_tiles<64, 128, 2, 2, 3>(a, s);
+    if (p.splits > 1) grad_sum<<<dim3((a.K / 4 + 255) / 256, std::min(a.M, 65535u)), 256, 0, s>>>(a);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 

@@ -6,10 +6,13 @@
 
 namespace entq {
 
-// LDS rows of the tiles are 128 bytes: 8 chunks of 16. Chunk c of row r lies
-// at position c ^ (r & 7), so that 8 consecutive rows read at one chunk touch
-// all 32 banks once (ds_read_b128 takes 8 lanes at a time).
+// LDS rows of the tiles are 128 bytes: 8 chunks of 16, chunk c of row r at
+// position c ^ swizzle(r). A row fills half of the 64 banks; 16 consecutive
+// rows read at one chunk, which ds_read_b128 takes at once, touch every bank
+// once (with c ^ (r & 7) the counters showed half of all LDS cycles lost to
+// conflicts).
 constexpr uint32_t kRowBytes = 128;
+__device__ __forceinline__ uint32_t swizzle(uint32_t row) { return row / 2 % 8; }
 
 // One 16-byte load per active lane from base + offset straight into LDS at
 // lds + 16 lane. The compiler does not count this load: wait_loads() does.
@@ -23,10 +26,12 @@ __device__ __forceinline__ void load_lds16(const void *base, uint32_t offset, ui
 }
 #pragma clang diagnostic pop
 
-// Every load of this wave has landed and every LDS read of it is done; then
-// all waves of the workgroup are here.
+// All loads of this wave but the last N have landed and every LDS read of it
+// is done; then all waves of the workgroup are here.
+template <int N>
 __device__ __forceinline__ void wait_loads_and_meet() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    static_assert(N >= 0 && N < 64, "");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) { return (uint32_t)(uintptr_t)p; }

@@ -674,7 +674,7 @@ entq_status entq_int8_gated(const entq_rows *x, const entq_rows *gate, const ent
  * same for all n, that keeps it in range) for the 16-bit matrix cores, sums
  * are fp32. x: the codes and scales the forward pass used (ENTQ_I8).
  * d_dx or d_dw_scales may be NULL: that gradient is not computed. M = 0
- * leaves dsw = 0; N = 0 leaves dx = 0. */
+ * leaves dsw = 0; N = 0 leaves dx = 0. N <= 2^22. */
 uint64_t entq_int8_gemm_backward_workspace_bytes(const entq_rows *dy, const entq_rows *x,
                                                  const entq_rows *w);
 entq_status entq_int8_gemm_backward(const entq_rows *dy, const entq_rows *x, const entq_rows *w,
