@@ -18,12 +18,13 @@ namespace entq {
 enum Int8Mode { kFwd = 0, kGated = 1, kBwd = 2, kGatedBwd = 3 };
 
 struct Int8Args {
-    const int8_t *x;        // [M][ldx]
+    const int8_t *x;        // [M][ldx]; activations themselves where x_type is not ENTQ_I8
     const int8_t *w[2];     // [N][ldw]
     const float *sx;        // [M]
     const float *sw[2];     // [N]
     uint64_t ldx, ldw[2];
     uint32_t M, N, K;
+    int x_type;             // only the few-token kernel takes other than ENTQ_I8
     int act;
     void *y;                // forward: the result; backward: the incoming gradient
     int type;               // its entq_eltype
@@ -32,6 +33,8 @@ struct Int8Args {
     uint16_t *d[2];         // backward: 16-bit scaled gradients [M][ldd], or null
     uint64_t ldd;           // a multiple of 64; columns N..ldd-1 are written as 0
     float *part[2];         // backward: partial column sums [token blocks][N], or null
+    uint32_t splits;        // of K; above 1, integer sums go to
+    int32_t *sums;          // [splits][weights][M][N rounded up to 4]
     const float *norm;      // F16 backward: the power of two that multiplies sw, then its inverse
 };
 
@@ -64,6 +67,48 @@ __device__ __forceinline__ v4i load16_any(const int8_t *row, uint32_t k, uint32_
     for (uint32_t i = 0; i < 15; ++i)
         if (k + i < K) b[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
     return v4i{(int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+// Row quantisation (entq_quantize_rows): element i of a 16-byte piece of
+// activations, and from the bits of a row's largest magnitude (as integers
+// infinities and NaNs come out on top) its scale and codes.
+template <int TYPE>
+__device__ __forceinline__ float act_of(v4i piece, int i) {
+    if (TYPE == ENTQ_F32) return __int_as_float(piece[i]);
+    return from16((uint16_t)((uint32_t)piece[i / 2] >> (16 * (i % 2))), TYPE == ENTQ_F16);
+}
+
+constexpr float kMinScale = 0x1p-100f;  // its inverse is finite
+
+struct Quantizer {
+    float scale, inv;
+    bool finite;
+    __device__ explicit Quantizer(uint32_t big) {
+        finite = big < 0x7F800000u;
+        const float s = fmaxf(__uint_as_float(big) * (float)(1.0 / 127), kMinScale);
+        inv = 1.0f / s;
+        scale = finite ? s : __uint_as_float(0x7FC00000u);
+    }
+    __device__ uint32_t code(float v) const {
+        return finite ? (uint32_t)(int)fminf(fmaxf(rintf(v * inv), -127.0f), 127.0f) & 0xFFu : 0u;
+    }
+    template <int TYPE>
+    __device__ uint32_t code4(v4i piece, int first) const {
+        return code(act_of<TYPE>(piece, first)) | code(act_of<TYPE>(piece, first + 1)) << 8 |
+               code(act_of<TYPE>(piece, first + 2)) << 16 | code(act_of<TYPE>(piece, first + 3)) << 24;
+    }
+};
+
+template <int TYPE>
+__device__ __forceinline__ float load_act(const void *x, uint64_t at) {
+    if (TYPE == ENTQ_F32) return ((const float *)x)[at];
+    return from16(((const uint16_t *)x)[at], TYPE == ENTQ_F16);
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int o = 32; o; o /= 2) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+    return v;
 }
 
 // act(v) and, for the backward pass, act'(v). exp is the hardware's 2^x after
@@ -108,18 +153,18 @@ __device__ __forceinline__ void load_scales(const Int8Args &a, uint32_t n, float
     }
 }
 
-// The results for token m and the 4 channels n..n+3 (n a multiple of 4), or
+// The results for token m (of scale sx) and the 4 channels n..n+3 (n a multiple of 4), or
 // the gradients, whose contributions to the channel sums are added to sg, su.
 // Channels of N and beyond are not stored; in a backward pass a token of M
 // and beyond adds nothing.
 template <int MODE>
-__device__ __forceinline__ void epilogue4(const Int8Args &a, const float (&scale)[2][4], float norm, uint32_t m,
-                                          uint32_t n, v4i ag, v4i au, float (&sg)[4], float (&su)[4]) {
+__device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const float (&scale)[2][4], float norm,
+                                          uint32_t m, uint32_t n, v4i ag, v4i au, float (&sg)[4],
+                                          float (&su)[4]) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
     constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
     if (m >= a.M || n >= (kBack ? (uint32_t)a.ldd : a.N)) return;
     const bool whole = n + 4 <= a.N;
-    const float sx = a.sx[m];
     const uint64_t at = (uint64_t)m * a.ldy + n;
     if constexpr (!kBack) {
         float v[4];
@@ -210,15 +255,68 @@ struct GradArgs {
     const float *norm;      // F16: result times norm[1]; or null
 };
 
+// The choice between tile sizes and splits of the sum is made by what each
+// would take, in us: `step` for one step of a workgroup's sum with one and
+// with two workgroups on a CU (256-token tiles fill one), `tile` for a tile's
+// end, the weights' bytes at `bytes_us`, and for a split sum a second launch
+// that adds partial results. The constants are fitted to times measured on
+// MI355X over 180 shapes (1 .. 2,048 tokens, sides 512 .. 32,000) with every
+// tile and 1 .. 24 splits; the choice is then on average 1 % (products) and
+// 0.2 % (gradients) slower than the best variant of each shape.
+struct TileCost {
+    uint32_t tokens;        // of a tile
+    float step[2], tile;
+};
+struct SplitCost {
+    float launch, bytes_us, second, per_split, per_value;
+};
+inline float tile_cost(const TileCost &t, const SplitCost &c, uint32_t tiles, uint32_t steps, uint32_t splits,
+                       uint64_t weight_bytes, uint64_t results) {
+    const uint32_t slots = t.tokens == 256 ? 256 : 512, groups = tiles * splits;
+    const uint32_t full = groups / slots, rest = groups % slots;
+    const float work = (float)((steps + splits - 1) / splits) *
+                           (full * t.step[1] + (rest == 0 ? 0.0f : t.step[rest > 256])) +
+                       t.tile * (full + (rest > 0));
+    const float memory = weight_bytes / c.bytes_us;
+    float us = c.launch + (work > memory ? work : memory);
+    if (splits > 1) us += c.second + splits * (c.per_split + c.per_value * results);
+    return us;
+}
+// The cheapest tile and split. tiles(tokens): how many tiles of that size.
+struct TileChoice {
+    uint32_t tokens, splits;
+    float us;
+};
+template <class Tiles>
+TileChoice cheapest_tile(const TileCost (&kinds)[3], const SplitCost &c, Tiles tiles, uint32_t steps,
+                         uint64_t weight_bytes, uint64_t results) {
+    TileChoice best{0, 1, 0.0f};
+    for (const TileCost &t : kinds) {
+        const uint64_t n = tiles(t.tokens);
+        for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u, 24u}) {
+            if (s > 1 && (s > steps || n * s > 1100)) break;
+            const float us = tile_cost(t, c, (uint32_t)(n > 0x7FFFFFFF ? 0x7FFFFFFF : n), steps, s, weight_bytes,
+                                       results);
+            if (!best.tokens || us < best.us) best = {t.tokens, s, us};
+        }
+    }
+    return best;
+}
+
 // How a product runs.
 struct Int8Plan {
+    bool few;               // the few-token kernel; else tiles:
+    bool quantizes;         // the few-token kernel quantises the activations itself
+    uint32_t splits;        // of K; above 1 the sums pass through memory
     int tile;               // tokens of a tile
     uint32_t part_rows;     // rows of Int8Args::part
 };
-Int8Plan int8_plan(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K);
+Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K);
 
 // Launchers; each returns an entq_status. Rows of x and w must start at
 // multiples of 16 bytes, strides below 2^23, K be a multiple of 16.
+bool few_quantizes(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K);
+int launch_int8_few(Int8Mode mode, const Int8Args &a, hipStream_t s);
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s);
 
 struct GradPlan {

@@ -12,26 +12,10 @@ namespace {
 // quantiser
 // ---------------------------------------------------------------------------
 
-constexpr float kMinScale = 0x1p-100f;  // its inverse is finite
-
-template <int TYPE>
-__device__ __forceinline__ float load_act(const void *x, uint64_t at) {
-    if (TYPE == ENTQ_F32) return ((const float *)x)[at];
-    return from16(((const uint16_t *)x)[at], TYPE == ENTQ_F16);
-}
-
-// Element i of a 16-byte piece of activations.
-template <int TYPE>
-__device__ __forceinline__ float act_of(v4i piece, int i) {
-    if (TYPE == ENTQ_F32) return __int_as_float(piece[i]);
-    return from16((uint16_t)((uint32_t)piece[i / 2] >> (16 * (i % 2))), TYPE == ENTQ_F16);
-}
-
 // One workgroup per row, which is read once: VECS pieces of 16 bytes a thread
 // stay in registers between the maximum and the rounding (VECS 0: any length,
 // read twice, the second time out of the L2). Pieces may lie at any address.
-// The largest magnitude is found on the bits of |x| as integers, where
-// infinities and NaNs come out on top. Columns K..pad-1 are written as 0.
+// Columns K..pad-1 are written as 0.
 template <int TYPE, int VECS, int THREADS>
 __global__ __launch_bounds__(THREADS) void quantize_rows(const void *x, uint64_t ldx, uint32_t K, int8_t *codes,
                                                          uint64_t ldc, uint32_t pad, float *scales) {
@@ -65,29 +49,18 @@ __global__ __launch_bounds__(THREADS) void quantize_rows(const void *x, uint64_t
     const uint32_t rest = full * kPer + threadIdx.x;  // the last columns, one a thread
     float last = 0.0f;
     if (rest < K) take(last = load_act<TYPE>(src, rest));
-#pragma unroll
-    for (int o = 32; o; o /= 2) big = max(big, (uint32_t)__shfl_xor((int)big, o));
+    big = wave_max(big);
     if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < THREADS / 64; ++i) big = max(big, top[i]);
-    const bool finite = big < 0x7F800000u;
-    const float scale = fmaxf(__uint_as_float(big) * (float)(1.0 / 127), kMinScale);
-    const float inv = 1.0f / scale;
-    if (threadIdx.x == 0) scales[row] = finite ? scale : __uint_as_float(0x7FC00000u);
-    auto code = [&](float v) {
-        return finite ? (uint32_t)(int)fminf(fmaxf(rintf(v * inv), -127.0f), 127.0f) & 0xFFu : 0u;
-    };
+    const Quantizer z(big);
+    if (threadIdx.x == 0) scales[row] = z.scale;
     auto put = [&](uint32_t p, v4i v) {
-        uint32_t b[2];
-#pragma unroll
-        for (int h = 0; h < kPer / 4; ++h)
-            b[h] = code(act_of<TYPE>(v, 4 * h)) | code(act_of<TYPE>(v, 4 * h + 1)) << 8 |
-                   code(act_of<TYPE>(v, 4 * h + 2)) << 16 | code(act_of<TYPE>(v, 4 * h + 3)) << 24;
-        if (kPer == 8)
-            ((any8 *)(dst + p * 8))->v = v2i{(int)b[0], (int)b[1]};
+        if constexpr (kPer == 8)
+            ((any8 *)(dst + p * 8))->v = v2i{(int)z.code4<TYPE>(v, 0), (int)z.code4<TYPE>(v, 4)};
         else
-            ((any4 *)(dst + p * 4))->v = (int)b[0];
+            ((any4 *)(dst + p * 4))->v = (int)z.code4<TYPE>(v, 0);
     };
     if (VECS) {
 #pragma unroll
@@ -98,7 +71,7 @@ __global__ __launch_bounds__(THREADS) void quantize_rows(const void *x, uint64_t
     } else {
         for (uint32_t p = threadIdx.x; p < full; p += THREADS) put(p, piece(p));
     }
-    if (rest < K) dst[rest] = (int8_t)code(last);
+    if (rest < K) dst[rest] = (int8_t)z.code(last);
     for (uint32_t c = K + threadIdx.x; c < pad; c += THREADS) dst[c] = 0;
 }
 
@@ -171,8 +144,7 @@ __global__ __launch_bounds__(1024) void scale_norm(const float *a, const float *
         big = max(big, __float_as_uint(a[i]) & 0x7FFFFFFFu);
         if (b) big = max(big, __float_as_uint(b[i]) & 0x7FFFFFFFu);
     }
-#pragma unroll
-    for (int o = 32; o; o /= 2) big = max(big, (uint32_t)__shfl_xor((int)big, o));
+    big = wave_max(big);
     if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -195,6 +167,33 @@ __global__ __launch_bounds__(256) void sum_parts(const float *p0, const float *p
     float s = 0.0f;
     for (uint32_t b = 0; b < blocks; ++b) s += p[(uint64_t)b * n + i];
     out[i] = s;
+}
+
+// d = dy sw in 16 bits, zeros in columns N..ldd-1: what the backward epilogue
+// writes, for a call that needs no sums of codes. A thread: 4 channels.
+__global__ __launch_bounds__(256) void scale_gradient(Int8Args a) {
+    const uint32_t n = 4 * (blockIdx.x * 256 + threadIdx.x);
+    if (n >= a.ldd) return;
+    const bool f16 = a.type == ENTQ_F16;
+    const float norm = a.norm ? a.norm[0] : 1.0f;
+    float scale[2][4];
+    load_scales<kBwd>(a, n, scale);
+    for (uint64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
+        const uint16_t *y = (const uint16_t *)a.y + m * a.ldy + n;
+        uint16_t b[4] = {0, 0, 0, 0}, d[4];
+        if (a.vec && n + 4 <= a.N) {
+            const uint2 v = *(const uint2 *)y;
+            b[0] = (uint16_t)v.x, b[1] = (uint16_t)(v.x >> 16), b[2] = (uint16_t)v.y, b[3] = (uint16_t)(v.y >> 16);
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                if (n + i < a.N) b[i] = y[i];
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            d[i] = n + i < a.N ? bits16(from16(b[i], f16) * (scale[0][i] * norm), f16) : 0;
+        *(uint2 *)(a.d[0] + m * a.ldd + n) = make_uint2(d[0] | (uint32_t)d[1] << 16, d[2] | (uint32_t)d[3] << 16);
+    }
 }
 
 __global__ __launch_bounds__(256) void fill_zero(uint8_t *p, uint64_t ld, uint32_t bytes) {
@@ -289,6 +288,7 @@ struct Layout {
     uint64_t ldc;
     int8_t *w[2];       // aligned copies of weights, or null
     uint32_t ldw;
+    int32_t *sums;      // the splits' integer sums, or null
     uint16_t *d[2];     // scaled gradients
     uint64_t ldd;
     float *part[2];
@@ -306,15 +306,17 @@ Layout lay_out(const Call &c, void *ws) {
     l.ldc = (c.x->cols + 127ull) / 128 * 128;
     l.ldd = (N + 63) / 64 * 64;
     l.ldw = (c.x->cols + 15) / 16 * 16;
-    l.plan = int8_plan(c.mode, (uint32_t)M, (uint32_t)N, l.ldw);
-    if (c.x->type != ENTQ_I8) {
+    l.plan = int8_plan(c.mode, c.x->type, (uint32_t)M, (uint32_t)N, l.ldw);
+    if (c.x->type != ENTQ_I8 && !l.plan.quantizes) {
         l.codes = p.take<int8_t>(M * l.ldc);
         l.scales = p.take<float>(M);
-    } else if (!direct(*c.x)) {
+    } else if (c.x->type == ENTQ_I8 && !l.plan.few && !direct(*c.x)) {
         l.codes = p.take<int8_t>(M * l.ldc);
     }
+    const bool copies = !l.plan.few || c.mode == kBwd || c.mode == kGatedBwd;
+    if (l.plan.splits > 1) l.sums = p.take<int32_t>(l.plan.splits * c.n_w * M * ((N + 3) / 4 * 4));
     for (int i = 0; i < c.n_w; ++i)
-        if (!direct(*c.w[i])) l.w[i] = p.take<int8_t>(N * l.ldw);
+        if (copies && !direct(*c.w[i])) l.w[i] = p.take<int8_t>(N * l.ldw);
     if (c.mode == kBwd || c.mode == kGatedBwd) {
         for (int i = 0; i < c.n_w; ++i) {
             l.d[i] = p.take<uint16_t>(M * l.ldd);
@@ -347,12 +349,15 @@ entq_status operands(const Call &c, const Layout &l, Int8Args &a, hipStream_t s)
     a = Int8Args{};
     a.M = c.x->rows;
     a.N = c.w[0]->rows;
-    a.K = l.ldw;
+    a.K = l.plan.few ? c.x->cols : l.ldw;
+    a.splits = l.plan.splits;
+    a.sums = l.sums;
     a.x = (const int8_t *)c.x->d_data;
     a.sx = c.x->d_scales;
     a.ldx = c.x->ld;
     int r = ENTQ_OK;
-    if (c.x->type != ENTQ_I8) {
+    a.x_type = l.plan.quantizes ? c.x->type : (int)ENTQ_I8;
+    if (c.x->type != ENTQ_I8 && !l.plan.quantizes) {
         r = launch_quantize(*c.x, l.codes, l.ldc, (uint32_t)l.ldc, l.scales, s);
         a.sx = l.scales;
     } else if (l.codes) {
@@ -435,8 +440,12 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
         a.d[i] = dx ? l.d[i] : nullptr;
         a.part[i] = (i ? ds1 : ds0) ? l.part[i] : nullptr;
     }
-    int r = launch_int8_product(c.mode, l.plan, a, s);
-    if (r != ENTQ_OK) return (entq_status)r;
+    int r = ENTQ_OK;
+    if (c.mode == kBwd && !ds0)
+        scale_gradient<<<dim3((uint32_t)(l.ldd / 4 + 255) / 256, std::min(M, 65535u)), 256, 0, s>>>(a);
+    else
+        r = launch_int8_product(c.mode, l.plan, a, s);
+    if (r != ENTQ_OK || hipGetLastError() != hipSuccess) return r != ENTQ_OK ? (entq_status)r : ENTQ_EHIP;
     if (ds0 || ds1) {
         sum_parts<<<dim3((N + 255) / 256, c.n_w), 256, 0, s>>>(l.part[0], l.part[1], l.plan.part_rows, N, ds0,
                                                                ds1);

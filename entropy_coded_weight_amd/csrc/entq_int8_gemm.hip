@@ -7,6 +7,13 @@
 namespace entq {
 namespace {
 
+// Where a split's sums of token m, channels n..n+3 and weight t go.
+template <bool TWO>
+__device__ __forceinline__ int32_t *part_sums(const Int8Args &a, uint32_t split, uint32_t t, uint32_t m, uint32_t n) {
+    const uint64_t wide = (a.N + 3) / 4 * 4;
+    return a.sums + (((uint64_t)split * (TWO ? 2 : 1) + t) * a.M + m) * wide + n;
+}
+
 // A workgroup of 4 waves (WM x WN) computes BM tokens x BN weight rows; a
 // gated tile's rows alternate 32 of gate and 32 of up, so that a lane's
 // fragments hold both sums of a channel. K goes by in steps of 128 codes.
@@ -43,9 +50,12 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     // position l % 8 of row l / 8.
     const uint32_t kc = 16 * ((lane % 8) ^ swizzle(8 * wave + lane / 8));
     uint32_t xoff[kLoadsX], woff[kLoadsW];
-    const int8_t *xbase = a.x + (uint64_t)m0 * a.ldx;
-    const int8_t *wbase[2] = {a.w[0] + (uint64_t)n0 * a.ldw[0],
-                              kTwo ? a.w[1] + (uint64_t)n0 * a.ldw[1] : nullptr};
+    // this split's steps
+    const uint32_t all = (a.K + 127) / 128, first = all * blockIdx.y / a.splits;
+    const uint32_t steps = all * (blockIdx.y + 1) / a.splits - first, K = a.K - first * 128;
+    const int8_t *xbase = a.x + (uint64_t)m0 * a.ldx + first * 128;
+    const int8_t *wbase[2] = {a.w[0] + (uint64_t)n0 * a.ldw[0] + first * 128,
+                              kTwo ? a.w[1] + (uint64_t)n0 * a.ldw[1] + first * 128 : nullptr};
 #pragma unroll
     for (int i = 0; i < kLoadsX; ++i)
         xoff[i] = min(8 * (4 * i + wave) + lane / 8, a.M - 1 - m0) * (uint32_t)a.ldx + kc;
@@ -56,7 +66,6 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
     const uint32_t ldsw = lds0 + SX * kStageX;
-    const uint32_t steps = (a.K + 127) / 128;
     auto load_x = [&](int i, uint32_t step, uint32_t slot) {
         load_lds16(xbase + step * 128, xoff[i], lds0 + slot * kStageX + wave * 1024 + i * 4096);
     };
@@ -66,7 +75,7 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     // A whole step's loads; past the rows' end tokens are zeros and weights
     // whatever is there.
     auto load_step_x = [&](uint32_t step, uint32_t slot) {
-        const bool in = step * 128 + kc < a.K;
+        const bool in = step * 128 + kc < K;
 #pragma unroll
         for (int i = 0; i < kLoadsX; ++i) {
             if (in)
@@ -76,7 +85,7 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
         }
     };
     auto load_step_w = [&](uint32_t step, uint32_t slot) {
-        if (step * 128 + kc < a.K) {
+        if (step * 128 + kc < K) {
 #pragma unroll
             for (int i = 0; i < kLoadsW; ++i) load_w(i, step, slot);
         }
@@ -198,11 +207,19 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
 #pragma unroll 1
         for (uint32_t t = lane / kQuads; t < 32; t += kTokens) {
             const uint8_t *p = mine + t * kRow + at;
-            epilogue4<MODE>(a, scale, norm, m0 + wm * (BM / WM) + g * 32 + t, n, *(const v4i *)p,
-                            *(const v4i *)(p + (kTwo ? 128 : 0)), sg, su);
+            const uint32_t m = m0 + wm * (BM / WM) + g * 32 + t;
+            const v4i s0 = *(const v4i *)p, s1 = *(const v4i *)(p + (kTwo ? 128 : 0));
+            if (a.splits > 1) {
+                if (m < a.M && n < a.N) {
+                    *(v4i *)part_sums<kTwo>(a, blockIdx.y, 0, m, n) = s0;
+                    if (kTwo) *(v4i *)part_sums<kTwo>(a, blockIdx.y, 1, m, n) = s1;
+                }
+            } else {
+                epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, norm, m, n, s0, s1, sg, su);
+            }
         }
     }
-    if constexpr (kBack) {
+    if (kBack && a.splits == 1) {
 #pragma unroll
         for (int w = 0; w < (kTwo ? 2 : 1); ++w) {
             if (!a.part[w]) continue;
@@ -217,33 +234,118 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     }
 }
 
+// Adds the splits' sums up (integers: in any order the same) and finishes
+// them. A workgroup: 256 channels (a wave's lanes 4 each), its 4 waves a
+// token each, or backward, where a workgroup adds its tokens up, 16 in turn.
+constexpr uint32_t finish_tokens(Int8Mode mode) { return mode == kBwd || mode == kGatedBwd ? 16 : 4; }
+template <int MODE>
+__global__ __launch_bounds__(256) void int8_finish(Int8Args a) {
+    constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
+    constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
+    __shared__ float waves[4][2][4][64];
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const uint32_t n = blockIdx.x * 256 + lane * 4;
+    float scale[2][4], sg[4] = {}, su[4] = {};
+    load_scales<MODE>(a, n, scale);
+    const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
+    for (uint32_t i = wave; i < finish_tokens((Int8Mode)MODE); i += 4) {
+        const uint32_t m = blockIdx.y * finish_tokens((Int8Mode)MODE) + i;
+        v4i s[2] = {};
+        if (m < a.M && n < a.N) {
+#pragma unroll 4
+            for (uint32_t k = 0; k < a.splits; ++k) {
+                s[0] += *(const v4i *)part_sums<kTwo>(a, k, 0, m, n);
+                if (kTwo) s[1] += *(const v4i *)part_sums<kTwo>(a, k, 1, m, n);
+            }
+        }
+        epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, norm, m, n, s[0], s[1], sg, su);
+    }
+    if constexpr (kBack) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            waves[wave][0][i][lane] = sg[i];
+            waves[wave][1][i][lane] = su[i];
+        }
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (int t = 0; t < (kTwo ? 2 : 1); ++t) {
+            if (!a.part[t]) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float s = waves[0][t][i][lane];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) s += waves[w][t][i][lane];
+                if (n + i < a.N) a.part[t][(uint64_t)blockIdx.y * a.N + n + i] = s;
+            }
+        }
+    }
+}
+
 template <int BM, int BN, int WM, int WN, int SX, int SW>
 void launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     const bool two = mode == kGated || mode == kGatedBwd;
     const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
     const uint32_t ch = two ? BN / 2 : BN;
     const uint32_t nb_m = (a.M + BM - 1) / BM, nb_n = (cols + ch - 1) / ch;
-    const dim3 grid(nb_m * nb_n);
+    const dim3 grid(nb_m * nb_n, a.splits);
     if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
     if (mode == kGated) int8_tiles<kGated, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
     if (mode == kBwd) int8_tiles<kBwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
     if (mode == kGatedBwd) int8_tiles<kGatedBwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
 }
 
+void launch_finish(Int8Mode mode, const Int8Args &a, hipStream_t s) {
+    const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
+    const dim3 grid((cols + 255) / 256, (a.M + finish_tokens(mode) - 1) / finish_tokens(mode));
+    if (mode == kFwd) int8_finish<kFwd><<<grid, 256, 0, s>>>(a);
+    if (mode == kGated) int8_finish<kGated><<<grid, 256, 0, s>>>(a);
+    if (mode == kBwd) int8_finish<kBwd><<<grid, 256, 0, s>>>(a);
+    if (mode == kGatedBwd) int8_finish<kGatedBwd><<<grid, 256, 0, s>>>(a);
+}
+
 }  // namespace
 
-Int8Plan int8_plan(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K) {
+Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K) {
+    static const TileCost kinds[3] = {{64, {0.353f, 0.885f}, 1.6f}, {128, {0.878f, 1.04f}, 1.7f},
+                                      {256, {1.61f, 1.63f}, 4.9f}};
+    static const SplitCost cost = {3.3f, 8.7e6f, 2.5f, 0.13f, 1.38e-6f};
+    const uint64_t n_w = mode == kGated || mode == kGatedBwd ? 2 : 1;
+    const TileChoice t = cheapest_tile(
+        kinds, cost,
+        [&](uint32_t tokens) {
+            const uint64_t rows = tokens == 256 ? 256 : 128;
+            return (uint64_t)((M + tokens - 1) / tokens) * ((N * n_w + rows - 1) / rows);
+        },
+        (K + 127) / 128, n_w * N * K, n_w * M * (uint64_t)N);
     Int8Plan p{};
-    const char *f = getenv("ENTQ_TILE");
-    p.tile = f ? atoi(f) : 256;
-    p.part_rows = (M + p.tile - 1) / p.tile * 2;
+    p.tile = (int)t.tokens;
+    p.splits = t.splits;
+    if (M <= 64) {
+        // The few-token kernel: limited by a wave's turns over K, all the more
+        // the more groups of tokens it has, or by the weights' bytes. (At 1 and
+        // 4 tokens it was the fastest, or within 1 %, for every shape.)
+        const uint32_t groups = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+        const float turns = (K + 1023) / 1024 * (0.28f + 0.47f * groups) * std::max(1.0f, n_w * N / 3730.0f);
+        const float memory = n_w * N * (float)K * (1 / 5.2e6f + 2.6e-9f * M);
+        p.few = M <= 4 || 4.1f + std::max(turns, memory) < t.us;
+        if (p.few) {
+            p.quantizes = x_type != ENTQ_I8 && few_quantizes(mode, M, N, K);
+            p.splits = 1;
+            p.part_rows = groups;
+            return p;
+        }
+    }
+    p.part_rows = p.splits > 1 ? (M + 15) / 16 : (M + p.tile - 1) / p.tile * 2;
     return p;
 }
 
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s) {
+    if (p.few) return launch_int8_few(mode, a, s);
     if (p.tile == 256) launch_tiles<256, 256, 2, 2, 3, 2>(mode, a, s);
     if (p.tile == 128) launch_tiles<128, 128, 2, 2, 3, 2>(mode, a, s);
     if (p.tile == 64) launch_tiles<64, 128, 2, 2, 3, 3>(mode, a, s);
+    if (a.splits > 1) launch_finish(mode, a, s);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 

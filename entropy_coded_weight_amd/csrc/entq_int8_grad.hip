@@ -222,6 +222,7 @@ __global__ __launch_bounds__(256) void grad_sum(GradArgs a) {
     if (k >= a.K) return;
     for (uint64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
         v4f v = {0, 0, 0, 0};
+#pragma unroll 4
         for (uint32_t s = 0; s < a.splits; ++s) v += *(const v4f *)(a.parts + ((uint64_t)s * a.M + m) * a.K + k);
         for (uint32_t i = 0; i < 4; ++i)
             if (k + i < a.cols) ((uint16_t *)a.dx)[m * a.lddx + k + i] = bits16(v[i] * back, a.f16);
@@ -241,13 +242,17 @@ void launch_tiles(const GradArgs &a, hipStream_t s) {
 }  // namespace
 
 GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, int n_w) {
-    GradPlan p{};
-    const char *f = getenv("ENTQ_GTILE");
-    p.tile = f ? atoi(f) : 256;
-    const char *g = getenv("ENTQ_GSPLIT");
-    p.splits = g ? atoi(g) : 1;
-    p.splits = std::min(p.splits, n_w * ((N + 63) / 64));
-    return p;
+    static const TileCost kinds[3] = {{64, {0.542f, 0.857f}, 0.0f}, {128, {0.625f, 1.13f}, 0.0f},
+                                      {256, {1.32f, 1.64f}, 1.9f}};
+    static const SplitCost cost = {6.6f, 9.2e6f, 1.7f, 0.125f, 1.54e-6f};
+    const TileChoice t = cheapest_tile(
+        kinds, cost,
+        [&](uint32_t tokens) {
+            const uint64_t cols = tokens == 256 ? 256 : 128;
+            return (uint64_t)((M + tokens - 1) / tokens) * ((K + cols - 1) / cols);
+        },
+        n_w * ((N + 63) / 64), (uint64_t)n_w * N * K, (uint64_t)M * K);
+    return {(int)t.tokens, t.splits};
 }
 
 int launch_grad_product(const GradPlan &p, const GradArgs &a, hipStream_t s) {
