@@ -62,6 +62,13 @@ ENCODE_JOB = np.dtype([("symbols", "<u8"), ("n_symbols", "<u8"), ("chunk_symbols
                        ("scratch_bytes", "<u8"), ("n_words", "<u8")])
 
 
+class Rows(ctypes.Structure):
+    """entq_rows (include/entq.h): device pointers as integers"""
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_uint64), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_uint32)]
+
+
 class EntqError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -81,6 +88,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         c = ctypes
         vp, u64, i64 = c.c_void_p, c.c_uint64, c.c_int64
+        rows = c.POINTER(Rows)
         sigs = {
             "entq_plan_workspace_bytes": (c.c_size_t, [c.c_int, i64]),
             "entq_plan": (c.c_int, [vp, c.c_int, vp, vp, i64, u64, vp, c.c_size_t, vp,
@@ -127,16 +135,18 @@ def lib():
             "entq_decode_gemm_tiles": (c.c_int, [vp, vp, vp, vp, c.c_int, vp, u64, vp, vp]),
             "entq_decode_gemm_tiles_bf16_split": (c.c_int, [vp, vp, vp, vp, c.c_int, vp, u64, vp,
                                                             vp]),
-            "entq_quantize_rows": (c.c_int, [vp, vp, u64, vp, vp]),
-            "entq_int8_gemm_workspace_bytes": (u64, [vp, vp]),
-            "entq_int8_gemm": (c.c_int, [vp, vp, vp, c.c_int, u64, vp, u64, vp]),
-            "entq_int8_gated_workspace_bytes": (u64, [vp, vp, vp]),
-            "entq_int8_gated": (c.c_int, [vp, vp, vp, c.c_int, vp, c.c_int, u64, vp, u64, vp]),
-            "entq_int8_gemm_backward_workspace_bytes": (u64, [vp, vp, vp]),
-            "entq_int8_gemm_backward": (c.c_int, [vp, vp, vp, vp, u64, vp, vp, u64, vp]),
-            "entq_int8_gated_backward_workspace_bytes": (u64, [vp, vp, vp, vp]),
-            "entq_int8_gated_backward": (c.c_int, [vp, vp, vp, vp, c.c_int, vp, u64, vp, vp, vp,
-                                                   u64, vp]),
+            # (entq_rows by reference: a structure passes for its address)
+            "entq_quantize_rows": (c.c_int, [rows, vp, u64, vp, vp]),
+            "entq_int8_gemm_workspace_bytes": (u64, [rows, rows]),
+            "entq_int8_gemm": (c.c_int, [rows, rows, vp, c.c_int, u64, vp, u64, vp]),
+            "entq_int8_gated_workspace_bytes": (u64, [rows, rows, rows]),
+            "entq_int8_gated": (c.c_int, [rows, rows, rows, c.c_int, vp, c.c_int, u64, vp, u64,
+                                          vp]),
+            "entq_int8_gemm_backward_workspace_bytes": (u64, [rows, rows, rows]),
+            "entq_int8_gemm_backward": (c.c_int, [rows, rows, rows, vp, u64, vp, vp, u64, vp]),
+            "entq_int8_gated_backward_workspace_bytes": (u64, [rows, rows, rows, rows]),
+            "entq_int8_gated_backward": (c.c_int, [rows, rows, rows, rows, c.c_int, vp, u64, vp,
+                                                   vp, vp, u64, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)

@@ -238,6 +238,26 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
     }
 }
 
+// Channel sums out of the token blocks' partial sums, added in block order.
+struct SumArgs {
+    const float *part[2];
+    float *out[2];          // or null
+    uint32_t rows, n;
+};
+constexpr uint32_t kSumThreads = 256;
+inline uint32_t sum_blocks(const SumArgs &a) { return a.rows ? 2 * ((a.n + kSumThreads - 1) / kSumThreads) : 0; }
+__device__ __forceinline__ void sum_parts_block(const SumArgs &a, uint32_t block) {
+    const uint32_t half = (a.n + kSumThreads - 1) / kSumThreads, t = block >= half;
+    const uint32_t i = (block - t * half) * kSumThreads + threadIdx.x;
+    const float *p = t ? a.part[1] : a.part[0];
+    float *out = t ? a.out[1] : a.out[0];
+    if (i >= a.n || !out) return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (uint32_t b = 0; b < a.rows; ++b) s += p[(uint64_t)b * a.n + i];
+    out[i] = s;
+}
+
 // dX = sum over the weights t of d[t] . W_t, a product along the channels.
 struct GradArgs {
     const uint16_t *d[2];   // [M][ldd], zero beyond column N
@@ -253,6 +273,7 @@ struct GradArgs {
     uint64_t lddx;
     bool vec;               // dx's rows start at multiples of 4 elements
     const float *norm;      // F16: result times norm[1]; or null
+    SumArgs sums;           // channel sums to finish in the same launch (rows 0: none)
 };
 
 // The choice between tile sizes and splits of the sum is made by what each

@@ -95,6 +95,7 @@ void quantize_typed(const entq_rows &x, uint32_t rows, uint64_t skip, int8_t *co
 
 int launch_quantize(const entq_rows &x, int8_t *codes, uint64_t ldc, uint32_t pad, float *scales,
                     hipStream_t s) {
+    if (x.rows == 0) return ENTQ_OK;
     constexpr uint32_t kRows = 1u << 20;  // a launch's threads stay below 2^32
     for (uint64_t r = 0; r < x.rows; r += kRows) {
         const uint32_t n = (uint32_t)std::min<uint64_t>(kRows, x.rows - r);
@@ -157,17 +158,7 @@ __global__ __launch_bounds__(1024) void scale_norm(const float *a, const float *
     }
 }
 
-// Column sums of the token blocks' partial sums, in block order.
-__global__ __launch_bounds__(256) void sum_parts(const float *p0, const float *p1, uint32_t blocks, uint32_t n,
-                                                 float *out0, float *out1) {
-    const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-    const float *p = blockIdx.y ? p1 : p0;
-    float *out = blockIdx.y ? out1 : out0;
-    if (i >= n || !out) return;
-    float s = 0.0f;
-    for (uint32_t b = 0; b < blocks; ++b) s += p[(uint64_t)b * n + i];
-    out[i] = s;
-}
+__global__ __launch_bounds__(kSumThreads) void sum_parts(SumArgs a) { sum_parts_block(a, blockIdx.x); }
 
 // d = dy sw in 16 bits, zeros in columns N..ldd-1: what the backward epilogue
 // writes, for a call that needs no sums of codes. A thread: 4 channels.
@@ -436,22 +427,28 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     a.ldy = c.dy->ld;
     a.vec = vec4(a.y, a.ldy, a.type);
     a.ldd = l.ldd;
+    // (one block of tokens: its sums are the results)
+    const bool direct_sums = l.plan.part_rows == 1;
+    float *const ds[2] = {ds0, ds1};
+    SumArgs sums{};
+    sums.n = N;
     for (int i = 0; i < c.n_w; ++i) {
         a.d[i] = dx ? l.d[i] : nullptr;
-        a.part[i] = (i ? ds1 : ds0) ? l.part[i] : nullptr;
+        a.part[i] = !ds[i] ? nullptr : direct_sums ? ds[i] : l.part[i];
+        sums.part[i] = l.part[i];
+        sums.out[i] = ds[i];
     }
+    if ((ds0 || ds1) && !direct_sums) sums.rows = l.plan.part_rows;
     int r = ENTQ_OK;
     if (c.mode == kBwd && !ds0)
         scale_gradient<<<dim3((uint32_t)(l.ldd / 4 + 255) / 256, std::min(M, 65535u)), 256, 0, s>>>(a);
     else
         r = launch_int8_product(c.mode, l.plan, a, s);
     if (r != ENTQ_OK || hipGetLastError() != hipSuccess) return r != ENTQ_OK ? (entq_status)r : ENTQ_EHIP;
-    if (ds0 || ds1) {
-        sum_parts<<<dim3((N + 255) / 256, c.n_w), 256, 0, s>>>(l.part[0], l.part[1], l.plan.part_rows, N, ds0,
-                                                               ds1);
-        if (hipGetLastError() != hipSuccess) return ENTQ_EHIP;
+    if (!dx) {
+        if (sums.rows) sum_parts<<<sum_blocks(sums), kSumThreads, 0, s>>>(sums);
+        return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
     }
-    if (!dx) return ENTQ_OK;
     GradArgs g{};
     for (int i = 0; i < c.n_w; ++i) {
         g.d[i] = l.d[i];
@@ -471,6 +468,7 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     g.lddx = lddx;
     g.vec = vec4(dx, lddx, c.dy->type);
     g.norm = a.norm;
+    g.sums = sums;
     return (entq_status)launch_grad_product(l.grad, g, s);
 }
 

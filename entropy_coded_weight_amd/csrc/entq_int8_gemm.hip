@@ -236,8 +236,7 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
 
 // Adds the splits' sums up (integers: in any order the same) and finishes
 // them. A workgroup: 256 channels (a wave's lanes 4 each), its 4 waves a
-// token each, or backward, where a workgroup adds its tokens up, 16 in turn.
-constexpr uint32_t finish_tokens(Int8Mode mode) { return mode == kBwd || mode == kGatedBwd ? 16 : 4; }
+// token each.
 template <int MODE>
 __global__ __launch_bounds__(256) void int8_finish(Int8Args a) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
@@ -248,18 +247,16 @@ __global__ __launch_bounds__(256) void int8_finish(Int8Args a) {
     float scale[2][4], sg[4] = {}, su[4] = {};
     load_scales<MODE>(a, n, scale);
     const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
-    for (uint32_t i = wave; i < finish_tokens((Int8Mode)MODE); i += 4) {
-        const uint32_t m = blockIdx.y * finish_tokens((Int8Mode)MODE) + i;
-        v4i s[2] = {};
-        if (m < a.M && n < a.N) {
+    const uint32_t m = blockIdx.y * 4 + wave;
+    v4i s[2] = {};
+    if (m < a.M && n < a.N) {
 #pragma unroll 4
-            for (uint32_t k = 0; k < a.splits; ++k) {
-                s[0] += *(const v4i *)part_sums<kTwo>(a, k, 0, m, n);
-                if (kTwo) s[1] += *(const v4i *)part_sums<kTwo>(a, k, 1, m, n);
-            }
+        for (uint32_t k = 0; k < a.splits; ++k) {
+            s[0] += *(const v4i *)part_sums<kTwo>(a, k, 0, m, n);
+            if (kTwo) s[1] += *(const v4i *)part_sums<kTwo>(a, k, 1, m, n);
         }
-        epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, norm, m, n, s[0], s[1], sg, su);
     }
+    epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, norm, m, n, s[0], s[1], sg, su);
     if constexpr (kBack) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -297,7 +294,7 @@ void launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
 
 void launch_finish(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
-    const dim3 grid((cols + 255) / 256, (a.M + finish_tokens(mode) - 1) / finish_tokens(mode));
+    const dim3 grid((cols + 255) / 256, (a.M + 3) / 4);
     if (mode == kFwd) int8_finish<kFwd><<<grid, 256, 0, s>>>(a);
     if (mode == kGated) int8_finish<kGated><<<grid, 256, 0, s>>>(a);
     if (mode == kBwd) int8_finish<kBwd><<<grid, 256, 0, s>>>(a);
@@ -336,7 +333,7 @@ Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K
             return p;
         }
     }
-    p.part_rows = p.splits > 1 ? (M + 15) / 16 : (M + p.tile - 1) / p.tile * 2;
+    p.part_rows = p.splits > 1 ? (M + 3) / 4 : (M + p.tile - 1) / p.tile * 2;
     return p;
 }
 

@@ -48,6 +48,11 @@ __global__ __launch_bounds__(256) void grad_tiles(GradArgs a, uint32_t nb_m, uin
     // lanes read at once (8 rows, 2 neighbouring columns chunks) fill all banks
     auto twist = [](uint32_t r) { return BK == 256 ? 2 * (r % 8) : 2 * (r / 2 % 4); };
 
+    // the workgroups after the tiles finish the channel sums of the kernel before
+    if (blockIdx.x >= nb_m * nb_k) {
+        if (blockIdx.y == 0) sum_parts_block(a.sums, blockIdx.x - nb_m * nb_k);
+        return;
+    }
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t wm = wave % WM, wn = wave / WM;
     uint32_t tm, tk;
@@ -232,7 +237,7 @@ __global__ __launch_bounds__(256) void grad_sum(GradArgs a) {
 template <int BM, int BK, int WM, int WN, int S>
 void launch_tiles(const GradArgs &a, hipStream_t s) {
     const uint32_t nb_m = (a.M + BM - 1) / BM, nb_k = (a.K + BK - 1) / BK;
-    const dim3 grid(nb_m * nb_k, a.splits);
+    const dim3 grid(nb_m * nb_k + sum_blocks(a.sums), a.splits);
     if (a.f16)
         grad_tiles<true, BM, BK, WM, WN, S><<<grid, 256, 0, s>>>(a, nb_m, nb_k);
     else

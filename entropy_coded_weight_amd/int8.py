@@ -14,11 +14,9 @@ for the call.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from . import EINVAL, EntqError, _check, lib
+from . import EINVAL, EntqError, Rows, _check, lib
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 MAX_COLS = 131071  # keeps every sum of code products inside int32
@@ -27,97 +25,111 @@ _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3}
 _BF16, _F16, _F32, _I8 = 0, 1, 2, 3
 
 
-class _Rows(ctypes.Structure):  # entq_rows
-    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_uint64), ("scales", ctypes.c_void_p),
-                ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("type", ctypes.c_int32),
-                ("reserved", ctypes.c_uint32)]
-
-
-def _matrix(name, t, device, types, shape=None):
-    """(type, row stride) of a 2-D device matrix with unit-stride rows."""
+def _matrix(name, t, index, types, shape=None):
+    """(type, row stride) of a 2-D matrix with unit-stride rows on GPU
+    ``index``."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise EntqError(EINVAL, f"{name}: a torch tensor on a GPU is required")
-    if device is not None and t.device != device:
-        raise EntqError(EINVAL, f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise EntqError(EINVAL, f"{name} is on {t.device}, expected cuda:{index}")
     kind = _TYPES.get(t.dtype)
     if kind not in types:
         raise EntqError(EINVAL, f"{name} has dtype {t.dtype}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise EntqError(EINVAL, f"{name} has shape {tuple(t.shape)}"
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
+        raise EntqError(EINVAL, f"{name} has shape {tuple(size)}"
                                 + ("" if shape is None else f", expected {tuple(shape)}"))
     ld, unit = t.stride()
-    rows, cols = t.shape
-    if rows <= 1 or cols == 0:
-        ld = max(ld, cols)
-    if (unit != 1 and cols > 1) or ld < cols:
-        raise EntqError(EINVAL, f"{name}: strides {t.stride()}; rows of unit stride that do not "
-                                "overlap are required")
+    rows, cols = size
+    if unit != 1 or ld < cols:
+        if rows <= 1 or cols == 0:
+            ld = max(ld, cols)
+        if (unit != 1 and cols > 1) or ld < cols:
+            raise EntqError(EINVAL, f"{name}: strides {t.stride()}; rows of unit stride that do "
+                                    "not overlap are required")
     return kind, ld
 
 
-def _vector(name, t, device, n):
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise EntqError(EINVAL, f"{name}: a torch tensor on {device} is required")
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+def _vector(name, t, index, n):
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise EntqError(EINVAL, f"{name}: a torch tensor on cuda:{index} is required")
+    if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
         raise EntqError(EINVAL, f"{name}: {t.dtype} {tuple(t.shape)}; a contiguous float32 vector "
                                 f"of {n} is required")
     return t.data_ptr()
 
 
-def _x_rows(x, x_scales, types=(_BF16, _F16, _F32, _I8)):
-    kind, ld = _matrix("x", x, None, types)
+def _gpu(name, t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise EntqError(EINVAL, f"{name}: a torch tensor on a GPU is required")
+    return t.get_device()
+
+
+def _x_rows(x, x_scales, index, types=(_BF16, _F16, _F32, _I8)):
+    kind, ld = _matrix("x", x, index, types)
     m, k = x.shape
     if k > MAX_COLS:
         raise EntqError(EINVAL, f"x has {k} columns, at most {MAX_COLS} are taken")
     if kind == _I8:
-        s = _vector("x_scales", x_scales, x.device, m)
+        s = _vector("x_scales", x_scales, index, m)
     elif x_scales is not None:
         raise EntqError(EINVAL, f"x_scales go with int8 codes, x has dtype {x.dtype}")
     else:
         s = 0
-    return _Rows(x.data_ptr(), ld, s, m, k, kind, 0)
+    return Rows(x.data_ptr(), ld, s, m, k, kind, 0)
 
 
-def _w_rows(name, w, scales, x, shape=None):
-    _, ld = _matrix(name, w, x.device, (_I8,), shape)
+def _w_rows(name, w, scales, index, columns, shape=None):
+    _, ld = _matrix(name, w, index, (_I8,), shape)
     n, k = w.shape
-    if k != x.shape[1]:
-        raise EntqError(EINVAL, f"{name} has {k} columns, x has {x.shape[1]}")
-    return _Rows(w.data_ptr(), ld, _vector(name + "_scales", scales, x.device, n), n, k, _I8, 0)
+    if k != columns:
+        raise EntqError(EINVAL, f"{name} has {k} columns, x has {columns}")
+    return Rows(w.data_ptr(), ld, _vector(name + "_scales", scales, index, n), n, k, _I8, 0)
 
 
-def _grad_rows(name, t, x, n):
-    kind, ld = _matrix(name, t, x.device, (_BF16, _F16), (x.shape[0], n))
-    return _Rows(t.data_ptr(), ld, 0, t.shape[0], n, kind, 0)
+def _grad_rows(name, t, index, rows, n):
+    kind, ld = _matrix(name, t, index, (_BF16, _F16), (rows, n))
+    return Rows(t.data_ptr(), ld, 0, rows, n, kind, 0)
 
 
-def _enqueue(what, call, need, device, stream, workspace):
+def _enqueue(what, call, need, index, stream, workspace):
     """Runs ``call(workspace pointer, bytes, stream handle)`` on ``stream``
     with a workspace of ``need`` bytes, allocated on that stream when none is
     given (so that its memory is ordered with what else uses it there)."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _enqueue(what, call, need, device, stream, workspace)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _enqueue(what, call, need, index, stream, workspace)
     if workspace is not None:
-        if not isinstance(workspace, torch.Tensor) or workspace.device != device:
-            raise EntqError(EINVAL, f"workspace: a torch tensor on {device} is required")
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index:
+            raise EntqError(EINVAL, f"workspace: a torch tensor on cuda:{index} is required")
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise EntqError(EINVAL, "workspace: a contiguous uint8 tensor is required")
         if workspace.numel() < need:
             raise EntqError(EINVAL, f"workspace holds {workspace.numel()} bytes, {need} needed")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif isinstance(stream, int):
-        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
-                  else torch.cuda.default_stream(device))
-    if workspace is None and need:
-        if stream == torch.cuda.current_stream(device):
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
+        handle = _current_stream(index)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=index)
+    else:
+        if isinstance(stream, int):
+            stream = (torch.cuda.ExternalStream(stream, device=index) if stream
+                      else torch.cuda.default_stream(index))
+        handle = stream.cuda_stream
+        if workspace is None and need:
             with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    ptr, n = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (0, 0)
-    _check(call(ptr, n, stream.cuda_stream), what)
+                workspace = torch.empty(need, dtype=torch.uint8, device=index)
+    if workspace is None:
+        _check(call(0, 0, handle), what)
+    else:
+        _check(call(workspace.data_ptr(), workspace.numel(), handle), what)
+
+
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without a Stream object around it (1.9 us of a call's 10)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def quantize_rows(x, codes, scales, stream=None):
@@ -125,29 +137,26 @@ def quantize_rows(x, codes, scales, stream=None):
     [M, K]) into ``codes`` (int8 [M, K]) and ``scales`` (float32 [M]):
     scale = max(|x|) / 127 (at least 2^-100), code = x / scale rounded half
     to even. A row with a NaN or an infinity gets a NaN scale and codes 0."""
-    kind, ld = _matrix("x", x, None, (_BF16, _F16, _F32))
-    m, k = x.shape
-    if k > MAX_COLS:
-        raise EntqError(EINVAL, f"x has {k} columns, at most {MAX_COLS} are taken")
-    _, ldc = _matrix("codes", codes, x.device, (_I8,), x.shape)
-    s = _vector("scales", scales, x.device, m)
-    r = _Rows(x.data_ptr(), ld, 0, m, k, kind, 0)
+    index = _gpu("x", x)
+    r = _x_rows(x, None, index, (_BF16, _F16, _F32))
+    _, ldc = _matrix("codes", codes, index, (_I8,), x.shape)
+    s = _vector("scales", scales, index, r.rows)
     _enqueue("entq_quantize_rows",
-             lambda w, n, st: lib().entq_quantize_rows(ctypes.byref(r), codes.data_ptr(), ldc, s, st),
-             0, x.device, stream, None)
+             lambda w, n, st: lib().entq_quantize_rows(r, codes.data_ptr(), ldc, s, st),
+             0, index, stream, None)
 
 
 def gemm(x, x_scales, w, w_scales, y, stream=None, workspace=None):
     """Y = X . W^T into y (bfloat16, float16 or float32 [M, N]):
     y[m][n] = sx[m] sw[n] sum_k x[m][k] w[n][k], the sum exact in int32."""
-    xr = _x_rows(x, x_scales)
-    wr = _w_rows("w", w, w_scales, x)
-    kind, ldy = _matrix("y", y, x.device, (_BF16, _F16, _F32), (x.shape[0], w.shape[0]))
+    index = _gpu("x", x)
+    a = _x_rows(x, x_scales, index)
+    b = _w_rows("w", w, w_scales, index, a.cols)
+    kind, ldy = _matrix("y", y, index, (_BF16, _F16, _F32), (a.rows, b.rows))
     L = lib()
-    a, b = ctypes.byref(xr), ctypes.byref(wr)
     _enqueue("entq_int8_gemm",
              lambda p, n, s: L.entq_int8_gemm(a, b, y.data_ptr(), kind, ldy, p, n, s),
-             L.entq_int8_gemm_workspace_bytes(a, b), x.device, stream, workspace)
+             L.entq_int8_gemm_workspace_bytes(a, b), index, stream, workspace)
 
 
 def gated(x, x_scales, gate, gate_scales, up, up_scales, h, activation="silu", stream=None,
@@ -155,16 +164,16 @@ def gated(x, x_scales, gate, gate_scales, up, up_scales, h, activation="silu", s
     """H = act(X . gate^T) * (X . up^T) into h (bfloat16, float16 or float32
     [M, N]), both products, the activation and the product in one kernel.
     activation: "silu", "gelu", "gelu_tanh" or "relu"."""
-    xr = _x_rows(x, x_scales)
-    gr = _w_rows("gate", gate, gate_scales, x)
-    ur = _w_rows("up", up, up_scales, x, gate.shape)
-    kind, ldh = _matrix("h", h, x.device, (_BF16, _F16, _F32), (x.shape[0], gate.shape[0]))
+    index = _gpu("x", x)
+    a = _x_rows(x, x_scales, index)
+    g = _w_rows("gate", gate, gate_scales, index, a.cols)
+    u = _w_rows("up", up, up_scales, index, a.cols, gate.shape)
+    kind, ldh = _matrix("h", h, index, (_BF16, _F16, _F32), (a.rows, g.rows))
     act = _activation(activation)
     L = lib()
-    a, g, u = ctypes.byref(xr), ctypes.byref(gr), ctypes.byref(ur)
     _enqueue("entq_int8_gated",
              lambda p, n, s: L.entq_int8_gated(a, g, u, act, h.data_ptr(), kind, ldh, p, n, s),
-             L.entq_int8_gated_workspace_bytes(a, g, u), x.device, stream, workspace)
+             L.entq_int8_gated_workspace_bytes(a, g, u), index, stream, workspace)
 
 
 def gemm_backward(dy, x, x_scales, w, w_scales, dx=None, dw_scales=None, stream=None,
@@ -173,16 +182,16 @@ def gemm_backward(dy, x, x_scales, w, w_scales, dx=None, dw_scales=None, stream=
     type, [M, K]; the quantiser of x passed straight through) and dw_scales
     (float32 [N]). x: the int8 codes of the forward pass. A gradient whose
     tensor is None is not computed."""
-    xr = _x_rows(x, x_scales, (_I8,))
-    wr = _w_rows("w", w, w_scales, x)
-    dr = _grad_rows("dy", dy, x, w.shape[0])
-    dxp, lddx = _dx(dx, dy, x)
-    ds = _vector("dw_scales", dw_scales, x.device, w.shape[0]) if dw_scales is not None else 0
+    index = _gpu("x", x)
+    a = _x_rows(x, x_scales, index, (_I8,))
+    b = _w_rows("w", w, w_scales, index, a.cols)
+    d = _grad_rows("dy", dy, index, a.rows, b.rows)
+    dxp, lddx = _dx(dx, d, x, index)
+    ds = _vector("dw_scales", dw_scales, index, b.rows) if dw_scales is not None else 0
     L = lib()
-    d, a, b = ctypes.byref(dr), ctypes.byref(xr), ctypes.byref(wr)
     _enqueue("entq_int8_gemm_backward",
              lambda p, n, s: L.entq_int8_gemm_backward(d, a, b, dxp, lddx, ds, p, n, s),
-             L.entq_int8_gemm_backward_workspace_bytes(d, a, b), x.device, stream, workspace)
+             L.entq_int8_gemm_backward_workspace_bytes(d, a, b), index, stream, workspace)
 
 
 def gated_backward(dh, x, x_scales, gate, gate_scales, up, up_scales, dx=None,
@@ -191,20 +200,19 @@ def gated_backward(dh, x, x_scales, gate, gate_scales, up, up_scales, dx=None,
     """Gradients of ``gated`` for dh (bfloat16 or float16 [M, N]): dx (dh's
     type, [M, K]), dgate_scales and dup_scales (float32 [N]); x, None and the
     rest as ``gemm_backward``."""
-    xr = _x_rows(x, x_scales, (_I8,))
-    gr = _w_rows("gate", gate, gate_scales, x)
-    ur = _w_rows("up", up, up_scales, x, gate.shape)
-    n = gate.shape[0]
-    dr = _grad_rows("dh", dh, x, n)
-    dxp, lddx = _dx(dx, dh, x)
-    dsg = _vector("dgate_scales", dgate_scales, x.device, n) if dgate_scales is not None else 0
-    dsu = _vector("dup_scales", dup_scales, x.device, n) if dup_scales is not None else 0
+    index = _gpu("x", x)
+    a = _x_rows(x, x_scales, index, (_I8,))
+    g = _w_rows("gate", gate, gate_scales, index, a.cols)
+    u = _w_rows("up", up, up_scales, index, a.cols, gate.shape)
+    d = _grad_rows("dh", dh, index, a.rows, g.rows)
+    dxp, lddx = _dx(dx, d, x, index)
+    dsg = _vector("dgate_scales", dgate_scales, index, g.rows) if dgate_scales is not None else 0
+    dsu = _vector("dup_scales", dup_scales, index, g.rows) if dup_scales is not None else 0
     act = _activation(activation)
     L = lib()
-    d, a, g, u = ctypes.byref(dr), ctypes.byref(xr), ctypes.byref(gr), ctypes.byref(ur)
     _enqueue("entq_int8_gated_backward",
-             lambda p, b, s: L.entq_int8_gated_backward(d, a, g, u, act, dxp, lddx, dsg, dsu, p, b, s),
-             L.entq_int8_gated_backward_workspace_bytes(d, a, g, u), x.device, stream, workspace)
+             lambda p, n, s: L.entq_int8_gated_backward(d, a, g, u, act, dxp, lddx, dsg, dsu, p, n, s),
+             L.entq_int8_gated_backward_workspace_bytes(d, a, g, u), index, stream, workspace)
 
 
 def _activation(name):
@@ -214,10 +222,10 @@ def _activation(name):
     return act
 
 
-def _dx(dx, dy, x):
+def _dx(dx, d, x, index):
     if dx is None:
         return 0, x.shape[1]
-    _, ld = _matrix("dx", dx, x.device, (_TYPES[dy.dtype],), x.shape)
+    _, ld = _matrix("dx", dx, index, (d.type,), x.shape)
     return dx.data_ptr(), ld
 
 
@@ -230,9 +238,10 @@ def workspace_bytes(op, x, x_scales, *weights_and_scales, dy=None):
             len(weights_and_scales) != (4 if two else 2):
         raise EntqError(EINVAL, f"workspace_bytes of {op!r} with {len(weights_and_scales)} "
                                 "weights and scales")
-    args = [_x_rows(x, x_scales)]
+    index = _gpu("x", x)
+    args = [_x_rows(x, x_scales, index)]
     for i in range(0, len(weights_and_scales), 2):
-        args.append(_w_rows(f"w{i // 2}", *weights_and_scales[i:i + 2], x))
+        args.append(_w_rows(f"w{i // 2}", *weights_and_scales[i:i + 2], index, args[0].cols))
     if op.endswith("backward"):
-        args.insert(0, _grad_rows("dy", dy, x, weights_and_scales[0].shape[0]))
-    return int(getattr(lib(), f"entq_int8_{op}_workspace_bytes")(*map(ctypes.byref, args)))
+        args.insert(0, _grad_rows("dy", dy, index, args[0].rows, args[1].rows))
+    return int(getattr(lib(), f"entq_int8_{op}_workspace_bytes")(*args))

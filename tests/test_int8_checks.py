@@ -99,13 +99,13 @@ def test_host_tensors_are_refused(E, I):
 A = 1 << 20
 
 
-def rows(I, r, c, kind=3, ld=None, data=A, scales=A, reserved=0):
-    return I._Rows(data, c if ld is None else ld, scales if kind == 3 else 0, r, c, kind, reserved)
+def rows(E, r, c, kind=3, ld=None, data=A, scales=A, reserved=0):
+    return E.Rows(data, c if ld is None else ld, scales if kind == 3 else 0, r, c, kind, reserved)
 
 
 def forward(E, I, x=None, w=None, up=None, y=A, kind=0, ldy=None, act=0, ws=A, ws_bytes=1 << 40):
-    x = x or rows(I, 4, 32)
-    w = w or rows(I, 8, 32)
+    x = x or rows(E, 4, 32)
+    w = w or rows(E, 8, 32)
     ldy = w.rows if ldy is None else ldy
     b = ctypes.byref
     if up is None:
@@ -117,36 +117,36 @@ EALIGN, EWORKSPACE = -4, -5
 
 
 def test_c_refusals_forward(E, I):
-    bad = [dict(x=rows(I, 4, 31)), dict(x=rows(I, 4, 32, ld=31)), dict(x=rows(I, 4, 32, data=0)),
-           dict(x=rows(I, 4, 32, scales=0)), dict(x=rows(I, 4, 32, kind=4)), dict(x=rows(I, 4, 32, kind=-1)),
-           dict(x=rows(I, 4, 32, reserved=1)), dict(w=rows(I, 8, 32, kind=0)), dict(w=rows(I, 8, 32, scales=0)),
-           dict(w=rows(I, 8, 32, ld=1 << 41)), dict(y=0), dict(kind=3), dict(kind=7), dict(ldy=7),
-           dict(x=rows(I, 4, 131072), w=rows(I, 8, 131072)), dict(x=rows(I, 1 << 31, 32)),
-           dict(up=rows(I, 7, 32)), dict(up=rows(I, 8, 32, kind=2)), dict(up=rows(I, 8, 33)),
-           dict(up=rows(I, 8, 32), act=4), dict(up=rows(I, 8, 32), act=-1)]
+    bad = [dict(x=rows(E, 4, 31)), dict(x=rows(E, 4, 32, ld=31)), dict(x=rows(E, 4, 32, data=0)),
+           dict(x=rows(E, 4, 32, scales=0)), dict(x=rows(E, 4, 32, kind=4)), dict(x=rows(E, 4, 32, kind=-1)),
+           dict(x=rows(E, 4, 32, reserved=1)), dict(w=rows(E, 8, 32, kind=0)), dict(w=rows(E, 8, 32, scales=0)),
+           dict(w=rows(E, 8, 32, ld=1 << 41)), dict(y=0), dict(kind=3), dict(kind=7), dict(ldy=7),
+           dict(x=rows(E, 4, 131072), w=rows(E, 8, 131072)), dict(x=rows(E, 1 << 31, 32)),
+           dict(up=rows(E, 7, 32)), dict(up=rows(E, 8, 32, kind=2)), dict(up=rows(E, 8, 33)),
+           dict(up=rows(E, 8, 32), act=4), dict(up=rows(E, 8, 32), act=-1)]
     for k in bad:
         assert forward(E, I, **k) == E.EINVAL, {n: getattr(v, "cols", v) for n, v in k.items()}
-    x = I._Rows(A, 32, A, 4, 32, 0, 0)  # activations with scales
+    x = E.Rows(A, 32, A, 4, 32, 0, 0)  # activations with scales
     assert forward(E, I, x=x) == E.EINVAL
     L, b = E.lib(), ctypes.byref
-    assert L.entq_int8_gemm(None, b(rows(I, 8, 32)), A, 0, 8, A, 1 << 40, None) == E.EINVAL
-    assert L.entq_int8_gemm(b(rows(I, 8, 32)), None, A, 0, 8, A, 1 << 40, None) == E.EINVAL
-    for k in (dict(y=A + 1), dict(y=A + 2, kind=2), dict(x=rows(I, 4, 32, scales=A + 2)),
-              dict(x=rows(I, 4, 32, kind=0, data=A + 1)), dict(x=rows(I, 4, 32, kind=2, data=A + 2)),
-              dict(x=rows(I, 4, 32, kind=0), ws=A + 128)):
+    assert L.entq_int8_gemm(None, b(rows(E, 8, 32)), A, 0, 8, A, 1 << 40, None) == E.EINVAL
+    assert L.entq_int8_gemm(b(rows(E, 8, 32)), None, A, 0, 8, A, 1 << 40, None) == E.EINVAL
+    for k in (dict(y=A + 1), dict(y=A + 2, kind=2), dict(x=rows(E, 4, 32, scales=A + 2)),
+              dict(x=rows(E, 4, 32, kind=0, data=A + 1)), dict(x=rows(E, 4, 32, kind=2, data=A + 2)),
+              dict(x=rows(E, 4, 32, kind=0), ws=A + 128)):
         assert forward(E, I, **k) == EALIGN
-    act = rows(I, 4, 32, kind=0)
-    need = E.lib().entq_int8_gemm_workspace_bytes(b(act), b(rows(I, 8, 32)))
+    act = rows(E, 4, 32, kind=0)
+    need = E.lib().entq_int8_gemm_workspace_bytes(b(act), b(rows(E, 8, 32)))
     assert need > 0
     assert forward(E, I, x=act, ws_bytes=need - 1) == EWORKSPACE
     assert forward(E, I, x=act, ws=0, ws_bytes=0) == EWORKSPACE
-    assert E.lib().entq_int8_gemm_workspace_bytes(b(act), b(rows(I, 8, 33))) == 0
+    assert E.lib().entq_int8_gemm_workspace_bytes(b(act), b(rows(E, 8, 33))) == 0
     assert E.lib().entq_int8_gemm_workspace_bytes(None, None) == 0
 
 
 def test_c_refusals_backward(E, I):
     L, b = E.lib(), ctypes.byref
-    x, w, dy = rows(I, 4, 32), rows(I, 8, 32), rows(I, 4, 8, kind=0)
+    x, w, dy = rows(E, 4, 32), rows(E, 8, 32), rows(E, 4, 8, kind=0)
 
     def back(dy=dy, x=x, w=w, dx=A, lddx=32, ds=A, ws=A, n=1 << 40):
         return L.entq_int8_gemm_backward(dy and b(dy), x and b(x), w and b(w), dx, lddx, ds, ws, n, None)
@@ -154,14 +154,14 @@ def test_c_refusals_backward(E, I):
     def gated(dy=dy, up=w, act=0, dx=A, lddx=32, ds=A, du=A, ws=A, n=1 << 40):
         return L.entq_int8_gated_backward(dy and b(dy), b(x), b(w), up and b(up), act, dx, lddx, ds, du, ws, n, None)
 
-    for k in (dict(dy=rows(I, 4, 9, kind=0)), dict(dy=rows(I, 5, 8, kind=0)), dict(dy=rows(I, 4, 8, kind=2)),
-              dict(dy=rows(I, 4, 8)), dict(dy=rows(I, 4, 8, kind=0, ld=7)), dict(dy=rows(I, 4, 8, kind=0, data=0)),
+    for k in (dict(dy=rows(E, 4, 9, kind=0)), dict(dy=rows(E, 5, 8, kind=0)), dict(dy=rows(E, 4, 8, kind=2)),
+              dict(dy=rows(E, 4, 8)), dict(dy=rows(E, 4, 8, kind=0, ld=7)), dict(dy=rows(E, 4, 8, kind=0, data=0)),
               dict(dy=None), dict(lddx=31)):
         assert back(**k) == E.EINVAL, k
         assert gated(**k) == E.EINVAL, k
-    assert back(x=rows(I, 4, 32, kind=0)) == E.EINVAL
-    assert gated(act=9) == E.EINVAL and gated(up=rows(I, 9, 32)) == E.EINVAL and gated(up=None) == E.EINVAL
-    for k in (dict(dx=A + 1), dict(ds=A + 2), dict(ws=A + 64), dict(dy=rows(I, 4, 8, kind=1, data=A + 1))):
+    assert back(x=rows(E, 4, 32, kind=0)) == E.EINVAL
+    assert gated(act=9) == E.EINVAL and gated(up=rows(E, 9, 32)) == E.EINVAL and gated(up=None) == E.EINVAL
+    for k in (dict(dx=A + 1), dict(ds=A + 2), dict(ws=A + 64), dict(dy=rows(E, 4, 8, kind=1, data=A + 1))):
         assert back(**k) == EALIGN and gated(**k) == EALIGN, k
     assert gated(du=A + 1) == EALIGN
     assert back(n=255) == EWORKSPACE and gated(ws=0) == EWORKSPACE
@@ -170,11 +170,11 @@ def test_c_refusals_backward(E, I):
 
 def test_c_refusals_quantize(E, I):
     L, b = E.lib(), ctypes.byref
-    for r, q, ld, s, want in ((rows(I, 4, 32), A, 32, A, E.EINVAL), (rows(I, 4, 32, kind=0), A, 31, A, E.EINVAL),
-                              (rows(I, 4, 32, kind=0), 0, 32, A, E.EINVAL),
-                              (rows(I, 4, 32, kind=0), A, 32, 0, E.EINVAL),
-                              (rows(I, 4, 32, kind=0), A, 32, A + 1, EALIGN),
-                              (rows(I, 4, 131072, kind=0), A, 131072, A, E.EINVAL),
-                              (rows(I, 0, 32, kind=0), 0, 32, 0, 0)):
+    for r, q, ld, s, want in ((rows(E, 4, 32), A, 32, A, E.EINVAL), (rows(E, 4, 32, kind=0), A, 31, A, E.EINVAL),
+                              (rows(E, 4, 32, kind=0), 0, 32, A, E.EINVAL),
+                              (rows(E, 4, 32, kind=0), A, 32, 0, E.EINVAL),
+                              (rows(E, 4, 32, kind=0), A, 32, A + 1, EALIGN),
+                              (rows(E, 4, 131072, kind=0), A, 131072, A, E.EINVAL),
+                              (rows(E, 0, 32, kind=0), 0, 32, 0, 0)):
         assert L.entq_quantize_rows(b(r), q, ld, s, None) == want
     assert L.entq_quantize_rows(None, A, 32, A, None) == E.EINVAL
