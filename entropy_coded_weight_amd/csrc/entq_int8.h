@@ -153,20 +153,32 @@ __device__ __forceinline__ void load_scales(const Int8Args &a, uint32_t n, float
     }
 }
 
+// The incoming gradient (4 values of 16 bits) at token m, channels n..n+3.
+__device__ __forceinline__ uint2 load_grad4(const Int8Args &a, uint32_t m, uint32_t n) {
+    if (m >= a.M || n >= a.N) return make_uint2(0, 0);
+    const uint16_t *y = (const uint16_t *)a.y + (uint64_t)m * a.ldy + n;
+    if (a.vec && n + 4 <= a.N) return *(const uint2 *)y;
+    uint32_t b[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+        if (n + i < a.N) b[i] = y[i];
+    return make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+}
+
 // The results for token m (of scale sx) and the 4 channels n..n+3 (n a multiple of 4), or
 // the gradients, whose contributions to the channel sums are added to sg, su.
 // Channels of N and beyond are not stored; in a backward pass a token of M
 // and beyond adds nothing.
 template <int MODE>
 __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const float (&scale)[2][4], float norm,
-                                          uint32_t m, uint32_t n, v4i ag, v4i au, float (&sg)[4],
-                                          float (&su)[4]) {
+                                          uint32_t m, uint32_t n, v4i ag, v4i au, uint2 dy4,
+                                          float (&sg)[4], float (&su)[4]) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
     constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
     if (m >= a.M || n >= (kBack ? (uint32_t)a.ldd : a.N)) return;
-    const bool whole = n + 4 <= a.N;
-    const uint64_t at = (uint64_t)m * a.ldy + n;
     if constexpr (!kBack) {
+        const bool whole = n + 4 <= a.N;
+        const uint64_t at = (uint64_t)m * a.ldy + n;
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -196,20 +208,10 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
         }
     } else {
         const bool f16 = a.type == ENTQ_F16;
-        const uint16_t *y = (const uint16_t *)a.y + at;
-        uint16_t b[4] = {0, 0, 0, 0};
-        if (whole && a.vec) {
-            const uint2 v = *(const uint2 *)y;
-            b[0] = (uint16_t)v.x, b[1] = (uint16_t)(v.x >> 16);
-            b[2] = (uint16_t)v.y, b[3] = (uint16_t)(v.y >> 16);
-        } else {
-            for (int i = 0; i < 4; ++i)
-                if (n + i < a.N) b[i] = y[i];
-        }
         uint16_t d[2][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float dy = from16(b[i], f16);
+            const float dy = from16((uint16_t)((i < 2 ? dy4.x : dy4.y) >> (16 * (i % 2))), f16);
             const float g0 = (float)ag[i] * sx;  // before the channel's scale
             const bool in = n + i < a.N;
             if (!kTwo) {

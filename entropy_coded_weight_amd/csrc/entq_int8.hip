@@ -110,21 +110,49 @@ int launch_quantize(const entq_rows &x, int8_t *codes, uint64_t ldc, uint32_t pa
 // aligned copies
 // ---------------------------------------------------------------------------
 
-// Rows of K codes at any address into rows of ldc (a multiple of 16), zeros
-// after column K.
-__global__ __launch_bounds__(256) void align_rows(const int8_t *src, uint64_t ld, uint32_t rows, uint32_t K,
-                                                  int8_t *dst, uint32_t ldc) {
-    const uint32_t c = 16 * (blockIdx.x * 256 + threadIdx.x);
-    if (c >= ldc) return;
-    for (uint64_t r = blockIdx.y; r < rows; r += gridDim.y)
-        *(v4i *)(dst + r * ldc + c) = load16_any(src + r * ld, c, K);
+// Up to 3 matrices' rows of K codes at any address into rows of ldc (a
+// multiple of 16), zeros after column K. A thread moves 16 codes.
+struct AlignJob {
+    const int8_t *src;
+    uint64_t ld;
+    int8_t *dst;
+    uint32_t rows, ldc, first;  // first: its first workgroup
+};
+struct AlignArgs {
+    AlignJob job[3];
+    uint32_t K;
+};
+
+__global__ __launch_bounds__(256) void align_rows(AlignArgs a) {
+    const AlignJob &j = a.job[blockIdx.x >= a.job[2].first ? 2 : blockIdx.x >= a.job[1].first ? 1 : 0];
+    const uint64_t i = (uint64_t)(blockIdx.x - j.first) * 256 + threadIdx.x;
+    const uint32_t pieces = j.ldc / 16;
+    const uint64_t r = i / pieces;
+    if (r >= j.rows) return;
+    const uint32_t c = (uint32_t)(i - r * pieces) * 16;
+    *(v4i *)(j.dst + r * j.ldc + c) = load16_any(j.src + r * j.ld, c, a.K);
 }
 
-int launch_align(const entq_rows &m, int8_t *dst, uint32_t ldc, hipStream_t s) {
-    align_rows<<<dim3((ldc / 16 + 255) / 256, std::min(m.rows, 65535u)), 256, 0, s>>>(
-        (const int8_t *)m.d_data, m.ld, m.rows, m.cols, dst, ldc);
-    return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
-}
+// Collects copies and launches them together.
+struct Aligner {
+    AlignArgs a{};
+    uint32_t n = 0, blocks = 0;
+    bool too_many = false;  // workgroups for one launch
+    void add(const entq_rows &m, int8_t *dst, uint32_t ldc) {
+        a.K = m.cols;
+        a.job[n++] = {(const int8_t *)m.d_data, m.ld, dst, m.rows, ldc, blocks};
+        const uint64_t more = ((uint64_t)m.rows * (ldc / 16) + 255) / 256;
+        if (blocks + more >= 1u << 23) too_many = true;
+        blocks += (uint32_t)more;
+    }
+    int launch(hipStream_t s) {
+        if (!n) return ENTQ_OK;
+        if (too_many) return ENTQ_ETOOLARGE;
+        for (uint32_t i = n; i < 3; ++i) a.job[i].first = 0xFFFFFFFFu;
+        align_rows<<<blocks, 256, 0, s>>>(a);
+        return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
+    }
+};
 
 // Whether the products can read the codes where they are.
 bool direct(const entq_rows &m) {
@@ -170,16 +198,9 @@ __global__ __launch_bounds__(256) void scale_gradient(Int8Args a) {
     float scale[2][4];
     load_scales<kBwd>(a, n, scale);
     for (uint64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
-        const uint16_t *y = (const uint16_t *)a.y + m * a.ldy + n;
-        uint16_t b[4] = {0, 0, 0, 0}, d[4];
-        if (a.vec && n + 4 <= a.N) {
-            const uint2 v = *(const uint2 *)y;
-            b[0] = (uint16_t)v.x, b[1] = (uint16_t)(v.x >> 16), b[2] = (uint16_t)v.y, b[3] = (uint16_t)(v.y >> 16);
-        } else {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)
-                if (n + i < a.N) b[i] = y[i];
-        }
+        const uint2 v = load_grad4(a, (uint32_t)m, n);
+        const uint16_t b[4] = {(uint16_t)v.x, (uint16_t)(v.x >> 16), (uint16_t)v.y, (uint16_t)(v.y >> 16)};
+        uint16_t d[4];
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i)
             d[i] = n + i < a.N ? bits16(from16(b[i], f16) * (scale[0][i] * norm), f16) : 0;
@@ -351,24 +372,24 @@ entq_status operands(const Call &c, const Layout &l, Int8Args &a, hipStream_t s)
     if (c.x->type != ENTQ_I8 && !l.plan.quantizes) {
         r = launch_quantize(*c.x, l.codes, l.ldc, (uint32_t)l.ldc, l.scales, s);
         a.sx = l.scales;
-    } else if (l.codes) {
-        r = launch_align(*c.x, l.codes, (uint32_t)l.ldc, s);
     }
+    Aligner copies;
+    if (c.x->type == ENTQ_I8 && l.codes) copies.add(*c.x, l.codes, (uint32_t)l.ldc);
     if (l.codes) {
         a.x = l.codes;
         a.ldx = l.ldc;
     }
-    for (int i = 0; i < c.n_w && r == ENTQ_OK; ++i) {
+    for (int i = 0; i < c.n_w; ++i) {
         a.w[i] = (const int8_t *)c.w[i]->d_data;
         a.ldw[i] = c.w[i]->ld;
         a.sw[i] = c.w[i]->d_scales;
         if (l.w[i]) {
-            r = launch_align(*c.w[i], l.w[i], l.ldw, s);
+            copies.add(*c.w[i], l.w[i], l.ldw);
             a.w[i] = l.w[i];
             a.ldw[i] = l.ldw;
         }
     }
-    return (entq_status)r;
+    return (entq_status)(r != ENTQ_OK ? r : copies.launch(s));
 }
 
 entq_status check_workspace(const void *ws, uint64_t bytes, uint64_t need) {

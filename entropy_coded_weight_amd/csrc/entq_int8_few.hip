@@ -175,7 +175,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few(Int8Args a) {
         load_scales<MODE>(a, n, scale);
         const uint32_t m = g * 16 + lane % 16;
         const float sx = XT == ENTQ_I8 ? a.sx[min(m, a.M - 1)] : own_scale;
-        epilogue4<MODE>(a, sx, scale, norm, m, n, s0, s1, sg, su);
+        const uint2 dy4 = kBack ? load_grad4(a, m, n) : make_uint2(0, 0);
+        epilogue4<MODE>(a, sx, scale, norm, m, n, s0, s1, dy4, sg, su);
         if constexpr (kBack) {
 #pragma unroll
             for (int t = 0; t < NW; ++t) {

@@ -177,25 +177,43 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
         sx = nx;
         sw = nw;
     }
+    // The sums pass through LDS, 32 tokens of this wave at a time, so that
+    // neighbouring lanes then hold neighbouring channels of one token. Those
+    // tokens' scales and incoming gradients are read one such group ahead, and
+    // through LDS too, into a loop short enough for the instruction cache.
+    constexpr uint32_t kRow = FN * 128 + 16;                  // bytes of a token's sums; 16 spread the banks
+    constexpr uint32_t kQuads = FN * 8 / (kTwo ? 2 : 1);      // groups of 4 channels
+    constexpr uint32_t kTokens = 64 / kQuads;                 // that the wave handles at once
+    constexpr uint32_t kTurns = 32 / kTokens;
+    constexpr uint32_t kArea = 32 * kRow + (kBack ? kTurns * 512 : 0) + 128;
+    static_assert(4 * kArea <= kLds, "");
+    const uint32_t quad = lane % kQuads, r = wn * (BN / WN) + (kTwo ? quad / 8 * 64 : 0);
+    const uint32_t n = n0 + (kTwo ? r / 2 + quad % 8 * 4 : r + quad * 4);
+    const uint32_t at = kTwo ? quad / 8 * 256 + quad % 8 * 16 : quad * 16;
+    const uint32_t mw = m0 + wm * (BM / WM);
+    float sx32;
+    uint2 dy4[kBack ? kTurns : 1];
+    auto read_ahead = [&](int g) {
+        if (a.splits > 1) return;
+        sx32 = a.sx[min(mw + g * 32 + lane % 32, a.M - 1)];
+        if (kBack) {
+#pragma unroll
+            for (uint32_t i = 0; i < kTurns; ++i) dy4[i] = load_grad4(a, mw + g * 32 + i * kTokens + lane / kQuads, n);
+        }
+    };
+    read_ahead(0);
+    float scale[2][4], sg[4] = {}, su[4] = {};
+    load_scales<MODE>(a, n, scale);
+    const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
 #pragma unroll
     for (int i = 0; i < FN * FM; ++i)
         acc[i / FM][i % FM] =
             __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[1][i / FM], xf[1][i % FM], acc[i / FM][i % FM], 0, 0, 0);
 
-    // The sums pass through LDS, 32 tokens of this wave at a time, so that
-    // neighbouring lanes then hold neighbouring channels of one token.
-    constexpr uint32_t kRow = FN * 128 + 16;                  // bytes of a token's sums; 16 spread the banks
-    constexpr uint32_t kQuads = FN * 8 / (kTwo ? 2 : 1);      // groups of 4 channels
-    constexpr uint32_t kTokens = 64 / kQuads;                 // that the wave handles at once
-    static_assert(4 * 32 * kRow <= kLds, "");
     __syncthreads();
-    uint8_t *mine = lds + wave * 32 * kRow;
-    const uint32_t quad = lane % kQuads, r = wn * (BN / WN) + (kTwo ? quad / 8 * 64 : 0);
-    const uint32_t n = n0 + (kTwo ? r / 2 + quad % 8 * 4 : r + quad * 4);
-    const uint32_t at = kTwo ? quad / 8 * 256 + quad % 8 * 16 : quad * 16;
-    float scale[2][4], sg[4] = {}, su[4] = {};
-    load_scales<MODE>(a, n, scale);
-    const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
+    uint8_t *mine = lds + wave * kArea;
+    float *const sx_at = (float *)(mine + 32 * kRow);
+    uint2 *const dy_at = (uint2 *)(mine + 32 * kRow + 128);
 #pragma unroll
     for (int g = 0; g < FM; ++g) {
 #pragma unroll
@@ -204,10 +222,18 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
             for (int q = 0; q < 4; ++q)
                 *(v4i *)(mine + lane % 32 * kRow + f * 128 + q * 32 + lane / 32 * 16) =
                     v4i{acc[f][g][4 * q], acc[f][g][4 * q + 1], acc[f][g][4 * q + 2], acc[f][g][4 * q + 3]};
+        if (a.splits == 1) {
+            sx_at[lane % 32] = sx32;
+            if (kBack) {
+#pragma unroll
+                for (uint32_t i = 0; i < kTurns; ++i) dy_at[i * 64 + lane] = dy4[i];
+            }
+        }
+        if (g + 1 < FM) read_ahead(g + 1);
 #pragma unroll 1
-        for (uint32_t t = lane / kQuads; t < 32; t += kTokens) {
+        for (uint32_t i = 0; i < kTurns; ++i) {
+            const uint32_t t = i * kTokens + lane / kQuads, m = mw + g * 32 + t;
             const uint8_t *p = mine + t * kRow + at;
-            const uint32_t m = m0 + wm * (BM / WM) + g * 32 + t;
             const v4i s0 = *(const v4i *)p, s1 = *(const v4i *)(p + (kTwo ? 128 : 0));
             if (a.splits > 1) {
                 if (m < a.M && n < a.N) {
@@ -215,7 +241,8 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
                     if (kTwo) *(v4i *)part_sums<kTwo>(a, blockIdx.y, 1, m, n) = s1;
                 }
             } else {
-                epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, norm, m, n, s0, s1, sg, su);
+                epilogue4<MODE>(a, sx_at[t], scale, norm, m, n, s0, s1,
+                                kBack ? dy_at[i * 64 + lane] : make_uint2(0, 0), sg, su);
             }
         }
     }
@@ -256,7 +283,8 @@ __global__ __launch_bounds__(256) void int8_finish(Int8Args a) {
             if (kTwo) s[1] += *(const v4i *)part_sums<kTwo>(a, k, 1, m, n);
         }
     }
-    epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, norm, m, n, s[0], s[1], sg, su);
+    epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, norm, m, n, s[0], s[1],
+                    kBack ? load_grad4(a, m, n) : make_uint2(0, 0), sg, su);
     if constexpr (kBack) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
