@@ -14,7 +14,7 @@ __device__ __forceinline__ int32_t *part_sums(const Int8Args &a, uint32_t split,
     return a.sums + (((uint64_t)split * (TWO ? 2 : 1) + t) * a.M + m) * wide + n;
 }
 
-// A workgroup of 4 waves (WM x WN) computes BM tokens x BN weight rows; a
+// A workgroup of WM x WN waves computes BM tokens x BN weight rows; a
 // gated tile's rows alternate 32 of gate and 32 of up, so that a lane's
 // fragments hold both sums of a channel. K goes by in steps of 128 codes.
 // Weights are the matrix instruction's first operand: a lane's results are 4
@@ -26,18 +26,18 @@ __device__ __forceinline__ int32_t *part_sums(const Int8Args &a, uint32_t split,
 // per load instruction, and loads that wait for their turn hold up the
 // wave's products.
 template <int MODE, int BM, int BN, int WM, int WN, int SX, int SW>
-__global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uint32_t nb_n) {
+__global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t nb_m, uint32_t nb_n) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
     constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
-    constexpr int kLoadsX = BM / 32, kLoadsW = BN / 32;  // of a wave and step: 8 rows each
+    constexpr int kWaves = WM * WN, kLoadsX = BM / 8 / kWaves, kLoadsW = BN / 8 / kWaves;  // of a wave and step
     constexpr uint32_t kStageX = BM * kRowBytes, kStageW = BN * kRowBytes;
     constexpr uint32_t kLds = SX * kStageX + SW * kStageW;
     constexpr uint32_t kChannels = kTwo ? BN / 2 : BN;
     // loads that may be in flight while the next step is read: those issued
     // after the last one of that step
     constexpr int kFlying = (SX - SW) * kLoadsX + (SW - 2) * (kLoadsX + kLoadsW);
-    static_assert(WM * WN == 4 && (!kTwo || FN % 2 == 0) && (SX == SW || SX == SW + 1), "");
+    static_assert((!kTwo || FN % 2 == 0) && (SX == SW || SX == SW + 1), "");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
 
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -54,23 +54,23 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     const uint32_t all = (a.K + 127) / 128, first = all * blockIdx.y / a.splits;
     const uint32_t steps = all * (blockIdx.y + 1) / a.splits - first, K = a.K - first * 128;
     const int8_t *xbase = a.x + (uint64_t)m0 * a.ldx + first * 128;
-    const int8_t *wbase[2] = {a.w[0] + (uint64_t)n0 * a.ldw[0] + first * 128,
-                              kTwo ? a.w[1] + (uint64_t)n0 * a.ldw[1] + first * 128 : nullptr};
+    const int8_t *wbase0 = a.w[0] + (uint64_t)n0 * a.ldw[0] + first * 128;
+    const int8_t *wbase1 = kTwo ? a.w[1] + (uint64_t)n0 * a.ldw[1] + first * 128 : wbase0;
 #pragma unroll
     for (int i = 0; i < kLoadsX; ++i)
-        xoff[i] = min(8 * (4 * i + wave) + lane / 8, a.M - 1 - m0) * (uint32_t)a.ldx + kc;
+        xoff[i] = min(8 * (kWaves * i + wave) + lane / 8, a.M - 1 - m0) * (uint32_t)a.ldx + kc;
 #pragma unroll
     for (int i = 0; i < kLoadsW; ++i) {
-        const uint32_t r = 8 * (4 * i + wave), c = kTwo ? r / 64 * 32 + r % 32 : r;
-        woff[i] = min(c + lane / 8, a.N - 1 - n0) * (uint32_t)a.ldw[kTwo ? i % 2 : 0] + kc;
+        const uint32_t r = 8 * (kWaves * i + wave), c = kTwo ? r / 64 * 32 + r % 32 : r;
+        woff[i] = min(c + lane / 8, a.N - 1 - n0) * (uint32_t)(kTwo && r / 32 % 2 ? a.ldw[1] : a.ldw[0]) + kc;
     }
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds));
     const uint32_t ldsw = lds0 + SX * kStageX;
     auto load_x = [&](int i, uint32_t step, uint32_t slot) {
-        load_lds16(xbase + step * 128, xoff[i], lds0 + slot * kStageX + wave * 1024 + i * 4096);
+        load_lds16(xbase + step * 128, xoff[i], lds0 + slot * kStageX + (kWaves * i + wave) * 1024);
     };
     auto load_w = [&](int i, uint32_t step, uint32_t slot) {
-        load_lds16(wbase[kTwo ? i % 2 : 0] + step * 128, woff[i], ldsw + slot * kStageW + wave * 1024 + i * 4096);
+        load_lds16((kTwo && (kWaves * i + wave) / 4 % 2 ? wbase1 : wbase0) + step * 128, woff[i], ldsw + slot * kStageW + (kWaves * i + wave) * 1024);
     };
     // A whole step's loads; past the rows' end tokens are zeros and weights
     // whatever is there.
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
             if (in)
                 load_x(i, step, slot);
             else
-                *(v4i *)(lds + slot * kStageX + wave * 1024 + i * 4096 + lane * 16) = v4i{0, 0, 0, 0};
+                *(v4i *)(lds + slot * kStageX + (kWaves * i + wave) * 1024 + lane * 16) = v4i{0, 0, 0, 0};
         }
     };
     auto load_step_w = [&](uint32_t step, uint32_t slot) {
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(256) void int8_tiles(Int8Args a, uint32_t nb_m, uin
     constexpr uint32_t kTokens = 64 / kQuads;                 // that the wave handles at once
     constexpr uint32_t kTurns = 32 / kTokens;
     constexpr uint32_t kArea = 32 * kRow + (kBack ? kTurns * 512 : 0) + 128;
-    static_assert(4 * kArea <= kLds, "");
+    static_assert(kWaves * kArea <= kLds, "");
     const uint32_t quad = lane % kQuads, r = wn * (BN / WN) + (kTwo ? quad / 8 * 64 : 0);
     const uint32_t n = n0 + (kTwo ? r / 2 + quad % 8 * 4 : r + quad * 4);
     const uint32_t at = kTwo ? quad / 8 * 256 + quad % 8 * 16 : quad * 16;
@@ -307,17 +307,23 @@ __global__ __launch_bounds__(256) void int8_finish(Int8Args a) {
     }
 }
 
-template <int BM, int BN, int WM, int WN, int SX, int SW>
+// WNB: waves along the weight rows where the epilogue is long (two waves on a
+// SIMD cover each other's), WN for the plain product. Measured for 256-token
+// tiles, 4 and 8 waves: product 4096 x 8192 x 28672 750 and 785 us (a wave's
+// fragments serve fewer products, more LDS reads), gated 4096 x 28672 x 8192
+// 1605 and 1596, product back 2048 x 8192 x 8192 329 and 322.
+template <int BM, int BN, int WM, int WN, int WNB, int SX, int SW>
 void launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     const bool two = mode == kGated || mode == kGatedBwd;
     const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
     const uint32_t ch = two ? BN / 2 : BN;
     const uint32_t nb_m = (a.M + BM - 1) / BM, nb_n = (cols + ch - 1) / ch;
     const dim3 grid(nb_m * nb_n, a.splits);
-    if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
-    if (mode == kGated) int8_tiles<kGated, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
-    if (mode == kBwd) int8_tiles<kBwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
-    if (mode == kGatedBwd) int8_tiles<kGatedBwd, BM, BN, WM, WN, SX, SW><<<grid, 256, 0, s>>>(a, nb_m, nb_n);
+    constexpr int kOne = 64 * WM * WN, kLong = 64 * WM * WNB;
+    if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN, SX, SW><<<grid, kOne, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kGated) int8_tiles<kGated, BM, BN, WM, WNB, SX, SW><<<grid, kLong, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kBwd) int8_tiles<kBwd, BM, BN, WM, WNB, SX, SW><<<grid, kLong, 0, s>>>(a, nb_m, nb_n);
+    if (mode == kGatedBwd) int8_tiles<kGatedBwd, BM, BN, WM, WNB, SX, SW><<<grid, kLong, 0, s>>>(a, nb_m, nb_n);
 }
 
 void launch_finish(Int8Mode mode, const Int8Args &a, hipStream_t s) {
@@ -367,9 +373,9 @@ Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K
 
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s) {
     if (p.few) return launch_int8_few(mode, a, s);
-    if (p.tile == 256) launch_tiles<256, 256, 2, 2, 3, 2>(mode, a, s);
-    if (p.tile == 128) launch_tiles<128, 128, 2, 2, 3, 2>(mode, a, s);
-    if (p.tile == 64) launch_tiles<64, 128, 2, 2, 3, 3>(mode, a, s);
+    if (p.tile == 256) launch_tiles<256, 256, 2, 2, 4, 3, 2>(mode, a, s);
+    if (p.tile == 128) launch_tiles<128, 128, 2, 2, 2, 3, 2>(mode, a, s);
+    if (p.tile == 64) launch_tiles<64, 128, 2, 2, 2, 3, 3>(mode, a, s);
     if (a.splits > 1) launch_finish(mode, a, s);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
