@@ -28,7 +28,6 @@ struct Int8Args {
     int act;
     void *y;                // forward: the result; backward: the incoming gradient
     int type;               // its entq_eltype
-    bool vec;               // y's rows start at multiples of 4 elements (address and stride)
     uint64_t ldy;
     uint16_t *d[2];         // backward: 16-bit scaled gradients [M][ldd], or null
     uint64_t ldd;           // a multiple of 64; columns N..ldd-1 are written as 0
@@ -121,8 +120,15 @@ __device__ __forceinline__ float act_and_grad(int act, float v, float &grad) {
         return v * p;
     }
     if (act == ENTQ_ACT_GELU) {
-        const float p = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
-        grad = p + v * 0.39894228040143268f * __expf(-0.5f * v * v);
+        // erfc by Abramowitz and Stegun 7.1.26 (absolute error 1.5e-7), whose
+        // exp(-v^2 / 2) the gradient needs anyway
+        const float e = __expf(-0.5f * v * v);
+        const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * 0.70710678118654752f * fabsf(v));
+        const float poly =
+            t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+        const float q = 0.5f * poly * e;
+        const float p = v >= 0.0f ? 1.0f - q : q;
+        grad = p + v * 0.39894228040143268f * e;
         return v * p;
     }
     if (act == ENTQ_ACT_GELU_TANH) {
@@ -157,7 +163,10 @@ __device__ __forceinline__ void load_scales(const Int8Args &a, uint32_t n, float
 __device__ __forceinline__ uint2 load_grad4(const Int8Args &a, uint32_t m, uint32_t n) {
     if (m >= a.M || n >= a.N) return make_uint2(0, 0);
     const uint16_t *y = (const uint16_t *)a.y + (uint64_t)m * a.ldy + n;
-    if (a.vec && n + 4 <= a.N) return *(const uint2 *)y;
+    if (n + 4 <= a.N) {
+        const v2i v = ((const any8 *)y)->v;
+        return make_uint2((uint32_t)v[0], (uint32_t)v[1]);
+    }
     uint32_t b[4] = {0, 0, 0, 0};
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i)
@@ -187,8 +196,8 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
         }
         if (a.type == ENTQ_F32) {
             float *y = (float *)a.y + at;
-            if (whole && a.vec) {
-                *(v4f *)y = v4f{v[0], v[1], v[2], v[3]};
+            if (whole) {
+                ((any16 *)y)->v = __builtin_bit_cast(v4i, v4f{v[0], v[1], v[2], v[3]});
             } else {
                 for (int i = 0; i < 4; ++i)
                     if (n + i < a.N) y[i] = v[i];
@@ -199,8 +208,8 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
             uint16_t b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = bits16(v[i], f16);
-            if (whole && a.vec) {
-                *(uint2 *)y = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+            if (whole) {
+                ((any8 *)y)->v = v2i{(int)(b[0] | (uint32_t)b[1] << 16), (int)(b[2] | (uint32_t)b[3] << 16)};
             } else {
                 for (int i = 0; i < 4; ++i)
                     if (n + i < a.N) y[i] = b[i];
@@ -273,7 +282,6 @@ struct GradArgs {
     bool f16;
     void *dx;               // [M][lddx], bf16 or f16
     uint64_t lddx;
-    bool vec;               // dx's rows start at multiples of 4 elements
     const float *norm;      // F16: result times norm[1]; or null
     SumArgs sums;           // channel sums to finish in the same launch (rows 0: none)
 };

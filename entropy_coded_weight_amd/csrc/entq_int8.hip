@@ -9,16 +9,75 @@ namespace entq {
 namespace {
 
 // ---------------------------------------------------------------------------
+// aligned copies
+// ---------------------------------------------------------------------------
+
+// Up to 3 matrices' rows of K codes at any address into rows of ldc (a
+// multiple of 16), zeros after column K. A thread moves 16 codes.
+struct AlignJob {
+    const int8_t *src;
+    uint64_t ld;
+    int8_t *dst;
+    uint32_t rows, ldc, first;  // first: its first workgroup
+};
+struct AlignArgs {
+    AlignJob job[3];
+    uint32_t K;
+};
+
+__device__ __forceinline__ void align_block(const AlignArgs &a, uint32_t block, uint32_t threads) {
+    const AlignJob &j = a.job[block >= a.job[2].first ? 2 : block >= a.job[1].first ? 1 : 0];
+    const uint64_t i = (uint64_t)(block - j.first) * threads + threadIdx.x;
+    const uint32_t pieces = j.ldc / 16;
+    const uint64_t r = i / pieces;
+    if (r >= j.rows) return;
+    const uint32_t c = (uint32_t)(i - r * pieces) * 16;
+    *(v4i *)(j.dst + r * j.ldc + c) = load16_any(j.src + r * j.ld, c, a.K);
+}
+
+__global__ __launch_bounds__(256) void align_rows(AlignArgs a) { align_block(a, blockIdx.x, 256); }
+
+// Collects copies; they run beside the quantiser where there is one, else in
+// a launch of their own.
+struct Aligner {
+    AlignArgs a{};
+    uint32_t n = 0;
+    void add(const entq_rows &m, int8_t *dst, uint32_t ldc) {
+        a.K = m.cols;
+        a.job[n++] = {(const int8_t *)m.d_data, m.ld, dst, m.rows, ldc, 0};
+    }
+    // Their workgroups of that many threads; 0 where one launch cannot hold them.
+    uint32_t blocks(uint32_t threads) {
+        uint64_t all = 0;
+        for (uint32_t i = 0; i < 3; ++i) {
+            a.job[i].first = i < n ? (uint32_t)all : 0xFFFFFFFFu;
+            if (i < n) all += ((uint64_t)a.job[i].rows * (a.job[i].ldc / 16) + threads - 1) / threads;
+            if (all * threads >= 1ull << 31) return 0;
+        }
+        return (uint32_t)all;
+    }
+    int launch(hipStream_t s) {
+        if (!n) return ENTQ_OK;
+        const uint32_t b = blocks(256);
+        if (!b) return ENTQ_ETOOLARGE;
+        align_rows<<<b, 256, 0, s>>>(a);
+        return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
+    }
+};
+
+// ---------------------------------------------------------------------------
 // quantiser
 // ---------------------------------------------------------------------------
 
 // One workgroup per row, which is read once: VECS pieces of 16 bytes a thread
 // stay in registers between the maximum and the rounding (VECS 0: any length,
 // read twice, the second time out of the L2). Pieces may lie at any address.
-// Columns K..pad-1 are written as 0.
+// Columns K..pad-1 are written as 0. The workgroups after the rows make copies.
 template <int TYPE, int VECS, int THREADS>
 __global__ __launch_bounds__(THREADS) void quantize_rows(const void *x, uint64_t ldx, uint32_t K, int8_t *codes,
-                                                         uint64_t ldc, uint32_t pad, float *scales) {
+                                                         uint64_t ldc, uint32_t pad, float *scales, uint32_t rows,
+                                                         AlignArgs copies) {
+    if (blockIdx.x >= rows) return align_block(copies, blockIdx.x - rows, THREADS);
     constexpr int kPer = TYPE == ENTQ_F32 ? 4 : 8, kBytes = TYPE == ENTQ_F32 ? 4 : 2;
     __shared__ uint32_t top[THREADS / 64];
     const uint64_t row = blockIdx.x;
@@ -77,82 +136,37 @@ __global__ __launch_bounds__(THREADS) void quantize_rows(const void *x, uint64_t
 
 template <int TYPE>
 void quantize_typed(const entq_rows &x, uint32_t rows, uint64_t skip, int8_t *codes, uint64_t ldc, uint32_t pad,
-                    float *scales, hipStream_t s) {
+                    float *scales, Aligner &copies, hipStream_t s) {
     const void *p = (const uint8_t *)x.d_data + skip * x.ld * (TYPE == ENTQ_F32 ? 4 : 2);
     int8_t *c = codes + skip * ldc;
     float *sc = scales + skip;
     const uint32_t pieces = x.cols / (TYPE == ENTQ_F32 ? 4 : 8);
-    const dim3 grid(rows);
+    const uint32_t threads = pieces <= 256 ? 256 : pieces <= 1024 ? 512 : 1024;
+    const uint32_t more = copies.n ? copies.blocks(threads) : 0;
+    const dim3 grid(rows + more);
     if (pieces <= 256)
-        quantize_rows<TYPE, 1, 256><<<grid, 256, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc);
+        quantize_rows<TYPE, 1, 256><<<grid, 256, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc, rows, copies.a);
     else if (pieces <= 1024)
-        quantize_rows<TYPE, 2, 512><<<grid, 512, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc);
+        quantize_rows<TYPE, 2, 512><<<grid, 512, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc, rows, copies.a);
     else if (pieces <= 4096)
-        quantize_rows<TYPE, 4, 1024><<<grid, 1024, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc);
+        quantize_rows<TYPE, 4, 1024><<<grid, 1024, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc, rows, copies.a);
     else
-        quantize_rows<TYPE, 0, 1024><<<grid, 1024, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc);
+        quantize_rows<TYPE, 0, 1024><<<grid, 1024, 0, s>>>(p, x.ld, x.cols, c, ldc, pad, sc, rows, copies.a);
+    if (more) copies.n = 0;  // done
 }
 
 int launch_quantize(const entq_rows &x, int8_t *codes, uint64_t ldc, uint32_t pad, float *scales,
-                    hipStream_t s) {
+                    Aligner &copies, hipStream_t s) {
     if (x.rows == 0) return ENTQ_OK;
     constexpr uint32_t kRows = 1u << 20;  // a launch's threads stay below 2^32
     for (uint64_t r = 0; r < x.rows; r += kRows) {
         const uint32_t n = (uint32_t)std::min<uint64_t>(kRows, x.rows - r);
-        if (x.type == ENTQ_BF16) quantize_typed<ENTQ_BF16>(x, n, r, codes, ldc, pad, scales, s);
-        if (x.type == ENTQ_F16) quantize_typed<ENTQ_F16>(x, n, r, codes, ldc, pad, scales, s);
-        if (x.type == ENTQ_F32) quantize_typed<ENTQ_F32>(x, n, r, codes, ldc, pad, scales, s);
+        if (x.type == ENTQ_BF16) quantize_typed<ENTQ_BF16>(x, n, r, codes, ldc, pad, scales, copies, s);
+        if (x.type == ENTQ_F16) quantize_typed<ENTQ_F16>(x, n, r, codes, ldc, pad, scales, copies, s);
+        if (x.type == ENTQ_F32) quantize_typed<ENTQ_F32>(x, n, r, codes, ldc, pad, scales, copies, s);
     }
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
-
-// ---------------------------------------------------------------------------
-// aligned copies
-// ---------------------------------------------------------------------------
-
-// Up to 3 matrices' rows of K codes at any address into rows of ldc (a
-// multiple of 16), zeros after column K. A thread moves 16 codes.
-struct AlignJob {
-    const int8_t *src;
-    uint64_t ld;
-    int8_t *dst;
-    uint32_t rows, ldc, first;  // first: its first workgroup
-};
-struct AlignArgs {
-    AlignJob job[3];
-    uint32_t K;
-};
-
-__global__ __launch_bounds__(256) void align_rows(AlignArgs a) {
-    const AlignJob &j = a.job[blockIdx.x >= a.job[2].first ? 2 : blockIdx.x >= a.job[1].first ? 1 : 0];
-    const uint64_t i = (uint64_t)(blockIdx.x - j.first) * 256 + threadIdx.x;
-    const uint32_t pieces = j.ldc / 16;
-    const uint64_t r = i / pieces;
-    if (r >= j.rows) return;
-    const uint32_t c = (uint32_t)(i - r * pieces) * 16;
-    *(v4i *)(j.dst + r * j.ldc + c) = load16_any(j.src + r * j.ld, c, a.K);
-}
-
-// Collects copies and launches them together.
-struct Aligner {
-    AlignArgs a{};
-    uint32_t n = 0, blocks = 0;
-    bool too_many = false;  // workgroups for one launch
-    void add(const entq_rows &m, int8_t *dst, uint32_t ldc) {
-        a.K = m.cols;
-        a.job[n++] = {(const int8_t *)m.d_data, m.ld, dst, m.rows, ldc, blocks};
-        const uint64_t more = ((uint64_t)m.rows * (ldc / 16) + 255) / 256;
-        if (blocks + more >= 1u << 23) too_many = true;
-        blocks += (uint32_t)more;
-    }
-    int launch(hipStream_t s) {
-        if (!n) return ENTQ_OK;
-        if (too_many) return ENTQ_ETOOLARGE;
-        for (uint32_t i = n; i < 3; ++i) a.job[i].first = 0xFFFFFFFFu;
-        align_rows<<<blocks, 256, 0, s>>>(a);
-        return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
-    }
-};
 
 // Whether the products can read the codes where they are.
 bool direct(const entq_rows &m) {
@@ -242,10 +256,6 @@ entq_status check_out(const void *p, int type, uint64_t ld, uint32_t rows, uint3
     if (rows && cols && !p) return ENTQ_EINVAL;
     if ((uintptr_t)p % type_bytes(type)) return ENTQ_EALIGN;
     return ENTQ_OK;
-}
-
-bool vec4(const void *p, uint64_t ld, int type) {
-    return (uintptr_t)p % (4 * type_bytes(type)) == 0 && ld % 4 == 0;
 }
 
 // Takes pieces of the workspace in order; with base null it only counts.
@@ -367,17 +377,12 @@ entq_status operands(const Call &c, const Layout &l, Int8Args &a, hipStream_t s)
     a.x = (const int8_t *)c.x->d_data;
     a.sx = c.x->d_scales;
     a.ldx = c.x->ld;
-    int r = ENTQ_OK;
     a.x_type = l.plan.quantizes ? c.x->type : (int)ENTQ_I8;
-    if (c.x->type != ENTQ_I8 && !l.plan.quantizes) {
-        r = launch_quantize(*c.x, l.codes, l.ldc, (uint32_t)l.ldc, l.scales, s);
-        a.sx = l.scales;
-    }
     Aligner copies;
-    if (c.x->type == ENTQ_I8 && l.codes) copies.add(*c.x, l.codes, (uint32_t)l.ldc);
     if (l.codes) {
         a.x = l.codes;
         a.ldx = l.ldc;
+        if (c.x->type == ENTQ_I8) copies.add(*c.x, l.codes, (uint32_t)l.ldc);
     }
     for (int i = 0; i < c.n_w; ++i) {
         a.w[i] = (const int8_t *)c.w[i]->d_data;
@@ -388,6 +393,11 @@ entq_status operands(const Call &c, const Layout &l, Int8Args &a, hipStream_t s)
             a.w[i] = l.w[i];
             a.ldw[i] = l.ldw;
         }
+    }
+    int r = ENTQ_OK;
+    if (c.x->type != ENTQ_I8 && !l.plan.quantizes) {
+        r = launch_quantize(*c.x, l.codes, l.ldc, (uint32_t)l.ldc, l.scales, copies, s);
+        a.sx = l.scales;
     }
     return (entq_status)(r != ENTQ_OK ? r : copies.launch(s));
 }
@@ -413,7 +423,6 @@ entq_status forward(const Call &c, int act, void *y, int type, uint64_t ldy, voi
     a.y = y;
     a.type = type;
     a.ldy = ldy;
-    a.vec = vec4(y, ldy, type);
     return (entq_status)launch_int8_product(c.mode, l.plan, a, s);
 }
 
@@ -446,7 +455,6 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     a.y = const_cast<void *>(c.dy->d_data);
     a.type = c.dy->type;
     a.ldy = c.dy->ld;
-    a.vec = vec4(a.y, a.ldy, a.type);
     a.ldd = l.ldd;
     // (one block of tokens: its sums are the results)
     const bool direct_sums = l.plan.part_rows == 1;
@@ -487,7 +495,6 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     g.f16 = f16;
     g.dx = dx;
     g.lddx = lddx;
-    g.vec = vec4(dx, lddx, c.dy->type);
     g.norm = a.norm;
     g.sums = sums;
     return (entq_status)launch_grad_product(l.grad, g, s);
@@ -509,7 +516,8 @@ entq_status entq_quantize_rows(const entq_rows *x, int8_t *d_codes, uint64_t ldc
     if (ldc < x->cols || ldc > (1ull << 40)) return ENTQ_EINVAL;
     if (x->rows && ((x->cols && !d_codes) || !d_scales)) return ENTQ_EINVAL;
     if ((uintptr_t)d_scales % 4) return ENTQ_EALIGN;
-    return (entq_status)entq::launch_quantize(*x, d_codes, ldc, x->cols, d_scales, (hipStream_t)stream);
+    entq::Aligner none;
+    return (entq_status)entq::launch_quantize(*x, d_codes, ldc, x->cols, d_scales, none, (hipStream_t)stream);
 }
 
 uint64_t entq_int8_gemm_workspace_bytes(const entq_rows *x, const entq_rows *w) {

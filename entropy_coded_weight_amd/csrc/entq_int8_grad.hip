@@ -209,8 +209,8 @@ __global__ __launch_bounds__(256) void grad_tiles(GradArgs a, uint32_t nb_m, uin
 #pragma unroll
                 for (int i = 0; i < 4; ++i) b[i] = bits16(v[i] * back, F16);
                 uint16_t *to = (uint16_t *)a.dx + (uint64_t)m * a.lddx + k;
-                if (a.vec && k + 4 <= a.cols) {
-                    *(uint2 *)to = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+                if (k + 4 <= a.cols) {
+                    ((any8 *)to)->v = v2i{(int)(b[0] | (uint32_t)b[1] << 16), (int)(b[2] | (uint32_t)b[3] << 16)};
                 } else {
 #pragma unroll
                     for (uint32_t i = 0; i < 4; ++i)
@@ -261,7 +261,7 @@ GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, int n_w) {
 }
 
 int launch_grad_product(const GradPlan &p, const GradArgs &a, hipStream_t s) {
-    if (p.tile == 256) launch_tiles<256, 256, 2, 2, 3>(a, s);
+    if (p.tile == 256) launch_tiles<256, 256, 1, 4, 3>(a, s);
     if (p.tile == 128) launch_tiles<128, 128, 2, 2, 3>(a, s);
     if (p.tile == 64) launch_tiles<64, 128, 2, 2, 3>(a, s);
     if (p.splits > 1) grad_sum<<<dim3((a.K / 4 + 255) / 256, std::min(a.M, 65535u)), 256, 0, s>>>(a);
