@@ -110,42 +110,49 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return v;
 }
 
-// act(v) and, for the backward pass, act'(v). exp is the hardware's 2^x after
+// act(v) of 4 values and, with GRAD, act'(v). exp is the hardware's 2^x after
 // a product with log2 e (relative error about 1e-7 times the exponent, which
-// is small where the result is not), 1 / x the hardware's (1 ulp).
-__device__ __forceinline__ float act_and_grad(int act, float v, float &grad) {
+// is small where the result is not), 1 / x the hardware's (1 ulp). The choice
+// of activation is made once for the 4 values, whose chains then overlap.
+template <bool GRAD>
+__device__ __forceinline__ void activate4(int act, const float (&x)[4], float (&r)[4], float (&grad)[4]) {
     if (act == ENTQ_ACT_SILU) {
-        const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-v));
-        grad = p * (1.0f + v * (1.0f - p));
-        return v * p;
-    }
-    if (act == ENTQ_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v = x[i], p = __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+            r[i] = v * p;
+            if (GRAD) grad[i] = p * (1.0f + v * (1.0f - p));
+        }
+    } else if (act == ENTQ_ACT_GELU) {
         // erfc by Abramowitz and Stegun 7.1.26 (absolute error 1.5e-7), whose
         // exp(-v^2 / 2) the gradient needs anyway
-        const float e = __expf(-0.5f * v * v);
-        const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * 0.70710678118654752f * fabsf(v));
-        const float poly =
-            t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-        const float q = 0.5f * poly * e;
-        const float p = v >= 0.0f ? 1.0f - q : q;
-        grad = p + v * 0.39894228040143268f * e;
-        return v * p;
-    }
-    if (act == ENTQ_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v = x[i], e = __expf(-0.5f * v * v);
+            const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * 0.70710678118654752f * fabsf(v));
+            const float poly =
+                t * (0.254829592f +
+                     t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+            const float q = 0.5f * poly * e, p = v >= 0.0f ? 1.0f - q : q;
+            r[i] = v * p;
+            if (GRAD) grad[i] = p + v * 0.39894228040143268f * e;
+        }
+    } else if (act == ENTQ_ACT_GELU_TANH) {
         // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
-        const float z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
-        const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z2));
-        grad = p + v * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * v * v);
-        return v * p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float v = x[i], z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
+            const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z2));
+            r[i] = v * p;
+            if (GRAD) grad[i] = p + v * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * v * v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // a NaN stays one
+            r[i] = x[i] > 0.0f ? x[i] : x[i] != x[i] ? x[i] : 0.0f;
+            if (GRAD) grad[i] = x[i] > 0.0f ? 1.0f : 0.0f;
+        }
     }
-    // a NaN stays one
-    grad = v > 0.0f ? 1.0f : 0.0f;
-    return v > 0.0f ? v : v != v ? v : 0.0f;
-}
-
-__device__ __forceinline__ float act_only(int act, float v) {
-    float grad;
-    return act_and_grad(act, v, grad);
 }
 
 // The scales of channels n..n+3, 0 beyond N.
@@ -190,9 +197,12 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
         const uint64_t at = (uint64_t)m * a.ldy + n;
         float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = ((float)ag[i] * sx) * scale[0][i];
-            if (kTwo) v[i] = act_only(a.act, v[i]) * (((float)au[i] * sx) * scale[1][i]);
+        for (int i = 0; i < 4; ++i) v[i] = ((float)ag[i] * sx) * scale[0][i];
+        if (kTwo) {
+            float r[4], none[4];
+            activate4<false>(a.act, v, r, none);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = r[i] * (((float)au[i] * sx) * scale[1][i]);
         }
         if (a.type == ENTQ_F32) {
             float *y = (float *)a.y + at;
@@ -218,24 +228,24 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
     } else {
         const bool f16 = a.type == ENTQ_F16;
         uint16_t d[2][4];
+        float g0[4], u0[4], g[4], act[4], grad[4];  // g0, u0: before the channel's scale
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            g0[i] = (float)ag[i] * sx;
+            u0[i] = (float)au[i] * sx;
+            g[i] = g0[i] * scale[0][i];
+        }
+        if (kTwo) activate4<true>(a.act, g, act, grad);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float dy = from16((uint16_t)((i < 2 ? dy4.x : dy4.y) >> (16 * (i % 2))), f16);
-            const float g0 = (float)ag[i] * sx;  // before the channel's scale
             const bool in = n + i < a.N;
-            if (!kTwo) {
-                if (in) sg[i] += dy * g0;
-                d[0][i] = in ? bits16(dy * (scale[0][i] * norm), f16) : 0;
-            } else {
-                const float u0 = (float)au[i] * sx;
-                float grad;
-                const float act = act_and_grad(a.act, g0 * scale[0][i], grad);
-                const float dg = dy * (u0 * scale[1][i]) * grad, du = dy * act;
-                if (in) {
-                    sg[i] += dg * g0;
-                    su[i] += du * u0;
-                }
-                d[0][i] = in ? bits16(dg * (scale[0][i] * norm), f16) : 0;
+            const float dg = kTwo ? dy * (u0[i] * scale[1][i]) * grad[i] : dy;
+            if (in) sg[i] += dg * g0[i];
+            d[0][i] = in ? bits16(dg * (scale[0][i] * norm), f16) : 0;
+            if (kTwo) {
+                const float du = dy * act[i];
+                if (in) su[i] += du * u0[i];
                 d[1][i] = in ? bits16(du * (scale[1][i] * norm), f16) : 0;
             }
         }
