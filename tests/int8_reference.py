@@ -1,19 +1,23 @@
-"""The int8 products and their gradients written out in 64 bits (numpy), from
-their formulas, with bounds on what fp32 and 16-bit arithmetic may add."""
+"""The int8 products and their gradients written out in 64 bits (torch, on
+whatever device the arguments are), from their formulas, with bounds on what
+fp32 and 16-bit arithmetic may add. Arguments are numpy arrays or tensors."""
 import math
 
 import numpy as np
+import torch
 
 EPS = 2.0 ** -24                       # unit roundoff of fp32
 ROUND = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
 TINY = {"bf16": 2.0 ** -133, "f16": 2.0 ** -25, "f32": 2.0 ** -149}  # half the smallest step
 
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+
+def f64(a):
+    return torch.as_tensor(a).double()
 
 
 def quantize(x):
     """Codes and scales of the rows of x (any float array), by the stated fp32
-    arithmetic."""
+    arithmetic, in numpy."""
     x = np.asarray(x, np.float32)
     with np.errstate(all="ignore"):
         top = np.max(np.abs(x), axis=1, initial=0.0)
@@ -28,32 +32,32 @@ def quantize(x):
 
 def act(name, v):
     """act(v), act'(v)"""
-    with np.errstate(over="ignore"):
-        if name == "silu":
-            p = 1 / (1 + np.exp(-v))
-            return v * p, p * (1 + v * (1 - p))
-        if name == "gelu":
-            p = 0.5 * (1 + _erf(v / math.sqrt(2)))
-            return v * p, p + v * np.exp(-v * v / 2) / math.sqrt(2 * math.pi)
-        if name == "gelu_tanh":
-            c = math.sqrt(2 / math.pi)
-            t = np.tanh(c * (v + 0.044715 * v ** 3))
-            return 0.5 * v * (1 + t), 0.5 * (1 + t) + 0.5 * v * (1 - t * t) * c * (1 + 3 * 0.044715 * v * v)
-    return np.where(v > 0, v, 0.0), (v > 0) * 1.0
+    v = f64(v)
+    if name == "silu":
+        p = 1 / (1 + torch.exp(-v))
+        return v * p, p * (1 + v * (1 - p))
+    if name == "gelu":
+        p = 0.5 * torch.erfc(-v / math.sqrt(2))
+        return v * p, p + v * torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    if name == "gelu_tanh":
+        c = math.sqrt(2 / math.pi)
+        t = torch.tanh(c * (v + 0.044715 * v ** 3))
+        return 0.5 * v * (1 + t), 0.5 * (1 + t) + 0.5 * v * (1 - t * t) * c * (1 + 3 * 0.044715 * v * v)
+    return torch.where(v > 0, v, 0 * v), (v > 0) * 1.0
 
 
 def sums(q, w):
-    return q.astype(np.int64) @ w.astype(np.int64).T
+    return f64(q) @ f64(w).T  # exact: every sum is an integer below 2^31
 
 
 def gated(q, sx, wg, sg, wu, su, name):
     """H and the fp32 error it may carry: g and u have three roundings each,
     exp an error of its argument's rounding, the rest a few more; 16 EPS
     |g| |u| (1 + |g|) covers them for every activation."""
-    sx, sg, su = (np.asarray(v, np.float64) for v in (sx, sg, su))
+    sx, sg, su = f64(sx), f64(sg), f64(su)
     g = sums(q, wg) * sx[:, None] * sg
     u = sums(q, wu) * sx[:, None] * su
-    return act(name, g)[0] * u, 16 * EPS * np.abs(g) * np.abs(u) * (1 + np.abs(g))
+    return act(name, g)[0] * u, 16 * EPS * g.abs() * u.abs() * (1 + g.abs())
 
 
 def _dx(d, derr, scales, weights, kind):
@@ -61,42 +65,40 @@ def _dx(d, derr, scales, weights, kind):
     (F16: also to steps of 2^-24 max|s|, below its smallest normal value), fp32
     sums in any order."""
     n = weights[0].shape[0]
-    top = max((np.max(np.abs(s), initial=0.0) for s in scales))
+    top = max(float(s.abs().max()) for s in scales) if n else 0.0
     dx, bound = 0.0, 0.0
     for v, e, s, w in zip(d, derr, scales, weights):
-        w = w.astype(np.float64)
+        w = f64(w)
         dx = dx + (v * s) @ w
-        size = np.abs(v * s)
-        per = size * (ROUND[kind] + (2 * n + 20) * EPS) + e * np.abs(s)
+        per = (v * s).abs() * (ROUND[kind] + (2 * n + 20) * EPS) + e * s.abs()
         if kind == "f16":
             per = per + TINY["f16"] * top
-        bound = bound + per @ np.abs(w)
-    return dx, bound + ROUND[kind] * np.abs(dx) + TINY[kind]
+        bound = bound + per @ w.abs()
+    return dx, bound + ROUND[kind] * dx.abs() + TINY[kind]
 
 
 def gemm_backward(dy, q, sx, w, sw, kind):
     """((dX, bound), (dsw, bound)); dy float64."""
-    sx, sw = np.asarray(sx, np.float64), np.asarray(sw, np.float64)
-    raw = sums(q, w) * sx[:, None]
-    t = dy * raw
+    dy, sx, sw = f64(dy), f64(sx), f64(sw)
+    t = dy * (sums(q, w) * sx[:, None])
     m = len(sx)
     return (_dx([dy], [0 * dy], [sw], [w], kind),
-            (t.sum(0), (m + 8) * EPS * np.abs(t).sum(0)))
+            (t.sum(0), (m + 8) * EPS * t.abs().sum(0)))
 
 
 def gated_backward(dh, q, sx, wg, sg, wu, su, name, kind):
     """((dX, bound), (dsg, bound), (dsu, bound)). act' carries at most
     32 EPS (1 + |g|)^2, act 16 EPS |g| (1 + |g|)."""
-    sx, sg, su = (np.asarray(v, np.float64) for v in (sx, sg, su))
+    dh, sx, sg, su = f64(dh), f64(sx), f64(sg), f64(su)
     g0, u0 = sums(q, wg) * sx[:, None], sums(q, wu) * sx[:, None]
     g, u = g0 * sg, u0 * su
     a, da = act(name, g)
     dg, du = dh * u * da, dh * a
-    eg = np.abs(dh * u) * 32 * EPS * (1 + np.abs(g)) ** 2
-    eu = np.abs(dh) * 16 * EPS * np.abs(g) * (1 + np.abs(g))
+    eg = (dh * u).abs() * 32 * EPS * (1 + g.abs()) ** 2
+    eu = dh.abs() * 16 * EPS * g.abs() * (1 + g.abs())
     m = len(sx)
     ends = [_dx([dg, du], [eg, eu], [sg, su], [wg, wu], kind)]
     for d, e, raw in ((dg, eg, g0), (du, eu, u0)):
         t = d * raw
-        ends.append((t.sum(0), (m + 8) * EPS * np.abs(t).sum(0) + (e * np.abs(raw)).sum(0)))
+        ends.append((t.sum(0), (m + 8) * EPS * t.abs().sum(0) + (e * raw.abs()).sum(0)))
     return ends

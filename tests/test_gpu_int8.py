@@ -106,7 +106,7 @@ def test_quantize_special_rows(I):
 
 def _product(q, sx, w, sw):
     """fp32 results of the product, every rounding as stated."""
-    acc = R.sums(q, w).astype(np.float32)
+    acc = R.sums(q, w).numpy().astype(np.float32)
     return (acc * sx[:, None]).astype(np.float32) * sw
 
 
@@ -204,10 +204,10 @@ def test_empty_sizes(I):
 
 
 def _near(got, want, bound, what):
-    got = host(got)
-    off = np.abs(got - want)
-    worst = np.unravel_index(np.argmax(off - bound), off.shape)
-    assert (off <= bound).all(), (what, worst, got[worst], want[worst], bound[worst])
+    got = got.detach().to(want.device).double()
+    off = (got - want).abs() - bound
+    worst = int(off.argmax())
+    assert float(off.max()) <= 0, (what, worst, *(float(t.flatten()[worst]) for t in (got, want, bound)))
 
 
 ACTS = ["silu", "gelu", "gelu_tanh", "relu"]
@@ -224,7 +224,7 @@ def test_gated(I, m, n, k):
         h = torch.full((m + 1, n), 9.0, dtype=TYPES[out], device="cuda")
         I.gated(dev(q), dev(sx * size), dev(wg), dev(sg * 20), dev(wu), dev(su), h[:m], name)
         want, err = R.gated(q, sx * size, wg, sg * 20, wu, su, name)
-        _near(h[:m], want, err + R.ROUND[out] * np.abs(want) + R.TINY[out], name)
+        _near(h[:m], want, err + R.ROUND[out] * want.abs() + R.TINY[out], name)
         assert (h[m] == 9.0).all()
 
 
@@ -238,7 +238,7 @@ def test_gated_far_activations(I):
         I.gated(dev(q), dev(one5), dev(w), dev(s), dev(w), dev(np.ones(4, np.float32)), h, name)
         want, err = R.gated(q, one5, w, s, w, np.ones(4), name)
         assert np.isfinite(host(h)).all()
-        _near(h, want, err + R.EPS * np.abs(want) + 1e-37, name)
+        _near(h, want, err + R.EPS * want.abs() + 1e-37, name)
 
 
 @pytest.mark.parametrize("m,n,k", [(3, 40, 64), (70, 130, 200), (20, 64, 128)])
@@ -349,9 +349,61 @@ def test_f16_gradients_do_not_leave_their_range(I, top):
     dx = torch.empty(m, k, dtype=torch.float16, device="cuda")
     I.gemm_backward(dy.cuda(), dev(q), dev(sx), dev(w), dev(sw), dx)
     wx, bx = R.gemm_backward(host(dy), q, sx, w, sw, "f16")[0]
-    fits = np.abs(wx) < 60000
-    got = host(dx)
-    assert (np.abs(got - wx)[fits] <= bx[fits]).all()
+    fits = wx.abs() < 60000
+    got = dx.cpu().double()
+    assert bool(((got - wx).abs()[fits] <= bx[fits]).all())
+
+
+# products that take every tile size, whole and with the sum split, each with
+# sides that end inside a tile; 64-bit references on the GPU
+LARGE = [(1100, 8200, 272), (520, 2001, 4096), (700, 16390, 1040), (256, 8192, 28672), (1000, 5000, 4000),
+         (512, 8190, 28672), (25, 2000, 2048), (40, 3000, 640), (3001, 300, 2064)]
+
+
+def _large(m, n, k, seed, weights):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    code = lambda *s: torch.randint(-128, 128, s, generator=g, device="cuda", dtype=torch.int8)  # noqa: E731
+    scale = lambda r: (torch.rand(r, generator=g, device="cuda") + 0.5) * 0.01  # noqa: E731
+    q = code(m, k)
+    sx = scale(m) * (4.0 / (k ** 0.5 * 74 * 74 * 0.01 * 0.01))  # |g| up to 10 or so
+    return (q, sx) + tuple(t for _ in range(weights) for t in (code(n, k), scale(n)))
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_large_forward(I, m, n, k):
+    _say("large forward", m, n, k)
+    q, sx, wg, sg, wu, su = _large(m, n, k, m + n, 2)
+    y = torch.full((m + 1, n + 3), 7.0, device="cuda")
+    I.gemm(q, sx, wg, sg, y[:m, :n])
+    acc = R.sums(q, wg).float()
+    assert torch.equal(y[:m, :n], acc * sx[:, None] * sg)
+    assert (y[m] == 7).all() and (y[:, n:] == 7).all()
+    for out in ("f32", "bf16"):
+        h = torch.full((m + 1, n + 3), 7.0, device="cuda").to(TYPES[out])
+        I.gated(q, sx, wg, sg, wu, su, h[:m, :n], "gelu")
+        want, err = R.gated(q, sx, wg, sg, wu, su, "gelu")
+        _near(h[:m, :n], want, err + R.ROUND[out] * want.abs() + R.TINY[out], out)
+        assert (h[m] == 7).all() and (h[:, n:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(1100, 8200, 272), (520, 2001, 4096), (1000, 5000, 4000), (2050, 3001, 4103),
+                                   (256, 8192, 8192), (40, 3000, 640)])
+def test_large_backward(I, m, n, k, kind):
+    _say("large backward", m, n, k, kind)
+    q, sx, wg, sg, wu, su = _large(m, n, k, m + n, 2)
+    dh = (torch.randn(m, n, device="cuda") * 0.1).to(TYPES[kind])
+    new = lambda *s: torch.full(s, 7.0, device="cuda")  # noqa: E731
+    dx, ds = new(m + 1, k + 3).to(TYPES[kind]), new(n)
+    I.gemm_backward(dh, q, sx, wg, sg, dx[:m, :k], ds)
+    for got, (want, bound), what in zip((dx[:m, :k], ds), R.gemm_backward(dh, q, sx, wg, sg, kind), ("dx", "ds")):
+        _near(got, want, bound, what)
+    dx, dsg, dsu = new(m + 1, k + 3).to(TYPES[kind]), new(n), new(n)
+    I.gated_backward(dh, q, sx, wg, sg, wu, su, dx[:m, :k], dsg, dsu, "silu")
+    for got, (want, bound), what in zip((dx[:m, :k], dsg, dsu),
+                                        R.gated_backward(dh, q, sx, wg, sg, wu, su, "silu", kind), ("dx", "dsg", "dsu")):
+        _near(got, want, bound, what)
+    assert (dx[m] == 7).all() and (dx[:, k:] == 7).all()
 
 
 def test_other_stream_given_workspace_and_repeats(I):

@@ -40,12 +40,12 @@ def test_gradient_formulas_against_differences(name):
 
     def loss(x, sg, su):  # x: the activations the codes stand for
         g, u = x @ wg.T.astype(float) * sg, x @ wu.T.astype(float) * su
-        return (dh * R.act(name, g)[0] * u).sum()
+        return (dh * R.act(name, g)[0].numpy() * u).sum()
 
     x = q * sx[:, None]
     (dx, _), (dsg, _), (dsu, _) = R.gated_backward(dh, q, sx, wg, sg, wu, su, name, "bf16")
     e = 1e-5  # central differences: error of order e^2 and 1e-16 / e
-    for want, at in ((dx, 0), (dsg, 1), (dsu, 2)):
+    for want, at in ((dx.numpy(), 0), (dsg.numpy(), 1), (dsu.numpy(), 2)):
         args = [x, sg, su]
         for i in np.ndindex(want.shape):
             up, down = [a.copy() for a in args], [a.copy() for a in args]
@@ -61,6 +61,7 @@ def test_plain_product_gradient_against_differences():
     q, w = rng.integers(-9, 10, (m, k)).astype(np.int8), rng.integers(-9, 10, (n, k)).astype(np.int8)
     sx, sw, dy = rng.uniform(0.1, 1, m), rng.uniform(-1, 1, n), rng.standard_normal((m, n))
     (dx, _), (ds, _) = R.gemm_backward(dy, q, sx, w, sw, "f16")
+    dx, ds = dx.numpy(), ds.numpy()
     loss = lambda x, s: (dy * (x @ w.T.astype(float) * s)).sum()  # noqa: E731
     x = q * sx[:, None]
     for i in np.ndindex(dx.shape):
