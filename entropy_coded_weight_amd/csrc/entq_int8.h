@@ -301,11 +301,12 @@ struct GradArgs {
 // with two workgroups on a CU (256-token tiles fill one), `tile` for a tile's
 // end, the weights' bytes at `bytes_us`, and for a split sum a second launch
 // that adds partial results. The constants are fitted to times measured on
-// MI355X over 180 shapes (1 .. 2,048 tokens, sides 512 .. 32,000) with every
-// tile and 1 .. 24 splits; the choice is then on average 1 % (products) and
-// 0.2 % (gradients) slower than the best variant of each shape.
+// MI355X over 214 shapes (1 .. 2,048 tokens, sides 512 .. 32,000) with every
+// tile and 1 .. 24 splits, as graphs of launches; `second` has 2 us more for
+// what a second launch costs outside a graph. The choice is on average about
+// 1 % slower than the best variant of each shape.
 struct TileCost {
-    uint32_t tokens;        // of a tile
+    uint32_t tokens, width; // of a tile; width: weight rows, or columns of dX
     float step[2], tile;
 };
 struct SplitCost {
@@ -323,22 +324,24 @@ inline float tile_cost(const TileCost &t, const SplitCost &c, uint32_t tiles, ui
     if (splits > 1) us += c.second + splits * (c.per_split + c.per_value * results);
     return us;
 }
-// The cheapest tile and split. tiles(tokens): how many tiles of that size.
+// The cheapest kind of tile and split for M tokens and a width.
 struct TileChoice {
-    uint32_t tokens, splits;
+    int kind;
+    uint32_t splits;
     float us;
 };
-template <class Tiles>
-TileChoice cheapest_tile(const TileCost (&kinds)[3], const SplitCost &c, Tiles tiles, uint32_t steps,
-                         uint64_t weight_bytes, uint64_t results) {
-    TileChoice best{0, 1, 0.0f};
-    for (const TileCost &t : kinds) {
-        const uint64_t n = tiles(t.tokens);
+template <int KINDS>
+TileChoice cheapest_tile(const TileCost (&kinds)[KINDS], const SplitCost &c, uint32_t M, uint64_t width,
+                         uint32_t steps, uint64_t weight_bytes, uint64_t results) {
+    TileChoice best{-1, 1, 0.0f};
+    for (int kind = 0; kind < KINDS; ++kind) {
+        const TileCost &t = kinds[kind];
+        const uint64_t n = (uint64_t)((M + t.tokens - 1) / t.tokens) * ((width + t.width - 1) / t.width);
         for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u, 24u}) {
             if (s > 1 && (s > steps || n * s > 1100)) break;
             const float us = tile_cost(t, c, (uint32_t)(n > 0x7FFFFFFF ? 0x7FFFFFFF : n), steps, s, weight_bytes,
                                        results);
-            if (!best.tokens || us < best.us) best = {t.tokens, s, us};
+            if (best.kind < 0 || us < best.us) best = {kind, s, us};
         }
     }
     return best;
@@ -349,7 +352,7 @@ struct Int8Plan {
     bool few;               // the few-token kernel; else tiles:
     bool quantizes;         // the few-token kernel quantises the activations itself
     uint32_t splits;        // of K; above 1 the sums pass through memory
-    int tile;               // tokens of a tile
+    int kind;               // of tile
     uint32_t part_rows;     // rows of Int8Args::part
 };
 Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K);
@@ -361,7 +364,7 @@ int launch_int8_few(Int8Mode mode, const Int8Args &a, hipStream_t s);
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s);
 
 struct GradPlan {
-    int tile;
+    int kind;               // of tile
     uint32_t splits;
 };
 GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, int n_w);

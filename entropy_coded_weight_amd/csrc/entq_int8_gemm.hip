@@ -337,29 +337,31 @@ void launch_finish(Int8Mode mode, const Int8Args &a, hipStream_t s) {
 
 }  // namespace
 
+// tokens x weight rows of the kinds of tiles. (64 x 64 tiles were measured
+// too: 0.2 % better on average, not kept.)
+static const TileCost kTiles[3] = {{64, 128, {0.427f, 0.81f}, 1.3f},
+                                   {128, 128, {0.80f, 1.24f}, 1.5f},
+                                   {256, 256, {1.58f, 1.63f}, 4.9f}};
+static const SplitCost kSplits = {3.0f, 7.2e6f, 5.0f, 0.1f, 1.25e-6f};
+
 Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K) {
-    static const TileCost kinds[3] = {{64, {0.353f, 0.885f}, 1.6f}, {128, {0.878f, 1.04f}, 1.7f},
-                                      {256, {1.61f, 1.63f}, 4.9f}};
-    static const SplitCost cost = {3.3f, 8.7e6f, 2.5f, 0.13f, 1.38e-6f};
     const uint64_t n_w = mode == kGated || mode == kGatedBwd ? 2 : 1;
-    const TileChoice t = cheapest_tile(
-        kinds, cost,
-        [&](uint32_t tokens) {
-            const uint64_t rows = tokens == 256 ? 256 : 128;
-            return (uint64_t)((M + tokens - 1) / tokens) * ((N * n_w + rows - 1) / rows);
-        },
-        (K + 127) / 128, n_w * N * K, n_w * M * (uint64_t)N);
+    const TileChoice t =
+        cheapest_tile(kTiles, kSplits, M, n_w * N, (K + 127) / 128, n_w * N * K, n_w * M * (uint64_t)N);
     Int8Plan p{};
-    p.tile = (int)t.tokens;
+    p.kind = t.kind;
     p.splits = t.splits;
     if (M <= 64) {
         // The few-token kernel: limited by a wave's turns over K, all the more
         // the more groups of tokens it has, or by the weights' bytes. (At 1 and
-        // 4 tokens it was the fastest, or within 1 %, for every shape.)
+        // 4 tokens it was the fastest, or within 2 %, for every shape; at 16 it
+        // is faster where the latency counts, 1024 x 1024 4.3 us against 6.9,
+        // and slower where the bytes do, 32000 x 8192 66 us against 52.)
         const uint32_t groups = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-        const float turns = (K + 1023) / 1024 * (0.28f + 0.47f * groups) * std::max(1.0f, n_w * N / 3730.0f);
-        const float memory = n_w * N * (float)K * (1 / 5.2e6f + 2.6e-9f * M);
-        p.few = M <= 4 || 4.1f + std::max(turns, memory) < t.us;
+        const float rounds = 1 + 0.87f * ((n_w * N + 4095) / 4096 - 1);  // of workgroups on a CU
+        const float turns = (K + 1023) / 1024 * (0.60f + 0.40f * groups) * rounds;
+        const float memory = n_w * N * (float)K * (1 / 5.4e6f + 2.5e-8f * groups);
+        p.few = M <= 4 || 3.4f + std::max(turns, memory) < t.us;
         if (p.few) {
             p.quantizes = x_type != ENTQ_I8 && few_quantizes(mode, M, N, K);
             p.splits = 1;
@@ -367,15 +369,16 @@ Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K
             return p;
         }
     }
-    p.part_rows = p.splits > 1 ? (M + 3) / 4 : (M + p.tile - 1) / p.tile * 2;
+    const uint32_t tokens = kTiles[p.kind].tokens;
+    p.part_rows = p.splits > 1 ? (M + 3) / 4 : (M + tokens - 1) / tokens * 2;
     return p;
 }
 
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s) {
     if (p.few) return launch_int8_few(mode, a, s);
-    if (p.tile == 256) launch_tiles<256, 256, 2, 2, 4, 3, 2>(mode, a, s);
-    if (p.tile == 128) launch_tiles<128, 128, 2, 2, 2, 3, 2>(mode, a, s);
-    if (p.tile == 64) launch_tiles<64, 128, 2, 2, 2, 3, 3>(mode, a, s);
+    if (p.kind == 0) launch_tiles<64, 128, 2, 2, 2, 3, 3>(mode, a, s);
+    if (p.kind == 1) launch_tiles<128, 128, 2, 2, 2, 3, 2>(mode, a, s);
+    if (p.kind == 2) launch_tiles<256, 256, 2, 2, 4, 3, 2>(mode, a, s);
     if (a.splits > 1) launch_finish(mode, a, s);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }

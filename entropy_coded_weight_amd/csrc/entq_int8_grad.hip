@@ -246,24 +246,22 @@ void launch_tiles(const GradArgs &a, hipStream_t s) {
 
 }  // namespace
 
+// tokens x columns of the kinds of tiles
+static const TileCost kTiles[3] = {{64, 128, {0.542f, 0.857f}, 0.0f},
+                                   {128, 128, {0.625f, 1.13f}, 0.0f},
+                                   {256, 256, {1.32f, 1.64f}, 1.9f}};
+static const SplitCost kSplits = {6.6f, 9.2e6f, 3.5f, 0.125f, 1.54e-6f};
+
 GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, int n_w) {
-    static const TileCost kinds[3] = {{64, {0.542f, 0.857f}, 0.0f}, {128, {0.625f, 1.13f}, 0.0f},
-                                      {256, {1.32f, 1.64f}, 1.9f}};
-    static const SplitCost cost = {6.6f, 9.2e6f, 1.7f, 0.125f, 1.54e-6f};
-    const TileChoice t = cheapest_tile(
-        kinds, cost,
-        [&](uint32_t tokens) {
-            const uint64_t cols = tokens == 256 ? 256 : 128;
-            return (uint64_t)((M + tokens - 1) / tokens) * ((K + cols - 1) / cols);
-        },
-        n_w * ((N + 63) / 64), (uint64_t)n_w * N * K, (uint64_t)M * K);
-    return {(int)t.tokens, t.splits};
+    const TileChoice t = cheapest_tile(kTiles, kSplits, M, K, n_w * ((N + 63) / 64), (uint64_t)n_w * N * K,
+                                       (uint64_t)M * K);
+    return {t.kind, t.splits};
 }
 
 int launch_grad_product(const GradPlan &p, const GradArgs &a, hipStream_t s) {
-    if (p.tile == 256) launch_tiles<256, 256, 1, 4, 3>(a, s);
-    if (p.tile == 128) launch_tiles<128, 128, 2, 2, 3>(a, s);
-    if (p.tile == 64) launch_tiles<64, 128, 2, 2, 3>(a, s);
+    if (p.kind == 0) launch_tiles<64, 128, 2, 2, 3>(a, s);
+    if (p.kind == 1) launch_tiles<128, 128, 2, 2, 3>(a, s);
+    if (p.kind == 2) launch_tiles<256, 256, 1, 4, 3>(a, s);
     if (p.splits > 1) grad_sum<<<dim3((a.K / 4 + 255) / 256, std::min(a.M, 65535u)), 256, 0, s>>>(a);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
