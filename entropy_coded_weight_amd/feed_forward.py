@@ -1,0 +1,95 @@
+"""A transformer's feed-forward block on compressed Int8 weights:
+
+    y = (act(x . gate^T) * (x . up^T)) . down^T
+
+The three matrices are one plan (Int8 tensors in the order gate, up, down).
+They are decoded to codes right before the block uses them [EntQuant,
+"Float8@2bits ...", technical summary §2 "Decodificación en Tiempo de
+Inferencia"] and multiplied as codes: activations are quantised to int8 per
+row, both first products and the activation are one kernel, and its result is
+quantised again for the last product. The backward pass gives the gradients
+of x and of every row scale; the codes are constants.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import EINVAL, KIND_INT8, OUT_CODES, EntqError, Plan, _device_buffer, decode, int8
+
+
+def _on(stream, device):
+    """Makes ``stream`` (torch stream, raw handle or None) the current one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+class FeedForward:
+    """p: the plan of gate [F, D], up [F, D] and down [E, F]; scales: device
+    float32 with the plan's row scales. ``decode`` fills the code buffer, which
+    ``forward`` and ``backward`` then use; a caller that walks over layers gives
+    several blocks one buffer (``codes``: device int8, at least out_elems)."""
+
+    def __init__(self, p: Plan, scales, activation="silu", codes=None):
+        t = p.tensors
+        if p.n_tensors != 3 or any(int(k) & 0xFF != KIND_INT8 for k in t["kind"]):
+            raise EntqError(EINVAL, "a feed-forward block is three Int8 tensors: gate, up, down")
+        (f, d), (f2, d2), (e, f3) = ((int(r["rows"]), int(r["cols"])) for r in t)
+        if (f, d) != (f2, d2) or f3 != f:
+            raise EntqError(EINVAL, f"gate {f} x {d}, up {f2} x {d2}, down {e} x {f3}: gate and "
+                                    "up have one shape, down a column for each of their rows")
+        if activation not in int8.ACTIVATIONS:
+            raise EntqError(EINVAL, f"activation {activation!r}: one of "
+                                    f"{', '.join(int8.ACTIVATIONS)}")
+        _device_buffer(p, "scales", scales, p.scale_rows, dtypes=(torch.float32,))
+        if codes is None:
+            codes = torch.empty(p.out_elems, dtype=torch.int8, device=p.device)
+        _device_buffer(p, "codes", codes, p.out_elems, dtypes=(torch.int8,))
+        self.plan, self.scales, self.activation, self.codes = p, scales, activation, codes
+        self.hidden = f
+        self._w = []  # code matrix and its scales
+        self._at = []  # where a tensor's scales are
+        for r in t:
+            rows, cols = int(r["rows"]), int(r["cols"])
+            o, s = int(r["out_elem_offset"]), int(r["scale_row_offset"])
+            self._at.append(slice(s, s + rows))
+            self._w += [codes[o:o + rows * cols].view(rows, cols), scales[s:s + rows]]
+
+    def decode(self, compressed, chunk_status=None, stream=None):
+        """Enqueue the decode of the block's codes."""
+        decode(self.plan, compressed, self.codes, OUT_CODES, None, chunk_status, stream)
+
+    def forward(self, x, y, stream=None):
+        """y = block(x): x bfloat16, float16 or float32 [m, D], y of any of
+        these types [m, E]. The hidden values between have x's type."""
+        with _on(stream, self.plan.device):
+            h = torch.empty(x.shape[0], self.hidden, dtype=x.dtype, device=x.device)
+            int8.gated(x, None, *self._w[:4], h, self.activation)
+            int8.gemm(h, None, *self._w[4:], y)
+
+    def backward(self, dy, x, dx=None, dscales=None, stream=None):
+        """Gradients for dy = dL/dy (bfloat16 or float16 [m, E], x's type):
+        dx (that type, [m, D]) and dscales (float32 [scale_rows], the plan's
+        order); None: not computed. The forward pass is done again from x."""
+        if x.dtype != dy.dtype:
+            raise EntqError(EINVAL, f"dy has dtype {dy.dtype}, x {x.dtype}")
+        if dscales is not None:
+            _device_buffer(self.plan, "dscales", dscales, self.plan.scale_rows,
+                           dtypes=(torch.float32,))
+        with _on(stream, self.plan.device):
+            m = x.shape[0]
+            new = lambda n, t: torch.empty(m, n, dtype=t, device=x.device)  # noqa: E731
+            q, h, qh = new(x.shape[1], torch.int8), new(self.hidden, x.dtype), new(self.hidden, torch.int8)
+            sx, sh = (torch.empty(m, dtype=torch.float32, device=x.device) for _ in range(2))
+            dh = new(self.hidden, dy.dtype)
+            int8.quantize_rows(x, q, sx)
+            int8.gated(q, sx, *self._w[:4], h, self.activation)
+            int8.quantize_rows(h, qh, sh)
+            dg, du, dd = (dscales[s] if dscales is not None else None for s in self._at)
+            int8.gemm_backward(dy, qh, sh, *self._w[4:], dh, dd)
+            int8.gated_backward(dh, q, sx, *self._w[:4], dx, dg, du, self.activation)

@@ -13,8 +13,8 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (EINVAL, KIND_BF16EXP, LAYOUT_TILES, OUT_BF16, EntqError, Plan, _gemm_io, decode,
-               decode_gemm, decode_gemm_tiles)
+from . import (EINVAL, KIND_BF16EXP, KIND_INT8, LAYOUT_TILES, OUT_BF16, OUT_CODES, EntqError, Plan,
+               _device_buffer, _gemm_io, decode, decode_gemm, decode_gemm_tiles)
 
 FUSED_MAX_ROWS = 64
 
@@ -65,3 +65,30 @@ def linear(p: Plan, compressed, scales, xs, ys, weights=None, chunk_status=None,
             off = int(p.tensors[t]["out_elem_offset"])
             wt = w[off:off + rows * cols].view(rows, cols)
             ys[t][:, :rows].copy_(torch.mm(xs[t][:, :cols], wt.t(), out_dtype=torch.float32))
+
+
+def linear_int8(p: Plan, compressed, scales, xs, ys, codes=None, chunk_status=None, stream=None):
+    """Y_t = X_t . W_t^T for every tensor t of a plan of Int8 tensors, with the
+    activations quantised to int8 per row: the plan is decoded to codes (half
+    the bytes of bf16 weights) into ``codes`` (device int8, at least out_elems;
+    allocated when None), then each product runs on the int8 matrix cores
+    (int8.gemm). xs[t]: device bfloat16, float16 or float32 [m, cols]; ys[t]: any
+    of these types [m, rows]; stream as in ``linear``."""
+    import torch
+
+    from . import int8
+    from .feed_forward import _on
+    if len(xs) != p.n_tensors or len(ys) != p.n_tensors:
+        raise EntqError(EINVAL, f"{len(xs)} activation and {len(ys)} result matrices for "
+                                f"{p.n_tensors} tensors")
+    if np.any((p.tensors["kind"] & 0xFF) != KIND_INT8):
+        raise EntqError(EINVAL, "linear_int8 takes Int8 tensors")
+    _device_buffer(p, "scales", scales, p.scale_rows, dtypes=(torch.float32,))
+    with _on(stream, p.device):
+        if codes is None:
+            codes = torch.empty(p.out_elems, dtype=torch.int8, device=p.device)
+        decode(p, compressed, codes, OUT_CODES, None, chunk_status)
+        for t, r in enumerate(p.tensors):
+            rows, cols = int(r["rows"]), int(r["cols"])
+            o, s = int(r["out_elem_offset"]), int(r["scale_row_offset"])
+            int8.gemm(xs[t], None, codes[o:o + rows * cols].view(rows, cols), scales[s:s + rows], ys[t])

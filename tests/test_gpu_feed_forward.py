@@ -1,0 +1,139 @@
+"""GPU tests of the feed-forward block on compressed Int8 weights and of the
+int8 form of linear: decode, products and gradients together, against the same
+operators called on the source codes (each of which has tests of its own), and
+against the block in 64 bits with a bound from its two quantisations."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def E():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import entropy_coded_weight_amd as E
+    E.lib()
+    return E
+
+
+def _block(E, f, d, e, tiles=False):
+    specs = [synth.random_int8_tensor(r, c, 2.0, 40 + i, c * 2) for i, (r, c) in enumerate(((f, d), (f, d), (e, f)))]
+    for sp in specs:
+        sp["scales"] = (np.asarray(sp["scales"], np.float32) / np.abs(sp["scales"]).max() * 0.02).astype(np.float32)
+    b = E.encode_batch(specs, n_threads=4)
+    p = E.plan(b.tensors, b.freq, b.chunks, b.blob.size)
+    scales = torch.from_numpy(np.concatenate([sp["scales"] for sp in specs])).cuda()
+    ws = []
+    for sp in specs:
+        codes = torch.from_numpy(np.asarray(sp["symbols"]).view(np.int8).reshape(sp["rows"], sp["cols"])).cuda()
+        ws += [codes, torch.from_numpy(sp["scales"]).cuda()]
+    return p, torch.from_numpy(b.blob).cuda(), scales, ws
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("m", [1, 6, 70])
+def test_block_is_its_operators(E, m, kind):
+    from entropy_coded_weight_amd import int8
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    f, d, e = 352, 256, 192
+    p, blob, scales, ws = _block(E, f, d, e)
+    block = FeedForward(p, scales, "gelu")
+    status = torch.full((p.n_chunks,), -1, dtype=torch.int32, device="cuda")
+    block.decode(blob, status)
+    torch.manual_seed(m)
+    x, dy = torch.randn(m, d, device="cuda").to(kind), torch.randn(m, e, device="cuda").to(kind)
+    y = torch.empty(m, e, device="cuda")
+    block.forward(x, y)
+    assert (status == 0).all()
+
+    h, want = torch.empty(m, f, dtype=kind, device="cuda"), torch.empty_like(y)
+    int8.gated(x, None, *ws[:4], h, "gelu")
+    int8.gemm(h, None, *ws[4:], want)
+    assert torch.equal(y, want)
+
+    dx, ds = torch.empty_like(x), torch.empty_like(scales)
+    block.backward(dy, x, dx, ds)
+    q, sx = torch.empty(m, d, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    qh, sh = torch.empty(m, f, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    int8.quantize_rows(x, q, sx)
+    int8.quantize_rows(h, qh, sh)
+    dh, dx2 = torch.empty_like(h), torch.empty_like(dx)
+    g, u, dn = (torch.empty(n, device="cuda") for n in (f, f, e))
+    int8.gemm_backward(dy, qh, sh, *ws[4:], dh, dn)
+    int8.gated_backward(dh, q, sx, *ws[:4], dx2, g, u, "gelu")
+    assert torch.equal(dx, dx2) and torch.equal(ds, torch.cat([g, u, dn]))
+
+    # on a stream of the caller, with a code buffer of the caller
+    side = torch.cuda.Stream()
+    codes = torch.empty(p.out_elems, dtype=torch.int8, device="cuda")
+    other, y2, dx3, ds3 = FeedForward(p, scales, "gelu", codes), torch.empty_like(y), torch.empty_like(dx), torch.empty_like(ds)
+    torch.cuda.synchronize()
+    other.decode(blob, stream=side)
+    other.forward(x, y2, side)
+    other.backward(dy, x, dx3, ds3, side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(y2, y) and torch.equal(dx3, dx) and torch.equal(ds3, ds)
+
+
+def test_block_near_the_real_numbers(E):
+    """Codes are off by half a step at most: x by sx / 2 and h by sh / 2 in each
+    element, which bounds what y may differ from the block in 64 bits."""
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    f, d, e, m = 352, 256, 192, 40
+    p, blob, scales, ws = _block(E, f, d, e)
+    block = FeedForward(p, scales, "relu")
+    block.decode(blob)
+    torch.manual_seed(5)
+    x, y = torch.randn(m, d, device="cuda"), torch.empty(m, e, device="cuda")
+    block.forward(x, y)
+    wg, wu, wd = (ws[2 * i].double() * ws[2 * i + 1].double()[:, None] for i in range(3))
+    xd = x.double()
+    g, u = xd @ wg.T, xd @ wu.T
+    h = g.clamp_min(0) * u
+    slack = 1 + 1e-5  # fp32 arithmetic
+    ex = (x.abs().amax(1, keepdim=True) / 127 / 2 * slack).double().expand_as(xd)
+    eg, eu = ex @ wg.abs().T, ex @ wu.abs().T
+    eh = eg * u.abs() + g.abs() * eu + eg * eu + 1e-5 * (g * u).abs()  # |relu(a) - relu(b)| <= |a - b|
+    eq = ((h.abs() + eh).amax(1, keepdim=True) / 127 / 2 * slack).expand_as(h)
+    bound = (eh + eq) @ wd.abs().T
+    assert bool(((y.double() - h @ wd.T).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("m", [1, 90])
+def test_linear_int8(E, m):
+    from entropy_coded_weight_amd import int8
+    from entropy_coded_weight_amd.linear import linear_int8
+    p, blob, scales, ws = _block(E, 128, 256, 64)
+    torch.manual_seed(m)
+    xs = [torch.randn(m, int(r["cols"]), device="cuda").bfloat16() for r in p.tensors]
+    ys = [torch.empty(m, int(r["rows"]), device="cuda") for r in p.tensors]
+    linear_int8(p, blob, scales, xs, ys)
+    for t in range(3):
+        want = torch.empty_like(ys[t])
+        int8.gemm(xs[t], None, ws[2 * t], ws[2 * t + 1], want)
+        assert torch.equal(ys[t], want)
+
+
+def test_refusals(E):
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    from entropy_coded_weight_amd.linear import linear_int8
+    p, blob, scales, _ = _block(E, 96, 64, 32)
+    bad = [lambda: FeedForward(p, scales, "swish"), lambda: FeedForward(p, scales[:-1]),
+           lambda: FeedForward(p, scales, codes=torch.empty(8, dtype=torch.int8, device="cuda")),
+           lambda: linear_int8(p, blob, scales, [], [])]
+    q, _, s, _ = _block(E, 96, 64, 32)
+    q.tensors["rows"][1] = 95
+    bad.append(lambda: FeedForward(q, s))
+    block = FeedForward(p, scales)
+    x = torch.zeros(2, 64, device="cuda").bfloat16()
+    bad += [lambda: block.forward(x[:, :63], torch.zeros(2, 32, device="cuda")),
+            lambda: block.forward(x, torch.zeros(2, 31, device="cuda")),
+            lambda: block.backward(torch.zeros(2, 32, device="cuda").half(), x),
+            lambda: block.backward(torch.zeros(2, 32, device="cuda").bfloat16(), x, None, torch.zeros(3, device="cuda"))]
+    for f in bad:
+        with pytest.raises(E.EntqError) as ei:
+            f()
+        assert ei.value.status == E.EINVAL

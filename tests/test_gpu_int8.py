@@ -477,3 +477,38 @@ def test_graph_capture(I):
         torch.cuda.synchronize()
         for a, b in zip((q, sx, h, dx, *ds), (*e[:4], *e[4])):
             assert torch.equal(a, b), i
+
+
+def test_refusals(I):
+    """What the binding refuses on the GPU, before any launch."""
+    from entropy_coded_weight_amd import EINVAL, EntqError
+    new = lambda *s, d=torch.float32: torch.zeros(s, device="cuda").to(d)  # noqa: E731
+    i8, bf = torch.int8, torch.bfloat16
+    x, q, sx, w, sw, y = new(4, 32, d=bf), new(4, 32, d=i8), new(4), new(8, 32, d=i8), new(8), new(4, 8)
+    dy = new(4, 8, d=bf)
+    bad = [lambda: I.gemm(x, sx, w, sw, y), lambda: I.gemm(q, None, w, sw, y), lambda: I.gemm(q, sx[:3], w, sw, y),
+           lambda: I.gemm(x, None, w[:, :31], sw, y), lambda: I.gemm(x, None, x, sw, y), lambda: I.gemm(x, None, w, sw[:7], y),
+           lambda: I.gemm(x, None, w, sw.double(), y), lambda: I.gemm(x, None, w, sw, y[:3]),
+           lambda: I.gemm(x, None, w, sw, y[:, :7]), lambda: I.gemm(x, None, w, sw, y.double()),
+           lambda: I.gemm(x, None, w, sw, y.cpu()), lambda: I.gemm(x, None, w.t().contiguous().t(), sw, y),
+           lambda: I.gemm(x[0], None, w, sw, y), lambda: I.gemm(x[:1].expand(4, 32), None, w, sw, y),
+           lambda: I.gemm(x, None, w, sw, y, workspace=new(3, d=torch.uint8)),
+           lambda: I.gemm(x, None, w, sw, y, workspace=new(1 << 16)),
+           lambda: I.gemm(new(1, I.MAX_COLS + 1), None, new(1, I.MAX_COLS + 1, d=i8), sw[:1], y[:1, :1]),
+           lambda: I.gated(x, None, w, sw, w[:7], sw[:7], y), lambda: I.gated(x, None, w, sw, w, sw, y, "tanh"),
+           lambda: I.quantize_rows(q, q, sx), lambda: I.quantize_rows(x, q[:, :31], sx), lambda: I.quantize_rows(x, q, sx[:2]),
+           lambda: I.quantize_rows(x, x, sx),
+           lambda: I.gemm_backward(dy.float(), q, sx, w, sw), lambda: I.gemm_backward(dy, x, None, w, sw),
+           lambda: I.gemm_backward(dy[:, :7], q, sx, w, sw), lambda: I.gemm_backward(dy, q, sx, w, sw, x.half()),
+           lambda: I.gemm_backward(dy, q, sx, w, sw, x[:3]), lambda: I.gemm_backward(dy, q, sx, w, sw, x, sw[:7]),
+           lambda: I.gated_backward(dy, q, sx, w, sw, w, sw, x, sw, sw[:7]),
+           lambda: I.gated_backward(dy, q, sx, w, sw, w, sw, x, activation=None),
+           lambda: I.workspace_bytes("gated", x, None, w, sw), lambda: I.workspace_bytes("gemm_backward", q, sx, w, sw)]
+    for f in bad:
+        with pytest.raises(EntqError) as e:
+            f()
+        assert e.value.status == EINVAL
+    # strided rows, a parameter's subclass and a one-row tensor of any stride pass
+    I.gemm(torch.nn.Parameter(x, requires_grad=False), None, w, sw, y)
+    I.gemm(new(4, 64, d=bf)[:, ::2][:, :0].reshape(4, 0), None, new(8, 0, d=i8), sw, y)
+    I.gemm(new(9, 32, d=bf)[::9], None, w, sw, y[:1])
