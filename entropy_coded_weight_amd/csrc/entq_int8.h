@@ -357,7 +357,11 @@ struct Int8Plan {
 };
 Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K);
 
-// Launchers; each returns an entq_status. Rows of x and w must start at
+// Whether a launch's threads can be counted in 32 bits, as HIP requires.
+inline bool launchable(uint64_t groups, uint32_t threads) { return groups && groups * threads < 1ull << 32; }
+
+// Launchers; each returns an entq_status (ENTQ_EINVAL for more workgroups
+// than one launch holds). Rows of x and w must start at
 // multiples of 16 bytes, strides below 2^23, K be a multiple of 16.
 bool few_quantizes(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K);
 int launch_int8_few(Int8Mode mode, const Int8Args &a, hipStream_t s);

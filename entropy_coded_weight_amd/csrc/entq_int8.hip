@@ -59,7 +59,7 @@ struct Aligner {
     int launch(hipStream_t s) {
         if (!n) return ENTQ_OK;
         const uint32_t b = blocks(256);
-        if (!b) return ENTQ_ETOOLARGE;
+        if (!b) return ENTQ_EINVAL;
         align_rows<<<b, 256, 0, s>>>(a);
         return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
     }

@@ -12,50 +12,53 @@ constexpr int kFewWaves = 8;
 // Bytes of a token's codes in LDS: whole blocks.
 __host__ __device__ constexpr uint32_t few_codes(uint32_t K) { return (K + 127) / 128 * 128; }
 
-// A workgroup computes 16 RG channels (of both weights, gated) for MT groups
-// of 16 tokens; its 8 waves take the 128-code blocks of K in turn and add
-// their sums up in LDS. Lane l reads codes 32 (l / 16) .. + 31 of a block of
-// row l % 16, for weights and tokens alike: a wave's two loads cover 16 whole
-// 128-byte lines, and the order of K inside a block does not matter to the
-// sum. Rows may lie at any address.
+// A workgroup computes 16 channels (of both weights, gated) for MT groups of
+// 16 tokens; its 8 waves take the 128-code blocks of K in turn, four of them in
+// flight, and add their sums up in LDS. Lane l reads codes 32 (l / 16) .. + 31
+// of a block of row l % 16, for weights and tokens alike: a wave's two loads
+// cover 16 whole 128-byte lines, and the order of K inside a block does not
+// matter to the sum. Rows may lie at any address. Every weight byte is read
+// once, so the bound is memory: one token takes 15.0 us for 8192 x 8192 (67
+// MB, 4.5 TB/s with the launch in it), 45 us for 8192 x 28672 (5.2 TB/s), 81 us
+// for gated 28672 x 8192 (5.8 TB/s; a copy reaches 4.7 TB/s of reads and
+// writes). With 16 tokens the activations are as many bytes again out of the
+// L2, and 64-token tiles win where the bytes count. 32 channels a workgroup
+// (half the activation reads, half the workgroups) took 21.1 us and 111 us
+// where this takes 17.5 and 86 (both with the quantiser), 16 waves the same
+// for one weight and 5-10 % more for two.
 //
 // XT other than ENTQ_I8: one token, whose activations every workgroup
 // quantises for itself into its LDS while the first weights are on their way.
-template <int MODE, int MT, int RG, int XT>
+template <int MODE, int MT, int XT>
 __global__ __launch_bounds__(64 * kFewWaves) void int8_few(Int8Args a) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
     constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
-    constexpr int NW = kTwo ? 2 : 1, kSums = NW * RG * MT;
-    constexpr int kDepth = NW * RG * MT >= 8 ? 2 : 4;  // blocks in flight
+    constexpr int NW = kTwo ? 2 : 1, kSums = NW * MT;
+    constexpr int kDepth = kSums >= 8 ? 2 : 4;  // blocks in flight
     __shared__ v4i sums[kFewWaves][kSums][64];
     extern __shared__ __attribute__((aligned(16))) int8_t codes[];  // the token's, XT not ENTQ_I8
     __shared__ uint32_t top[kFewWaves];
     float own_scale = 0.0f;
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const uint32_t n0 = blockIdx.x * 16 * RG, kc = lane / 16 * 32;
+    const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32;
 
-    const int8_t *w[NW][RG], *x[MT];
+    const int8_t *w[NW], *x[MT];
 #pragma unroll
-    for (int t = 0; t < NW; ++t)
-#pragma unroll
-        for (int r = 0; r < RG; ++r)
-            w[t][r] = a.w[t] + (uint64_t)min(n0 + r * 16 + lane % 16, a.N - 1) * a.ldw[t] + kc;
+    for (int t = 0; t < NW; ++t) w[t] = a.w[t] + (uint64_t)min(n0 + lane % 16, a.N - 1) * a.ldw[t] + kc;
 #pragma unroll
     for (int g = 0; g < MT; ++g)
         x[g] = XT == ENTQ_I8 ? a.x + (uint64_t)min(g * 16 + lane % 16, a.M - 1) * a.ldx + kc
                              : codes + kc;
 
-    v4i acc[NW][RG][MT] = {};
+    v4i acc[NW][MT] = {};
     struct Block {
-        v4i w[NW][RG][2], x[MT][2];
+        v4i w[NW][2], x[MT][2];
     };
     auto load = [&](Block &b, uint32_t k) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int t = 0; t < NW; ++t)
-#pragma unroll
-                for (int r = 0; r < RG; ++r) b.w[t][r][h] = ((const any16 *)(w[t][r] + k + 16 * h))->v;
+            for (int t = 0; t < NW; ++t) b.w[t][h] = ((const any16 *)(w[t] + k + 16 * h))->v;
 #pragma unroll
             for (int g = 0; g < MT; ++g)
                 if (XT == ENTQ_I8) b.x[g][h] = ((const any16 *)(x[g] + k + 16 * h))->v;
@@ -74,11 +77,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few(Int8Args a) {
 #pragma unroll
             for (int t = 0; t < NW; ++t)
 #pragma unroll
-                for (int r = 0; r < RG; ++r)
-#pragma unroll
-                    for (int g = 0; g < MT; ++g)
-                        acc[t][r][g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b.w[t][r][h], b.x[g][h], acc[t][r][g],
-                                                                             0, 0, 0);
+                for (int g = 0; g < MT; ++g)
+                    acc[t][g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b.w[t][h], b.x[g][h], acc[t][g], 0, 0, 0);
     };
     const uint32_t blocks = a.K / 128;  // whole ones
     const uint32_t mine = blocks > wave ? (blocks - wave + kFewWaves - 1) / kFewWaves : 0;
@@ -143,9 +143,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few(Int8Args a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int t = 0; t < NW; ++t)
-#pragma unroll
-                for (int r = 0; r < RG; ++r) e.w[t][r][h] = load16_any(w[t][r] - kc, k + kc + 16 * h, a.K);
+            for (int t = 0; t < NW; ++t) e.w[t][h] = load16_any(w[t] - kc, k + kc + 16 * h, a.K);
 #pragma unroll
             for (int g = 0; g < MT; ++g)
                 if (XT == ENTQ_I8) e.x[g][h] = load16_any(x[g] - kc, k + kc + 16 * h, a.K);
@@ -157,20 +155,18 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few(Int8Args a) {
 #pragma unroll
     for (int t = 0; t < NW; ++t)
 #pragma unroll
-        for (int r = 0; r < RG; ++r)
-#pragma unroll
-            for (int g = 0; g < MT; ++g) sums[wave][(t * RG + r) * MT + g][lane] = acc[t][r][g];
+        for (int g = 0; g < MT; ++g) sums[wave][t * MT + g][lane] = acc[t][g];
     __syncthreads();
     const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
-    for (int p = wave; p < RG * MT; p += kFewWaves) {
+    if (wave < MT) {
+        const uint32_t g = wave;
         v4i s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
 #pragma unroll
         for (int v = 0; v < kFewWaves; ++v) {
-            s0 += sums[v][p][lane];
-            if (kTwo) s1 += sums[v][RG * MT + p][lane];
+            s0 += sums[v][g][lane];
+            if (kTwo) s1 += sums[v][MT + g][lane];
         }
-        const int r = p / MT, g = p % MT;
-        const uint32_t n = n0 + r * 16 + lane / 16 * 4;
+        const uint32_t n = n0 + lane / 16 * 4;
         float scale[2][4], sg[4] = {}, su[4] = {};
         load_scales<MODE>(a, n, scale);
         const uint32_t m = g * 16 + lane % 16;
@@ -194,17 +190,19 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few(Int8Args a) {
 }
 
 template <int MT, int XT>
-void launch_few(Int8Mode mode, const Int8Args &a, hipStream_t s) {
+int launch_few(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
-    const dim3 grid((cols + 15) / 16);
     constexpr int kThreads = 64 * kFewWaves;
+    const dim3 grid(cols / 16 + (cols % 16 != 0));
+    if (!launchable(grid.x, kThreads)) return ENTQ_EINVAL;
     const uint32_t lds = XT == ENTQ_I8 ? 0 : few_codes(a.K);
-    if (mode == kFwd) int8_few<kFwd, MT, 1, XT><<<grid, kThreads, lds, s>>>(a);
-    if (mode == kGated) int8_few<kGated, MT, 1, XT><<<grid, kThreads, lds, s>>>(a);
+    if (mode == kFwd) int8_few<kFwd, MT, XT><<<grid, kThreads, lds, s>>>(a);
+    if (mode == kGated) int8_few<kGated, MT, XT><<<grid, kThreads, lds, s>>>(a);
     if constexpr (XT == ENTQ_I8) {
-        if (mode == kBwd) int8_few<kBwd, MT, 1, XT><<<grid, kThreads, lds, s>>>(a);
-        if (mode == kGatedBwd) int8_few<kGatedBwd, MT, 1, XT><<<grid, kThreads, lds, s>>>(a);
+        if (mode == kBwd) int8_few<kBwd, MT, XT><<<grid, kThreads, lds, s>>>(a);
+        if (mode == kGatedBwd) int8_few<kGatedBwd, MT, XT><<<grid, kThreads, lds, s>>>(a);
     }
+    return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
 }  // namespace
@@ -219,19 +217,12 @@ bool few_quantizes(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K) {
 }
 
 int launch_int8_few(Int8Mode mode, const Int8Args &a, hipStream_t s) {
-    if (a.x_type == ENTQ_BF16)
-        launch_few<1, ENTQ_BF16>(mode, a, s);
-    else if (a.x_type == ENTQ_F16)
-        launch_few<1, ENTQ_F16>(mode, a, s);
-    else if (a.x_type == ENTQ_F32)
-        launch_few<1, ENTQ_F32>(mode, a, s);
-    else if (a.M <= 16)
-        launch_few<1, ENTQ_I8>(mode, a, s);
-    else if (a.M <= 32)
-        launch_few<2, ENTQ_I8>(mode, a, s);
-    else
-        launch_few<4, ENTQ_I8>(mode, a, s);
-    return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
+    if (a.x_type == ENTQ_BF16) return launch_few<1, ENTQ_BF16>(mode, a, s);
+    if (a.x_type == ENTQ_F16) return launch_few<1, ENTQ_F16>(mode, a, s);
+    if (a.x_type == ENTQ_F32) return launch_few<1, ENTQ_F32>(mode, a, s);
+    if (a.M <= 16) return launch_few<1, ENTQ_I8>(mode, a, s);
+    if (a.M <= 32) return launch_few<2, ENTQ_I8>(mode, a, s);
+    return launch_few<4, ENTQ_I8>(mode, a, s);
 }
 
 }  // namespace entq

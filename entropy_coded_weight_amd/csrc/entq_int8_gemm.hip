@@ -313,17 +313,19 @@ __global__ __launch_bounds__(256) void int8_finish(Int8Args a) {
 // fragments serve fewer products, more LDS reads), gated 4096 x 28672 x 8192
 // 1605 and 1596, product back 2048 x 8192 x 8192 329 and 322.
 template <int BM, int BN, int WM, int WN, int WNB, int SX, int SW>
-void launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
+int launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     const bool two = mode == kGated || mode == kGatedBwd;
     const uint32_t cols = mode == kBwd || mode == kGatedBwd ? (uint32_t)a.ldd : a.N;
     const uint32_t ch = two ? BN / 2 : BN;
     const uint32_t nb_m = (a.M + BM - 1) / BM, nb_n = (cols + ch - 1) / ch;
-    const dim3 grid(nb_m * nb_n, a.splits);
     constexpr int kOne = 64 * WM * WN, kLong = 64 * WM * WNB;
+    if (!launchable((uint64_t)nb_m * nb_n * a.splits, kLong)) return ENTQ_EINVAL;
+    const dim3 grid(nb_m * nb_n, a.splits);
     if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN, SX, SW><<<grid, kOne, 0, s>>>(a, nb_m, nb_n);
     if (mode == kGated) int8_tiles<kGated, BM, BN, WM, WNB, SX, SW><<<grid, kLong, 0, s>>>(a, nb_m, nb_n);
     if (mode == kBwd) int8_tiles<kBwd, BM, BN, WM, WNB, SX, SW><<<grid, kLong, 0, s>>>(a, nb_m, nb_n);
     if (mode == kGatedBwd) int8_tiles<kGatedBwd, BM, BN, WM, WNB, SX, SW><<<grid, kLong, 0, s>>>(a, nb_m, nb_n);
+    return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
 void launch_finish(Int8Mode mode, const Int8Args &a, hipStream_t s) {
@@ -376,10 +378,11 @@ Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K
 
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s) {
     if (p.few) return launch_int8_few(mode, a, s);
-    if (p.kind == 0) launch_tiles<64, 128, 2, 2, 2, 3, 3>(mode, a, s);
-    if (p.kind == 1) launch_tiles<128, 128, 2, 2, 2, 3, 2>(mode, a, s);
-    if (p.kind == 2) launch_tiles<256, 256, 2, 2, 4, 3, 2>(mode, a, s);
-    if (a.splits > 1) launch_finish(mode, a, s);
+    const int r = p.kind == 0   ? launch_tiles<64, 128, 2, 2, 2, 3, 3>(mode, a, s)
+                  : p.kind == 1 ? launch_tiles<128, 128, 2, 2, 2, 3, 2>(mode, a, s)
+                                : launch_tiles<256, 256, 2, 2, 4, 3, 2>(mode, a, s);
+    if (r != ENTQ_OK || a.splits == 1) return r;
+    launch_finish(mode, a, s);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 

@@ -235,13 +235,15 @@ __global__ __launch_bounds__(256) void grad_sum(GradArgs a) {
 }
 
 template <int BM, int BK, int WM, int WN, int S>
-void launch_tiles(const GradArgs &a, hipStream_t s) {
+int launch_tiles(const GradArgs &a, hipStream_t s) {
     const uint32_t nb_m = (a.M + BM - 1) / BM, nb_k = (a.K + BK - 1) / BK;
+    if (!launchable(((uint64_t)nb_m * nb_k + sum_blocks(a.sums)) * a.splits, 256)) return ENTQ_EINVAL;
     const dim3 grid(nb_m * nb_k + sum_blocks(a.sums), a.splits);
     if (a.f16)
         grad_tiles<true, BM, BK, WM, WN, S><<<grid, 256, 0, s>>>(a, nb_m, nb_k);
     else
         grad_tiles<false, BM, BK, WM, WN, S><<<grid, 256, 0, s>>>(a, nb_m, nb_k);
+    return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
 }  // namespace
@@ -259,10 +261,11 @@ GradPlan grad_plan(uint32_t M, uint32_t N, uint32_t K, int n_w) {
 }
 
 int launch_grad_product(const GradPlan &p, const GradArgs &a, hipStream_t s) {
-    if (p.kind == 0) launch_tiles<64, 128, 2, 2, 3>(a, s);
-    if (p.kind == 1) launch_tiles<128, 128, 2, 2, 3>(a, s);
-    if (p.kind == 2) launch_tiles<256, 256, 1, 4, 3>(a, s);
-    if (p.splits > 1) grad_sum<<<dim3((a.K / 4 + 255) / 256, std::min(a.M, 65535u)), 256, 0, s>>>(a);
+    const int r = p.kind == 0   ? launch_tiles<64, 128, 2, 2, 3>(a, s)
+                  : p.kind == 1 ? launch_tiles<128, 128, 2, 2, 3>(a, s)
+                                : launch_tiles<256, 256, 1, 4, 3>(a, s);
+    if (r != ENTQ_OK || p.splits == 1) return r;
+    grad_sum<<<dim3((a.K / 4 + 255) / 256, std::min(a.M, 65535u)), 256, 0, s>>>(a);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 

@@ -607,8 +607,10 @@ entq_status entq_pack_device_adaptive_batch(const entq_pack_adaptive_job *jobs, 
  * sw[n] w[n][k]. The calls below take such codes as they are, quantise the
  * activations to int8 with one scale per row (token) and multiply on the
  * int8 matrix cores, whose sums are exact in int32. All are enqueued on
- * stream, allocate nothing, and are deterministic: the same inputs give the
- * same bits. Results never overlap inputs or each other. */
+ * stream (of the current device), allocate nothing, and are deterministic:
+ * the same inputs give the same bits. Results never overlap inputs or each
+ * other. ENTQ_EINVAL also where a matrix is too large for one launch (2^32
+ * threads, beyond some 2^37 results). */
 
 typedef enum { ENTQ_BF16 = 0, ENTQ_F16 = 1, ENTQ_F32 = 2, ENTQ_I8 = 3 } entq_eltype;
 
