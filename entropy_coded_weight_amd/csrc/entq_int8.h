@@ -45,7 +45,11 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// An fp32 value rounded to 16 bits. The value is an fp32 register first: a
+// product's rounding to F16 would else be fused into a mixed-precision
+// instruction in some kernels and not in others, with other last bits.
 __device__ __forceinline__ uint16_t bits16(float v, bool f16) {
+    asm("" : "+v"(v));
     return f16 ? __builtin_bit_cast(uint16_t, (_Float16)v) : __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
@@ -239,14 +243,15 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float dy = from16((uint16_t)((i < 2 ? dy4.x : dy4.y) >> (16 * (i % 2))), f16);
-            const bool in = n + i < a.N;
+            // (beyond N: dy and the scales are 0, so d is 0, or NaN in a row
+            // whose dX is NaN anyway; the sums are not used)
             const float dg = kTwo ? dy * (u0[i] * scale[1][i]) * grad[i] : dy;
-            if (in) sg[i] += dg * g0[i];
-            d[0][i] = in ? bits16(dg * (scale[0][i] * norm), f16) : 0;
+            sg[i] += dg * g0[i];
+            d[0][i] = bits16(dg * (scale[0][i] * norm), f16);
             if (kTwo) {
                 const float du = dy * act[i];
-                if (in) su[i] += du * u0[i];
-                d[1][i] = in ? bits16(du * (scale[1][i] * norm), f16) : 0;
+                su[i] += du * u0[i];
+                d[1][i] = bits16(du * (scale[1][i] * norm), f16);
             }
         }
         if (a.d[0]) {
