@@ -43,7 +43,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t 
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t wm = wave % WM, wn = wave / WM;
     uint32_t tm, tn;
-    tile_of(blockIdx.x, nb_m, nb_n, 8, tm, tn);
+    tile_of(blockIdx.x, nb_m, nb_n, tm, tn);
     const uint32_t m0 = tm * BM, n0 = tn * kChannels;
 
     // This wave's loads: rows 8 (4 i + wave) .. + 7 of a tile. Lane l fills

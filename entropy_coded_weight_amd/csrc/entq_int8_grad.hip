@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256) void grad_tiles(GradArgs a, uint32_t nb_m, uin
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t wm = wave % WM, wn = wave / WM;
     uint32_t tm, tk;
-    tile_of(blockIdx.x, nb_m, nb_k, 8, tm, tk);
+    tile_of(blockIdx.x, nb_m, nb_k, tm, tk);
     const uint32_t m0 = tm * BM, k0 = tk * BK;
 
     const uint32_t per = (uint32_t)(a.ldd / 64);  // steps of one weight
