@@ -72,6 +72,9 @@ struct Aligner {
 // One workgroup per row, which is read once: VECS pieces of 16 bytes a thread
 // stay in registers between the maximum and the rounding (VECS 0: any length,
 // read twice, the second time out of the L2). Pieces may lie at any address.
+// Bound by memory: 4096 x 28672 bf16 in 65.6 us, 5.4 TB/s, 4096 x 8192 fp32 in
+// 24.7 us, 6.8 TB/s (in part out of the last-level cache); reading each element
+// twice as single values took 233 us for the first.
 // Columns K..pad-1 are written as 0. The workgroups after the rows make copies.
 template <int TYPE, int VECS, int THREADS>
 __global__ __launch_bounds__(THREADS) void quantize_rows(const void *x, uint64_t ldx, uint32_t K, int8_t *codes,

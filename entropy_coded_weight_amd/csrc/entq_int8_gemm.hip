@@ -24,7 +24,20 @@ __device__ __forceinline__ int32_t *part_sums(const Int8Args &a, uint32_t split,
 // Once a step is read by every wave its place is loaded again, a quarter of
 // the loads beside each quarter step of products: a CU takes about 24 cycles
 // per load instruction, and loads that wait for their turn hold up the
-// wave's products.
+// wave's products. A wave's fragments for a quarter step are read during the
+// one before, so one barrier a step is all that the waves wait for.
+//
+// What bounds it: for many tokens the matrix units and the card's power. At
+// 4096 x 8192 x 28672 the 256-token tiles keep the matrix units busy 74 % of
+// the cycles at 1.7 GHz (of 2.4) and take 0.70 to 0.72 ms, 2.7 POP/s (the
+// library's int8 product reaches 2.6); busier kernels ran at lower clocks. For up to some
+// 200 tokens the weights' bytes: 32000 x 8192 with 16 tokens 50 to 61 us with
+// the quantiser, 4.3 to 5.3 TB/s. Steps: one after the other, alone the compiler reads
+// each fragment right before its use (gated 4096 x 28672 x 8192 2.65 ms); fixed
+// order 1.76; five half-stages of 32 KB with the loads spread 1.73 (product
+// 0.81 -> 0.74); epilogue through LDS with its scales read ahead and one choice
+// of activation per 4 values 1.56; bands of 4 tiles 1.55. Steps of 64 codes in 4
+// or 5 stages: 1.90 (a load instruction then touches twice the lines).
 template <int MODE, int BM, int BN, int WM, int WN, int SX, int SW>
 __global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t nb_m, uint32_t nb_n) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
@@ -70,7 +83,8 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t 
         load_lds16(xbase + step * 128, xoff[i], lds0 + slot * kStageX + (kWaves * i + wave) * 1024);
     };
     auto load_w = [&](int i, uint32_t step, uint32_t slot) {
-        load_lds16((kTwo && (kWaves * i + wave) / 4 % 2 ? wbase1 : wbase0) + step * 128, woff[i], ldsw + slot * kStageW + (kWaves * i + wave) * 1024);
+        const int8_t *base = kTwo && (kWaves * i + wave) / 4 % 2 ? wbase1 : wbase0;
+        load_lds16(base + step * 128, woff[i], ldsw + slot * kStageW + (kWaves * i + wave) * 1024);
     };
     // A whole step's loads; past the rows' end tokens are zeros and weights
     // whatever is there.

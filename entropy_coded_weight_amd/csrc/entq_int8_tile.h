@@ -15,7 +15,9 @@ constexpr uint32_t kRowBytes = 128;
 __device__ __forceinline__ uint32_t swizzle(uint32_t row) { return row / 2 % 8; }
 
 // One 16-byte load per active lane from base + offset straight into LDS at
-// lds + 16 lane. The compiler does not count this load: wait_loads() does.
+// lds + 16 lane. The compiler does not
+// count this load; wait_loads_and_meet() does. (s_nop: a written m0 needs one
+// wait state before such a load.)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(const void *base, uint32_t offset, uint32_t lds) {
