@@ -35,6 +35,7 @@ struct Int8Args {
     uint32_t splits;        // of K; above 1, integer sums go to
     int32_t *sums;          // [splits][weights][M][N rounded up to 4]
     const float *norm;      // F16 backward: the power of two that multiplies sw, then its inverse
+    float *norm_out;        // splits above 1: written by the tiles' launch, for the one that finishes; or null
 };
 
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -361,6 +362,30 @@ struct Int8Plan {
     uint32_t part_rows;     // rows of Int8Args::part
 };
 Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K);
+
+// norm[0]: a power of two that brings the largest |scale| into [1, 2), and
+// norm[1] its inverse: dy sw then spans the range dy itself has, which F16
+// holds by the caller's choice. 1 where all scales are 0 or one is not finite.
+// One workgroup of up to 16 waves, which gives 64 bytes of LDS; b may be null.
+__device__ __forceinline__ void scale_norm_block(const float *a, const float *b, uint32_t n, float *norm,
+                                                 uint32_t *top) {
+    uint32_t big = 0;
+    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
+        big = max(big, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+        if (b) big = max(big, __float_as_uint(b[i]) & 0x7FFFFFFFu);
+    }
+    big = wave_max(big);
+    if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 1; i < blockDim.x / 64; ++i) big = max(big, top[i]);
+        int e = (int)(big >> 23) - 127;
+        if (big == 0 || big >= 0x7F800000u) e = 0;
+        e = max(-126, min(126, e));
+        norm[0] = __uint_as_float((uint32_t)(127 - e) << 23);
+        norm[1] = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+}
 
 // Whether a launch's threads can be counted in 32 bits, as HIP requires.
 inline bool launchable(uint64_t groups, uint32_t threads) { return groups && groups * threads < 1ull << 32; }

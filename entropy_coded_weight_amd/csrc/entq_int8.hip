@@ -180,27 +180,9 @@ bool direct(const entq_rows &m) {
 // backward helpers
 // ---------------------------------------------------------------------------
 
-// norm[0]: a power of two that brings the largest |scale| into [1, 2), and
-// norm[1] its inverse: dy sw then spans the range dy itself has, which F16
-// holds by the caller's choice. 1 where all scales are 0 or one is not finite.
 __global__ __launch_bounds__(1024) void scale_norm(const float *a, const float *b, uint32_t n, float *norm) {
     __shared__ uint32_t top[16];
-    uint32_t big = 0;
-    for (uint32_t i = threadIdx.x; i < n; i += 1024) {
-        big = max(big, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-        if (b) big = max(big, __float_as_uint(b[i]) & 0x7FFFFFFFu);
-    }
-    big = wave_max(big);
-    if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 16; ++i) big = max(big, top[i]);
-        int e = (int)(big >> 23) - 127;
-        if (big == 0 || big >= 0x7F800000u) e = 0;
-        e = max(-126, min(126, e));
-        norm[0] = __uint_as_float((uint32_t)(127 - e) << 23);
-        norm[1] = __uint_as_float((uint32_t)(127 + e) << 23);
-    }
+    scale_norm_block(a, b, n, norm, top);
 }
 
 __global__ __launch_bounds__(kSumThreads) void sum_parts(SumArgs a) { sum_parts_block(a, blockIdx.x); }
@@ -451,8 +433,11 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     if ((st = operands(c, l, a, s)) != ENTQ_OK) return st;
     const bool f16 = c.dy->type == ENTQ_F16;
     if (f16 && dx) {
-        scale_norm<<<1, 1024, 0, s>>>(a.sw[0], a.sw[1], N, l.norm);
         a.norm = l.norm;
+        if (l.plan.splits > 1 && (c.mode == kGatedBwd || ds0))
+            a.norm_out = l.norm;
+        else
+            scale_norm<<<1, 1024, 0, s>>>(a.sw[0], a.sw[1], N, l.norm);
     }
     a.act = act;
     a.y = const_cast<void *>(c.dy->d_data);

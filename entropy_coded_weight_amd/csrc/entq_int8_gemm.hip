@@ -53,6 +53,11 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t 
     static_assert((!kTwo || FN % 2 == 0) && (SX == SW || SX == SW + 1), "");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
 
+    if (kBack && blockIdx.x >= nb_m * nb_n) {  // a workgroup after the tiles
+        if (blockIdx.y == 0)
+            scale_norm_block(a.sw[0], kTwo ? a.sw[1] : nullptr, a.N, a.norm_out, (uint32_t *)lds);
+        return;
+    }
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t wm = wave % WM, wn = wave / WM;
     uint32_t tm, tn;
@@ -218,7 +223,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t 
     read_ahead(0);
     float scale[2][4], sg[4] = {}, su[4] = {};
     load_scales<MODE>(a, n, scale);
-    const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
+    const float norm = kBack && a.norm && a.splits == 1 ? a.norm[0] : 1.0f;
 #pragma unroll
     for (int i = 0; i < FN * FM; ++i)
         acc[i / FM][i % FM] =
@@ -333,8 +338,9 @@ int launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     const uint32_t ch = two ? BN / 2 : BN;
     const uint32_t nb_m = (a.M + BM - 1) / BM, nb_n = (cols + ch - 1) / ch;
     constexpr int kOne = 64 * WM * WN, kLong = 64 * WM * WNB;
-    if (!launchable((uint64_t)nb_m * nb_n * a.splits, kLong)) return ENTQ_EINVAL;
-    const dim3 grid(nb_m * nb_n, a.splits);
+    const uint64_t groups = (uint64_t)nb_m * nb_n + (a.norm_out != nullptr);
+    if (!launchable(groups * a.splits, kLong)) return ENTQ_EINVAL;
+    const dim3 grid((uint32_t)groups, a.splits);
     if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN, SX, SW><<<grid, kOne, 0, s>>>(a, nb_m, nb_n);
     if (mode == kGated) int8_tiles<kGated, BM, BN, WM, WNB, SX, SW><<<grid, kLong, 0, s>>>(a, nb_m, nb_n);
     if (mode == kBwd) int8_tiles<kBwd, BM, BN, WM, WNB, SX, SW><<<grid, kLong, 0, s>>>(a, nb_m, nb_n);

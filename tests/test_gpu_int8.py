@@ -388,7 +388,8 @@ def test_large_forward(I, m, n, k):
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("m,n,k", [(1100, 8200, 272), (520, 2001, 4096), (1000, 5000, 4000), (2050, 3001, 4103),
-                                   (256, 8192, 8192), (40, 3000, 640)])
+                                   (256, 8192, 8192), (40, 3000, 640), (90, 200, 4112), (96, 1000, 8192),
+                                   (70, 130, 3000)])
 def test_large_backward(I, m, n, k, kind):
     _say("large backward", m, n, k, kind)
     q, sx, wg, sg, wu, su = _large(m, n, k, m + n, 2)
