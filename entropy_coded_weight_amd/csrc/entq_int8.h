@@ -66,6 +66,21 @@ struct __attribute__((packed)) any4 { int v; };
 // Codes k..k+15 of a row of K codes at any address, zeros past its end.
 __device__ __forceinline__ v4i load16_any(const int8_t *row, uint32_t k, uint32_t K) {
     if (k + 16 <= K) return ((const any16 *)(row + k))->v;
+    if (k >= K) return v4i{0, 0, 0, 0};
+    if (K >= 16) {  // the row's last 16 codes, moved down
+        const v4i v = ((const any16 *)(row + K - 16))->v;
+        uint64_t lo = (uint32_t)v[0] | (uint64_t)(uint32_t)v[1] << 32;
+        uint64_t hi = (uint32_t)v[2] | (uint64_t)(uint32_t)v[3] << 32;
+        const uint32_t shift = 8 * (16 - (K - k));  // 8 .. 120
+        if (shift >= 64) {
+            lo = hi >> (shift - 64);
+            hi = 0;
+        } else {
+            lo = lo >> shift | hi << (64 - shift);
+            hi >>= shift;
+        }
+        return v4i{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
+    }
     uint32_t b[4] = {0, 0, 0, 0};
 #pragma unroll
     for (uint32_t i = 0; i < 15; ++i)

@@ -13,7 +13,7 @@ namespace {
 // ---------------------------------------------------------------------------
 
 // Up to 3 matrices' rows of K codes at any address into rows of ldc (a
-// multiple of 16), zeros after column K. A thread moves 16 codes.
+// multiple of 16), zeros after column K.
 struct AlignJob {
     const int8_t *src;
     uint64_t ld;
@@ -25,14 +25,25 @@ struct AlignArgs {
     uint32_t K;
 };
 
+// Pieces of 16 codes a thread. 1, 2 and 4 (us): the product of 333 x 5121 x
+// 4099 29.3, 28.3, 27.6, gated back 515 x 2753 x 1031, whose copies are an
+// eighth the size, 42.8, 42.9, 43.9.
+constexpr uint32_t kAlignPieces = 2;
+
 __device__ __forceinline__ void align_block(const AlignArgs &a, uint32_t block, uint32_t threads) {
     const AlignJob &j = a.job[block >= a.job[2].first ? 2 : block >= a.job[1].first ? 1 : 0];
-    const uint64_t i = (uint64_t)(block - j.first) * threads + threadIdx.x;
-    const uint32_t pieces = j.ldc / 16;
-    const uint64_t r = i / pieces;
-    if (r >= j.rows) return;
-    const uint32_t c = (uint32_t)(i - r * pieces) * 16;
-    *(v4i *)(j.dst + r * j.ldc + c) = load16_any(j.src + r * j.ld, c, a.K);
+    const uint32_t i = (block - j.first) * threads * kAlignPieces + threadIdx.x, pieces = j.ldc / 16;
+    v4i v[kAlignPieces];
+    int8_t *to[kAlignPieces];
+#pragma unroll
+    for (uint32_t u = 0; u < kAlignPieces; ++u) {
+        const uint32_t p = i + u * threads, r = p / pieces, c = (p - r * pieces) * 16;
+        to[u] = r < j.rows ? j.dst + (uint64_t)r * j.ldc + c : nullptr;
+        if (to[u]) v[u] = load16_any(j.src + r * j.ld, c, a.K);
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < kAlignPieces; ++u)
+        if (to[u]) *(v4i *)to[u] = v[u];
 }
 
 __global__ __launch_bounds__(256) void align_rows(AlignArgs a) { align_block(a, blockIdx.x, 256); }
@@ -51,8 +62,9 @@ struct Aligner {
         uint64_t all = 0;
         for (uint32_t i = 0; i < 3; ++i) {
             a.job[i].first = i < n ? (uint32_t)all : 0xFFFFFFFFu;
-            if (i < n) all += ((uint64_t)a.job[i].rows * (a.job[i].ldc / 16) + threads - 1) / threads;
-            if (all * threads >= 1ull << 31) return 0;
+            const uint64_t per = threads * kAlignPieces;
+            if (i < n) all += ((uint64_t)a.job[i].rows * (a.job[i].ldc / 16) + per - 1) / per;
+            if (all * per >= 1ull << 32) return 0;
         }
         return (uint32_t)all;
     }
