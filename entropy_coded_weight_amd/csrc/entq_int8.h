@@ -29,13 +29,14 @@ struct Int8Args {
     void *y;                // forward: the result; backward: the incoming gradient
     int type;               // its entq_eltype
     uint64_t ldy;
-    uint16_t *d[2];         // backward: 16-bit scaled gradients [M][ldd], or null
+    uint16_t *d[2];         // backward: 16-bit scaled gradients [M][ldd], or null; F16's are narrow_row's
+    float *wide[2];         // gated backward of F16: the scaled gradients [M][ldd] before, or null
+    float *back;            // backward of F16: [M], what undoes a row's power of two
     uint64_t ldd;           // a multiple of 64; columns N..ldd-1 are written as 0
     float *part[2];         // backward: partial column sums [token blocks][N], or null
     uint32_t splits;        // of K; above 1, integer sums go to
     int32_t *sums;          // [splits][weights][M][N rounded up to 4]
-    const float *norm;      // F16 backward: the power of two that multiplies sw, then its inverse
-    float *norm_out;        // splits above 1: written by the tiles' launch, for the one that finishes; or null
+    bool narrows;           // kBwd: workgroups after the tiles run narrow_row
 };
 
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -206,9 +207,9 @@ __device__ __forceinline__ uint2 load_grad4(const Int8Args &a, uint32_t m, uint3
 // Channels of N and beyond are not stored; in a backward pass a token of M
 // and beyond adds nothing.
 template <int MODE>
-__device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const float (&scale)[2][4], float norm,
-                                          uint32_t m, uint32_t n, v4i ag, v4i au, uint2 dy4,
-                                          float (&sg)[4], float (&su)[4]) {
+__device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const float (&scale)[2][4], uint32_t m,
+                                          uint32_t n, v4i ag, v4i au, uint2 dy4, float (&sg)[4],
+                                          float (&su)[4]) {
     constexpr bool kTwo = MODE == kGated || MODE == kGatedBwd;
     constexpr bool kBack = MODE == kBwd || MODE == kGatedBwd;
     if (m >= a.M || n >= (kBack ? (uint32_t)a.ldd : a.N)) return;
@@ -247,7 +248,7 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
         }
     } else {
         const bool f16 = a.type == ENTQ_F16;
-        uint16_t d[2][4];
+        float d[2][4];
         float g0[4], u0[4], g[4], act[4], grad[4];  // g0, u0: before the channel's scale
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -263,19 +264,25 @@ __device__ __forceinline__ void epilogue4(const Int8Args &a, float sx, const flo
             // whose dX is NaN anyway; the sums are not used)
             const float dg = kTwo ? dy * (u0[i] * scale[1][i]) * grad[i] : dy;
             sg[i] += dg * g0[i];
-            d[0][i] = bits16(dg * (scale[0][i] * norm), f16);
+            d[0][i] = dg * scale[0][i];
             if (kTwo) {
                 const float du = dy * act[i];
                 su[i] += du * u0[i];
-                d[1][i] = bits16(du * (scale[1][i] * norm), f16);
+                d[1][i] = du * scale[1][i];
             }
         }
-        if (a.d[0]) {
-            const uint64_t to = (uint64_t)m * a.ldd + n;
+        const uint64_t to = (uint64_t)m * a.ldd + n;
+        if (kTwo && a.wide[0]) {
 #pragma unroll
-            for (int t = 0; t < (kTwo ? 2 : 1); ++t)
-                *(uint2 *)(a.d[t] + to) = make_uint2(d[t][0] | (uint32_t)d[t][1] << 16,
-                                                     d[t][2] | (uint32_t)d[t][3] << 16);
+            for (int t = 0; t < 2; ++t) *(v4f *)(a.wide[t] + to) = v4f{d[t][0], d[t][1], d[t][2], d[t][3]};
+        } else if (a.d[0] && !f16) {
+#pragma unroll
+            for (int t = 0; t < (kTwo ? 2 : 1); ++t) {
+                uint16_t b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = bits16(d[t][i], false);
+                *(uint2 *)(a.d[t] + to) = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+            }
         }
     }
 }
@@ -313,7 +320,7 @@ struct GradArgs {
     bool f16;
     void *dx;               // [M][lddx], bf16 or f16
     uint64_t lddx;
-    const float *norm;      // F16: result times norm[1]; or null
+    const float *back;      // F16: [M], what row m of the result is multiplied with
     SumArgs sums;           // channel sums to finish in the same launch (rows 0: none)
 };
 
@@ -378,28 +385,68 @@ struct Int8Plan {
 };
 Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K);
 
-// norm[0]: a power of two that brings the largest |scale| into [1, 2), and
-// norm[1] its inverse: dy sw then spans the range dy itself has, which F16
-// holds by the caller's choice. 1 where all scales are 0 or one is not finite.
-// One workgroup of up to 16 waves, which gives 64 bytes of LDS; b may be null.
-__device__ __forceinline__ void scale_norm_block(const float *a, const float *b, uint32_t n, float *norm,
-                                                 uint32_t *top) {
+// Row m of the scaled gradients in F16 (a.d) and what undoes its power of two
+// (a.back[m]): dy sw, or with TWO the rows of a.wide. fp32 holds these values
+// and F16 does not (its normal range spans 2^30): the power of two brings the
+// largest of the row, over both weights, into [2^14, 2^15), so none overflows,
+// those within 2^-28 of the largest keep 11 bits and those below are rounded
+// to steps of 2^-38 of it. A row with an infinity or a NaN takes the power
+// that fits every finite fp32 value. One workgroup of up to 16 waves, which
+// gives 64 bytes of LDS; a thread keeps its first HELD groups of 4 channels in
+// registers and reads the others twice.
+template <bool TWO, int HELD>
+__device__ __forceinline__ void narrow_row(const Int8Args &a, uint32_t m, uint32_t *top) {
+    const uint32_t per = (uint32_t)(a.ldd / 4), all = TWO ? 2 * per : per;
+    auto read = [&](uint32_t q) {
+        const uint32_t t = TWO && q >= per, n = 4 * (q - t * per);
+        if (TWO) return *(const v4f *)((t ? a.wide[1] : a.wide[0]) + (uint64_t)m * a.ldd + n);
+        const uint2 g = load_grad4(a, m, n);
+        v4f scale = {0, 0, 0, 0};
+        if (n + 4 <= a.N)
+            scale = __builtin_bit_cast(v4f, ((const any16 *)(a.sw[0] + n))->v);
+        else
+            for (uint32_t i = 0; i < 3; ++i)
+                if (n + i < a.N) scale[i] = a.sw[0][n + i];
+        // (beyond N both are 0)
+        return v4f{from16((uint16_t)g.x, true) * scale[0], from16((uint16_t)(g.x >> 16), true) * scale[1],
+                   from16((uint16_t)g.y, true) * scale[2], from16((uint16_t)(g.y >> 16), true) * scale[3]};
+    };
     uint32_t big = 0;
-    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
-        big = max(big, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-        if (b) big = max(big, __float_as_uint(b[i]) & 0x7FFFFFFFu);
+    auto take = [&](v4f v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    };
+    v4f held[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const uint32_t q = i * blockDim.x + threadIdx.x;
+        held[i] = q < all ? read(q) : v4f{0, 0, 0, 0};
     }
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) take(held[i]);
+    for (uint32_t q = HELD * blockDim.x + threadIdx.x; q < all; q += blockDim.x) take(read(q));
     big = wave_max(big);
     if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (uint32_t i = 1; i < blockDim.x / 64; ++i) big = max(big, top[i]);
-        int e = (int)(big >> 23) - 127;
-        if (big == 0 || big >= 0x7F800000u) e = 0;
-        e = max(-126, min(126, e));
-        norm[0] = __uint_as_float((uint32_t)(127 - e) << 23);
-        norm[1] = __uint_as_float((uint32_t)(127 + e) << 23);
+    for (uint32_t i = 0; i < blockDim.x / 64; ++i) big = max(big, top[i]);
+    // (at most 2^126, whose inverse is a normal number)
+    const int up = big >= 0x7F800000u ? -113 : big ? 14 - max(-112, (int)(big >> 23) - 127) : 0;
+    const float by = __uint_as_float((uint32_t)(127 + up) << 23);
+    if (threadIdx.x == 0) a.back[m] = __uint_as_float((uint32_t)(127 - up) << 23);
+    auto put = [&](uint32_t q, v4f v) {
+        const uint32_t t = TWO && q >= per;
+        uint16_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = bits16(v[i] * by, true);
+        *(uint2 *)((t ? a.d[1] : a.d[0]) + (uint64_t)m * a.ldd + 4 * (q - t * per)) =
+            make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const uint32_t q = i * blockDim.x + threadIdx.x;
+        if (q < all) put(q, held[i]);
     }
+    for (uint32_t q = HELD * blockDim.x + threadIdx.x; q < all; q += blockDim.x) put(q, read(q));
 }
 
 // Whether a launch's threads can be counted in 32 bits, as HIP requires.

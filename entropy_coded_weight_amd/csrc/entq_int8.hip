@@ -192,20 +192,35 @@ bool direct(const entq_rows &m) {
 // backward helpers
 // ---------------------------------------------------------------------------
 
-__global__ __launch_bounds__(1024) void scale_norm(const float *a, const float *b, uint32_t n, float *norm) {
+// The scaled gradients' rows in F16. Bound by memory: gated back 2048 x 28672 x
+// 8192 takes 2.48 ms with it, 2.25 ms in bf16, whose products write 16 bits
+// themselves; product back 2048 x 8192 x 8192 341 us (bf16 320).
+template <bool TWO, int THREADS, int HELD>
+__global__ __launch_bounds__(THREADS) void narrow_rows(Int8Args a) {
     __shared__ uint32_t top[16];
-    scale_norm_block(a, b, n, norm, top);
+    for (uint32_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        narrow_row<TWO, HELD>(a, m, top);
+        __syncthreads();
+    }
+}
+
+template <bool TWO>
+void launch_narrow(const Int8Args &a, hipStream_t s) {
+    const dim3 grid(std::min(a.M, 65535u));
+    const uint64_t quads = a.ldd / 4 * (TWO ? 2 : 1);
+    if (quads <= 2048)
+        narrow_rows<TWO, 256, 8><<<grid, 256, 0, s>>>(a);
+    else
+        narrow_rows<TWO, 1024, 8><<<grid, 1024, 0, s>>>(a);
 }
 
 __global__ __launch_bounds__(kSumThreads) void sum_parts(SumArgs a) { sum_parts_block(a, blockIdx.x); }
 
-// d = dy sw in 16 bits, zeros in columns N..ldd-1: what the backward epilogue
+// d = dy sw in bf16, zeros in columns N..ldd-1: what the backward epilogue
 // writes, for a call that needs no sums of codes. A thread: 4 channels.
 __global__ __launch_bounds__(256) void scale_gradient(Int8Args a) {
     const uint32_t n = 4 * (blockIdx.x * 256 + threadIdx.x);
     if (n >= a.ldd) return;
-    const bool f16 = a.type == ENTQ_F16;
-    const float norm = a.norm ? a.norm[0] : 1.0f;
     float scale[2][4];
     load_scales<kBwd>(a, n, scale);
     for (uint64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
@@ -214,7 +229,7 @@ __global__ __launch_bounds__(256) void scale_gradient(Int8Args a) {
         uint16_t d[4];
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i)
-            d[i] = n + i < a.N ? bits16(from16(b[i], f16) * (scale[0][i] * norm), f16) : 0;
+            d[i] = n + i < a.N ? bits16(from16(b[i], false) * scale[0][i], false) : 0;
         *(uint2 *)(a.d[0] + m * a.ldd + n) = make_uint2(d[0] | (uint32_t)d[1] << 16, d[2] | (uint32_t)d[3] << 16);
     }
 }
@@ -309,9 +324,10 @@ struct Layout {
     uint32_t ldw;
     int32_t *sums;      // the splits' integer sums, or null
     uint16_t *d[2];     // scaled gradients
+    float *wide[2];     // in fp32, or null
+    float *back;        // F16: one for each token
     uint64_t ldd;
     float *part[2];
-    float *norm;
     Int8Plan plan;
     GradPlan grad;
     float *parts;       // partial sums of dX, or null
@@ -339,9 +355,10 @@ Layout lay_out(const Call &c, void *ws) {
     if (c.mode == kBwd || c.mode == kGatedBwd) {
         for (int i = 0; i < c.n_w; ++i) {
             l.d[i] = p.take<uint16_t>(M * l.ldd);
+            if (c.mode == kGatedBwd && c.dy->type == ENTQ_F16) l.wide[i] = p.take<float>(M * l.ldd);
             l.part[i] = p.take<float>((uint64_t)l.plan.part_rows * N);
         }
-        l.norm = p.take<float>(2);
+        if (c.dy->type == ENTQ_F16) l.back = p.take<float>(M);
         l.grad = grad_plan((uint32_t)M, (uint32_t)N, l.ldw, c.n_w);
         if (l.grad.splits > 1) l.parts = p.take<float>((uint64_t)l.grad.splits * M * l.ldw);
     }
@@ -444,13 +461,6 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     Int8Args a;
     if ((st = operands(c, l, a, s)) != ENTQ_OK) return st;
     const bool f16 = c.dy->type == ENTQ_F16;
-    if (f16 && dx) {
-        a.norm = l.norm;
-        if (l.plan.splits > 1 && (c.mode == kGatedBwd || ds0))
-            a.norm_out = l.norm;
-        else
-            scale_norm<<<1, 1024, 0, s>>>(a.sw[0], a.sw[1], N, l.norm);
-    }
     a.act = act;
     a.y = const_cast<void *>(c.dy->d_data);
     a.type = c.dy->type;
@@ -463,16 +473,23 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     sums.n = N;
     for (int i = 0; i < c.n_w; ++i) {
         a.d[i] = dx ? l.d[i] : nullptr;
+        a.wide[i] = dx ? l.wide[i] : nullptr;
         a.part[i] = !ds[i] ? nullptr : direct_sums ? ds[i] : l.part[i];
         sums.part[i] = l.part[i];
         sums.out[i] = ds[i];
     }
     if ((ds0 || ds1) && !direct_sums) sums.rows = l.plan.part_rows;
     int r = ENTQ_OK;
-    if (c.mode == kBwd && !ds0)
-        scale_gradient<<<dim3((uint32_t)(l.ldd / 4 + 255) / 256, std::min(M, 65535u)), 256, 0, s>>>(a);
-    else
+    const bool narrow = f16 && dx;
+    a.back = l.back;
+    a.narrows = narrow && c.mode == kBwd && ds0 && l.plan.splits > 1;
+    if (narrow && c.mode == kBwd && !a.narrows) launch_narrow<false>(a, s);
+    if (c.mode == kBwd && !ds0) {
+        if (!f16) scale_gradient<<<dim3((uint32_t)(l.ldd / 4 + 255) / 256, std::min(M, 65535u)), 256, 0, s>>>(a);
+    } else {
         r = launch_int8_product(c.mode, l.plan, a, s);
+    }
+    if (narrow && c.mode == kGatedBwd && r == ENTQ_OK) launch_narrow<true>(a, s);
     if (r != ENTQ_OK || hipGetLastError() != hipSuccess) return r != ENTQ_OK ? (entq_status)r : ENTQ_EHIP;
     if (!dx) {
         if (sums.rows) sum_parts<<<sum_blocks(sums), kSumThreads, 0, s>>>(sums);
@@ -495,7 +512,7 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
     g.f16 = f16;
     g.dx = dx;
     g.lddx = lddx;
-    g.norm = a.norm;
+    g.back = a.back;
     g.sums = sums;
     return (entq_status)launch_grad_product(l.grad, g, s);
 }

@@ -157,7 +157,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few(Int8Args a) {
 #pragma unroll
         for (int g = 0; g < MT; ++g) sums[wave][t * MT + g][lane] = acc[t][g];
     __syncthreads();
-    const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
     if (wave < MT) {
         const uint32_t g = wave;
         v4i s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
@@ -172,7 +171,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void int8_few(Int8Args a) {
         const uint32_t m = g * 16 + lane % 16;
         const float sx = XT == ENTQ_I8 ? a.sx[min(m, a.M - 1)] : own_scale;
         const uint2 dy4 = kBack ? load_grad4(a, m, n) : make_uint2(0, 0);
-        epilogue4<MODE>(a, sx, scale, norm, m, n, s0, s1, dy4, sg, su);
+        epilogue4<MODE>(a, sx, scale, m, n, s0, s1, dy4, sg, su);
         if constexpr (kBack) {
 #pragma unroll
             for (int t = 0; t < NW; ++t) {

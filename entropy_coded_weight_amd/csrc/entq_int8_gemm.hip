@@ -53,9 +53,9 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t 
     static_assert((!kTwo || FN % 2 == 0) && (SX == SW || SX == SW + 1), "");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
 
-    if (kBack && blockIdx.x >= nb_m * nb_n) {  // a workgroup after the tiles
-        if (blockIdx.y == 0)
-            scale_norm_block(a.sw[0], kTwo ? a.sw[1] : nullptr, a.N, a.norm_out, (uint32_t *)lds);
+    if (MODE == kBwd && blockIdx.x >= nb_m * nb_n) {  // a workgroup after the tiles: one token
+        const uint32_t m = (blockIdx.x - nb_m * nb_n) * a.splits + blockIdx.y;
+        if (m < a.M) narrow_row<false, 4>(a, m, (uint32_t *)lds);
         return;
     }
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -223,7 +223,6 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t 
     read_ahead(0);
     float scale[2][4], sg[4] = {}, su[4] = {};
     load_scales<MODE>(a, n, scale);
-    const float norm = kBack && a.norm && a.splits == 1 ? a.norm[0] : 1.0f;
 #pragma unroll
     for (int i = 0; i < FN * FM; ++i)
         acc[i / FM][i % FM] =
@@ -260,7 +259,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles(Int8Args a, uint32_t 
                     if (kTwo) *(v4i *)part_sums<kTwo>(a, blockIdx.y, 1, m, n) = s1;
                 }
             } else {
-                epilogue4<MODE>(a, sx_at[t], scale, norm, m, n, s0, s1,
+                epilogue4<MODE>(a, sx_at[t], scale, m, n, s0, s1,
                                 kBack ? dy_at[i * 64 + lane] : make_uint2(0, 0), sg, su);
             }
         }
@@ -292,7 +291,6 @@ __global__ __launch_bounds__(256) void int8_finish(Int8Args a) {
     const uint32_t n = blockIdx.x * 256 + lane * 4;
     float scale[2][4], sg[4] = {}, su[4] = {};
     load_scales<MODE>(a, n, scale);
-    const float norm = kBack && a.norm ? a.norm[0] : 1.0f;
     const uint32_t m = blockIdx.y * 4 + wave;
     v4i s[2] = {};
     if (m < a.M && n < a.N) {
@@ -302,7 +300,7 @@ __global__ __launch_bounds__(256) void int8_finish(Int8Args a) {
             if (kTwo) s[1] += *(const v4i *)part_sums<kTwo>(a, k, 1, m, n);
         }
     }
-    epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, norm, m, n, s[0], s[1],
+    epilogue4<MODE>(a, a.sx[min(m, a.M - 1)], scale, m, n, s[0], s[1],
                     kBack ? load_grad4(a, m, n) : make_uint2(0, 0), sg, su);
     if constexpr (kBack) {
 #pragma unroll
@@ -338,7 +336,7 @@ int launch_tiles(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     const uint32_t ch = two ? BN / 2 : BN;
     const uint32_t nb_m = (a.M + BM - 1) / BM, nb_n = (cols + ch - 1) / ch;
     constexpr int kOne = 64 * WM * WN, kLong = 64 * WM * WNB;
-    const uint64_t groups = (uint64_t)nb_m * nb_n + (a.norm_out != nullptr);
+    const uint64_t groups = (uint64_t)nb_m * nb_n + (a.narrows ? (a.M + a.splits - 1) / a.splits : 0);
     if (!launchable(groups * a.splits, kLong)) return ENTQ_EINVAL;
     const dim3 grid((uint32_t)groups, a.splits);
     if (mode == kFwd) int8_tiles<kFwd, BM, BN, WM, WN, SX, SW><<<grid, kOne, 0, s>>>(a, nb_m, nb_n);

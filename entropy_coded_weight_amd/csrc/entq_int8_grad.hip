@@ -200,7 +200,10 @@ __global__ __launch_bounds__(256) void grad_tiles(GradArgs a, uint32_t nb_m, uin
     }
     quarter(1, slot, 0, -1, 0, 0);  // (what it reads is not used)
 
-    const float back = a.norm ? a.norm[1] : 1.0f;
+    float back[FM];
+#pragma unroll
+    for (int g = 0; g < FM; ++g)
+        back[g] = F16 && a.splits == 1 ? a.back[min(m0 + wm * (BM / WM) + g * 32 + lane % 32, a.M - 1)] : 1.0f;
 #pragma unroll
     for (int f = 0; f < FN; ++f)
 #pragma unroll
@@ -217,7 +220,7 @@ __global__ __launch_bounds__(256) void grad_tiles(GradArgs a, uint32_t nb_m, uin
                 }
                 uint16_t b[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) b[i] = bits16(v[i] * back, F16);
+                for (int i = 0; i < 4; ++i) b[i] = bits16(v[i] * back[g], F16);
                 uint16_t *to = (uint16_t *)a.dx + (uint64_t)m * a.lddx + k;
                 if (k + 4 <= a.cols) {
                     ((any8 *)to)->v = v2i{(int)(b[0] | (uint32_t)b[1] << 16), (int)(b[2] | (uint32_t)b[3] << 16)};
@@ -232,10 +235,10 @@ __global__ __launch_bounds__(256) void grad_tiles(GradArgs a, uint32_t nb_m, uin
 
 // dX from the splits' partial sums, added in order.
 __global__ __launch_bounds__(256) void grad_sum(GradArgs a) {
-    const float back = a.norm ? a.norm[1] : 1.0f;
     const uint32_t k = 4 * (blockIdx.x * 256 + threadIdx.x);
     if (k >= a.K) return;
     for (uint64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
+        const float back = a.f16 ? a.back[m] : 1.0f;
         v4f v = {0, 0, 0, 0};
 #pragma unroll 4
         for (uint32_t s = 0; s < a.splits; ++s) v += *(const v4f *)(a.parts + ((uint64_t)s * a.M + m) * a.K + k);

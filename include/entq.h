@@ -672,9 +672,12 @@ entq_status entq_int8_gated(const entq_rows *x, const entq_rows *gate, const ent
  * through:
  *   dx[m][k] = sum_n (dy[m][n] sw[n]) w[n][k]      (dy's type, [M][lddx >= K])
  *   dsw[n] = sum_m dy[m][n] sx[m] sum_k x[m][k] w[n][k]          (fp32, [N])
- * dy sw is rounded to dy's type (F16: after division by a power of two, the
- * same for all n, that keeps it in range) for the 16-bit matrix cores, sums
- * are fp32. x: the codes and scales the forward pass used (ENTQ_I8).
+ * dy sw is rounded to dy's type for the 16-bit matrix cores, sums are fp32.
+ * For F16 a power of two of its own first brings each token's largest |dy sw|
+ * into [2^14, 2^15) and is taken out of the sums: whatever the sizes of dy and sw,
+ * products within 2^-28 of the token's largest keep F16's 11 bits, smaller
+ * ones are rounded to steps of 2^-38 of it, and dx overflows only where it is
+ * itself beyond F16. x: the codes and scales the forward pass used (ENTQ_I8).
  * d_dx or d_dw_scales may be NULL: that gradient is not computed. M = 0
  * leaves dsw = 0; N = 0 leaves dx = 0. N <= 2^22. */
 uint64_t entq_int8_gemm_backward_workspace_bytes(const entq_rows *dy, const entq_rows *x,
@@ -688,7 +691,8 @@ entq_status entq_int8_gemm_backward(const entq_rows *dy, const entq_rows *x, con
  *   dx[m][k] = sum_n (dg[m][n] sg[n]) gate[n][k] + (du[m][n] su[n]) up[n][k]
  *   dsg[n] = sum_m dg[m][n] g[m][n] / sg[n], dsu[n] likewise (without the
  *   division: g / sg is the scaled sum before its channel scale).
- * Rounding, NULL gradients and empty sizes as entq_int8_gemm_backward. */
+ * Rounding (of dg sg and du su, one power of two for both), NULL gradients and
+ * empty sizes as entq_int8_gemm_backward. */
 uint64_t entq_int8_gated_backward_workspace_bytes(const entq_rows *dh, const entq_rows *x,
                                                   const entq_rows *gate, const entq_rows *up);
 entq_status entq_int8_gated_backward(const entq_rows *dh, const entq_rows *x,

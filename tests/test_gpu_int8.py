@@ -354,6 +354,129 @@ def test_f16_gradients_do_not_leave_their_range(I, top):
     assert bool(((got - wx).abs()[fits] <= bx[fits]).all())
 
 
+# tokens and sides that take the few-token kernel, whole and split tiles, and
+# every way in which scaled gradients get into 16 bits
+RANGE = [(1, 1, 1), (3, 70, 33), (40, 300, 1031), (96, 1000, 4112), (300, 520, 256), (1100, 2100, 300)]
+
+
+def _f16_ends(d, scales_of, weights):
+    """dX = sum over t of (d_t s_t) w_t for F16, with a bound that knows no more
+    of a row than the row itself: each d s rounded to 11 bits, or to steps of
+    2^-24 once the token's largest is in [2^14, 2^15), fp32 sums in any order."""
+    n = weights[0].shape[0]
+    ds = [v * R.f64(s) for v, s in zip(d, scales_of)]
+    top = torch.stack([v.abs().amax(1) for v in ds]).amax(0)
+    dx, bound = 0.0, 0.0
+    for v, w in zip(ds, weights):
+        w = R.f64(w)
+        dx = dx + v @ w
+        bound = bound + (v.abs() * (R.ROUND["f16"] + (2 * n + 30) * R.EPS) + 2.0 ** -39 * top[:, None]) @ w.abs()
+    return dx, bound + R.ROUND["f16"] * dx.abs() + R.TINY["f16"]
+
+
+def _f16_product(I, dy, q, sx, w, sw):
+    m, n, k = *dy.shape, q.shape[1]
+    dx, alone = (torch.empty(m, k, dtype=torch.float16, device="cuda") for _ in range(2))
+    ds = torch.empty(n, device="cuda")
+    args = (dy.cuda(), dev(q), dev(sx), dev(w), dev(sw))
+    I.gemm_backward(*args, dx, ds)
+    I.gemm_backward(*args, alone)
+    assert torch.equal(dx, alone)
+    want, bound = _f16_ends([R.f64(dy)], [sw], [w])
+    assert float(want.abs().max()) < 65000
+    _near(dx.cpu(), want, bound, "dx")
+
+
+@pytest.mark.parametrize("m,n,k", RANGE)
+def test_f16_product_gradients_of_any_size(I, m, n, k):
+    """dY up to F16's largest value, tokens of very different size, and a
+    channel whose scale stands far out but which adds nothing to dX."""
+    rng = np.random.default_rng(m + n + k)
+    q, sx, w = codes(rng, m, k), scales(rng, m), codes(rng, n, k)
+    sw = (np.float32(0.0155 / 8 / np.sqrt(n)) * rng.uniform(0.5, 1, n)).astype(np.float32)
+    _say("f16 product, large", m, n, k)
+    dy = torch.from_numpy(rng.choice([-1.0, 1.0], (m, n)) * rng.uniform(40000, 65504, (m, n))).half()
+    _f16_product(I, dy, q, sx, w, sw)
+    _say("f16 product, tokens apart", m, n, k)
+    dy = dy / torch.from_numpy(2.0 ** rng.integers(0, 28, (m, 1))).float()
+    _f16_product(I, dy.half(), q, sx, w, sw)
+    for far in (1e4, 1e8):
+        _say("f16 product, one scale far out", m, n, k, far)
+        dy = torch.from_numpy(rng.standard_normal((m, n)) * 1e-3).half()
+        sw = (0.01 * rng.uniform(0.5, 1, n)).astype(np.float32)
+        sw[n // 2] = far * 0.01
+        dy[:, n // 2] = 0
+        _f16_product(I, dy, q, sx, w, sw)
+        dy[:, n // 2] = 1e-3
+        w[n // 2] = 0
+        if far == 1e4:  # (the row's largest is this channel's: others keep 11 bits to 2^-29 of it)
+            _f16_product(I, dy, q, sx, w, sw)
+
+
+def _f16_gated(I, dh, q, sx, wg, sg, wu, su):
+    """relu, whose values and gradients carry no error of their own."""
+    m, n, k = *dh.shape, q.shape[1]
+    dx, alone = (torch.empty(m, k, dtype=torch.float16, device="cuda") for _ in range(2))
+    a, b = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    args = (dh.cuda(), dev(q), dev(sx), dev(wg), dev(sg), dev(wu), dev(su))
+    I.gated_backward(*args, dx, a, b, "relu")
+    I.gated_backward(*args, alone, activation="relu")
+    assert torch.equal(dx, alone)
+    g0, u0 = R.sums(q, wg) * R.f64(sx)[:, None], R.sums(q, wu) * R.f64(sx)[:, None]
+    h, dh = R.f64(dh), (g0 * R.f64(sg) > 0)
+    dg, du = h * dh * u0 * R.f64(su), h * dh * g0 * R.f64(sg)
+    want, bound = _f16_ends([dg, du], [sg, su], [wg, wu])
+    assert float(want.abs().max()) < 65000
+    _near(dx.cpu(), want, bound, "dx")
+    for got, d, raw in ((a, dg, g0), (b, du, u0)):
+        t = d * raw
+        _near(got.cpu(), t.sum(0), (m + 30) * R.EPS * t.abs().sum(0) + 1e-44, "ds")
+
+
+@pytest.mark.parametrize("m,n,k", RANGE)
+def test_f16_gated_gradients_of_any_size(I, m, n, k):
+    """Gates and up values far beyond F16's range of dh times them, tokens of
+    very different size, gate and up scales of very different size, and a
+    channel far out that adds nothing to dX."""
+    rng = np.random.default_rng(2 * m + n + k)
+    q, wg, wu = codes(rng, m, k), codes(rng, n, k), codes(rng, n, k)
+    near = lambda size: (size * rng.uniform(0.5, 1, n)).astype(np.float32)  # noqa: E731
+    sx = near(1)[:1].repeat(m) * np.float32(8 / (3 * 4 * 3 * 4 * np.sqrt(k)))  # sums times sx around 1
+    dh = torch.from_numpy(64 * rng.standard_normal((m, n))).half()
+    _say("f16 gated, large", m, n, k)
+    # g and u of some 2000, dg and du of some 10^5
+    small = 1e-3 / np.sqrt(n)
+    _f16_gated(I, dh, q, sx * np.float32(2000 / small), wg, near(small), wu, near(small))
+    _say("f16 gated, tokens apart", m, n, k)
+    rows = (2.0 ** -rng.integers(0, 20, m)).astype(np.float32)
+    _f16_gated(I, dh, q, sx * np.float32(2000 / small) * rows, wg, near(small), wu, near(small))
+    _say("f16 gated, up far below gate", m, n, k)
+    _f16_gated(I, dh / 6.4e6, q, sx, wg, near(1e3), wu, near(1e-3))
+    _f16_gated(I, dh / 6.4e6, q, sx, wg, near(1e-3), wu, near(1e3))
+    _say("f16 gated, one scale far out", m, n, k)
+    sg, su = near(1e-2), near(1e-2)
+    sg[n // 2] = su[n - 1] = 1e6
+    dh[:, n // 2] = dh[:, n - 1] = 0
+    _f16_gated(I, dh / 64, q, sx, wg, sg, wu, su)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [3, 40, 300])
+def test_an_infinite_gradient_gives_infinities(I, m, kind):
+    """One infinity in dY: dX of that token is an infinity of the code's sign,
+    NaN where the code is 0, and no other token sees it."""
+    rng = np.random.default_rng(m)
+    n, k = 200, 96
+    q, sx, w, sw = codes(rng, m, k), scales(rng, m), codes(rng, n, k), np.abs(scales(rng, n))
+    dy = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32)).to(TYPES[kind])
+    dy[1, 7] = float("inf")
+    dx = torch.empty(m, k, dtype=TYPES[kind], device="cuda")
+    I.gemm_backward(dy.cuda(), dev(q), dev(sx), dev(w), dev(sw), dx, torch.empty(n, device="cuda"))
+    want = np.where(w[7] > 0, np.inf, np.where(w[7] < 0, -np.inf, np.nan))
+    assert np.array_equal(host(dx)[1], want, equal_nan=True)
+    assert np.isfinite(np.delete(host(dx), 1, axis=0)).all()
+
+
 # products that take every tile size, whole and with the sum split, each with
 # sides that end inside a tile; 64-bit references on the GPU
 LARGE = [(1100, 8200, 272), (520, 2001, 4096), (700, 16390, 1040), (256, 8192, 28672), (1000, 5000, 4000),
