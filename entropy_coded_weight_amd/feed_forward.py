@@ -13,6 +13,7 @@ of x and of every row scale; the codes are constants.
 from __future__ import annotations
 
 import contextlib
+import weakref
 
 import torch
 
@@ -29,11 +30,46 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+class _Memory:
+    """Orders the use of memory that was allocated on the stream ``home`` with
+    what home's allocator does with it before and after: work on another
+    stream starts after what home had queued when it was allocated, and home
+    waits for the last such work when the memory goes back to it. (Events, not
+    record_stream: a caller's raw stream may be gone by then.)"""
+
+    def __init__(self, owner, home):
+        self.home, self.ends = home, {}
+        self.begin = home.record_event()
+        weakref.finalize(owner, self.give_back, home, self.ends).atexit = False
+
+    @staticmethod
+    def give_back(home, ends):
+        for end in ends.values():
+            home.wait_event(end)
+
+    @contextlib.contextmanager
+    def on(self, stream):
+        if stream == self.home or torch.cuda.is_current_stream_capturing():
+            # (a capture cannot wait for events from outside it; torch.cuda.graph
+            # starts one after all work queued before has ended)
+            yield
+            return
+        stream.wait_event(self.begin)
+        try:
+            yield
+        finally:
+            self.ends.setdefault(stream.cuda_stream, torch.cuda.Event()).record(stream)
+
+
 class FeedForward:
     """p: the plan of gate [F, D], up [F, D] and down [E, F]; scales: device
     float32 with the plan's row scales. ``decode`` fills the code buffer, which
     ``forward`` and ``backward`` then use; a caller that walks over layers gives
-    several blocks one buffer (``codes``: device int8, at least out_elems)."""
+    several blocks one buffer (``codes``: device int8, at least out_elems).
+    Every call may run on a stream of its own. The caller orders them (a decode
+    before the products that use it); a buffer that the block allocated itself
+    needs no further care, but a block that a graph captured has to outlive
+    the graph."""
 
     def __init__(self, p: Plan, scales, activation="silu", codes=None):
         t = p.tensors
@@ -47,8 +83,11 @@ class FeedForward:
             raise EntqError(EINVAL, f"activation {activation!r}: one of "
                                     f"{', '.join(int8.ACTIVATIONS)}")
         _device_buffer(p, "scales", scales, p.scale_rows, dtypes=(torch.float32,))
+        self._memory = None
         if codes is None:
             codes = torch.empty(p.out_elems, dtype=torch.int8, device=p.device)
+            if not torch.cuda.is_current_stream_capturing():
+                self._memory = _Memory(self, torch.cuda.current_stream(p.device))
         _device_buffer(p, "codes", codes, p.out_elems, dtypes=(torch.int8,))
         self.plan, self.scales, self.activation, self.codes = p, scales, activation, codes
         self.hidden = f
@@ -60,14 +99,25 @@ class FeedForward:
             self._at.append(slice(s, s + rows))
             self._w += [codes[o:o + rows * cols].view(rows, cols), scales[s:s + rows]]
 
+    @contextlib.contextmanager
+    def _using_codes(self, stream):
+        """Makes ``stream`` the current one for work on the code buffer."""
+        with _on(stream, self.plan.device):
+            if self._memory is None:
+                yield
+            else:
+                with self._memory.on(torch.cuda.current_stream(self.plan.device)):
+                    yield
+
     def decode(self, compressed, chunk_status=None, stream=None):
         """Enqueue the decode of the block's codes."""
-        decode(self.plan, compressed, self.codes, OUT_CODES, None, chunk_status, stream)
+        with self._using_codes(stream):
+            decode(self.plan, compressed, self.codes, OUT_CODES, None, chunk_status)
 
     def forward(self, x, y, stream=None):
         """y = block(x): x bfloat16, float16 or float32 [m, D], y of any of
         these types [m, E]. The hidden values between have x's type."""
-        with _on(stream, self.plan.device):
+        with self._using_codes(stream):
             h = torch.empty(x.shape[0], self.hidden, dtype=x.dtype, device=x.device)
             int8.gated(x, None, *self._w[:4], h, self.activation)
             int8.gemm(h, None, *self._w[4:], y)
@@ -81,7 +131,7 @@ class FeedForward:
         if dscales is not None:
             _device_buffer(self.plan, "dscales", dscales, self.plan.scale_rows,
                            dtypes=(torch.float32,))
-        with _on(stream, self.plan.device):
+        with self._using_codes(stream):
             m = x.shape[0]
             new = lambda n, t: torch.empty(m, n, dtype=t, device=x.device)  # noqa: E731
             q, h, qh = new(x.shape[1], torch.int8), new(self.hidden, x.dtype), new(self.hidden, torch.int8)

@@ -78,6 +78,83 @@ def test_block_is_its_operators(E, m, kind):
     assert torch.equal(y2, y) and torch.equal(dx3, dx) and torch.equal(ds3, ds)
 
 
+def test_own_buffer_on_other_streams(E):
+    """The block's own code buffer, used on a stream that is not the one it was
+    allocated on, without a synchronisation by the caller: the decode waits
+    for what still reads that memory, and a block that is dropped keeps it
+    until its last product has run."""
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    f, d, e, m = 352, 256, 192, 40
+    p, blob, scales, _ = _block(E, f, d, e)
+    torch.manual_seed(7)
+    x, dy = torch.randn(m, d, device="cuda").bfloat16(), torch.randn(m, e, device="cuda").bfloat16()
+    outs = lambda: (torch.empty(m, e, device="cuda"), torch.empty_like(x), torch.empty_like(scales))  # noqa: E731
+    block, want = FeedForward(p, scales), outs()
+    block.decode(blob)
+    block.forward(x, want[0])
+    block.backward(dy, x, *want[1:])
+    side = torch.cuda.Stream()
+    a = torch.randn(4096, 4096, device="cuda").bfloat16()
+    b = torch.empty_like(a)
+    got, again = outs(), outs()
+
+    def busy():  # some milliseconds of the current stream
+        for _ in range(40):
+            torch.mm(a, a, out=b)
+
+    old = torch.full((p.out_elems,), 7, dtype=torch.int8, device="cuda")
+    kept = torch.empty_like(old)
+    del block
+    torch.cuda.synchronize()
+    busy()
+    kept.copy_(old)
+    del old  # its memory goes to the next allocation of this stream
+    block = FeedForward(p, scales)
+    block.decode(blob, stream=side)
+    block.forward(x, got[0], side)
+    block.backward(dy, x, *got[1:], side)
+    with torch.cuda.stream(side):
+        busy()
+    block.forward(x, again[0], side)
+    block.backward(dy, x, *again[1:], side.cuda_stream)
+    del block
+    junk = [torch.full((p.out_elems,), 99, dtype=torch.int8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert (kept == 7).all() and all((j == 99).all() for j in junk)
+    for t in (got, again):
+        assert all(torch.equal(u, v) for u, v in zip(t, want))
+
+
+def test_block_in_a_graph(E):
+    """Decode and both passes captured, replayed between eager calls."""
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    f, d, e, m = 352, 256, 192, 40
+    p, blob, scales, _ = _block(E, f, d, e)
+    block = FeedForward(p, scales)
+    x, dy = torch.zeros(m, d, device="cuda").half(), torch.zeros(m, e, device="cuda").half()
+    outs = lambda: (torch.empty(m, e, device="cuda"), torch.empty_like(x), torch.empty_like(scales))  # noqa: E731
+
+    def step(y, dx, ds):
+        block.decode(blob)
+        block.forward(x, y)
+        block.backward(dy, x, dx, ds)
+
+    got = outs()
+    step(*got)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(*got)
+    for i in range(4):
+        x.copy_(torch.randn(m, d, device="cuda"))
+        dy.copy_(torch.randn(m, e, device="cuda"))
+        g.replay()
+        want = outs()
+        step(*want)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(got, want)), i
+
+
 def test_block_near_the_real_numbers(E):
     """Codes are off by half a step at most: x by sx / 2 and h by sh / 2 in each
     element, which bounds what y may differ from the block in 64 bits."""
