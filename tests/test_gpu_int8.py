@@ -241,6 +241,35 @@ def test_gated_far_activations(I):
         _near(h, want, err + R.EPS * want.abs() + 1e-37, name)
 
 
+@pytest.mark.parametrize("m", [1, 40, 200])
+def test_gelu_relative_to_itself(I, m):
+    """gelu and its derivative keep their relative accuracy where the gate is
+    far below 0. g is exact here (a product of 1 and a scale). fp32 roundings:
+    exp's argument three (1.5 g^2 EPS), exp and the reciprocal 1 ulp, the
+    polynomial 17 EPS with what the reciprocal's error makes of it, three
+    products: (24 + 1.5 g^2) EPS of the tail Q(|g|)."""
+    rng = np.random.default_rng(m)
+    v = np.concatenate([np.linspace(-12, 6, 4001), rng.uniform(-6, 1, 3000), [-1e-30, 0.0, 1e-30]]).astype(np.float32)
+    n = len(v)
+    one = np.ones((n, 1), np.int8)
+    q, sx, ones = np.ones((m, 1), np.int8), np.ones(m, np.float32), np.ones(n, np.float32)
+    h = torch.empty(m, n, device="cuda")
+    I.gated(dev(q), dev(sx), dev(one), dev(v), dev(one), dev(ones), h, "gelu")
+    g = R.f64(v)
+    tail = 0.5 * torch.erfc(g.abs() / np.sqrt(2))
+    rel = (24 + 1.5 * g * g) * R.EPS * tail
+    want = R.act("gelu", v)[0]
+    _near(h.cpu(), want.expand(m, n), (g.abs() * rel + 3 * R.EPS * want.abs()).expand(m, n), "gelu")
+    # dh = 1, u = 1: the gate scale's gradient is the sum over m of act'(g)
+    ds = torch.empty(n, device="cuda")
+    I.gated_backward(torch.ones(m, n, device="cuda").half(), dev(q), dev(sx), dev(one), dev(v), dev(one), dev(ones),
+                     None, ds, None, "gelu")
+    phi = g.abs() * torch.exp(-g * g / 2) / np.sqrt(2 * np.pi)
+    want = R.act("gelu", v)[1]
+    bound = rel + phi * (6 + 1.5 * g * g) * R.EPS + (m + 8) * R.EPS * want.abs()
+    _near(ds.cpu(), m * want, m * bound, "gelu'")
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 40, 64), (70, 130, 200), (20, 64, 128)])
 def test_rows_with_nan_or_infinity_stay_alone(I, m, n, k):
     rng = np.random.default_rng(m)
