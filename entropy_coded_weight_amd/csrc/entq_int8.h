@@ -173,7 +173,9 @@ __device__ __forceinline__ void activate4(int act, const float (&x)[4], float (&
             const float v = x[i], z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
             const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z2));
             r[i] = v * p;
-            if (GRAD) grad[i] = p + v * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * v * v);
+            // (far out p (1 - p) is 0, where v^2 may be beyond fp32)
+            const float w = __builtin_amdgcn_fmed3f(v, -64.0f, 64.0f);
+            if (GRAD) grad[i] = p + w * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * w * w);
         }
     } else {
 #pragma unroll

@@ -345,6 +345,31 @@ def test_gated_backward(I, m, n, k, kind):
         assert torch.equal(dx2, dx[:m]) and torch.equal(g2, dsg) and torch.equal(u2, dsu)
 
 
+@pytest.mark.parametrize("m", [3, 70, 600])
+@pytest.mark.parametrize("name", ACTS)
+def test_far_gates_backward(I, m, name):
+    """Gates so far out that act' is 0 or 1 to the last bit and g^2 is beyond
+    fp32 (or exactly 0): the gradients are finite and right."""
+    rng = np.random.default_rng(m)
+    n, k = 130, 64
+    q, wg, wu = codes(rng, m, k), codes(rng, n, k), codes(rng, n, k)
+    sx, sg, su = np.full(m, 0.01, np.float32), np.full(n, 1e25, np.float32), np.abs(scales(rng, n)) * np.float32(1e-20)
+    sg[::3] = 1e21
+    g0, u0 = R.sums(q, wg) * R.f64(sx)[:, None], R.sums(q, wu) * R.f64(sx)[:, None]
+    g, u = g0 * R.f64(sg), u0 * R.f64(su)
+    dh = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32)).bfloat16()
+    dx = torch.empty(m, k, dtype=torch.bfloat16, device="cuda")
+    a, b = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    I.gated_backward(dh.cuda(), dev(q), dev(sx), dev(wg), dev(sg), dev(wu), dev(su), dx, a, b, name)
+    act, grad = R.act(name, g)
+    dg, du = R.f64(dh) * u * grad, R.f64(dh) * act
+    want, bound = R._dx([dg, du], [0 * dg, 0 * du], [R.f64(sg), R.f64(su)], [wg, wu], "bf16")
+    _near(dx.cpu(), want, bound + R.EPS * 20 * want.abs(), "dx")
+    for got, d, raw in ((a, dg, g0), (b, du, u0)):
+        t = d * raw
+        _near(got.cpu(), t.sum(0), (m + 30) * R.EPS * t.abs().sum(0) + 1e-44, "ds")
+
+
 @pytest.mark.parametrize("off,gap", [(1, 0), (2, 3), (16, 16)])
 @pytest.mark.parametrize("m,k", [(3, 64), (150, 201)])
 def test_backward_strides(I, m, k, off, gap):
