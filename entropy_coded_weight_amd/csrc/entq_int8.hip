@@ -234,8 +234,8 @@ __global__ __launch_bounds__(256) void scale_gradient(Int8Args a) {
     }
 }
 
-__global__ __launch_bounds__(256) void fill_zero(uint8_t *p, uint64_t ld, uint32_t bytes) {
-    for (uint32_t c = blockIdx.x * 256 + threadIdx.x; c < bytes; c += gridDim.x * 256)
+__global__ __launch_bounds__(256) void fill_zero(uint8_t *p, uint64_t ld, uint64_t bytes) {
+    for (uint64_t c = blockIdx.x * 256 + threadIdx.x; c < bytes; c += gridDim.x * 256)
         p[blockIdx.y * ld + c] = 0;
 }
 
@@ -370,11 +370,11 @@ uint64_t workspace_bytes_of(const Call &c) { return c.bad == ENTQ_OK ? lay_out(c
 
 entq_status zero_rows(void *p, int type, uint64_t ld, uint32_t rows, uint32_t cols, hipStream_t s) {
     if (!p || !rows || !cols) return ENTQ_OK;
-    const uint32_t b = type_bytes(type);
+    const uint64_t b = type_bytes(type), bytes = cols * b;
     for (uint32_t r = 0; r < rows; r += 65535) {
         const uint32_t n = std::min(rows - r, 65535u);
-        fill_zero<<<dim3(std::min(64u, cols * b / 256 + 1), n), 256, 0, s>>>((uint8_t *)p + (uint64_t)r * ld * b,
-                                                                             ld * b, cols * b);
+        const dim3 grid((uint32_t)std::min<uint64_t>(rows > 64 ? 64 : 4096, bytes / 256 + 1), n);
+        fill_zero<<<grid, 256, 0, s>>>((uint8_t *)p + r * ld * b, ld * b, bytes);
     }
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }

@@ -203,6 +203,17 @@ def test_empty_sizes(I):
         assert (dx == 0).all() and (a == 0).all() and (b == 0).all()
 
 
+def test_many_channels_of_no_columns(I):
+    """K = 0 with so many fp32 channels that a row has 2^32 bytes and more:
+    every result is 0."""
+    n = (1 << 30) + 5
+    w, sw = torch.empty(n, 0, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+    x, sx = torch.empty(1, 0, dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
+    y = torch.full((1, n), 3.0, device="cuda")
+    I.gemm(x, sx, w, sw, y)
+    assert float(y.abs().max()) == 0.0
+
+
 def _near(got, want, bound, what):
     got = got.detach().to(want.device).double()
     off = (got - want).abs() - bound
