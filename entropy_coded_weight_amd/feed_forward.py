@@ -79,6 +79,8 @@ class FeedForward:
         if (f, d) != (f2, d2) or f3 != f:
             raise EntqError(EINVAL, f"gate {f} x {d}, up {f2} x {d2}, down {e} x {f3}: gate and "
                                     "up have one shape, down a column for each of their rows")
+        if max(d, f) > int8.MAX_COLS:
+            raise EntqError(EINVAL, f"{max(d, f)} columns, at most {int8.MAX_COLS} are taken")
         if activation not in int8.ACTIVATIONS:
             raise EntqError(EINVAL, f"activation {activation!r}: one of "
                                     f"{', '.join(int8.ACTIVATIONS)}")
@@ -90,7 +92,7 @@ class FeedForward:
                 self._memory = _Memory(self, torch.cuda.current_stream(p.device))
         _device_buffer(p, "codes", codes, p.out_elems, dtypes=(torch.int8,))
         self.plan, self.scales, self.activation, self.codes = p, scales, activation, codes
-        self.hidden = f
+        self.width, self.hidden, self.out = d, f, e
         self._w = []  # code matrix and its scales
         self._at = []  # where a tensor's scales are
         for r in t:
@@ -117,8 +119,11 @@ class FeedForward:
     def forward(self, x, y, stream=None):
         """y = block(x): x bfloat16, float16 or float32 [m, D], y of any of
         these types [m, E]. The hidden values between have x's type."""
+        index = self.plan.device.index
+        m = int8._check_activations("x", x, index, self.width)
+        int8._check_result("y", y, index, m, self.out)
         with self._using_codes(stream):
-            h = torch.empty(x.shape[0], self.hidden, dtype=x.dtype, device=x.device)
+            h = torch.empty(m, self.hidden, dtype=x.dtype, device=x.device)
             int8.gated(x, None, *self._w[:4], h, self.activation)
             int8.gemm(h, None, *self._w[4:], y)
 
@@ -126,15 +131,19 @@ class FeedForward:
         """Gradients for dy = dL/dy (bfloat16 or float16 [m, E], x's type):
         dx (that type, [m, D]) and dscales (float32 [scale_rows], the plan's
         order); None: not computed. The forward pass is done again from x."""
+        index = self.plan.device.index
+        m = int8._check_activations("x", x, index, self.width, (int8._BF16, int8._F16))
+        int8._grad_rows("dy", dy, index, m, self.out)
         if x.dtype != dy.dtype:
             raise EntqError(EINVAL, f"dy has dtype {dy.dtype}, x {x.dtype}")
+        if dx is not None:
+            int8._matrix("dx", dx, index, (int8._TYPES[x.dtype],), (m, self.width))
         if dscales is not None:
             _device_buffer(self.plan, "dscales", dscales, self.plan.scale_rows,
                            dtypes=(torch.float32,))
         with self._using_codes(stream):
-            m = x.shape[0]
             new = lambda n, t: torch.empty(m, n, dtype=t, device=x.device)  # noqa: E731
-            q, h, qh = new(x.shape[1], torch.int8), new(self.hidden, x.dtype), new(self.hidden, torch.int8)
+            q, h, qh = new(self.width, torch.int8), new(self.hidden, x.dtype), new(self.hidden, torch.int8)
             sx, sh = (torch.empty(m, dtype=torch.float32, device=x.device) for _ in range(2))
             dh = new(self.hidden, dy.dtype)
             int8.quantize_rows(x, q, sx)

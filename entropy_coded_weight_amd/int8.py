@@ -79,6 +79,22 @@ def _x_rows(x, x_scales, index, types=(_BF16, _F16, _F32, _I8)):
     return Rows(x.data_ptr(), ld, s, m, k, kind, 0)
 
 
+def _check_activations(name, x, index, columns, types=(_BF16, _F16, _F32)):
+    """Activations of one of ``types`` for weights of that many columns: what a
+    call that runs several products checks before the first. Returns their
+    number of tokens."""
+    _matrix(name, x, index, types)
+    if x.shape[1] != columns:
+        raise EntqError(EINVAL, f"{name} has {x.shape[1]} columns, the weights have {columns}")
+    if columns > MAX_COLS:
+        raise EntqError(EINVAL, f"{name} has {columns} columns, at most {MAX_COLS} are taken")
+    return x.shape[0]
+
+
+def _check_result(name, y, index, rows, n):
+    _matrix(name, y, index, (_BF16, _F16, _F32), (rows, n))
+
+
 def _w_rows(name, w, scales, index, columns, shape=None):
     _, ld = _matrix(name, w, index, (_I8,), shape)
     n, k = w.shape

@@ -84,6 +84,11 @@ def linear_int8(p: Plan, compressed, scales, xs, ys, codes=None, chunk_status=No
     if np.any((p.tensors["kind"] & 0xFF) != KIND_INT8):
         raise EntqError(EINVAL, "linear_int8 takes Int8 tensors")
     _device_buffer(p, "scales", scales, p.scale_rows, dtypes=(torch.float32,))
+    if codes is not None:
+        _device_buffer(p, "codes", codes, p.out_elems, dtypes=(torch.int8,))
+    for t, r in enumerate(p.tensors):
+        m = int8._check_activations(f"x[{t}]", xs[t], p.device.index, int(r["cols"]))
+        int8._check_result(f"y[{t}]", ys[t], p.device.index, m, int(r["rows"]))
     with _on(stream, p.device):
         if codes is None:
             codes = torch.empty(p.out_elems, dtype=torch.int8, device=p.device)

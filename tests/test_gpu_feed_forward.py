@@ -214,3 +214,38 @@ def test_refusals(E):
         with pytest.raises(E.EntqError) as ei:
             f()
         assert ei.value.status == E.EINVAL
+
+
+def test_bad_arguments_are_refused_before_any_work(E, monkeypatch):
+    """A call that refuses one of its arguments has started nothing."""
+    from entropy_coded_weight_amd import feed_forward, int8, linear
+    f, d, e = 96, 64, 32
+    p, blob, scales, _ = _block(E, f, d, e)
+    block = feed_forward.FeedForward(p, scales)
+    started = []
+    for module, name in ((int8, "_enqueue"), (feed_forward, "decode"), (linear, "decode")):
+        monkeypatch.setattr(module, name, lambda *a, **k: started.append(a))
+    new = lambda *s, t=torch.float32: torch.zeros(s, device="cuda").to(t)  # noqa: E731
+    bf = torch.bfloat16
+    x, y, dy = new(2, d, t=bf), new(2, e), new(2, e, t=bf)
+    xs, ys = [new(2, d, t=bf), new(2, d, t=bf), new(2, f, t=bf)], [new(2, f), new(2, f), new(2, e)]
+    lin = lambda xs=xs, ys=ys, **k: linear.linear_int8(p, blob, scales, xs, ys, **k)  # noqa: E731
+    bad = [lambda: block.forward(x, y[:, :-1]), lambda: block.forward(x, y[:1]), lambda: block.forward(x, y.double()),
+           lambda: block.forward(x, y.cpu()), lambda: block.forward(None, y), lambda: block.forward(x, None),
+           lambda: block.forward(x[0], y), lambda: block.forward(x[:, :-1], y), lambda: block.forward(x.char(), y),
+           lambda: block.backward(dy.float(), x.float()), lambda: block.backward(dy[:, :-1], x),
+           lambda: block.backward(dy, x[:1]), lambda: block.backward(dy, x, x[:1]), lambda: block.backward(dy, x, x.half()),
+           lambda: block.backward(None, x), lambda: block.backward(dy, None), lambda: block.backward(dy.half(), x),
+           lambda: block.backward(dy, x, None, new(3)),
+           lambda: lin(ys=ys[:2] + [new(2, e - 1)]), lambda: lin(ys=ys[:2] + [new(3, e)]),
+           lambda: lin(ys=ys[:2] + [ys[2].char()]), lambda: lin(ys=ys[:2] + [None]), lambda: lin(xs=xs[:2] + [xs[2].cpu()]),
+           lambda: lin(xs=xs[:2] + [xs[2][:, :-1]]), lambda: lin(xs=xs[:2] + [xs[2].char()]),
+           lambda: lin(codes=new(p.out_elems, t=torch.uint8)), lambda: lin(codes=new(p.out_elems - 1, t=torch.int8))]
+    for i, call in enumerate(bad):
+        with pytest.raises(E.EntqError) as ei:
+            call()
+        assert ei.value.status == E.EINVAL and not started, i
+    lin()
+    block.forward(x, y)
+    block.backward(dy, x, torch.empty_like(x), torch.empty_like(scales))
+    assert len(started) == 4 + 2 + 5
