@@ -95,6 +95,7 @@ class FeedForward:
         self.width, self.hidden, self.out = d, f, e
         self._w = []  # code matrix and its scales
         self._at = []  # where a tensor's scales are
+        codes, scales = codes.view(-1), scales.view(-1)
         for r in t:
             rows, cols = int(r["rows"]), int(r["cols"])
             o, s = int(r["out_elem_offset"]), int(r["scale_row_offset"])
@@ -149,6 +150,6 @@ class FeedForward:
             int8.quantize_rows(x, q, sx)
             int8.gated(q, sx, *self._w[:4], h, self.activation)
             int8.quantize_rows(h, qh, sh)
-            dg, du, dd = (dscales[s] if dscales is not None else None for s in self._at)
+            dg, du, dd = (dscales.view(-1)[s] if dscales is not None else None for s in self._at)
             int8.gemm_backward(dy, qh, sh, *self._w[4:], dh, dd)
             int8.gated_backward(dh, q, sx, *self._w[:4], dx, dg, du, self.activation)

@@ -93,6 +93,7 @@ def linear_int8(p: Plan, compressed, scales, xs, ys, codes=None, chunk_status=No
         if codes is None:
             codes = torch.empty(p.out_elems, dtype=torch.int8, device=p.device)
         decode(p, compressed, codes, OUT_CODES, None, chunk_status)
+        codes, scales = codes.view(-1), scales.view(-1)
         for t, r in enumerate(p.tensors):
             rows, cols = int(r["rows"]), int(r["cols"])
             o, s = int(r["out_elem_offset"]), int(r["scale_row_offset"])

@@ -249,3 +249,34 @@ def test_bad_arguments_are_refused_before_any_work(E, monkeypatch):
     block.forward(x, y)
     block.backward(dy, x, torch.empty_like(x), torch.empty_like(scales))
     assert len(started) == 4 + 2 + 5
+
+
+def test_buffers_of_any_shape(E):
+    """Code and scale buffers are taken by their elements, whatever their shape."""
+    from entropy_coded_weight_amd import int8
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    from entropy_coded_weight_amd.linear import linear_int8
+    f, d, e = 96, 64, 32
+    p, blob, scales, ws = _block(E, f, d, e)
+    codes = torch.empty(p.out_elems // 32, 32, dtype=torch.int8, device="cuda")
+    x, y, want = torch.randn(3, d, device="cuda").bfloat16(), torch.empty(3, e, device="cuda"), torch.empty(3, e, device="cuda")
+    plain = FeedForward(p, scales)
+    plain.decode(blob)
+    plain.forward(x, want)
+    block = FeedForward(p, scales.view(-1, 2), codes=codes)
+    block.decode(blob)
+    block.forward(x, y)
+    assert torch.equal(y, want)
+    dy = torch.randn(3, e, device="cuda").bfloat16()
+    a, b = torch.zeros(p.scale_rows, device="cuda"), torch.zeros(p.scale_rows // 2, 2, device="cuda")
+    plain.backward(dy, x, None, a)
+    block.backward(dy, x, None, b)
+    assert torch.equal(a, b.view(-1)) and bool((a != 0).any())
+    xs = [x, x, torch.randn(3, f, device="cuda").bfloat16()]
+    for c in (None, codes):
+        ys = [torch.empty(3, n, device="cuda") for n in (f, f, e)]
+        linear_int8(p, blob, scales.view(2, -1), xs, ys, codes=c)
+        for t in range(3):
+            want = torch.empty_like(ys[t])
+            int8.gemm(xs[t], None, ws[2 * t], ws[2 * t + 1], want)
+            assert torch.equal(ys[t], want)
