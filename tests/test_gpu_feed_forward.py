@@ -194,6 +194,54 @@ def test_linear_int8(E, m):
         assert torch.equal(ys[t], want)
 
 
+def _specs(f, d, e):
+    specs = [synth.random_int8_tensor(r, c, 2.0, 60 + i, c * 2) for i, (r, c) in enumerate(((f, d), (f, d), (e, f)))]
+    for sp in specs:
+        sp["scales"] = (np.asarray(sp["scales"], np.float32) / np.abs(sp["scales"]).max() * 0.02).astype(np.float32)
+    return specs
+
+
+@pytest.mark.parametrize("layout,f,d,e", [("tiles", 352, 256, 192), ("tables", 512, 256, 48), ("rows", 351, 253, 191)])
+def test_plans_of_every_layout(E, layout, f, d, e):
+    """The block and linear_int8 on plans in tile order, with a table per chunk,
+    and with matrices that start and end anywhere: the operators on the source
+    codes, bit for bit."""
+    from entropy_coded_weight_amd import int8
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    from entropy_coded_weight_amd.linear import linear_int8
+    specs = _specs(f, d, e)
+    if layout == "tiles":
+        b = E.encode_batch([dict(sp, symbols=E.tile_order(sp["symbols"], sp["rows"], sp["cols"], 32),
+                                 chunk_symbols=16 * 32, kind=sp["kind"] | E.LAYOUT_TILES) for sp in specs])
+        p = E.plan(b.tensors, b.freq, b.chunks, b.blob.size)
+    else:
+        specs = [dict(sp, chunk_symbols=4096) for sp in specs]
+        b = E.encode_batch_adaptive(specs) if layout == "tables" else E.encode_batch(specs)
+        p = E.plan(b.tensors, b.freq, b.chunks, b.blob.size)
+    blob, scales = torch.from_numpy(b.blob).cuda(), torch.from_numpy(np.concatenate([sp["scales"] for sp in specs])).cuda()
+    ws = []
+    for sp in specs:
+        ws += [torch.from_numpy(np.asarray(sp["symbols"]).view(np.int8).reshape(sp["rows"], sp["cols"])).cuda(),
+               torch.from_numpy(sp["scales"]).cuda()]
+    torch.manual_seed(2)
+    for m in (1, 40):
+        x, y, want = torch.randn(m, d, device="cuda").half(), torch.empty(m, e, device="cuda"), torch.empty(m, e, device="cuda")
+        block = FeedForward(p, scales, "gelu_tanh")
+        block.decode(blob)
+        block.forward(x, y)
+        h = torch.empty(m, f, dtype=x.dtype, device="cuda")
+        int8.gated(x, None, *ws[:4], h, "gelu_tanh")
+        int8.gemm(h, None, *ws[4:], want)
+        assert torch.equal(y, want)
+        xs = [x, x, h]
+        ys = [torch.empty(m, n, device="cuda") for n in (f, f, e)]
+        linear_int8(p, blob, scales, xs, ys)
+        for t in range(3):
+            want = torch.empty_like(ys[t])
+            int8.gemm(xs[t], None, ws[2 * t], ws[2 * t + 1], want)
+            assert torch.equal(ys[t], want)
+
+
 def test_refusals(E):
     from entropy_coded_weight_amd.feed_forward import FeedForward
     from entropy_coded_weight_amd.linear import linear_int8

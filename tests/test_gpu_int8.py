@@ -306,6 +306,75 @@ def test_rows_with_nan_or_infinity_stay_alone(I, m, n, k):
         assert not nan[0].any() and not nan[2:].any() and nan[1].any()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,k", [(33, 1), (40, 127), (70, 1031), (50, 8192), (41, 8225), (20, 32768), (20, 32769),
+                                 (16384, 96), (16385, 96)])
+def test_one_token_of_activations(I, n, k, kind):
+    """One token that the call quantises itself, in the product's kernel or
+    before it: the plain product bit for bit, the gated one within its bound."""
+    rng = np.random.default_rng(n + k)
+    wg, sg, wu, su = codes(rng, n, k), scales(rng, n), codes(rng, n, k), scales(rng, n)
+    _say("one token", n, k, kind)
+    for off in (0, 1):
+        x = torch.from_numpy(rng.standard_normal((1, k)).astype(np.float32)).to(TYPES[kind])
+        q, sx = R.quantize(x.float().numpy())
+        size = np.float32(50 / np.sqrt(k))
+        xd = strided(x, k + off, off)
+        w, w2 = strided(wg, k + off, off), strided(wu, k + 2 * off, 3 * off)
+        y = torch.full((2, n), 9.0, device="cuda")
+        I.gemm(xd, None, w, dev(sg), y[:1])
+        assert np.array_equal(y[:1].cpu().numpy(), _product(q, sx, wg, sg))
+        for i, name in enumerate(ACTS):
+            out = ("f32", "bf16", "f16", "f32")[i]
+            h = torch.full((2, n), 9.0, dtype=TYPES[out], device="cuda")
+            I.gated(xd, None, w, dev(sg * size), w2, dev(su), h[:1], name)
+            want, err = R.gated(q, sx, wg, sg * size, wu, su, name)
+            _near(h[:1].cpu(), want, err + R.ROUND[out] * want.abs() + R.TINY[out], name)
+            assert (h[1] == 9.0).all()
+        assert (y[1] == 9.0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+def test_one_bad_token(I, kind, bad):
+    rng = np.random.default_rng(1)
+    n, k = 90, 1500
+    x = torch.from_numpy(rng.standard_normal((1, k)).astype(np.float32)).to(TYPES[kind])
+    x[0, 777] = float(bad)
+    w, sw = dev(codes(rng, n, k)), dev(scales(rng, n))
+    y, h = torch.empty(1, n, device="cuda"), torch.empty(1, n, device="cuda")
+    I.gemm(x.cuda(), None, w, sw, y)
+    I.gated(x.cuda(), None, w, sw, w, sw, h, "gelu")
+    assert torch.isnan(y).all() and torch.isnan(h).all()
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gemm_of_f16_activations_bit_for_bit(I, m, n, k):
+    rng = np.random.default_rng(m + 7 * n + 31 * k)
+    w, sw = codes(rng, n, k, full=True), scales(rng, n)
+    x = torch.from_numpy(rng.standard_normal((m, k)).astype(np.float32)).half()
+    q, sx = R.quantize(x.float().numpy())
+    y = torch.empty(m, n, device="cuda")
+    I.gemm(x.cuda(), None, dev(w), dev(sw), y)
+    assert np.array_equal(y.cpu().numpy(), _product(q, sx, w, sw))
+
+
+@pytest.mark.parametrize("m", [2, 40, 130])
+def test_gated_of_activations(I, m):
+    """Several tokens of activations against their codes, every type."""
+    rng = np.random.default_rng(m)
+    n, k = 150, 333
+    wg, sg, wu, su = codes(rng, n, k), scales(rng, n), codes(rng, n, k), scales(rng, n)
+    for kind in TYPES:
+        x = torch.from_numpy(rng.standard_normal((m, k)).astype(np.float32)).to(TYPES[kind])
+        q, sx = R.quantize(x.float().numpy())
+        for name in ACTS:
+            h = torch.empty(m, n, device="cuda")
+            I.gated(x.cuda(), None, dev(wg), dev(sg), dev(wu), dev(su), h, name)
+            want, err = R.gated(q, sx, wg, sg, wu, su, name)
+            _near(h.cpu(), want, err + R.EPS * want.abs() + R.TINY["f32"], (kind, name))
+
+
 BACK = [(1, 1, 1), (2, 70, 16), (17, 64, 65), (64, 130, 128), (65, 63, 200), (130, 257, 96), (257, 128, 272),
         (40, 300, 1031), (300, 520, 256), (1, 1000, 512), (600, 33, 33), (16, 1024, 48)]
 
