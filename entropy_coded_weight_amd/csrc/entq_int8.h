@@ -339,10 +339,11 @@ struct GradArgs {
 // with two workgroups on a CU (256-token tiles fill one), `tile` for a tile's
 // end, the weights' bytes at `bytes_us`, and for a split sum a second launch
 // that adds partial results. The constants are fitted to times measured on
-// MI355X over 214 shapes (1 .. 2,048 tokens, sides 512 .. 32,000) with every
-// tile and 1 .. 24 splits, as graphs of launches; `second` has 2 us more for
-// what a second launch costs outside a graph. The choice is on average about
-// 1 % slower than the best variant of each shape.
+// MI355X (1 .. 2,048 tokens, sides 512 .. 32,000) with every tile and 1 .. 24
+// splits, as graphs of launches; `second` has 2 us more for what a second
+// launch costs outside a graph. Over 284 shapes measured afterwards the choice
+// is on average 1.2 % slower than the best variant of each shape, more than
+// 10 % for 9 of them, 30 % at most.
 struct TileCost {
     uint32_t tokens, width; // of a tile; width: weight rows, or columns of dX
     float step[2], tile;
@@ -465,7 +466,7 @@ inline bool launchable(uint64_t groups, uint32_t threads) { return groups && gro
 // Launchers; each returns an entq_status (ENTQ_EINVAL for more workgroups
 // than one launch holds). Rows of x and w must start at
 // multiples of 16 bytes, strides below 2^23, K be a multiple of 16.
-bool few_quantizes(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K);
+bool few_quantizes(uint32_t M, uint32_t K);
 int launch_int8_few(Int8Mode mode, const Int8Args &a, hipStream_t s);
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s);
 

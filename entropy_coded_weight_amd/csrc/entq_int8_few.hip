@@ -207,13 +207,12 @@ int launch_few(Int8Mode mode, const Int8Args &a, hipStream_t s) {
 }  // namespace
 
 // One token, whose codes fit a share of the LDS. Measured against a launch of
-// the quantiser before (bf16, us): product 8192 x 8192 16.5 / 17.3, 1024 x
-// 1024 4.2 / 5.2, gated 28672 x 8192 85.3 / 89.0. For the product of 28672 x
-// 8192 it does not pay (50.3 / 47.9: more workgroups, each with half the
-// weights of a gated one), nor for several tokens (4: 21.3 / 18.7).
-bool few_quantizes(Int8Mode mode, uint32_t M, uint32_t N, uint32_t K) {
-    return M == 1 && K <= 32768 && (mode == kGated || N <= 16384);
-}
+// the quantiser before over sides of 512 .. 32,000 x 1,024 .. 32,768 (bf16,
+// us): product 1024 x 1024 3.9 / 5.1, 8192 x 8192 17.1 / 18.0, 28672 x 8192
+// 44.6 / 46.8, gated 28672 x 8192 84.1 / 86.2; it loses at most 4 %, where
+// there are many channels of many columns (28672 x 32768 189 / 182). For several
+// tokens it does not pay (4: 21.3 / 18.7).
+bool few_quantizes(uint32_t M, uint32_t K) { return M == 1 && K <= 32768; }
 
 int launch_int8_few(Int8Mode mode, const Int8Args &a, hipStream_t s) {
     if (a.x_type == ENTQ_BF16) return launch_few<1, ENTQ_BF16>(mode, a, s);

@@ -374,16 +374,17 @@ Int8Plan int8_plan(Int8Mode mode, int x_type, uint32_t M, uint32_t N, uint32_t K
     if (M <= 64) {
         // The few-token kernel: limited by a wave's turns over K, all the more
         // the more groups of tokens it has, or by the weights' bytes. (At 1 and
-        // 4 tokens it was the fastest, or within 2 %, for every shape; at 16 it
-        // is faster where the latency counts, 1024 x 1024 4.3 us against 6.9,
-        // and slower where the bytes do, 32000 x 8192 66 us against 52.)
+        // 4 tokens it was the fastest, or within 6 %, for 13 of 14 shapes, but
+        // 512 x 16384 takes 13.6 us where 16 splits take 10.4; at 16 it is
+        // faster where the latency counts, 1024 x 1024 4.2 us against 7.0,
+        // and slower where the bytes do, 32000 x 8192 66 us against 53.)
         const uint32_t groups = M <= 16 ? 1 : M <= 32 ? 2 : 4;
         const float rounds = 1 + 0.87f * ((n_w * N + 4095) / 4096 - 1);  // of workgroups on a CU
         const float turns = (K + 1023) / 1024 * (0.60f + 0.40f * groups) * rounds;
         const float memory = n_w * N * (float)K * (1 / 5.4e6f + 2.5e-8f * groups);
         p.few = M <= 4 || 3.4f + std::max(turns, memory) < t.us;
         if (p.few) {
-            p.quantizes = x_type != ENTQ_I8 && few_quantizes(mode, M, N, K);
+            p.quantizes = x_type != ENTQ_I8 && few_quantizes(M, K);
             p.splits = 1;
             p.part_rows = groups;
             return p;
