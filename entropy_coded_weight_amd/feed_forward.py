@@ -66,12 +66,16 @@ class FeedForward:
     float32 with the plan's row scales. ``decode`` fills the code buffer, which
     ``forward`` and ``backward`` then use; a caller that walks over layers gives
     several blocks one buffer (``codes``: device int8, at least out_elems).
+    hidden_type: the type of the hidden values between the products, which are
+    quantised again at once; None: x's type. In float16 a hidden value beyond
+    65,504 is an infinity, which makes its token NaN; torch.float32 has
+    neither that limit nor a rounding before the quantiser's.
     Every call may run on a stream of its own. The caller orders them (a decode
     before the products that use it); a buffer that the block allocated itself
     needs no further care, but a block that a graph captured has to outlive
     the graph."""
 
-    def __init__(self, p: Plan, scales, activation="silu", codes=None):
+    def __init__(self, p: Plan, scales, activation="silu", codes=None, hidden_type=None):
         t = p.tensors
         if p.n_tensors != 3 or any(int(k) & 0xFF != KIND_INT8 for k in t["kind"]):
             raise EntqError(EINVAL, "a feed-forward block is three Int8 tensors: gate, up, down")
@@ -84,6 +88,8 @@ class FeedForward:
         if activation not in int8.ACTIVATIONS:
             raise EntqError(EINVAL, f"activation {activation!r}: one of "
                                     f"{', '.join(int8.ACTIVATIONS)}")
+        if hidden_type not in (None, torch.bfloat16, torch.float16, torch.float32):
+            raise EntqError(EINVAL, f"hidden values of type {hidden_type}")
         _device_buffer(p, "scales", scales, p.scale_rows, dtypes=(torch.float32,))
         self._memory = None
         if codes is None:
@@ -93,6 +99,7 @@ class FeedForward:
         _device_buffer(p, "codes", codes, p.out_elems, dtypes=(torch.int8,))
         self.plan, self.scales, self.activation, self.codes = p, scales, activation, codes
         self.width, self.hidden, self.out = d, f, e
+        self.hidden_type = hidden_type
         self._w = []  # code matrix and its scales
         self._at = []  # where a tensor's scales are
         codes, scales = codes.view(-1), scales.view(-1)
@@ -119,12 +126,12 @@ class FeedForward:
 
     def forward(self, x, y, stream=None):
         """y = block(x): x bfloat16, float16 or float32 [m, D], y of any of
-        these types [m, E]. The hidden values between have x's type."""
+        these types [m, E]."""
         index = self.plan.device.index
         m = int8._check_activations("x", x, index, self.width)
         int8._check_result("y", y, index, m, self.out)
         with self._using_codes(stream):
-            h = torch.empty(m, self.hidden, dtype=x.dtype, device=x.device)
+            h = torch.empty(m, self.hidden, dtype=self.hidden_type or x.dtype, device=x.device)
             int8.gated(x, None, *self._w[:4], h, self.activation)
             int8.gemm(h, None, *self._w[4:], y)
 
@@ -144,7 +151,8 @@ class FeedForward:
                            dtypes=(torch.float32,))
         with self._using_codes(stream):
             new = lambda n, t: torch.empty(m, n, dtype=t, device=x.device)  # noqa: E731
-            q, h, qh = new(self.width, torch.int8), new(self.hidden, x.dtype), new(self.hidden, torch.int8)
+            h = new(self.hidden, self.hidden_type or x.dtype)
+            q, qh = new(self.width, torch.int8), new(self.hidden, torch.int8)
             sx, sh = (torch.empty(m, dtype=torch.float32, device=x.device) for _ in range(2))
             dh = new(self.hidden, dy.dtype)
             int8.quantize_rows(x, q, sx)

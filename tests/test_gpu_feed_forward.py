@@ -179,6 +179,45 @@ def test_block_near_the_real_numbers(E):
     assert bool(((y.double() - h @ wd.T).abs() <= bound).all())
 
 
+def test_hidden_values_beyond_float16(E):
+    """float16 activations whose hidden values are not float16 numbers: a NaN
+    token as stated, or with hidden_type the operators' results on fp32
+    hidden values, finite and within the quantiser's step of the block in 64 bits."""
+    from entropy_coded_weight_amd import int8
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    f, d, e, m = 352, 256, 192, 20
+    p, blob, scales, ws = _block(E, f, d, e)
+    torch.manual_seed(3)
+    x, dy = (4000 * torch.randn(m, d, device="cuda")).half(), torch.randn(m, e, device="cuda").half()
+    x[0] /= 4000
+    q, sx = torch.empty(m, d, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    int8.quantize_rows(x, q, sx)
+    h, want = torch.empty(m, f, device="cuda"), torch.empty(m, e, device="cuda")
+    int8.gated(q, sx, *ws[:4], h, "relu")
+    assert float(h.abs().amax(1)[1:].min()) > 70000 and float(h[0].abs().max()) < 60000
+    qh, sh = torch.empty(m, f, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    int8.quantize_rows(h, qh, sh)
+    int8.gemm(qh, sh, *ws[4:], want)
+    y, narrow = torch.empty_like(want), torch.empty_like(want)
+    block, plain = FeedForward(p, scales, "relu", hidden_type=torch.float32), FeedForward(p, scales, "relu")
+    block.decode(blob)
+    plain.decode(blob)
+    block.forward(x, y)
+    plain.forward(x, narrow)
+    assert torch.equal(y, want) and torch.isfinite(narrow[0]).all() and torch.isnan(narrow[1:]).all()
+    wd = ws[4].double() * ws[5].double()[:, None]
+    bound = (0.5 * (1 + 1e-5) * h.double().abs().amax(1, keepdim=True) / 127).expand_as(h) @ wd.abs().T
+    assert bool(((y.double() - h.double() @ wd.T).abs() <= bound).all())
+    dx, ds, dh, dx2 = torch.empty_like(x), torch.empty_like(scales), torch.empty(m, f, device="cuda").half(), torch.empty_like(x)
+    block.backward(dy, x, dx, ds)
+    g, u, dn = (torch.empty(n, device="cuda") for n in (f, f, e))
+    int8.gemm_backward(dy, qh, sh, *ws[4:], dh, dn)
+    int8.gated_backward(dh, q, sx, *ws[:4], dx2, g, u, "relu")
+    assert torch.equal(dx, dx2) and torch.equal(ds, torch.cat([g, u, dn])) and torch.isfinite(ds).all()
+    with pytest.raises(E.EntqError):
+        FeedForward(p, scales, hidden_type=torch.float64)
+
+
 @pytest.mark.parametrize("m", [1, 90])
 def test_linear_int8(E, m):
     from entropy_coded_weight_amd import int8
