@@ -8,7 +8,9 @@ They are decoded to codes right before the block uses them [EntQuant,
 Inferencia"] and multiplied as codes: activations are quantised to int8 per
 row, both first products and the activation are one kernel, and its result is
 quantised again for the last product. The backward pass gives the gradients
-of x and of every row scale; the codes are constants.
+of x and of every row scale; the codes are constants. Neither records an
+autograd graph, and an x or dy that would need one is refused: a
+torch.autograd.Function calls ``forward`` and ``backward`` for it.
 """
 from __future__ import annotations
 

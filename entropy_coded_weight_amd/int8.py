@@ -11,6 +11,12 @@ Results go to tensors of the caller. ``stream`` is a torch stream, a raw
 stream handle or None for the current stream; ``workspace`` a device uint8
 tensor of at least ``workspace_bytes(...)`` bytes, or None to allocate one
 for the call.
+
+The calls record no autograd graph. Activations and incoming gradients that
+require a gradient are refused while gradients are enabled, since the graph
+would end there unnoticed: a torch.autograd.Function around the forward and
+the backward call connects them (inside it gradients are disabled). Scales may
+be parameters; their gradients are what the backward calls write.
 """
 from __future__ import annotations
 
@@ -50,6 +56,13 @@ def _matrix(name, t, index, types, shape=None):
     return kind, ld
 
 
+def _no_graph(name, t):
+    if t.requires_grad and torch.is_grad_enabled():
+        raise EntqError(EINVAL, f"{name} requires a gradient, which this call does not record: call "
+                                "it from a torch.autograd.Function, under torch.no_grad() or "
+                                f"with {name}.detach()")
+
+
 def _vector(name, t, index, n):
     if not isinstance(t, torch.Tensor) or t.get_device() != index:
         raise EntqError(EINVAL, f"{name}: a torch tensor on cuda:{index} is required")
@@ -67,6 +80,7 @@ def _gpu(name, t):
 
 def _x_rows(x, x_scales, index, types=(_BF16, _F16, _F32, _I8)):
     kind, ld = _matrix("x", x, index, types)
+    _no_graph("x", x)
     m, k = x.shape
     if k > MAX_COLS:
         raise EntqError(EINVAL, f"x has {k} columns, at most {MAX_COLS} are taken")
@@ -84,6 +98,7 @@ def _check_activations(name, x, index, columns, types=(_BF16, _F16, _F32)):
     call that runs several products checks before the first. Returns their
     number of tokens."""
     _matrix(name, x, index, types)
+    _no_graph(name, x)
     if x.shape[1] != columns:
         raise EntqError(EINVAL, f"{name} has {x.shape[1]} columns, the weights have {columns}")
     if columns > MAX_COLS:
@@ -105,6 +120,7 @@ def _w_rows(name, w, scales, index, columns, shape=None):
 
 def _grad_rows(name, t, index, rows, n):
     kind, ld = _matrix(name, t, index, (_BF16, _F16), (rows, n))
+    _no_graph(name, t)
     return Rows(t.data_ptr(), ld, 0, rows, n, kind, 0)
 
 

@@ -367,3 +367,52 @@ def test_buffers_of_any_shape(E):
             want = torch.empty_like(ys[t])
             int8.gemm(xs[t], None, ws[2 * t], ws[2 * t + 1], want)
             assert torch.equal(ys[t], want)
+
+
+def test_autograd(E):
+    """Activations that need a graph are refused, and a function around the two
+    calls gives their gradients, the scales' among them."""
+    from entropy_coded_weight_amd import int8, linear
+    from entropy_coded_weight_amd.feed_forward import FeedForward
+    f, d, e, m = 96, 64, 32, 5
+    p, blob, scales, ws = _block(E, f, d, e)
+    scales.requires_grad_(True)
+    block = FeedForward(p, scales, "silu")
+    block.decode(blob)
+
+    class Block(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, scales):
+            ctx.save_for_backward(x)
+            y = torch.empty(m, e, dtype=x.dtype, device="cuda")
+            block.forward(x, y)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            dx, ds = torch.empty_like(ctx.saved_tensors[0]), torch.empty_like(scales)
+            block.backward(dy.contiguous(), ctx.saved_tensors[0], dx, ds)
+            return dx, ds
+
+    torch.manual_seed(1)
+    x = torch.randn(m, d, device="cuda").bfloat16().requires_grad_(True)
+    dy = torch.randn(m, e, device="cuda").bfloat16()
+    Block.apply(x, scales).backward(dy)
+    dx, ds = torch.empty_like(x), torch.empty_like(scales)
+    block.backward(dy, x.detach(), dx, ds)
+    assert torch.equal(x.grad, dx) and torch.equal(scales.grad, ds) and bool((ds != 0).any())
+
+    y, h = torch.empty(m, e, device="cuda"), torch.empty(m, f, device="cuda")
+    q, sx = torch.empty(m, d, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    dh = torch.zeros(m, f, device="cuda").half().requires_grad_(True)
+    calls = [lambda: block.forward(x, y), lambda: block.backward(dy, x), lambda: int8.quantize_rows(x, q, sx),
+             lambda: int8.gemm(x, None, *ws[:2], h), lambda: int8.gated(x, None, *ws[:4], h),
+             lambda: int8.gemm_backward(dh, q, sx, *ws[:2]), lambda: int8.gated_backward(dh, q, sx, *ws[:4]),
+             lambda: linear.linear_int8(p, blob, scales, [x, x, h.bfloat16()], [h, h.clone(), y])]
+    for call in calls:
+        with pytest.raises(E.EntqError, match="requires a gradient") as ei:
+            call()
+        assert ei.value.status == E.EINVAL
+    with torch.no_grad():
+        for call in calls:
+            call()
