@@ -34,8 +34,9 @@ __device__ __forceinline__ v2i widen4(int codes) {
 // S steps are kept in LDS. The weights stay int8 until they are in registers:
 // a transposing LDS read gives a lane 8 consecutive channels of its column,
 // which it widens to 16 bits (12 vector instructions per 8 codes, beside the
-// products of the fragments before). The waves divide the columns, not the
-// tokens, so that each code is widened once a workgroup.
+// products of the fragments before). In the 256 x 256 kind the waves divide the
+// columns, not the tokens, so that each code is widened once a workgroup; in
+// the smaller kinds, 2 x 2 waves, it is widened twice.
 //
 // What bounds it: at 2048 x 28672 x 8192 (two weights, 1.92 TFLOP) it takes
 // 1.40 to 1.44 ms, 1.35 PFLOP/s (the library's bf16 product of 8192 a side

@@ -706,7 +706,8 @@ entq_status entq_int8_gated_backward(const entq_rows *dh, const entq_rows *x,
  * matrices (else ENTQ_EWORKSPACE; 0 means NULL is fine, or invalid
  * arguments), not used by other work while the call runs. It holds quantised
  * activations, 16-byte aligned copies of matrices whose rows are not, partial
- * sums, and in a backward call the scaled gradients. */
+ * sums, and in a backward call the scaled gradients (of F16, gated: in fp32
+ * too). */
 
 #ifdef __cplusplus
 }

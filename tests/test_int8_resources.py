@@ -29,3 +29,12 @@ def test_no_spills_and_the_intended_residency(source, kernel, count):
         if kernel != "int8_few" and lds <= 80 * 1024:  # two workgroups of 4 waves on a CU
             assert vgprs <= 256, m.group(1)
     assert seen == count
+
+
+def test_the_small_kernels_do_not_spill():
+    from entropy_coded_weight_amd import build
+    with tempfile.TemporaryDirectory() as d:
+        txt = open(build.asm(os.path.join(d, "k.s"), "entq_int8.hip")).read()
+    kernels = re.findall(r"\.amdhsa_kernel (\S+)", txt)
+    assert sum("narrow_rows" in k for k in kernels) == 4 and sum("quantize_rows" in k for k in kernels) == 12
+    assert [int(n) for n in re.findall(r"ScratchSize: (\d+)", txt)] == [0] * len(kernels)
