@@ -13,8 +13,8 @@ namespace entq {
 // What a kernel computes from acc_w[m][n] = sum_k x[m][k] w[n][k]:
 //   kFwd       y = acc sx sw                       (one weight)
 //   kGated     y = act(g) u                        (two weights)
-//   kBwd       sums over m of dy acc sx, and dy sw in 16 bits
-//   kGatedBwd  the same for dg and du              (two weights)
+//   kBwd       sums over m of dy acc sx, and dy sw in bf16 (F16's: narrow_row)
+//   kGatedBwd  the same for dg and du              (two weights; in fp32 for F16)
 enum Int8Mode { kFwd = 0, kGated = 1, kBwd = 2, kGatedBwd = 3 };
 
 struct Int8Args {

@@ -664,6 +664,27 @@ def test_large_backward(I, m, n, k, kind):
     assert (dx[m] == 7).all() and (dx[:, k:] == 7).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(3, 40000, 64), (3, 20000, 64), (100, 5121, 4112), (70000, 5, 16)])
+def test_f16_rows_of_every_length(I, m, n, k):
+    """Rows longer than what a workgroup keeps of them in registers, beside
+    split tiles too, and more tokens than a launch has workgroups for."""
+    _say("f16 rows", m, n, k)
+    q, sx, wg, sg, wu, su = _large(m, n, k, m + n, 2)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    dh = (torch.randn(m, n, device="cuda", generator=g) * 0.1).half()
+    new = lambda *s: torch.full(s, 7.0, device="cuda")  # noqa: E731
+    dx, ds = new(m + 1, k + 3).half(), new(n)
+    I.gemm_backward(dh, q, sx, wg, sg, dx[:m, :k], ds)
+    for got, (want, bound), what in zip((dx[:m, :k], ds), R.gemm_backward(dh, q, sx, wg, sg, "f16"), ("dx", "ds")):
+        _near(got, want, bound, what)
+    dx, dsg, dsu = new(m + 1, k + 3).half(), new(n), new(n)
+    I.gated_backward(dh, q, sx, wg, sg, wu, su, dx[:m, :k], dsg, dsu, "silu")
+    for got, (want, bound), what in zip((dx[:m, :k], dsg, dsu),
+                                        R.gated_backward(dh, q, sx, wg, sg, wu, su, "silu", "f16"), ("dx", "dsg", "dsu")):
+        _near(got, want, bound, what)
+    assert (dx[m] == 7).all() and (dx[:, k:] == 7).all()
+
+
 def test_other_stream_given_workspace_and_repeats(I):
     """A stream of the caller, a workspace of the caller with other work's
     leftovers in it, and the same bits on every call."""
