@@ -21,6 +21,8 @@ Entry points (the C ABI in include/entq.h, same names):
   int8 (module)                       products of quantised activations with
                                       decoded Int8 codes, the gated
                                       feed-forward kernel, their gradients
+  norm (module)                       norms before and after a block, with its
+                                      gate and residual scale, their gradients
 """
 from __future__ import annotations
 
@@ -69,6 +71,16 @@ class Rows(ctypes.Structure):
                 ("reserved", ctypes.c_uint32)]
 
 
+class Norm(ctypes.Structure):
+    """entq_norm (include/entq.h): device pointers as integers"""
+    _fields_ = [("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("type", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32), ("x", ctypes.c_void_p), ("branch", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ldx", ctypes.c_uint64), ("ldbranch", ctypes.c_uint64),
+                ("ldgate", ctypes.c_uint64), ("post", ctypes.c_void_p), ("pre", ctypes.c_void_p),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_uint32)]
+
+
 class EntqError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -88,7 +100,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         c = ctypes
         vp, u64, i64 = c.c_void_p, c.c_uint64, c.c_int64
-        rows = c.POINTER(Rows)
+        rows, norm = c.POINTER(Rows), c.POINTER(Norm)
         sigs = {
             "entq_plan_workspace_bytes": (c.c_size_t, [c.c_int, i64]),
             "entq_plan": (c.c_int, [vp, c.c_int, vp, vp, i64, u64, vp, c.c_size_t, vp,
@@ -147,6 +159,10 @@ def lib():
             "entq_int8_gated_backward_workspace_bytes": (u64, [rows, rows, rows, rows]),
             "entq_int8_gated_backward": (c.c_int, [rows, rows, rows, rows, c.c_int, vp, u64, vp,
                                                    vp, vp, u64, vp]),
+            "entq_norm_block": (c.c_int, [norm, vp, u64, vp, c.c_int, u64, vp, vp]),
+            "entq_norm_block_backward_workspace_bytes": (u64, [norm]),
+            "entq_norm_block_backward": (c.c_int, [norm, vp, u64, vp, u64, vp, u64, vp, u64, vp,
+                                                   u64, vp, vp, vp, u64, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -173,7 +189,9 @@ EXPORTED = ["entq_plan_workspace_bytes", "entq_plan", "entq_decode", "entq_decod
             "entq_tile_order_device", "entq_quantize_rows", "entq_int8_gemm_workspace_bytes",
             "entq_int8_gemm", "entq_int8_gated_workspace_bytes", "entq_int8_gated",
             "entq_int8_gemm_backward_workspace_bytes", "entq_int8_gemm_backward",
-            "entq_int8_gated_backward_workspace_bytes", "entq_int8_gated_backward"]
+            "entq_int8_gated_backward_workspace_bytes", "entq_int8_gated_backward",
+            "entq_norm_block", "entq_norm_block_backward_workspace_bytes",
+            "entq_norm_block_backward"]
 
 
 def _str(status: int) -> str:

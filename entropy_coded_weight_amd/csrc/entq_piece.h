@@ -1,0 +1,92 @@
+// entq_piece.h -- rows of activations in pieces of 16 bytes, and sums over a
+// workgroup, as the norms and the distillation loss use them.
+#pragma once
+
+#include "entq_int8.h"
+
+namespace entq {
+
+// Values of a 16-byte piece.
+template <int TYPE>
+constexpr int kPer = TYPE == ENTQ_F32 ? 4 : 8;
+
+// Piece p of a row of n values at any address, zeros past its end.
+template <int TYPE>
+__device__ __forceinline__ v4i load_piece(const void *row, uint32_t p, uint32_t n) {
+    const uint32_t c = p * kPer<TYPE>;
+    if (c + kPer<TYPE> <= n) return ((const any16 *)((const uint8_t *)row + (uint64_t)p * 16))->v;
+    v4i v = {0, 0, 0, 0};
+    if (c >= n) return v;
+#pragma unroll
+    for (int i = 0; i < kPer<TYPE> - 1; ++i) {
+        if (c + i >= n) continue;
+        if (TYPE == ENTQ_F32)
+            v[i] = ((const int *)row)[c + i];
+        else
+            v[i / 2] |= (int)((uint32_t)((const uint16_t *)row)[c + i] << (16 * (i % 2)));
+    }
+    return v;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void store_piece(void *row, uint32_t p, uint32_t n, v4i v) {
+    const uint32_t c = p * kPer<TYPE>;
+    if (c + kPer<TYPE> <= n) {
+        ((any16 *)((uint8_t *)row + (uint64_t)p * 16))->v = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer<TYPE> - 1; ++i) {
+        if (c + i >= n) continue;
+        if (TYPE == ENTQ_F32)
+            ((int *)row)[c + i] = v[i];
+        else
+            ((uint16_t *)row)[c + i] = (uint16_t)((uint32_t)v[i / 2] >> (16 * (i % 2)));
+    }
+}
+
+// The values rounded to the type, as a piece.
+template <int TYPE>
+__device__ __forceinline__ v4i pack(const float (&f)[kPer<TYPE>]) {
+    v4i v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (TYPE == ENTQ_F32)
+            v[i] = __float_as_int(f[i]);
+        else
+            v[i] = (int)(bits16(f[2 * i], TYPE == ENTQ_F16) | (uint32_t)bits16(f[2 * i + 1], TYPE == ENTQ_F16) << 16);
+    }
+    return v;
+}
+
+// Values c.. of a vector of n fp32 values for piece p, zeros past its end.
+template <int TYPE>
+__device__ __forceinline__ void load_floats(const float *w, uint32_t p, uint32_t n, float (&f)[kPer<TYPE>]) {
+    const uint32_t c = p * kPer<TYPE>;
+    if (c + kPer<TYPE> <= n) {
+#pragma unroll
+        for (int h = 0; h < kPer<TYPE> / 4; ++h) {
+            const v4i v = ((const any16 *)(w + c + 4 * h))->v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[4 * h + i] = __int_as_float(v[i]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer<TYPE>; ++i) f[i] = c + i < n ? w[c + i] : 0.0f;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int o = 32; o; o /= 2) v += __shfl_xor(v, o);
+    return v;
+}
+
+// 1 / sqrt(v) of a positive 64-bit value, rounded to fp32 (0 for an infinity):
+// the hardware's estimate and one step of Newton's method.
+__device__ __forceinline__ float rsqrt64(double v) {
+    const double r = __builtin_amdgcn_rsq(v);
+    return (float)(v < __builtin_inf() ? r * (1.5 - 0.5 * v * r * r) : r);
+}
+
+}  // namespace entq

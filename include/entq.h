@@ -709,6 +709,68 @@ entq_status entq_int8_gated_backward(const entq_rows *dh, const entq_rows *x,
  * sums, and in a backward call the scaled gradients (of F16, gated: in fp32
  * too). */
 
+/* ---- Norms around a block ----
+ *
+ * What stands between two blocks of a transformer. Row by row (a row is a
+ * token), with rho(v) = 1 / sqrt(mean_c v[c]^2 + eps):
+ *   state = alpha x + beta gate v,   v = branch rho(branch) post   (branch without d_post)
+ *   y     = state rho(state) pre
+ * branch is the block's output and x the residual; without a branch the state
+ * is x itself. state is rounded to the type before its norm is taken, so y is
+ * what a later call makes of the stored state. Row sums are in 64 bits: no
+ * square overflows, rho is that of the exact sum to fp32's last bit, and an
+ * infinity in a row gives rho 0 (itself a NaN, the other values 0). */
+
+typedef enum {
+    ENTQ_GATE_NONE = 0,      /* 1                                               */
+    ENTQ_GATE_CHANNEL = 1,   /* fp32 [cols]                                     */
+    ENTQ_GATE_TOKEN = 2,     /* fp32, element r at index r ldgate (ldgate >= 1) */
+    ENTQ_GATE_FULL = 3       /* the matrices' type, [rows][ldgate >= cols]      */
+} entq_gate;
+
+/* Matrices are row-major in device memory, of `type` (ENTQ_BF16, F16 or F32),
+ * any row stride >= cols (in elements) and any alignment of the element's
+ * size. d_branch, d_post, d_gate and d_pre may be NULL (post and gate belong
+ * to a branch). cols <= ENTQ_INT8_MAX_COLS; eps > 0. */
+typedef struct {
+    uint32_t rows, cols;
+    int32_t type;            /* entq_eltype */
+    int32_t gate;            /* entq_gate */
+    const void *d_x, *d_branch, *d_gate;
+    uint64_t ldx, ldbranch, ldgate;
+    const float *d_post, *d_pre;   /* [cols] */
+    float alpha, beta, eps;
+    uint32_t reserved;       /* 0 */
+} entq_norm;
+
+/* d_out: the state ([rows][ldout], the type; with a branch only, and then
+ * required; it may be d_x itself with the same stride, and overlaps no other
+ * argument). d_y: the norm of the state, or NULL; y_type is the type, or
+ * ENTQ_I8: then d_y holds int8 codes and d_y_scales [rows] their scales, as
+ * entq_int8_gemm and entq_int8_gated take them:
+ *   t = fl(state pre), c = max(fl(max |t| fl(1/127)), 2^-100),
+ *   code = rint(fl(t fl(1 / c))) clamped to +-127, scale = c rho(state)
+ * (rho is one factor of a whole row: the codes do not depend on it). A row
+ * whose t holds a NaN or an infinity gets the scale NaN and codes 0. */
+entq_status entq_norm_block(const entq_norm *n, void *d_out, uint64_t ldout, void *d_y, int y_type,
+                            uint64_t ldy, float *d_y_scales, void *stream);
+
+/* Gradients of entq_norm_block for d_dout = dL/dstate and d_dy = dL/dy (the
+ * type; either may be NULL, not both; of codes: their quantiser is passed
+ * straight through). n as in the forward call, but d_x is the state, as the
+ * forward call stored it (x itself without a branch). d_dx and d_dbranch (the
+ * type), d_dgate (CHANNEL: fp32 [cols]; TOKEN: fp32 at r lddgate; FULL: the
+ * type, [rows][lddgate]), d_dpre and d_dpost (fp32 [cols]) may each be NULL:
+ * not computed. Sums over channels are in 64 bits, sums over tokens fp32 over
+ * strips of tokens, then 64 bits, in a fixed order. No overlap of results with
+ * anything. rows = 0 leaves the sums over tokens 0. */
+uint64_t entq_norm_block_backward_workspace_bytes(const entq_norm *n);
+entq_status entq_norm_block_backward(const entq_norm *n, const void *d_dout, uint64_t lddout,
+                                     const void *d_dy, uint64_t lddy, void *d_dx, uint64_t lddx,
+                                     void *d_dbranch, uint64_t lddbranch, void *d_dgate,
+                                     uint64_t lddgate, float *d_dpre, float *d_dpost,
+                                     void *d_workspace, uint64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
