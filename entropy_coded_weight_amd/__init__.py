@@ -23,6 +23,8 @@ Entry points (the C ABI in include/entq.h, same names):
                                       feed-forward kernel, their gradients
   norm (module)                       norms before and after a block, with its
                                       gate and residual scale, their gradients
+  distill (module)                    the loss of a student's logits against a
+                                      teacher's top logits, its gradient
 """
 from __future__ import annotations
 
@@ -81,6 +83,18 @@ class Norm(ctypes.Structure):
                 ("reserved", ctypes.c_uint32)]
 
 
+class Distill(ctypes.Structure):
+    """entq_distill (include/entq.h): device pointers as integers"""
+    _fields_ = [("rows", ctypes.c_uint32), ("classes", ctypes.c_uint32), ("top", ctypes.c_uint32),
+                ("type", ctypes.c_int32), ("teacher_type", ctypes.c_int32),
+                ("index_bytes", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("reserved", ctypes.c_uint32), ("logits", ctypes.c_void_p),
+                ("index", ctypes.c_void_p), ("teacher", ctypes.c_void_p),
+                ("ldlogits", ctypes.c_uint64), ("ldindex", ctypes.c_uint64),
+                ("ldteacher", ctypes.c_uint64), ("lse", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p)]
+
+
 class EntqError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -101,6 +115,7 @@ def lib():
         c = ctypes
         vp, u64, i64 = c.c_void_p, c.c_uint64, c.c_int64
         rows, norm = c.POINTER(Rows), c.POINTER(Norm)
+        distill = c.POINTER(Distill)
         sigs = {
             "entq_plan_workspace_bytes": (c.c_size_t, [c.c_int, i64]),
             "entq_plan": (c.c_int, [vp, c.c_int, vp, vp, i64, u64, vp, c.c_size_t, vp,
@@ -163,6 +178,8 @@ def lib():
             "entq_norm_block_backward_workspace_bytes": (u64, [norm]),
             "entq_norm_block_backward": (c.c_int, [norm, vp, u64, vp, u64, vp, u64, vp, u64, vp,
                                                    u64, vp, vp, vp, u64, vp]),
+            "entq_distill_loss": (c.c_int, [distill, vp, vp]),
+            "entq_distill_backward": (c.c_int, [distill, vp, vp, u64, vp, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -191,7 +208,7 @@ EXPORTED = ["entq_plan_workspace_bytes", "entq_plan", "entq_decode", "entq_decod
             "entq_int8_gemm_backward_workspace_bytes", "entq_int8_gemm_backward",
             "entq_int8_gated_backward_workspace_bytes", "entq_int8_gated_backward",
             "entq_norm_block", "entq_norm_block_backward_workspace_bytes",
-            "entq_norm_block_backward"]
+            "entq_norm_block_backward", "entq_distill_loss", "entq_distill_backward"]
 
 
 def _str(status: int) -> str:

@@ -771,6 +771,48 @@ entq_status entq_norm_block_backward(const entq_norm *n, const void *d_dout, uin
                                      uint64_t lddgate, float *d_dpre, float *d_dpost,
                                      void *d_workspace, uint64_t workspace_bytes, void *stream);
 
+/* ---- Distillation from a teacher's top logits ----
+ *
+ * For each row (token) the student's logits over `classes` classes and, of the
+ * teacher, up to `top` classes with their logits. With z = logits / T and L =
+ * log sum_c exp(z_c):
+ *   d_lse NULL: p = softmax of the row's entries / T,
+ *     loss = sum_j p_j (log p_j - z_(index j) + L)
+ *   d_lse: p_j = exp(t_j / T - lse), lse the teacher's log sum_c exp(t_c / T)
+ *     over all its classes; the mass outside the entries, pt = max(0, 1 - sum
+ *     p), is a class of its own (none where the entries cover every class):
+ *     loss = sum_j p_j (log p_j - z_(index j) + L) + pt (log pt - Lt + L),
+ *     Lt the log-sum of z over the classes that are no entry's
+ * times the row's weight. An entry with a negative index is none; a row
+ * without entries has loss and gradient 0, and so has one of weight 0,
+ * whatever its logits hold. Entries of one class count each (their p add up).
+ * An index of classes and beyond makes the row's loss and gradient NaN. The
+ * entries' terms are in 64 bits, the sums over classes in fp32. */
+#define ENTQ_DISTILL_MAX_TOP 256u
+#define ENTQ_DISTILL_MAX_CLASSES 262144u
+
+typedef struct {
+    uint32_t rows, classes, top;
+    int32_t type;            /* of the logits: ENTQ_BF16, F16 or F32 */
+    int32_t teacher_type;    /* of the teacher's */
+    int32_t index_bytes;     /* 4 or 8: int32 or int64 indices */
+    float temperature;       /* T, 1e-4 .. 1e4 */
+    uint32_t reserved;       /* 0 */
+    const void *d_logits, *d_index, *d_teacher;  /* [rows][ld...] */
+    uint64_t ldlogits, ldindex, ldteacher;       /* in elements */
+    const float *d_lse, *d_weight;               /* [rows], or NULL */
+} entq_distill;
+
+/* d_loss: fp32 [rows]. */
+entq_status entq_distill_loss(const entq_distill *d, float *d_loss, void *stream);
+
+/* d_dlogits ([rows][lddlogits >= classes], the logits' type; no overlap with
+ * anything) = the gradient of sum_r d_dloss[r] loss[r] (d_dloss NULL: of their
+ * sum). The logits are read as the loss reads them; d_loss, if not NULL, gets
+ * the loss too. */
+entq_status entq_distill_backward(const entq_distill *d, const float *d_dloss, void *d_dlogits,
+                                  uint64_t lddlogits, float *d_loss, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
