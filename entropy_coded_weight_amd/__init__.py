@@ -25,6 +25,8 @@ Entry points (the C ABI in include/entq.h, same names):
                                       gate and residual scale, their gradients
   distill (module)                    the loss of a student's logits against a
                                       teacher's top logits, its gradient
+  moe (module)                        a mixture-of-experts layer on decoded
+                                      Int8 codes for few tokens
 """
 from __future__ import annotations
 
@@ -95,6 +97,18 @@ class Distill(ctypes.Structure):
                 ("weight", ctypes.c_void_p)]
 
 
+class Experts(ctypes.Structure):
+    """entq_experts (include/entq.h): device pointers as integers"""
+    _fields_ = [("experts", ctypes.c_uint32), ("top_k", ctypes.c_uint32),
+                ("hidden", ctypes.c_uint32), ("out", ctypes.c_uint32),
+                ("activation", ctypes.c_int32), ("normalize", ctypes.c_int32),
+                ("router_type", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("router", ctypes.c_void_p), ("ldrouter", ctypes.c_uint64),
+                ("weights", ctypes.c_void_p * 3), ("scales", ctypes.c_void_p * 3),
+                ("ld", ctypes.c_uint64 * 3), ("stride", ctypes.c_uint64 * 3),
+                ("scale_stride", ctypes.c_uint64 * 3)]
+
+
 class EntqError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -115,7 +129,7 @@ def lib():
         c = ctypes
         vp, u64, i64 = c.c_void_p, c.c_uint64, c.c_int64
         rows, norm = c.POINTER(Rows), c.POINTER(Norm)
-        distill = c.POINTER(Distill)
+        distill, experts = c.POINTER(Distill), c.POINTER(Experts)
         sigs = {
             "entq_plan_workspace_bytes": (c.c_size_t, [c.c_int, i64]),
             "entq_plan": (c.c_int, [vp, c.c_int, vp, vp, i64, u64, vp, c.c_size_t, vp,
@@ -180,6 +194,8 @@ def lib():
                                                    u64, vp, vp, vp, u64, vp]),
             "entq_distill_loss": (c.c_int, [distill, vp, vp]),
             "entq_distill_backward": (c.c_int, [distill, vp, vp, u64, vp, vp]),
+            "entq_moe_few_workspace_bytes": (u64, [rows, experts]),
+            "entq_moe_few": (c.c_int, [rows, experts, vp, c.c_int, u64, vp, vp, vp, u64, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -208,7 +224,8 @@ EXPORTED = ["entq_plan_workspace_bytes", "entq_plan", "entq_decode", "entq_decod
             "entq_int8_gemm_backward_workspace_bytes", "entq_int8_gemm_backward",
             "entq_int8_gated_backward_workspace_bytes", "entq_int8_gated_backward",
             "entq_norm_block", "entq_norm_block_backward_workspace_bytes",
-            "entq_norm_block_backward", "entq_distill_loss", "entq_distill_backward"]
+            "entq_norm_block_backward", "entq_distill_loss", "entq_distill_backward",
+            "entq_moe_few_workspace_bytes", "entq_moe_few"]
 
 
 def _str(status: int) -> str:

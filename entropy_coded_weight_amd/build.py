@@ -15,7 +15,7 @@ SOURCES = ["entq_decode.hip", "entq_decode_gemv.hip", "entq_decode_gemm.hip",
            "entq_decode_tiles.hip", "entq_decode_adaptive.hip", "entq_plan.cpp",
            "entq_encode.cpp", "entq_encode_dev.hip", "entq_int8.hip", "entq_int8_gemm.hip",
            "entq_int8_few.hip", "entq_int8_grad.hip", "entq_norm.hip",
-           "entq_distill.hip"]
+           "entq_distill.hip", "entq_moe.hip"]
 
 
 def hipcc() -> str:

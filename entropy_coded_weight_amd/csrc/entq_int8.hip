@@ -520,6 +520,12 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
 bool bad_act(int act) { return act < ENTQ_ACT_SILU || act > ENTQ_ACT_RELU; }
 
 }  // namespace
+
+entq_status quantize_padded(const entq_rows &x, int8_t *codes, uint64_t ldc, float *scales, hipStream_t s) {
+    Aligner none;
+    return (entq_status)launch_quantize(x, codes, ldc, (uint32_t)ldc, scales, none, s);
+}
+
 }  // namespace entq
 
 using entq::describe;

@@ -63,7 +63,37 @@ class _Memory:
             self.ends.setdefault(stream.cuda_stream, torch.cuda.Event()).record(stream)
 
 
-class FeedForward:
+class DecodedCodes:
+    """The code buffer of a block of Int8 tensors: its checks, its decode, and
+    the order of its use on several streams."""
+
+    def __init__(self, p: Plan, scales, codes):
+        _device_buffer(p, "scales", scales, p.scale_rows, dtypes=(torch.float32,))
+        self._memory = None
+        if codes is None:
+            codes = torch.empty(p.out_elems, dtype=torch.int8, device=p.device)
+            if not torch.cuda.is_current_stream_capturing():
+                self._memory = _Memory(self, torch.cuda.current_stream(p.device))
+        _device_buffer(p, "codes", codes, p.out_elems, dtypes=(torch.int8,))
+        self.plan, self.scales, self.codes = p, scales, codes
+
+    @contextlib.contextmanager
+    def _using_codes(self, stream):
+        """Makes ``stream`` the current one for work on the code buffer."""
+        with _on(stream, self.plan.device):
+            if self._memory is None:
+                yield
+            else:
+                with self._memory.on(torch.cuda.current_stream(self.plan.device)):
+                    yield
+
+    def decode(self, compressed, chunk_status=None, stream=None):
+        """Enqueue the decode of the block's codes."""
+        with self._using_codes(stream):
+            decode(self.plan, compressed, self.codes, OUT_CODES, None, chunk_status)
+
+
+class FeedForward(DecodedCodes):
     """p: the plan of gate [F, D], up [F, D] and down [E, F]; scales: device
     float32 with the plan's row scales. ``decode`` fills the code buffer, which
     ``forward`` and ``backward`` then use; a caller that walks over layers gives
@@ -92,39 +122,18 @@ class FeedForward:
                                     f"{', '.join(int8.ACTIVATIONS)}")
         if hidden_type not in (None, torch.bfloat16, torch.float16, torch.float32):
             raise EntqError(EINVAL, f"hidden values of type {hidden_type}")
-        _device_buffer(p, "scales", scales, p.scale_rows, dtypes=(torch.float32,))
-        self._memory = None
-        if codes is None:
-            codes = torch.empty(p.out_elems, dtype=torch.int8, device=p.device)
-            if not torch.cuda.is_current_stream_capturing():
-                self._memory = _Memory(self, torch.cuda.current_stream(p.device))
-        _device_buffer(p, "codes", codes, p.out_elems, dtypes=(torch.int8,))
-        self.plan, self.scales, self.activation, self.codes = p, scales, activation, codes
+        super().__init__(p, scales, codes)
+        self.activation = activation
         self.width, self.hidden, self.out = d, f, e
         self.hidden_type = hidden_type
         self._w = []  # code matrix and its scales
         self._at = []  # where a tensor's scales are
-        codes, scales = codes.view(-1), scales.view(-1)
+        codes, scales = self.codes.view(-1), scales.view(-1)
         for r in t:
             rows, cols = int(r["rows"]), int(r["cols"])
             o, s = int(r["out_elem_offset"]), int(r["scale_row_offset"])
             self._at.append(slice(s, s + rows))
             self._w += [codes[o:o + rows * cols].view(rows, cols), scales[s:s + rows]]
-
-    @contextlib.contextmanager
-    def _using_codes(self, stream):
-        """Makes ``stream`` the current one for work on the code buffer."""
-        with _on(stream, self.plan.device):
-            if self._memory is None:
-                yield
-            else:
-                with self._memory.on(torch.cuda.current_stream(self.plan.device)):
-                    yield
-
-    def decode(self, compressed, chunk_status=None, stream=None):
-        """Enqueue the decode of the block's codes."""
-        with self._using_codes(stream):
-            decode(self.plan, compressed, self.codes, OUT_CODES, None, chunk_status)
 
     def forward(self, x, y, stream=None):
         """y = block(x): x bfloat16, float16 or float32 [m, D], y of any of

@@ -813,6 +813,46 @@ entq_status entq_distill_loss(const entq_distill *d, float *d_loss, void *stream
 entq_status entq_distill_backward(const entq_distill *d, const float *d_dloss, void *d_dlogits,
                                   uint64_t lddlogits, float *d_loss, void *stream);
 
+/* ---- A mixture-of-experts layer for few tokens ----
+ *
+ * For up to ENTQ_MOE_MAX_TOKENS tokens x [M][D] (BF16, F16 or F32):
+ *   l = x . router^T (64-bit sums), the top_k experts of largest l chosen
+ *     (a NaN counts as the largest, equal ones go to the lowest index),
+ *   p = softmax of l over the chosen (normalize = 1) or over all (0),
+ *   y[m] = sum over the chosen e of p_e (h_e . down_e^T),
+ *   h_e = act(x . gate_e^T) (x . up_e^T),
+ * the products as entq_int8_gated and entq_int8_gemm compute them: x and each
+ * h_e (fp32) quantised per row as entq_quantize_rows does, sums exact in int32
+ * over each wave's part of a row. Only the codes of experts that some token
+ * chose are read. The same inputs give the same bits. */
+#define ENTQ_MOE_MAX_TOKENS 64u
+#define ENTQ_MOE_MAX_EXPERTS 256u
+#define ENTQ_MOE_MAX_TOP 32u
+
+/* Expert e's matrices: int8 codes at d_weights[i] + e stride[i] (elements),
+ * i = 0 gate [hidden][ld >= D], 1 up [hidden][ld >= D], 2 down [out][ld >=
+ * hidden], any alignment; fp32 row scales at d_scales[i] + e scale_stride[i]. */
+typedef struct {
+    uint32_t experts, top_k, hidden, out;
+    int32_t activation;      /* entq_activation */
+    int32_t normalize;       /* 0 or 1 */
+    int32_t router_type;     /* ENTQ_BF16, F16 or F32 */
+    uint32_t reserved;       /* 0 */
+    const void *d_router;    /* [experts][ldrouter >= D] */
+    uint64_t ldrouter;
+    const int8_t *d_weights[3];
+    const float *d_scales[3];
+    uint64_t ld[3], stride[3], scale_stride[3];
+} entq_experts;
+
+/* d_y: [M][ldy >= out] of y_type (BF16, F16 or F32). d_experts and d_weights
+ * ([M][top_k], or NULL): a token's experts by descending logit, and their p.
+ * x->d_scales is NULL. Workspace as for the int8 calls. */
+uint64_t entq_moe_few_workspace_bytes(const entq_rows *x, const entq_experts *e);
+entq_status entq_moe_few(const entq_rows *x, const entq_experts *e, void *d_y, int y_type,
+                         uint64_t ldy, int32_t *d_experts, float *d_weights, void *d_workspace,
+                         uint64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
