@@ -193,7 +193,7 @@ def lib():
             "entq_norm_block_backward": (c.c_int, [norm, vp, u64, vp, u64, vp, u64, vp, u64, vp,
                                                    u64, vp, vp, vp, u64, vp]),
             "entq_distill_loss": (c.c_int, [distill, vp, vp]),
-            "entq_distill_backward": (c.c_int, [distill, vp, vp, u64, vp, vp]),
+            "entq_distill_backward": (c.c_int, [distill, vp, vp, c.c_int, u64, vp, vp]),
             "entq_moe_few_workspace_bytes": (u64, [rows, experts]),
             "entq_moe_few": (c.c_int, [rows, experts, vp, c.c_int, u64, vp, vp, vp, u64, vp]),
         }

@@ -27,11 +27,12 @@ struct DistillArgs {
     uint32_t M, V, K;
     int teacher_type;
     bool wide;              // 64-bit indices
-    float scale;            // log2(e) / T: logits times it are exponents of 2
-    double inv_t;           // 1 / T
+    float scale;            // log2(e) / T rounded
+    double scale64, inv_t;  // log2(e) / T, 1 / T
 };
 
 constexpr uint32_t kMaxTop = ENTQ_DISTILL_MAX_TOP;
+constexpr double kLn2 = 0.693147180559945309417;
 
 __device__ __forceinline__ float read_teacher(const DistillArgs &a, uint64_t at) {
     return a.teacher_type == ENTQ_F32 ? ((const float *)a.teacher)[at]
@@ -48,206 +49,304 @@ __device__ __forceinline__ float wave_sumf(float v) {
     for (int o = 32; o; o /= 2) v += __shfl_xor(v, o);
     return v;
 }
+// (a NaN wins)
+__device__ __forceinline__ double wave_max64(double v) {
+#pragma unroll
+    for (int o = 32; o; o /= 2) {
+        const double w = __shfl_xor(v, o);
+        v = w > v || w != w ? w : v;
+    }
+    return v;
+}
 
-// One workgroup per token, which reads the row twice (three times with the
-// gradient), the second time out of the L2.
-template <int TYPE, int WAVES>
+// Element i of a piece replaced by -infinity: a class that counts for nothing.
+template <int TYPE>
+__device__ __forceinline__ void remove(v4i &v, int i) {
+    if (TYPE == ENTQ_F32) {
+        v[i] = (int)0xFF800000u;
+    } else {
+        const uint32_t inf = TYPE == ENTQ_F16 ? 0xFC00u : 0xFF80u, shift = 16 * (i % 2);
+        v[i / 2] = (int)(((uint32_t)v[i / 2] & ~(0xFFFFu << shift)) | inf << shift);
+    }
+}
+
+// What the entries of a row come to, whatever the classes outside them.
+struct Entries {
+    double terms;           // sum p (log p - z)
+    double mass;            // sum p
+    double top2;            // with a tail: log2 of the student's sum over the entries' classes
+    uint32_t distinct;      // of these classes
+    uint32_t any;
+};
+
+// One workgroup per token. VECS pieces a thread stay in registers, so a row is
+// read once for the loss and its gradient; VECS 0: any length, read two or
+// three times, again out of the caches. What is computed of the few entries is
+// in 64 bits (the loss is a small difference of their terms) and done by one
+// wave while the row's loads are on their way.
+//
+// The exponentials are the hardware's 2^x of one fused multiply-add, x scale +
+// c, with c = 64 - (the largest logit) scale: differences from the largest, so
+// that the logits' own size does not blur them (what rounding scale and c does
+// to all of them alike is put right in 64 bits), and 2^64 above the smallest
+// exponents that the hardware flushes, so that the gradients have theirs.
+template <int TYPE, int GRAD, int VECS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void distill_rows(DistillArgs a, uint32_t row0) {
     constexpr int kP = kPer<TYPE>, kThreads = 64 * WAVES;
-    extern __shared__ uint32_t marks[];  // with a tail: a bit for each class of the top entries
-    __shared__ float part[WAVES], part2[WAVES];
+    extern __shared__ uint32_t marks[];  // a bit for each class of the entries
+    __shared__ float part[2][WAVES];
     __shared__ int32_t where[kMaxTop];   // an entry's class, -1: none
     __shared__ float mass[kMaxTop];      // the teacher's p of it
-    __shared__ float common[2];
-    __shared__ double log_sum;
+    __shared__ double z2[kMaxTop];       // the student's exponent of it
+    __shared__ uint8_t later[kMaxTop];   // an earlier entry has its class
+    __shared__ Entries found;
     const uint64_t m = (uint64_t)row0 + blockIdx.x;
     const uint32_t t = threadIdx.x, lane = t % 64, wave = t / 64;
     const uint32_t pieces = (a.V + kP - 1) / kP;
     const uint8_t *row = (const uint8_t *)a.logits + m * a.ld * (TYPE == ENTQ_F32 ? 4 : 2);
-    uint8_t *grad = (uint8_t *)a.dlogits + m * a.ldd * (TYPE == ENTQ_F32 ? 4 : 2);
+    uint8_t *grad = (uint8_t *)a.dlogits + m * a.ldd * (GRAD == ENTQ_F32 ? 4 : 2);
     const float weight = a.weight ? a.weight[m] : 1.0f;
+    auto put = [&](uint32_t p, const float(&g)[kP]) {
+        if constexpr (TYPE == GRAD) {
+            store_piece<TYPE>(grad, p, a.V, pack<TYPE>(g));
+        } else {  // 16-bit gradients of fp32 logits
+            uint16_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = bits16(g[i], GRAD == ENTQ_F16);
+            uint16_t *to = (uint16_t *)grad + p * 4;
+            if (p * 4 + 4 <= a.V) {
+                ((any8 *)to)->v = v2i{(int)(b[0] | (uint32_t)b[1] << 16), (int)(b[2] | (uint32_t)b[3] << 16)};
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < 3; ++i)
+                    if (p * 4 + i < a.V) to[i] = b[i];
+            }
+        }
+    };
     if (weight == 0.0f) {  // whatever the row holds
         if (a.loss && t == 0) a.loss[m] = 0.0f;
-        if (a.dlogits)
-            for (uint32_t p = t; p < pieces; p += kThreads) store_piece<TYPE>(grad, p, a.V, v4i{0, 0, 0, 0});
+        if (a.dlogits) {
+            const float none[kP] = {};
+            for (uint32_t p = t; p < pieces; p += kThreads) put(p, none);
+        }
         return;
     }
-    const bool tail = a.lse != nullptr;
-    if (tail) {
-        for (uint32_t i = t; i < (a.V + 31) / 32; i += kThreads) marks[i] = 0;
-        __syncthreads();
+    auto piece = [&](uint32_t p) {
+        v4i v = load_piece<TYPE>(row, p, a.V);
+        if ((p + 1) * kP > a.V) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                if (p * kP + i >= a.V) remove<TYPE>(v, i);
+        }
+        return v;
+    };
+    v4i held[VECS ? VECS : 1];
+    if (VECS) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) held[i] = piece(i * kThreads + t);
     }
-    bool bad = false;  // an index beyond the classes
+    const bool tail = a.lse != nullptr;
+    for (uint32_t i = t; i < (a.V + 31) / 32; i += kThreads) marks[i] = 0;
+    __syncthreads();
+    bool bad = false, twice = false;  // an index beyond the classes, a class with two entries
     for (uint32_t j = t; j < a.K; j += kThreads) {
         const int64_t i = a.wide ? ((const int64_t *)a.index)[m * a.ldi + j] : ((const int32_t *)a.index)[m * a.ldi + j];
         bad |= i >= (int64_t)a.V;
         const bool in = i >= 0 && i < (int64_t)a.V;
         where[j] = in ? (int32_t)i : -1;
-        if (tail && in) atomicOr(&marks[(uint32_t)i / 32], 1u << ((uint32_t)i % 32));
+        later[j] = 0;
+        if (in) twice |= atomicOr(&marks[(uint32_t)i / 32], 1u << ((uint32_t)i % 32)) >> ((uint32_t)i % 32) & 1;
     }
     bad = __syncthreads_or(bad);
-    auto marked = [&](uint32_t p) -> uint32_t {  // the piece's classes of the top entries
-        if (!tail) return 0;
-        const uint32_t c = p * kP;
-        return (marks[c / 32] >> (c % 32)) & ((1u << kP) - 1);
-    };
-    // the largest logit outside the marked classes; exponents are differences
-    // from it, which the logits' own sizes do not blur
-    float top = -INFINITY;
-    for (uint32_t p = t; p < pieces; p += kThreads) {
-        const v4i v = load_piece<TYPE>(row, p, a.V);
-        const uint32_t out = marked(p);
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-            if (p * kP + i < a.V && !(out >> i & 1)) top = fmaxf(top, act_of<TYPE>(v, i));
+    twice = __syncthreads_or(twice);
+    if (twice) {
+        for (uint32_t j = t; j < a.K; j += kThreads)
+            for (uint32_t i = 0; i < j; ++i)
+                if (where[i] >= 0 && where[i] == where[j]) later[j] = 1;
+        __syncthreads();
     }
-    top = wave_maxf(top);
-    if (lane == 0) part[wave] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[w]);
-    const float from = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    for (uint32_t p = t; p < pieces; p += kThreads) {
-        const v4i v = load_piece<TYPE>(row, p, a.V);
-        const uint32_t out = marked(p);
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-            if (p * kP + i < a.V && !(out >> i & 1)) sum += exp2f((act_of<TYPE>(v, i) - from) * a.scale);
-    }
-    sum = wave_sumf(sum);
-    if (lane == 0) part2[wave] = sum;
-    __syncthreads();
-    // The few entries: one wave, in 64 bits, since the loss is a small difference of their terms.
     if (wave == 0) {
-        double total = 0.0;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) total += part2[w];
-        const double lt = from * a.inv_t + log(total);  // outside the marks
-        // the teacher's log-sum
-        double most = -INFINITY, lse = 0.0;
-        if (!tail) {
+        Entries f{};
+        double most = -INFINITY, peak = -INFINITY;
+        for (uint32_t j = lane; j < a.K; j += 64) {
+            if (where[j] < 0) continue;
+            f.any = 1;
+            const double v = read_teacher(a, m * a.ldt + j) * a.inv_t;
+            most = v > most || v != v ? v : most;
+            const double z = load_act<TYPE>(row, (uint32_t)where[j]) * a.scale64;
+            z2[j] = z;
+            peak = z > peak || z != z ? z : peak;
+        }
+        f.any = __any(f.any);
+        double lse;
+        if (tail) {
+            lse = a.lse[m];
+            peak = wave_max64(peak);
+            double s = 0.0;
             for (uint32_t j = lane; j < a.K; j += 64)
-                if (where[j] >= 0) {
-                    const double v = read_teacher(a, m * a.ldt + j) * a.inv_t;
-                    most = v > most || v != v ? v : most;
+                if (where[j] >= 0 && !later[j]) {
+                    ++f.distinct;
+                    s += exp2(z2[j] - peak);
                 }
-            for (int o = 32; o; o /= 2) {
-                const double v = __shfl_xor(most, o);
-                most = v > most || v != v ? v : most;
-            }
+            f.top2 = peak + log2(wave_sum(s));
+#pragma unroll
+            for (int o = 32; o; o /= 2) f.distinct += __shfl_xor(f.distinct, o);
+        } else {
+            most = wave_max64(most);
             double s = 0.0;
             for (uint32_t j = lane; j < a.K; j += 64)
                 if (where[j] >= 0) s += exp(read_teacher(a, m * a.ldt + j) * a.inv_t - most);
             lse = most + log(wave_sum(s));
-        } else {
-            lse = a.lse[m];
         }
-        // the student's log-sum
-        double l = lt;
-        uint32_t distinct = 0;
-        if (tail) {
-            double peak = -INFINITY;
-            for (uint32_t j = lane; j < a.K; j += 64)
-                if (where[j] >= 0) {
-                    const double z = load_act<TYPE>(row, (uint32_t)where[j]) * a.inv_t;
-                    peak = z > peak || z != z ? z : peak;
-                }
-            for (int o = 32; o; o /= 2) {
-                const double v = __shfl_xor(peak, o);
-                peak = v > peak || v != v ? v : peak;
-            }
-            peak = lt > peak || lt != lt ? lt : peak;
-            double s = 0.0;
-            for (uint32_t j = lane; j < a.K; j += 64) {
-                if (where[j] < 0) continue;
-                bool first = true;  // of its class
-                for (uint32_t i = 0; i < j; ++i) first &= where[i] != where[j];
-                if (!first) continue;
-                ++distinct;
-                s += exp(load_act<TYPE>(row, (uint32_t)where[j]) * a.inv_t - peak);
-            }
-            s = wave_sum(s) + exp(lt - peak);
-            l = peak + log(s);
-            for (int o = 32; o; o /= 2) distinct += __shfl_xor(distinct, o);
-        }
-        double loss = 0.0, all = 0.0;
-        bool any = false;
         for (uint32_t j = lane; j < a.K; j += 64) {
-            if (where[j] < 0) {
-                mass[j] = 0.0f;
-                continue;
-            }
-            any = true;
-            const double logp = read_teacher(a, m * a.ldt + j) * a.inv_t - lse;
-            const double p = exp(logp), z = load_act<TYPE>(row, (uint32_t)where[j]) * a.inv_t;
+            if (where[j] < 0) continue;
+            const double logp = read_teacher(a, m * a.ldt + j) * a.inv_t - lse, p = exp(logp);
             mass[j] = (float)p;
-            all += p;
-            if (!(p == 0.0)) loss += p * (logp - z + l);
+            f.mass += p;
+            if (!(p == 0.0)) f.terms += p * (logp - z2[j] * kLn2);
         }
-        loss = wave_sum(loss);
-        all = wave_sum(all);
-        any = __any(any);
-        double factor = exp(lt - l);  // the student's mass outside the marks
-        if (!any) {
-            loss = 0.0;
-            factor = 0.0;
-        } else if (tail) {
-            double pt = fmax(0.0, 1.0 - all);
-            if (distinct == a.V) pt = 0.0;
-            if (pt > 0.0) loss += pt * (log(pt) - lt + l);
-            factor -= pt;
+        f.mass = wave_sum(f.mass);
+        f.terms = wave_sum(f.terms);
+        if (lane == 0) found = f;
+    }
+    // the entries' classes leave the row, with a tail
+    auto outside = [&](v4i &v, uint32_t p) {
+        const uint32_t c = p * kP, out = c < a.V ? (marks[c / 32] >> (c % 32)) & ((1u << kP) - 1) : 0;
+        if (out) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                if (out >> i & 1) remove<TYPE>(v, i);
         }
-        if (bad) loss = factor = NAN;
-        if (lane == 0) {
-            if (a.loss) a.loss[m] = (float)(loss * weight);
-            const double by = (double)weight * (a.dloss ? a.dloss[m] : 1.0f) * a.inv_t;
-            common[0] = factor == 0.0 ? 0.0f : (float)(factor / total * by);
-            common[1] = (float)by;
-            log_sum = l;
-        }
+    };
+    if (VECS && tail) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) outside(held[i], i * kThreads + t);
+    }
+    // (between two passes: values unpacked in one are not kept for the next,
+    // which would take twice the registers of the pieces)
+    auto forget = [&] {
+#pragma unroll
+        for (int i = 0; i < (VECS ? VECS : 1); ++i) asm("" : "+v"(held[i]));
+    };
+    auto again = [&](uint32_t p) {
+        v4i v = piece(p);
+        if (tail) outside(v, p);
+        return v;
+    };
+    float top = -INFINITY;
+    auto raise = [&](v4i v) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) top = fmaxf(top, act_of<TYPE>(v, i));
+    };
+    if (VECS) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) raise(held[i]);
+    } else {
+        for (uint32_t p = t; p < pieces; p += kThreads) raise(again(p));
+    }
+    forget();
+    top = wave_maxf(top);
+    if (lane == 0) part[0][wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[0][w]);
+    const float from = top == -INFINITY ? 0.0f : top;
+    const float c = (float)(64.0 - (double)from * a.scale);
+    auto power = [&](v4i v, int i) { return __builtin_amdgcn_exp2f(__builtin_fmaf(act_of<TYPE>(v, i), a.scale, c)); };
+    float sum = 0.0f;
+    auto add = [&](v4i v) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) sum += power(v, i);
+    };
+    if (VECS) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) add(held[i]);
+    } else {
+        for (uint32_t p = t; p < pieces; p += kThreads) add(again(p));
+    }
+    forget();
+    sum = wave_sumf(sum);
+    if (lane == 0) part[1][wave] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += part[1][w];
+    // log2 of the sum: its exponent, and the logarithm of a number in [1/2, 1)
+    const Entries f = found;
+    const double out2 = (double)__builtin_amdgcn_frexp_expf(sum) +
+                        (double)__builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(sum)) - (double)c +
+                        (double)from * (a.scale64 - (double)a.scale);
+    double all2 = sum == 0.0f ? -INFINITY : out2;
+    float factor = 1.0f;  // of the powers in the gradient, times their sum
+    double loss = f.terms;
+    if (tail) {
+        // the entries' classes and the others together
+        const double lo2 = all2;
+        const float d = (float)(f.top2 - lo2), u = __builtin_amdgcn_exp2f(-fabsf(d));
+        const float more = __builtin_amdgcn_logf(1.0f + u), inv = 1.0f / (1.0f + u);
+        all2 = (f.top2 > lo2 ? f.top2 : lo2) + more;
+        const float qt = d > 0.0f ? u * inv : inv;
+        const double pt = f.distinct == a.V ? 0.0 : fmax(0.0, 1.0 - f.mass);
+        factor = (float)((double)qt - pt);
+        if (pt > 0.0 && t == 0) loss += pt * (log(pt) + (all2 - lo2) * kLn2);
+    }
+    if (!f.any) factor = 0.0f;
+    if (bad) factor = NAN;
+    if (a.loss && t == 0) {
+        loss = f.any ? loss + f.mass * (all2 * kLn2) : 0.0;
+        a.loss[m] = bad ? NAN : (float)(loss * weight);
     }
     if (!a.dlogits) return;
-    __syncthreads();
-    const float factor = common[0], by = common[1];
-    const double l = log_sum;
-    for (uint32_t p = t; p < pieces; p += kThreads) {
-        const v4i v = load_piece<TYPE>(row, p, a.V);
+    const double by64 = (double)weight * (a.dloss ? a.dloss[m] : 1.0f) * a.inv_t;
+    const float by = (float)by64;
+    factor = factor == 0.0f ? 0.0f : (float)((double)factor / sum * by64);
+    auto write = [&](uint32_t p, v4i v) {
         float g[kP];
 #pragma unroll
-        for (int i = 0; i < kP; ++i)
-            g[i] = factor == 0.0f ? 0.0f : factor * exp2f((act_of<TYPE>(v, i) - from) * a.scale);
-        store_piece<TYPE>(grad, p, a.V, pack<TYPE>(g));
+        for (int i = 0; i < kP; ++i) g[i] = factor == 0.0f ? 0.0f : factor * power(v, i);
+        put(p, g);
+    };
+    if (VECS) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+            if (i * kThreads + t < pieces) write(i * kThreads + t, held[i]);
+    } else {
+        for (uint32_t p = t; p < pieces; p += kThreads) write(p, again(p));
     }
     __syncthreads();
     // the entries' classes again, each by its first entry
     for (uint32_t j = t; j < a.K; j += kThreads) {
-        if (where[j] < 0) continue;
-        bool first = true;
-        float p = 0.0f;
-        for (uint32_t i = 0; i < a.K; ++i)
-            if (where[i] == where[j]) {
-                first &= i >= j;
-                p += mass[i];
-            }
-        if (!first) continue;
-        const uint32_t c = (uint32_t)where[j];
-        const double z = load_act<TYPE>(row, c) * a.inv_t;
-        const float g = bad ? NAN : by * ((float)exp(z - l) - p);
-        if (TYPE == ENTQ_F32)
-            ((float *)grad)[c] = g;
+        if (where[j] < 0 || later[j]) continue;
+        float p = mass[j];
+        if (twice) {
+            for (uint32_t i = j + 1; i < a.K; ++i)
+                if (where[i] == where[j]) p += mass[i];
+        }
+        const float g = bad ? NAN : by * ((float)exp2(z2[j] - all2) - p);
+        if (GRAD == ENTQ_F32)
+            ((float *)grad)[where[j]] = g;
         else
-            ((uint16_t *)grad)[c] = bits16(g, TYPE == ENTQ_F16);
+            ((uint16_t *)grad)[where[j]] = bits16(g, GRAD == ENTQ_F16);
     }
 }
 
-template <int TYPE>
-int launch_distill(const DistillArgs &a, hipStream_t s) {
+template <int TYPE, int GRAD, int VECS, int WAVES>
+int launch_rows(const DistillArgs &a, hipStream_t s) {
     constexpr uint32_t kMost = 1u << 20;  // a launch's threads stay below 2^32
-    const uint32_t lds = a.lse ? (a.V + 31) / 32 * 4 : 0;
     for (uint64_t r = 0; r < a.M; r += kMost)
-        distill_rows<TYPE, 16><<<(uint32_t)std::min<uint64_t>(kMost, a.M - r), 1024, lds, s>>>(a, (uint32_t)r);
+        distill_rows<TYPE, GRAD, VECS, WAVES><<<(uint32_t)std::min<uint64_t>(kMost, a.M - r), 64 * WAVES,
+                                                (a.V + 31) / 32 * 4, s>>>(a, (uint32_t)r);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
+}
+
+template <int TYPE, int GRAD>
+int launch_distill(const DistillArgs &a, hipStream_t s) {
+    const uint32_t pieces = (a.V + kPer<TYPE> - 1) / kPer<TYPE>;
+    if (pieces <= 1024) return launch_rows<TYPE, GRAD, 4, 4>(a, s);
+    if (pieces <= 4096) return launch_rows<TYPE, GRAD, 8, 8>(a, s);
+    if (pieces <= 8192) return launch_rows<TYPE, GRAD, 8, 16>(a, s);
+    if (pieces <= 16384) return launch_rows<TYPE, GRAD, 16, 16>(a, s);
+    return launch_rows<TYPE, GRAD, 0, 16>(a, s);
 }
 
 uint32_t bytes_of(int t) { return t == ENTQ_F32 ? 4 : 2; }
@@ -273,7 +372,8 @@ entq_status check(const entq_distill *d) {
     return ENTQ_OK;
 }
 
-entq_status run(const entq_distill &d, float *loss, const float *dloss, void *dlogits, uint64_t ldd, hipStream_t s) {
+entq_status run(const entq_distill &d, float *loss, const float *dloss, void *dlogits, int dtype, uint64_t ldd,
+                hipStream_t s) {
     if (!d.rows) return ENTQ_OK;
     DistillArgs a{};
     a.logits = d.d_logits;
@@ -294,10 +394,13 @@ entq_status run(const entq_distill &d, float *loss, const float *dloss, void *dl
     a.teacher_type = d.teacher_type;
     a.wide = d.index_bytes == 8;
     a.inv_t = 1.0 / d.temperature;
-    a.scale = (float)(1.44269504088896340736 / d.temperature);
-    return (entq_status)(d.type == ENTQ_BF16  ? launch_distill<ENTQ_BF16>(a, s)
-                         : d.type == ENTQ_F16 ? launch_distill<ENTQ_F16>(a, s)
-                                              : launch_distill<ENTQ_F32>(a, s));
+    a.scale64 = 1.44269504088896340736 / d.temperature;
+    a.scale = (float)a.scale64;
+    if (d.type == ENTQ_BF16) return (entq_status)launch_distill<ENTQ_BF16, ENTQ_BF16>(a, s);
+    if (d.type == ENTQ_F16) return (entq_status)launch_distill<ENTQ_F16, ENTQ_F16>(a, s);
+    return (entq_status)(dtype == ENTQ_BF16  ? launch_distill<ENTQ_F32, ENTQ_BF16>(a, s)
+                         : dtype == ENTQ_F16 ? launch_distill<ENTQ_F32, ENTQ_F16>(a, s)
+                                             : launch_distill<ENTQ_F32, ENTQ_F32>(a, s));
 }
 
 }  // namespace
@@ -310,17 +413,18 @@ entq_status entq_distill_loss(const entq_distill *d, float *d_loss, void *stream
     if (st != ENTQ_OK) return st;
     if (d->rows && !d_loss) return ENTQ_EINVAL;
     if ((uintptr_t)d_loss % 4) return ENTQ_EALIGN;
-    return entq::run(*d, d_loss, nullptr, nullptr, d->classes, (hipStream_t)stream);
+    return entq::run(*d, d_loss, nullptr, nullptr, d->type, d->classes, (hipStream_t)stream);
 }
 
-entq_status entq_distill_backward(const entq_distill *d, const float *d_dloss, void *d_dlogits, uint64_t lddlogits,
-                                  float *d_loss, void *stream) {
+entq_status entq_distill_backward(const entq_distill *d, const float *d_dloss, void *d_dlogits, int dlogits_type,
+                                  uint64_t lddlogits, float *d_loss, void *stream) {
     const entq_status st = entq::check(d);
     if (st != ENTQ_OK) return st;
     if ((d->rows && !d_dlogits) || lddlogits < d->classes || lddlogits > (1ull << 40)) return ENTQ_EINVAL;
-    if ((uintptr_t)d_dlogits % entq::bytes_of(d->type) || (uintptr_t)d_dloss % 4 || (uintptr_t)d_loss % 4)
+    if (!entq::float_type(dlogits_type) || (dlogits_type != d->type && d->type != ENTQ_F32)) return ENTQ_EINVAL;
+    if ((uintptr_t)d_dlogits % entq::bytes_of(dlogits_type) || (uintptr_t)d_dloss % 4 || (uintptr_t)d_loss % 4)
         return ENTQ_EALIGN;
-    return entq::run(*d, d_loss, d_dloss, d_dlogits, lddlogits, (hipStream_t)stream);
+    return entq::run(*d, d_loss, d_dloss, d_dlogits, dlogits_type, lddlogits, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -82,13 +82,15 @@ def loss(logits, index, teacher, loss, teacher_lse=None, weight=None, temperatur
 def loss_backward(logits, index, teacher, dlogits, dloss=None, loss=None, teacher_lse=None,
                   weight=None, temperature=1.0, stream=None):
     """The gradient of sum(dloss * loss) (dloss float32 [M]; None: all 1) into
-    ``dlogits`` (the logits' type [M, V]), and, unless None, the losses into
+    ``dlogits`` (the logits' type [M, V], or of float32 logits any of the
+    types, as ``int8.gemm_backward`` takes 16 bits), and, unless None, the losses into
     ``loss``: a training step needs no call of ``loss`` before, and the logits
     are read once for both."""
     dev, d = _describe(logits, index, teacher, teacher_lse, weight, temperature)
-    _, ld = _matrix("dlogits", dlogits, dev, (d.type,), logits.shape)
+    kind, ld = _matrix("dlogits", dlogits, dev, _FLOATS if d.type == _F32 else (d.type,),
+                       logits.shape)
     g = 0 if dloss is None else _vector("dloss", dloss, dev, d.rows)
     p = 0 if loss is None else _vector("loss", loss, dev, d.rows)
     _enqueue("entq_distill_backward",
-             lambda w, n, s: lib().entq_distill_backward(d, g, dlogits.data_ptr(), ld, p, s), 0,
-             dev, stream, None)
+             lambda w, n, s: lib().entq_distill_backward(d, g, dlogits.data_ptr(), kind, ld, p,
+                                                          s), 0, dev, stream, None)

@@ -806,12 +806,13 @@ typedef struct {
 /* d_loss: fp32 [rows]. */
 entq_status entq_distill_loss(const entq_distill *d, float *d_loss, void *stream);
 
-/* d_dlogits ([rows][lddlogits >= classes], the logits' type; no overlap with
- * anything) = the gradient of sum_r d_dloss[r] loss[r] (d_dloss NULL: of their
+/* d_dlogits ([rows][lddlogits >= classes] of dlogits_type: the logits' type, or
+ * of fp32 logits any; no overlap with anything) = the gradient of sum_r d_dloss[r] loss[r] (d_dloss NULL: of their
  * sum). The logits are read as the loss reads them; d_loss, if not NULL, gets
  * the loss too. */
 entq_status entq_distill_backward(const entq_distill *d, const float *d_dloss, void *d_dlogits,
-                                  uint64_t lddlogits, float *d_loss, void *stream);
+                                  int dlogits_type, uint64_t lddlogits, float *d_loss,
+                                  void *stream);
 
 /* ---- A mixture-of-experts layer for few tokens ----
  *

@@ -76,8 +76,8 @@ def loss(E, d, out=A):
     return E.lib().entq_distill_loss(ctypes.byref(d) if d else None, out, None)
 
 
-def back(E, d, dloss=0, dl=A, ld=100, out=0):
-    return E.lib().entq_distill_backward(ctypes.byref(d) if d else None, dloss, dl, ld, out, None)
+def back(E, d, dloss=0, dl=A, kind=0, ld=100, out=0):
+    return E.lib().entq_distill_backward(ctypes.byref(d) if d else None, dloss, dl, kind, ld, out, None)
 
 
 @pytest.mark.parametrize("bad", [dict(reserved=1), dict(type=3), dict(type=-1), dict(teacher_type=3), dict(index_bytes=2),
@@ -95,6 +95,9 @@ def test_c_refusals(E):
     d = described(E)
     assert loss(E, None) == E.EINVAL and back(E, None) == E.EINVAL
     assert loss(E, d, 0) == E.EINVAL and back(E, d, dl=0) == E.EINVAL and back(E, d, ld=99) == E.EINVAL
+    for kind in (1, 2, 3, -1):
+        assert back(E, d, kind=kind) == E.EINVAL
+    assert back(E, described(E, type=2), kind=3) == E.EINVAL
     assert loss(E, d, A + 2) == EALIGN
     for k in (dict(dl=A + 1), dict(dloss=A + 1), dict(out=A + 2)):
         assert back(E, d, **k) == EALIGN

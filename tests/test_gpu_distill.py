@@ -51,14 +51,15 @@ def close(got, want, bound, what):
                            float(bound.expand_as(want)[bad][0]))
 
 
-def check(D, logits, index, teacher, lse, weight, kind, T=1.25, dloss=None):
+def check(D, logits, index, teacher, lse, weight, kind, T=1.25, dloss=None, grad_kind=None):
     m, v = logits.shape
+    grad_kind = grad_kind or kind
     loss, again = torch.full((m,), 9.0, device="cuda"), torch.full((m,), 9.0, device="cuda")
-    flat = torch.full((m, v + 3), 7.0, device="cuda").to(logits.dtype)
+    flat = torch.full((m, v + 3), 7.0, device="cuda").to(TYPES[grad_kind])
     grad = flat[:, 1:v + 1]
     D.loss(logits, index, teacher, loss, lse, weight, T)
     D.loss_backward(logits, index, teacher, grad, dloss, again, lse, weight, T)
-    want = R.distill(logits, index, teacher, lse, weight, T, dloss, kind)
+    want = R.distill(logits, index, teacher, lse, weight, T, dloss, grad_kind)
     close(loss, *want[0], "loss")
     close(again, *want[0], "loss beside the gradient")
     close(grad, *want[1], "gradient")
@@ -79,6 +80,14 @@ def test_loss_and_gradient(D, m, v, k, kind):
         logits, index, teacher, lse, w = inputs(m, v, k, kind, at, tail, wide, pad, tk, missing, weights)
         dloss = torch.linspace(-2, 1, m, device="cuda") if at % 2 else None
         check(D, logits, index, teacher, lse, w, kind, dloss=dloss)
+
+
+@pytest.mark.parametrize("grad_kind", ["bf16", "f16"])
+@pytest.mark.parametrize("v", [7, 1001, 9000, 33001, 70003])
+def test_16_bit_gradients_of_fp32_logits(D, v, grad_kind):
+    for tail in (False, True):
+        logits, index, teacher, lse, w = inputs(4, v, 12, "f32", 3, tail, missing=True, weights=True)
+        check(D, logits, index, teacher, lse, w, "f32", grad_kind=grad_kind)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -199,7 +208,7 @@ def test_refusals(D):
            lambda: D.loss(x, i, t, out, temperature=float("nan")), lambda: D.loss(x, i, t, out, temperature=2e4),
            lambda: D.loss(x, i.repeat(1, 50), t.repeat(1, 50), out), lambda: D.loss(x[:, :0], i, t, out),
            lambda: D.loss(x, i, t.int(), out), lambda: D.loss(torch.zeros(1, 262145, device="cuda"), i[:1], t[:1], out[:1]),
-           lambda: D.loss_backward(x, i, t, x.half()), lambda: D.loss_backward(x, i, t, x[:, :49]),
+           lambda: D.loss_backward(x.half(), i, t, x.clone()), lambda: D.loss_backward(x, i, t, x.double()), lambda: D.loss_backward(x, i, t, x[:, :49]),
            lambda: D.loss_backward(x, i, t, x.clone(), dloss=out[:1]), lambda: D.loss(x, i, t[0], out)]
     for n, call in enumerate(bad):
         with pytest.raises(E.EntqError) as e:
