@@ -76,39 +76,141 @@ struct Entries {
     double mass;            // sum p
     double top2;            // with a tail: log2 of the student's sum over the entries' classes
     uint32_t distinct;      // of these classes
-    uint32_t any;
+    bool any, bad, twice;   // an entry, an index beyond the classes, a class with two entries
 };
+struct EntryTable {
+    int32_t where[kMaxTop]; // an entry's class, -1: none
+    float mass[kMaxTop];    // the teacher's p of it
+    double z2[kMaxTop];     // the student's exponent of it
+    bool later[kMaxTop];    // an earlier entry has its class
+};
+// A lane's entries: lane, lane + 64, ...
+constexpr int kOwn = kMaxTop / 64;
+struct OwnEntries {
+    int32_t at[kOwn];       // the class, -1: none, -2: beyond the classes
+    float teacher[kOwn];
+};
+#define ENTQ_OWN_ENTRIES(i, j) \
+    _Pragma("unroll") for (int i = 0; i < kOwn; ++i) if (const uint32_t j = i * 64 + lane; j < a.K)
 
-// One workgroup per token. VECS pieces a thread stay in registers, so a row is
-// read once for the loss and its gradient; VECS 0: any length, read two or
-// three times, again out of the caches. What is computed of the few entries is
-// in 64 bits (the loss is a small difference of their terms) and done by one
-// wave while the row's loads are on their way.
+__device__ __forceinline__ void load_entries(const DistillArgs &a, uint64_t m, uint32_t lane, OwnEntries &o) {
+    ENTQ_OWN_ENTRIES(i, j) {
+        const int64_t c = a.wide ? ((const int64_t *)a.index)[m * a.ldi + j] : ((const int32_t *)a.index)[m * a.ldi + j];
+        o.at[i] = c < 0 ? -1 : c < (int64_t)a.V ? (int32_t)c : -2;
+        o.teacher[i] = read_teacher(a, m * a.ldt + j);
+    }
+}
+
+// A row's entries: their classes, marked in `marks`, and their sums, in 64
+// bits; one wave. The marks are set when `marked` is called.
+template <int TYPE, class Marked>
+__device__ __forceinline__ Entries sum_entries(const DistillArgs &a, uint64_t m, const void *row, uint32_t lane,
+                                               const OwnEntries &o, EntryTable &e, uint32_t *marks, Marked marked) {
+    Entries f{};
+    bool in[kOwn], first[kOwn];
+    float logit[kOwn];
+    ENTQ_OWN_ENTRIES(i, j) {
+        in[i] = o.at[i] >= 0;
+        f.bad |= o.at[i] == -2;
+        f.any |= in[i];
+        e.where[j] = o.at[i];
+        logit[i] = in[i] ? load_act<TYPE>(row, (uint32_t)o.at[i]) : 0.0f;
+        const uint32_t c = (uint32_t)o.at[i];
+        if (in[i]) f.twice |= atomicOr(&marks[c / 32], 1u << (c % 32)) >> (c % 32) & 1;
+    }
+    f.bad = __any(f.bad);
+    f.any = __any(f.any);
+    f.twice = __any(f.twice);
+    marked();
+    double most = -INFINITY, peak = -INFINITY;
+    ENTQ_OWN_ENTRIES(i, j) {
+        first[i] = in[i];
+        if (f.twice) {
+            for (uint32_t k = 0; k < j; ++k) first[i] &= e.where[k] != o.at[i];
+        }
+        e.later[j] = !first[i];
+        const double v = in[i] ? o.teacher[i] * a.inv_t : -INFINITY, z = in[i] ? logit[i] * a.scale64 : -INFINITY;
+        e.z2[j] = z;
+        most = v > most || v != v ? v : most;
+        peak = z > peak || z != z ? z : peak;
+    }
+    double lse;
+    if (a.lse) {
+        lse = a.lse[m];
+        peak = wave_max64(peak);
+        double s = 0.0;
+        ENTQ_OWN_ENTRIES(i, j) {
+            if (!first[i]) continue;
+            ++f.distinct;
+            s += exp2(logit[i] * a.scale64 - peak);
+        }
+        f.top2 = peak + log2(wave_sum(s));
+#pragma unroll
+        for (int o2 = 32; o2; o2 /= 2) f.distinct += __shfl_xor(f.distinct, o2);
+    } else {
+        most = wave_max64(most);
+        double s = 0.0;
+        ENTQ_OWN_ENTRIES(i, j) {
+            if (in[i]) s += exp(o.teacher[i] * a.inv_t - most);
+        }
+        lse = most + log(wave_sum(s));
+    }
+    ENTQ_OWN_ENTRIES(i, j) {
+        if (!in[i]) continue;
+        const double logp = o.teacher[i] * a.inv_t - lse, p = exp(logp);
+        e.mass[j] = (float)p;
+        f.mass += p;
+        if (!(p == 0.0)) f.terms += p * (logp - logit[i] * a.scale64 * kLn2);
+    }
+    f.mass = wave_sum(f.mass);
+    f.terms = wave_sum(f.terms);
+    return f;
+}
+
+// One workgroup per token: WAVES waves for the row, and one for the entries,
+// whose few terms are in 64 bits (the loss is a small difference of them) and
+// come out while the row is read. VECS pieces a thread stay in registers, so
+// that a row is read once for the loss and its gradient; VECS 0: any length,
+// read two or three times, again out of the caches.
 //
 // The exponentials are the hardware's 2^x of one fused multiply-add, x scale +
 // c, with c = 64 - (the largest logit) scale: differences from the largest, so
 // that the logits' own size does not blur them (what rounding scale and c does
 // to all of them alike is put right in 64 bits), and 2^64 above the smallest
 // exponents that the hardware flushes, so that the gradients have theirs.
+//
+// Bound by memory: 4096 x 32000 bf16 in 47.8 us (5.5 TB/s read), with the
+// gradient 107.4 us (4.9 TB/s; a copy reaches 5.1), 515 x 50021 f16 with it in
+// 24.8 us. What carries that are waves: a workgroup has a multiple of 4 (with
+// 9, one SIMD's three decide, and the first took 107 us), the entries have a
+// wave to themselves (in a wave of the row their 64-bit registers come on top
+// of the row's: 54.7 and 127.4 us), and the registers are held to 80 and 64
+// for 3 and 4 waves more on a SIMD (the third at 78: 28.8 us). Without the row
+// in registers the first two took 130 and 305 us.
+template <int VECS, int WAVES>
+constexpr int kResident = WAVES == 7 ? 6 : VECS == 7 ? 8 : 1;  // waves on a SIMD, at least
 template <int TYPE, int GRAD, int VECS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void distill_rows(DistillArgs a, uint32_t row0) {
+__global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void distill_rows(DistillArgs a, uint32_t row0) {
     constexpr int kP = kPer<TYPE>, kThreads = 64 * WAVES;
     extern __shared__ uint32_t marks[];  // a bit for each class of the entries
     __shared__ float part[2][WAVES];
-    __shared__ int32_t where[kMaxTop];   // an entry's class, -1: none
-    __shared__ float mass[kMaxTop];      // the teacher's p of it
-    __shared__ double z2[kMaxTop];       // the student's exponent of it
-    __shared__ uint8_t later[kMaxTop];   // an earlier entry has its class
+    __shared__ EntryTable entries;
     __shared__ Entries found;
     const uint64_t m = (uint64_t)row0 + blockIdx.x;
-    const uint32_t t = threadIdx.x, lane = t % 64, wave = t / 64;
+    const uint32_t t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
     const uint32_t pieces = (a.V + kP - 1) / kP;
     const uint8_t *row = (const uint8_t *)a.logits + m * a.ld * (TYPE == ENTQ_F32 ? 4 : 2);
     uint8_t *grad = (uint8_t *)a.dlogits + m * a.ldd * (GRAD == ENTQ_F32 ? 4 : 2);
     const float weight = a.weight ? a.weight[m] : 1.0f;
     auto put = [&](uint32_t p, const float(&g)[kP]) {
         if constexpr (TYPE == GRAD) {
-            store_piece<TYPE>(grad, p, a.V, pack<TYPE>(g));
+            // (not read again here: 111.8 us where ordinary stores take 115.5,
+            // 4096 x 32000 bf16)
+            const v4i v = pack<TYPE>(g);
+            if ((p + 1) * kP <= a.V)
+                __builtin_nontemporal_store(v, (any_v4i *)(grad + p * 16));
+            else
+                store_piece<TYPE>(grad, p, a.V, v);
         } else {  // 16-bit gradients of fp32 logits
             uint16_t b[4];
 #pragma unroll
@@ -125,12 +227,23 @@ __global__ __launch_bounds__(64 * WAVES) void distill_rows(DistillArgs a, uint32
     };
     if (weight == 0.0f) {  // whatever the row holds
         if (a.loss && t == 0) a.loss[m] = 0.0f;
-        if (a.dlogits) {
+        if (a.dlogits && t < kThreads) {
             const float none[kP] = {};
             for (uint32_t p = t; p < pieces; p += kThreads) put(p, none);
         }
         return;
     }
+    if (wave == WAVES) {
+        OwnEntries own;
+        load_entries(a, m, lane, own);
+        __syncthreads();  // the marks are clear
+        const Entries f = sum_entries<TYPE>(a, m, row, lane, own, entries, marks, [] { __syncthreads(); });
+        if (lane == 0) found = f;
+        __syncthreads();  // the largest logit
+        __syncthreads();  // the sum
+    }
+    float top = -INFINITY, sum = 0.0f, c;
+    const bool tail = a.lse != nullptr;
     auto piece = [&](uint32_t p) {
         v4i v = load_piece<TYPE>(row, p, a.V);
         if ((p + 1) * kP > a.V) {
@@ -140,134 +253,75 @@ __global__ __launch_bounds__(64 * WAVES) void distill_rows(DistillArgs a, uint32
         }
         return v;
     };
-    v4i held[VECS ? VECS : 1];
-    if (VECS) {
-#pragma unroll
-        for (int i = 0; i < VECS; ++i) held[i] = piece(i * kThreads + t);
-    }
-    const bool tail = a.lse != nullptr;
-    for (uint32_t i = t; i < (a.V + 31) / 32; i += kThreads) marks[i] = 0;
-    __syncthreads();
-    bool bad = false, twice = false;  // an index beyond the classes, a class with two entries
-    for (uint32_t j = t; j < a.K; j += kThreads) {
-        const int64_t i = a.wide ? ((const int64_t *)a.index)[m * a.ldi + j] : ((const int32_t *)a.index)[m * a.ldi + j];
-        bad |= i >= (int64_t)a.V;
-        const bool in = i >= 0 && i < (int64_t)a.V;
-        where[j] = in ? (int32_t)i : -1;
-        later[j] = 0;
-        if (in) twice |= atomicOr(&marks[(uint32_t)i / 32], 1u << ((uint32_t)i % 32)) >> ((uint32_t)i % 32) & 1;
-    }
-    bad = __syncthreads_or(bad);
-    twice = __syncthreads_or(twice);
-    if (twice) {
-        for (uint32_t j = t; j < a.K; j += kThreads)
-            for (uint32_t i = 0; i < j; ++i)
-                if (where[i] >= 0 && where[i] == where[j]) later[j] = 1;
-        __syncthreads();
-    }
-    if (wave == 0) {
-        Entries f{};
-        double most = -INFINITY, peak = -INFINITY;
-        for (uint32_t j = lane; j < a.K; j += 64) {
-            if (where[j] < 0) continue;
-            f.any = 1;
-            const double v = read_teacher(a, m * a.ldt + j) * a.inv_t;
-            most = v > most || v != v ? v : most;
-            const double z = load_act<TYPE>(row, (uint32_t)where[j]) * a.scale64;
-            z2[j] = z;
-            peak = z > peak || z != z ? z : peak;
-        }
-        f.any = __any(f.any);
-        double lse;
-        if (tail) {
-            lse = a.lse[m];
-            peak = wave_max64(peak);
-            double s = 0.0;
-            for (uint32_t j = lane; j < a.K; j += 64)
-                if (where[j] >= 0 && !later[j]) {
-                    ++f.distinct;
-                    s += exp2(z2[j] - peak);
-                }
-            f.top2 = peak + log2(wave_sum(s));
-#pragma unroll
-            for (int o = 32; o; o /= 2) f.distinct += __shfl_xor(f.distinct, o);
-        } else {
-            most = wave_max64(most);
-            double s = 0.0;
-            for (uint32_t j = lane; j < a.K; j += 64)
-                if (where[j] >= 0) s += exp(read_teacher(a, m * a.ldt + j) * a.inv_t - most);
-            lse = most + log(wave_sum(s));
-        }
-        for (uint32_t j = lane; j < a.K; j += 64) {
-            if (where[j] < 0) continue;
-            const double logp = read_teacher(a, m * a.ldt + j) * a.inv_t - lse, p = exp(logp);
-            mass[j] = (float)p;
-            f.mass += p;
-            if (!(p == 0.0)) f.terms += p * (logp - z2[j] * kLn2);
-        }
-        f.mass = wave_sum(f.mass);
-        f.terms = wave_sum(f.terms);
-        if (lane == 0) found = f;
-    }
     // the entries' classes leave the row, with a tail
     auto outside = [&](v4i &v, uint32_t p) {
-        const uint32_t c = p * kP, out = c < a.V ? (marks[c / 32] >> (c % 32)) & ((1u << kP) - 1) : 0;
+        const uint32_t at = p * kP, out = at < a.V ? (marks[at / 32] >> (at % 32)) & ((1u << kP) - 1) : 0;
         if (out) {
 #pragma unroll
             for (int i = 0; i < kP; ++i)
                 if (out >> i & 1) remove<TYPE>(v, i);
         }
     };
-    if (VECS && tail) {
+    auto again = [&](uint32_t p) {
+        v4i v = piece(p);
+        if (tail) outside(v, p);
+        return v;
+    };
+    auto raise = [&](v4i v) {
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) outside(held[i], i * kThreads + t);
-    }
+        for (int i = 0; i < kP; ++i) top = fmaxf(top, act_of<TYPE>(v, i));
+    };
+    auto power = [&](v4i v, int i) { return __builtin_amdgcn_exp2f(__builtin_fmaf(act_of<TYPE>(v, i), a.scale, c)); };
+    auto add = [&](v4i v) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) sum += power(v, i);
+    };
+    v4i held[VECS ? VECS : 1];
     // (between two passes: values unpacked in one are not kept for the next,
     // which would take twice the registers of the pieces)
     auto forget = [&] {
 #pragma unroll
         for (int i = 0; i < (VECS ? VECS : 1); ++i) asm("" : "+v"(held[i]));
     };
-    auto again = [&](uint32_t p) {
-        v4i v = piece(p);
-        if (tail) outside(v, p);
-        return v;
-    };
-    float top = -INFINITY;
-    auto raise = [&](v4i v) {
+    if (wave < WAVES) {
+        if (VECS) {
 #pragma unroll
-        for (int i = 0; i < kP; ++i) top = fmaxf(top, act_of<TYPE>(v, i));
-    };
-    if (VECS) {
+            for (int i = 0; i < VECS; ++i) held[i] = piece(i * kThreads + t);
+        }
+        for (uint32_t i = t; i < (a.V + 31) / 32; i += kThreads) marks[i] = 0;
+        __syncthreads();
+        __syncthreads();
+        if (VECS) {
+            if (tail) {
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) raise(held[i]);
-    } else {
-        for (uint32_t p = t; p < pieces; p += kThreads) raise(again(p));
+                for (int i = 0; i < VECS; ++i) outside(held[i], i * kThreads + t);
+            }
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) raise(held[i]);
+            forget();
+        } else {
+            for (uint32_t p = t; p < pieces; p += kThreads) raise(again(p));
+        }
+        top = wave_maxf(top);
+        if (lane == 0) part[0][wave] = top;
+        __syncthreads();
     }
-    forget();
-    top = wave_maxf(top);
-    if (lane == 0) part[0][wave] = top;
-    __syncthreads();
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[0][w]);
     const float from = top == -INFINITY ? 0.0f : top;
-    const float c = (float)(64.0 - (double)from * a.scale);
-    auto power = [&](v4i v, int i) { return __builtin_amdgcn_exp2f(__builtin_fmaf(act_of<TYPE>(v, i), a.scale, c)); };
-    float sum = 0.0f;
-    auto add = [&](v4i v) {
+    c = (float)(64.0 - (double)from * a.scale);
+    if (wave < WAVES) {
+        if (VECS) {
 #pragma unroll
-        for (int i = 0; i < kP; ++i) sum += power(v, i);
-    };
-    if (VECS) {
-#pragma unroll
-        for (int i = 0; i < VECS; ++i) add(held[i]);
-    } else {
-        for (uint32_t p = t; p < pieces; p += kThreads) add(again(p));
+            for (int i = 0; i < VECS; ++i) add(held[i]);
+            forget();
+        } else {
+            for (uint32_t p = t; p < pieces; p += kThreads) add(again(p));
+        }
+        sum = wave_sumf(sum);
+        if (lane == 0) part[1][wave] = sum;
+        __syncthreads();
     }
-    forget();
-    sum = wave_sumf(sum);
-    if (lane == 0) part[1][wave] = sum;
-    __syncthreads();
     sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) sum += part[1][w];
@@ -278,55 +332,58 @@ __global__ __launch_bounds__(64 * WAVES) void distill_rows(DistillArgs a, uint32
                         (double)from * (a.scale64 - (double)a.scale);
     double all2 = sum == 0.0f ? -INFINITY : out2;
     float factor = 1.0f;  // of the powers in the gradient, times their sum
-    double loss = f.terms;
+    double pt = 0.0;
+    const double lo2 = all2;
     if (tail) {
         // the entries' classes and the others together
-        const double lo2 = all2;
         const float d = (float)(f.top2 - lo2), u = __builtin_amdgcn_exp2f(-fabsf(d));
         const float more = __builtin_amdgcn_logf(1.0f + u), inv = 1.0f / (1.0f + u);
         all2 = (f.top2 > lo2 ? f.top2 : lo2) + more;
         const float qt = d > 0.0f ? u * inv : inv;
-        const double pt = f.distinct == a.V ? 0.0 : fmax(0.0, 1.0 - f.mass);
+        pt = f.distinct == a.V ? 0.0 : fmax(0.0, 1.0 - f.mass);
         factor = (float)((double)qt - pt);
-        if (pt > 0.0 && t == 0) loss += pt * (log(pt) + (all2 - lo2) * kLn2);
     }
     if (!f.any) factor = 0.0f;
-    if (bad) factor = NAN;
-    if (a.loss && t == 0) {
-        loss = f.any ? loss + f.mass * (all2 * kLn2) : 0.0;
-        a.loss[m] = bad ? NAN : (float)(loss * weight);
+    if (f.bad) factor = NAN;
+    if (a.loss && wave == WAVES && lane == 0) {
+        double loss = f.any ? f.terms + f.mass * (all2 * kLn2) : 0.0;
+        if (f.any && pt > 0.0) loss += pt * (log(pt) + (all2 - lo2) * kLn2);
+        a.loss[m] = f.bad ? NAN : (float)(loss * weight);
     }
     if (!a.dlogits) return;
-    const double by64 = (double)weight * (a.dloss ? a.dloss[m] : 1.0f) * a.inv_t;
-    const float by = (float)by64;
-    factor = factor == 0.0f ? 0.0f : (float)((double)factor / sum * by64);
-    auto write = [&](uint32_t p, v4i v) {
-        float g[kP];
+    const double by = (double)weight * (a.dloss ? a.dloss[m] : 1.0f) * a.inv_t;
+    if (wave < WAVES) {
+        factor = factor == 0.0f ? 0.0f : (float)((double)factor / sum * by);
+        auto write = [&](uint32_t p, v4i v) {
+            float g[kP];
 #pragma unroll
-        for (int i = 0; i < kP; ++i) g[i] = factor == 0.0f ? 0.0f : factor * power(v, i);
-        put(p, g);
-    };
-    if (VECS) {
+            for (int i = 0; i < kP; ++i) g[i] = factor == 0.0f ? 0.0f : factor * power(v, i);
+            put(p, g);
+        };
+        if (VECS) {
 #pragma unroll
-        for (int i = 0; i < VECS; ++i)
-            if (i * kThreads + t < pieces) write(i * kThreads + t, held[i]);
-    } else {
-        for (uint32_t p = t; p < pieces; p += kThreads) write(p, again(p));
-    }
-    __syncthreads();
-    // the entries' classes again, each by its first entry
-    for (uint32_t j = t; j < a.K; j += kThreads) {
-        if (where[j] < 0 || later[j]) continue;
-        float p = mass[j];
-        if (twice) {
-            for (uint32_t i = j + 1; i < a.K; ++i)
-                if (where[i] == where[j]) p += mass[i];
+            for (int i = 0; i < VECS; ++i)
+                if (i * kThreads + t < pieces) write(i * kThreads + t, held[i]);
+        } else {
+            for (uint32_t p = t; p < pieces; p += kThreads) write(p, again(p));
         }
-        const float g = bad ? NAN : by * ((float)exp2(z2[j] - all2) - p);
+        __syncthreads();
+        return;
+    }
+    // the entries' classes, each by its first entry, over what the row's waves wrote there
+    __syncthreads();
+    for (uint32_t j = lane; j < a.K; j += 64) {
+        if (entries.where[j] < 0 || entries.later[j]) continue;
+        float p = entries.mass[j];
+        if (f.twice) {
+            for (uint32_t i = j + 1; i < a.K; ++i)
+                if (entries.where[i] == entries.where[j]) p += entries.mass[i];
+        }
+        const float g = f.bad ? NAN : (float)by * ((float)exp2(entries.z2[j] - all2) - p);
         if (GRAD == ENTQ_F32)
-            ((float *)grad)[where[j]] = g;
+            ((float *)grad)[entries.where[j]] = g;
         else
-            ((uint16_t *)grad)[where[j]] = bits16(g, GRAD == ENTQ_F16);
+            ((uint16_t *)grad)[entries.where[j]] = bits16(g, GRAD == ENTQ_F16);
     }
 }
 
@@ -334,7 +391,7 @@ template <int TYPE, int GRAD, int VECS, int WAVES>
 int launch_rows(const DistillArgs &a, hipStream_t s) {
     constexpr uint32_t kMost = 1u << 20;  // a launch's threads stay below 2^32
     for (uint64_t r = 0; r < a.M; r += kMost)
-        distill_rows<TYPE, GRAD, VECS, WAVES><<<(uint32_t)std::min<uint64_t>(kMost, a.M - r), 64 * WAVES,
+        distill_rows<TYPE, GRAD, VECS, WAVES><<<(uint32_t)std::min<uint64_t>(kMost, a.M - r), 64 * WAVES + 64,
                                                 (a.V + 31) / 32 * 4, s>>>(a, (uint32_t)r);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
@@ -342,11 +399,12 @@ int launch_rows(const DistillArgs &a, hipStream_t s) {
 template <int TYPE, int GRAD>
 int launch_distill(const DistillArgs &a, hipStream_t s) {
     const uint32_t pieces = (a.V + kPer<TYPE> - 1) / kPer<TYPE>;
-    if (pieces <= 1024) return launch_rows<TYPE, GRAD, 4, 4>(a, s);
-    if (pieces <= 4096) return launch_rows<TYPE, GRAD, 8, 8>(a, s);
-    if (pieces <= 8192) return launch_rows<TYPE, GRAD, 8, 16>(a, s);
-    if (pieces <= 16384) return launch_rows<TYPE, GRAD, 16, 16>(a, s);
-    return launch_rows<TYPE, GRAD, 0, 16>(a, s);
+    if (pieces <= 768) return launch_rows<TYPE, GRAD, 4, 3>(a, s);
+    if (pieces <= 4032) return launch_rows<TYPE, GRAD, 9, 7>(a, s);
+    if (pieces <= 6720) return launch_rows<TYPE, GRAD, 7, 15>(a, s);
+    if (pieces <= 8640) return launch_rows<TYPE, GRAD, 9, 15>(a, s);
+    if (pieces <= 16320) return launch_rows<TYPE, GRAD, 17, 15>(a, s);
+    return launch_rows<TYPE, GRAD, 0, 15>(a, s);
 }
 
 uint32_t bytes_of(int t) { return t == ENTQ_F32 ? 4 : 2; }

@@ -10,11 +10,15 @@ namespace entq {
 template <int TYPE>
 constexpr int kPer = TYPE == ENTQ_F32 ? 4 : 8;
 
-// Piece p of a row of n values at any address, zeros past its end.
+typedef v4i __attribute__((aligned(1))) any_v4i;
+
+// Piece p of a row of n values at any address, zeros past its end. (A row has
+// fewer than 2^32 bytes: offsets of 32 bits beside a base that is the same for
+// the wave take half the address registers.)
 template <int TYPE>
 __device__ __forceinline__ v4i load_piece(const void *row, uint32_t p, uint32_t n) {
     const uint32_t c = p * kPer<TYPE>;
-    if (c + kPer<TYPE> <= n) return ((const any16 *)((const uint8_t *)row + (uint64_t)p * 16))->v;
+    if (c + kPer<TYPE> <= n) return ((const any16 *)((const uint8_t *)row + p * 16))->v;
     v4i v = {0, 0, 0, 0};
     if (c >= n) return v;
 #pragma unroll
@@ -32,7 +36,7 @@ template <int TYPE>
 __device__ __forceinline__ void store_piece(void *row, uint32_t p, uint32_t n, v4i v) {
     const uint32_t c = p * kPer<TYPE>;
     if (c + kPer<TYPE> <= n) {
-        ((any16 *)((uint8_t *)row + (uint64_t)p * 16))->v = v;
+        ((any16 *)((uint8_t *)row + p * 16))->v = v;
         return;
     }
 #pragma unroll
