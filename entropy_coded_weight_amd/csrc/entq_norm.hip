@@ -286,33 +286,57 @@ __device__ __forceinline__ RowStats row_stats(const NormArgs &a, const double (&
     return r;
 }
 
+// What the columns of a piece have of their own. Absent factors are 1.
+template <int TYPE>
+struct Columns {
+    float pre[kPer<TYPE>], post[kPer<TYPE>], gate[kPer<TYPE>];
+};
+template <int TYPE>
+__device__ __forceinline__ void load_columns(const NormArgs &a, uint32_t p, Columns<TYPE> &c) {
+#pragma unroll
+    for (int i = 0; i < kPer<TYPE>; ++i) c.pre[i] = c.post[i] = c.gate[i] = 1.0f;
+    if (a.pre) load_floats<TYPE>(a.pre, p, a.N, c.pre);
+    if (a.post) load_floats<TYPE>(a.post, p, a.N, c.post);
+    if (a.gate_kind == ENTQ_GATE_CHANNEL) load_floats<TYPE>((const float *)a.gate, p, a.N, c.gate);
+}
+
+// A piece of each of a row's matrices (zeros for those that are absent).
+struct RowPiece {
+    v4i s, b, dout, dy, gate;
+};
+template <int TYPE>
+__device__ __forceinline__ RowPiece load_row(const NormArgs &a, uint64_t m, uint32_t p) {
+    const v4i none = {0, 0, 0, 0};
+    RowPiece r;
+    r.s = load_piece<TYPE>(row_of<TYPE>(a.x, a.ldx, m), p, a.N);
+    r.b = a.branch ? load_piece<TYPE>(row_of<TYPE>(a.branch, a.ldb, m), p, a.N) : none;
+    r.dout = a.dout ? load_piece<TYPE>(row_of<TYPE>(a.dout, a.lddo, m), p, a.N) : none;
+    r.dy = a.dy ? load_piece<TYPE>(row_of<TYPE>(a.dy, a.lddy, m), p, a.N) : none;
+    r.gate = a.gate_kind == ENTQ_GATE_FULL ? load_piece<TYPE>(row_of<TYPE>(a.gate, a.ldg, m), p, a.N) : none;
+    return r;
+}
+
 // A piece's part of the row's sums.
 template <int TYPE>
-__device__ __forceinline__ void add_sums(const NormArgs &a, uint64_t m, uint32_t p, v4i s, v4i b, v4i dout, v4i dy,
+__device__ __forceinline__ void add_sums(const NormArgs &a, const RowPiece &r, const Columns<TYPE> &c,
                                          double (&sum)[kRowSums]) {
-    constexpr int kP = kPer<TYPE>;
-    float pre[kP], post[kP], g[kP];
-    const bool rows = a.branch && (a.post || a.gate_kind == ENTQ_GATE_TOKEN);
-    if (a.dy) load_floats<TYPE>(a.pre, p, a.N, pre);
-    if (a.post) load_floats<TYPE>(a.post, p, a.N, post);
-    if (rows) load_gate<TYPE>(a, m, p, 1.0f, g);
+    const bool rows = a.post || a.gate_kind == ENTQ_GATE_TOKEN;
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-        const double sv = act_of<TYPE>(s, i);
-        double w = 0.0;
-        if (rows) {
-            const double bv = act_of<TYPE>(b, i);
-            if (a.post) sum[kBB] += bv * bv;
-            w = bv * (double)(a.post ? post[i] * g[i] : g[i]);
-            if (a.dout) sum[kBD] += w * (double)act_of<TYPE>(dout, i);
-        }
+    for (int i = 0; i < kPer<TYPE>; ++i) {
+        const double s = act_of<TYPE>(r.s, i);
+        const double y = a.dy ? act_of<TYPE>(r.dy, i) * c.pre[i] : 0.0f;
         if (a.dy) {
-            const double y = act_of<TYPE>(dy, i) * pre[i];
-            sum[kSS] += sv * sv;
-            sum[kSY] += sv * y;
-            if (rows) {
+            sum[kSS] += s * s;
+            sum[kSY] += s * y;
+        }
+        if (rows) {
+            const float b = act_of<TYPE>(r.b, i);
+            const double w = b * (c.post[i] * (a.gate_kind == ENTQ_GATE_FULL ? act_of<TYPE>(r.gate, i) : c.gate[i]));
+            sum[kBB] += (double)b * (double)b;
+            sum[kBD] += w * (double)act_of<TYPE>(r.dout, i);
+            if (a.dy) {
                 sum[kBY] += w * y;
-                sum[kBS] += w * sv;
+                sum[kBS] += w * s;
             }
         }
     }
@@ -321,18 +345,17 @@ __device__ __forceinline__ void add_sums(const NormArgs &a, uint64_t m, uint32_t
 // A piece's gradients, and its part of the column sums.
 template <int TYPE>
 __device__ __forceinline__ void gradients(const NormArgs &a, const RowStats &r, uint64_t m, uint32_t p, float token,
-                                          v4i sp, v4i bp, v4i dop, v4i dyp, float (&c_pre)[kPer<TYPE>],
+                                          const RowPiece &v, const Columns<TYPE> &c, float (&c_pre)[kPer<TYPE>],
                                           float (&c_post)[kPer<TYPE>]) {
     constexpr int kP = kPer<TYPE>;
-    float D[kP], f[kP], g[kP], w[kP];
+    float D[kP], f[kP];
 #pragma unroll
-    for (int i = 0; i < kP; ++i) D[i] = a.dout ? act_of<TYPE>(dop, i) : 0.0f;
+    for (int i = 0; i < kP; ++i) D[i] = act_of<TYPE>(v.dout, i);
     if (a.dy) {
-        load_floats<TYPE>(a.pre, p, a.N, w);
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
-            const float unit = act_of<TYPE>(sp, i) * r.rho1, dy = act_of<TYPE>(dyp, i);
-            D[i] += r.rho1 * (dy * w[i] - unit * r.c1);
+            const float unit = act_of<TYPE>(v.s, i) * r.rho1, dy = act_of<TYPE>(v.dy, i);
+            D[i] += r.rho1 * (dy * c.pre[i] - unit * r.c1);
             c_pre[i] += dy * unit;
         }
     }
@@ -342,19 +365,102 @@ __device__ __forceinline__ void gradients(const NormArgs &a, const RowStats &r, 
         store_piece<TYPE>(const_cast<uint8_t *>(row_of<TYPE>(a.dx, a.lddx, m)), p, a.N, pack<TYPE>(f));
     }
     if (!a.branch) return;
-    load_gate<TYPE>(a, m, p, token, g);
-    if (a.post) load_floats<TYPE>(a.post, p, a.N, w);
-    const bool varies = a.gate_kind == ENTQ_GATE_TOKEN || a.gate_kind == ENTQ_GATE_FULL;
+    const bool full = a.gate_kind == ENTQ_GATE_FULL;
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
-        const float b = act_of<TYPE>(bp, i), unit = b * r.rho2, dv = a.beta * g[i] * D[i];
-        c_post[i] += (varies ? g[i] * D[i] : D[i]) * unit;
-        f[i] = a.post ? r.rho2 * (w[i] * dv - unit * r.c2) : dv;
-        D[i] = a.beta * D[i] * (a.post ? unit * w[i] : unit);
+        const float b = act_of<TYPE>(v.b, i), unit = b * r.rho2;
+        const float row = full ? act_of<TYPE>(v.gate, i) : token;  // the gate's part that differs between tokens
+        const float dv = a.beta * (full ? row : token * c.gate[i]) * D[i];
+        c_post[i] += row * D[i] * unit;
+        f[i] = a.post ? r.rho2 * (c.post[i] * dv - unit * r.c2) : dv;
+        D[i] = a.beta * D[i] * (unit * c.post[i]);
     }
     if (a.db) store_piece<TYPE>(const_cast<uint8_t *>(row_of<TYPE>(a.db, a.lddb, m)), p, a.N, pack<TYPE>(f));
-    if (a.dgate && a.gate_kind == ENTQ_GATE_FULL)
+    if (a.dgate && full)
         store_piece<TYPE>(const_cast<uint8_t *>(row_of<TYPE>(a.dgate, a.lddg, m)), p, a.N, pack<TYPE>(D));
+}
+
+// The column sums of a piece into row `strip` of the partial sums.
+template <int TYPE>
+__device__ __forceinline__ void store_columns(const NormArgs &a, uint64_t strip, uint32_t p,
+                                              const float (&c_pre)[kPer<TYPE>], const float (&c_post)[kPer<TYPE>]) {
+    auto put = [&](float *part, const float(&c)[kPer<TYPE>]) {
+        if (!part) return;
+#pragma unroll
+        for (int i = 0; i < kPer<TYPE>; ++i)
+            if (p * kPer<TYPE> + i < a.N) part[strip * a.N + p * kPer<TYPE> + i] = c[i];
+    };
+    put(a.part_pre, c_pre);
+    put(a.part_post, c_post);
+}
+
+// Rows that fit the registers, in one pass: a group of WAVES waves takes every
+// strips-th row, VECS pieces a thread, and keeps the columns' factors and sums
+// over all its rows. The next row's pieces are on their way while this one's
+// gradients are computed. One barrier a row, for its sums.
+template <int TYPE, int VECS, int WAVES>
+__global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_back_rows(NormArgs a) {
+    constexpr int kThreads = 64 * WAVES, kRows = WAVES < 4 ? 4 / WAVES : 1;
+    __shared__ double part[2][4 * WAVES][8];
+    const uint32_t lane = threadIdx.x % 64, t = WAVES < 4 ? threadIdx.x % kThreads : threadIdx.x;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t strip = blockIdx.x * kRows + (WAVES < 4 ? wave / WAVES : 0);
+    if (strip >= a.strips) return;  // (a whole wave, where rows are waves)
+    const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;
+    float c_pre[VECS][kPer<TYPE>] = {}, c_post[VECS][kPer<TYPE>] = {};
+    Columns<TYPE> columns[VECS];
+    RowPiece v[VECS];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        load_columns<TYPE>(a, i * kThreads + t, columns[i]);
+        v[i] = load_row<TYPE>(a, strip, i * kThreads + t);
+    }
+    uint32_t turn = 0;
+    for (uint64_t m = strip; m < a.M; m += a.strips, turn ^= 1) {
+        double sum[kRowSums] = {};
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) add_sums<TYPE>(a, v[i], columns[i], sum);
+        RowPiece next[VECS];
+        const uint64_t after = m + a.strips < a.M ? m + a.strips : m;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) next[i] = load_row<TYPE>(a, after, i * kThreads + t);
+        const float token = token_gate(a, m);
+#pragma unroll
+        for (int i = 0; i < kRowSums; ++i) sum[i] = row16_sum(sum[i]);
+        if constexpr (WAVES == 1) {
+#pragma unroll
+            for (int i = 0; i < kRowSums; ++i) {
+                sum[i] += __shfl_xor(sum[i], 16);
+                sum[i] += __shfl_xor(sum[i], 32);
+            }
+        } else {
+            if (lane % 16 == 0) {
+#pragma unroll
+                for (int i = 0; i < kRowSums; ++i) part[turn][wave * 4 + lane / 16][i] = sum[i];
+            }
+            __syncthreads();
+            // lane l: sum l % 8 of every eighth partial sum
+            double s = 0.0;
+#pragma unroll
+            for (int i = 0; i < WAVES / 2; ++i) s += part[turn][i * 8 + lane / 8][lane % 8];
+            s += __shfl_xor(s, 8);
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+#pragma unroll
+            for (int i = 0; i < kRowSums; ++i) sum[i] = __shfl(s, i);
+        }
+        const RowStats r = row_stats(a, sum, token);
+        if (a.dgate && a.gate_kind == ENTQ_GATE_TOKEN && t == 0) ((float *)a.dgate)[m * a.lddg] = r.dgate;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const uint32_t p = i * kThreads + t;
+            if (p < pieces) gradients<TYPE>(a, r, m, p, token, v[i], columns[i], c_pre[i], c_post[i]);
+            v[i] = next[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+        if (i * kThreads + t < pieces) store_columns<TYPE>(a, strip, i * kThreads + t, c_pre[i], c_post[i]);
 }
 
 // Rows of any length, in two launches: the rows' sums, one workgroup a row ...
@@ -364,14 +470,11 @@ __global__ __launch_bounds__(512) void norm_back_sums(NormArgs a) {
     __shared__ double part[kRowSums][kWaves];
     const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;
     for (uint64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-        const v4i none = {0, 0, 0, 0};
         double sum[kRowSums] = {};
         for (uint32_t p = threadIdx.x; p < pieces; p += kThreads) {
-            const v4i s = load_piece<TYPE>(row_of<TYPE>(a.x, a.ldx, m), p, a.N);
-            const v4i b = a.branch ? load_piece<TYPE>(row_of<TYPE>(a.branch, a.ldb, m), p, a.N) : none;
-            const v4i d = a.dout ? load_piece<TYPE>(row_of<TYPE>(a.dout, a.lddo, m), p, a.N) : none;
-            const v4i y = a.dy ? load_piece<TYPE>(row_of<TYPE>(a.dy, a.lddy, m), p, a.N) : none;
-            add_sums<TYPE>(a, m, p, s, b, d, y, sum);
+            Columns<TYPE> c;
+            load_columns<TYPE>(a, p, c);
+            add_sums<TYPE>(a, load_row<TYPE>(a, m, p), c, sum);
         }
 #pragma unroll
         for (int i = 0; i < kRowSums; ++i) {
@@ -401,24 +504,14 @@ __global__ __launch_bounds__(256) void norm_back_apply(NormArgs a) {
     const uint32_t p = blockIdx.x * 256 + threadIdx.x;
     if (p * kP >= a.N) return;
     float c_pre[kP] = {}, c_post[kP] = {};
-    const v4i none = {0, 0, 0, 0};
+    Columns<TYPE> c;
+    load_columns<TYPE>(a, p, c);
     for (uint64_t m = blockIdx.y; m < a.M; m += a.strips) {
         const v4f st = *(const v4f *)(a.stats + m * 4);
-        const RowStats r{st[0], st[1], st[2], st[3], 0.0f};
-        const v4i s = load_piece<TYPE>(row_of<TYPE>(a.x, a.ldx, m), p, a.N);
-        const v4i b = a.branch ? load_piece<TYPE>(row_of<TYPE>(a.branch, a.ldb, m), p, a.N) : none;
-        const v4i d = a.dout ? load_piece<TYPE>(row_of<TYPE>(a.dout, a.lddo, m), p, a.N) : none;
-        const v4i y = a.dy ? load_piece<TYPE>(row_of<TYPE>(a.dy, a.lddy, m), p, a.N) : none;
-        gradients<TYPE>(a, r, m, p, token_gate(a, m), s, b, d, y, c_pre, c_post);
+        gradients<TYPE>(a, RowStats{st[0], st[1], st[2], st[3], 0.0f}, m, p, token_gate(a, m), load_row<TYPE>(a, m, p),
+                        c, c_pre, c_post);
     }
-    auto put = [&](float *part, const float(&c)[kP]) {
-        if (!part) return;
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-            if (p * kP + i < a.N) part[(uint64_t)blockIdx.y * a.N + p * kP + i] = c[i];
-    };
-    put(a.part_pre, c_pre);
-    put(a.part_post, c_post);
+    store_columns<TYPE>(a, blockIdx.y, p, c_pre, c_post);
 }
 
 // The strips' column sums added up, in a fixed order, and what they give.
@@ -429,21 +522,30 @@ struct ColumnArgs {
     float beta;
     uint32_t strips, N;
 };
-__global__ __launch_bounds__(256) void norm_columns(ColumnArgs a) {
-    const uint32_t n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.N) return;
-    auto total = [&](const float *part) {
-        double s = 0.0;
+constexpr uint32_t kColumnGroups = 8;  // of strips, side by side in a workgroup
+__global__ __launch_bounds__(32 * kColumnGroups) void norm_columns(ColumnArgs a) {
+    __shared__ double part[kColumnGroups][32];
+    const uint32_t c = threadIdx.x % 32, group = threadIdx.x / 32, n = blockIdx.x * 32 + c;
+    const bool pre = blockIdx.y == 0;
+    if (pre ? !a.dpre : !(a.dpost || a.dgate)) return;
+    const float *from = pre ? a.part_pre : a.part_post;
+    double s = 0.0;
+    if (n < a.N) {
 #pragma unroll 8
-        for (uint32_t i = 0; i < a.strips; ++i) s += part[(uint64_t)i * a.N + n];
-        return (float)s;
-    };
-    if (a.dpre) a.dpre[n] = total(a.part_pre);
-    if (a.dpost || a.dgate) {
-        const float s = a.beta * total(a.part_post);
-        if (a.dpost) a.dpost[n] = a.gate ? s * a.gate[n] : s;
-        if (a.dgate) a.dgate[n] = a.post ? s * a.post[n] : s;
+        for (uint32_t i = group; i < a.strips; i += kColumnGroups) s += from[(uint64_t)i * a.N + n];
     }
+    part[group][c] = s;
+    __syncthreads();
+    if (group || n >= a.N) return;
+#pragma unroll
+    for (uint32_t i = 1; i < kColumnGroups; ++i) s += part[i][c];
+    if (pre) {
+        a.dpre[n] = (float)s;
+        return;
+    }
+    const float v = a.beta * (float)s;
+    if (a.dpost) a.dpost[n] = a.gate ? v * a.gate[n] : v;
+    if (a.dgate) a.dgate[n] = a.post ? v * a.post[n] : v;
 }
 
 // ---------------------------------------------------------------------------
@@ -513,10 +615,20 @@ void zero(float *p, uint64_t ld, uint32_t n, hipStream_t s) {
     if (p && n) fill<<<(n + 255) / 256, 256, 0, s>>>(p, ld, n);
 }
 
-// Strips of rows, each with column sums of its own.
-uint32_t strips_of(const entq_norm &n) {
-    const uint32_t wide = (n.cols + 2047) / 2048;
-    return std::max(1u, std::min(n.rows, std::max(1u, 1024 / std::max(1u, wide))));
+// How the backward pass runs: rows in the registers of `waves` waves, `vecs`
+// pieces a thread, or (vecs 0) in two launches; and its strips of rows, each
+// with column sums of its own.
+struct BackPlan {
+    uint32_t vecs, waves, strips;
+};
+BackPlan back_plan(const entq_norm &n) {
+    const uint32_t per = n.type == ENTQ_F32 ? 4 : 8, pieces = (n.cols + per - 1) / per;
+    const BackPlan p = pieces <= 64     ? BackPlan{1, 1, 1024}
+                       : pieces <= 256  ? BackPlan{1, 4, 512}
+                       : pieces <= 512  ? BackPlan{1, 8, 512}
+                       : pieces <= 1024 ? BackPlan{2, 8, 256}
+                                        : BackPlan{0, 8, std::max(1u, 1024 / ((n.cols + 2047) / 2048))};
+    return {p.vecs, p.waves, std::max(1u, std::min(n.rows, p.strips))};
 }
 
 struct Room {
@@ -526,17 +638,23 @@ Room room_of(const entq_norm &n) {
     const auto up = [](uint64_t b) { return (b + 255) / 256 * 256; };
     Room r{};
     r.pre = up((uint64_t)n.rows * 16);
-    const uint64_t one = up((uint64_t)strips_of(n) * n.cols * 4);
+    const uint64_t one = up((uint64_t)back_plan(n).strips * n.cols * 4);
     r.post = r.pre + one;
     r.all = r.post + one;
     return r;
 }
 
 template <int TYPE>
-int launch_back(const NormArgs &a, hipStream_t s) {
-    norm_back_sums<TYPE><<<std::min(a.M, 1u << 20), 512, 0, s>>>(a);
-    const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;
-    norm_back_apply<TYPE><<<dim3((pieces + 255) / 256, a.strips), 256, 0, s>>>(a);
+int launch_back(const BackPlan &p, const NormArgs &a, hipStream_t s) {
+    if (p.waves == 1) norm_back_rows<TYPE, 1, 1><<<(a.strips + 3) / 4, 256, 0, s>>>(a);
+    if (p.waves == 4) norm_back_rows<TYPE, 1, 4><<<a.strips, 256, 0, s>>>(a);
+    if (p.waves == 8 && p.vecs == 1) norm_back_rows<TYPE, 1, 8><<<a.strips, 512, 0, s>>>(a);
+    if (p.waves == 8 && p.vecs == 2) norm_back_rows<TYPE, 2, 8><<<a.strips, 512, 0, s>>>(a);
+    if (!p.vecs) {
+        norm_back_sums<TYPE><<<std::min(a.M, 1u << 20), 512, 0, s>>>(a);
+        const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;
+        norm_back_apply<TYPE><<<dim3((pieces + 255) / 256, a.strips), 256, 0, s>>>(a);
+    }
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
@@ -630,15 +748,16 @@ entq_status entq_norm_block_backward(const entq_norm *n, const void *d_dout, uin
     a.stats = (float *)d_workspace;
     a.part_pre = d_dpre ? (float *)((uint8_t *)d_workspace + room.pre) : nullptr;
     a.part_post = d_dpost || channel ? (float *)((uint8_t *)d_workspace + room.post) : nullptr;
-    a.strips = strips_of(*n);
-    const int r = n->type == ENTQ_BF16  ? launch_back<ENTQ_BF16>(a, s)
-                  : n->type == ENTQ_F16 ? launch_back<ENTQ_F16>(a, s)
-                                        : launch_back<ENTQ_F32>(a, s);
+    const BackPlan plan = back_plan(*n);
+    a.strips = plan.strips;
+    const int r = n->type == ENTQ_BF16  ? launch_back<ENTQ_BF16>(plan, a, s)
+                  : n->type == ENTQ_F16 ? launch_back<ENTQ_F16>(plan, a, s)
+                                        : launch_back<ENTQ_F32>(plan, a, s);
     if (r != ENTQ_OK || !(d_dpre || d_dpost || channel)) return (entq_status)r;
     const ColumnArgs c{a.part_pre, a.part_post, d_dpre, d_dpost, channel,
                        n->gate == ENTQ_GATE_CHANNEL ? (const float *)n->d_gate : nullptr, n->d_post, n->beta,
                        a.strips, n->cols};
-    norm_columns<<<(n->cols + 255) / 256, 256, 0, s>>>(c);
+    norm_columns<<<dim3((n->cols + 31) / 32, 2), 32 * kColumnGroups, 0, s>>>(c);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 

@@ -86,6 +86,23 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
+// A lane's value plus that of the lane that CTRL names in its row of 16.
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// The sum of each row of 16 lanes, in all of them: lanes 1 and 2 away, then the
+// mirrored half row and row.
+__device__ __forceinline__ double row16_sum(double v) {
+    v = add_dpp<0xB1>(v);
+    v = add_dpp<0x4E>(v);
+    v = add_dpp<0x141>(v);
+    return add_dpp<0x140>(v);
+}
+
 // 1 / sqrt(v) of a positive 64-bit value, rounded to fp32 (0 for an infinity):
 // the hardware's estimate and one step of Newton's method.
 __device__ __forceinline__ float rsqrt64(double v) {
