@@ -300,50 +300,74 @@ __device__ __forceinline__ void load_columns(const NormArgs &a, uint32_t p, Colu
     if (a.gate_kind == ENTQ_GATE_CHANNEL) load_floats<TYPE>((const float *)a.gate, p, a.N, c.gate);
 }
 
-// A piece of each of a row's matrices (zeros for those that are absent).
+// A piece of each of a row's matrices, zeros for those that are absent or not
+// needed (FULL: the gate is a matrix).
 struct RowPiece {
     v4i s, b, dout, dy, gate;
 };
-template <int TYPE>
+template <int TYPE, bool FULL>
 __device__ __forceinline__ RowPiece load_row(const NormArgs &a, uint64_t m, uint32_t p) {
-    const v4i none = {0, 0, 0, 0};
-    RowPiece r;
-    r.s = load_piece<TYPE>(row_of<TYPE>(a.x, a.ldx, m), p, a.N);
-    r.b = a.branch ? load_piece<TYPE>(row_of<TYPE>(a.branch, a.ldb, m), p, a.N) : none;
-    r.dout = a.dout ? load_piece<TYPE>(row_of<TYPE>(a.dout, a.lddo, m), p, a.N) : none;
-    r.dy = a.dy ? load_piece<TYPE>(row_of<TYPE>(a.dy, a.lddy, m), p, a.N) : none;
-    r.gate = a.gate_kind == ENTQ_GATE_FULL ? load_piece<TYPE>(row_of<TYPE>(a.gate, a.ldg, m), p, a.N) : none;
+    RowPiece r{};
+    const uint8_t *s = row_of<TYPE>(a.x, a.ldx, m), *b = row_of<TYPE>(a.branch, a.ldb, m),
+                  *dout = row_of<TYPE>(a.dout, a.lddo, m), *dy = row_of<TYPE>(a.dy, a.lddy, m),
+                  *gate = row_of<TYPE>(a.gate, a.ldg, m);
+    const bool unit = a.branch && (a.post || a.gate_kind != ENTQ_GATE_NONE);
+    if (whole_piece<TYPE>(p, a.N)) {
+        if (a.dout) r.dout = load_whole(dout, p);
+        if (a.dy) {
+            r.s = load_whole(s, p);
+            r.dy = load_whole(dy, p);
+        }
+        if (unit) r.b = load_whole(b, p);
+        if (FULL) r.gate = load_whole(gate, p);
+    } else {
+        if (a.dout) r.dout = load_rest<TYPE>(dout, p, a.N);
+        if (a.dy) {
+            r.s = load_rest<TYPE>(s, p, a.N);
+            r.dy = load_rest<TYPE>(dy, p, a.N);
+        }
+        if (unit) r.b = load_rest<TYPE>(b, p, a.N);
+        if (FULL) r.gate = load_rest<TYPE>(gate, p, a.N);
+    }
     return r;
 }
 
 // A piece's part of the row's sums.
-template <int TYPE>
+template <int TYPE, bool FULL>
 __device__ __forceinline__ void add_sums(const NormArgs &a, const RowPiece &r, const Columns<TYPE> &c,
                                          double (&sum)[kRowSums]) {
-    const bool rows = a.post || a.gate_kind == ENTQ_GATE_TOKEN;
+    constexpr int kP = kPer<TYPE>;
+    double y[kP], s[kP];
+    if (a.dy) {
 #pragma unroll
-    for (int i = 0; i < kPer<TYPE>; ++i) {
-        const double s = act_of<TYPE>(r.s, i);
-        const double y = a.dy ? act_of<TYPE>(r.dy, i) * c.pre[i] : 0.0f;
-        if (a.dy) {
-            sum[kSS] += s * s;
-            sum[kSY] += s * y;
+        for (int i = 0; i < kP; ++i) {
+            s[i] = act_of<TYPE>(r.s, i);
+            y[i] = act_of<TYPE>(r.dy, i) * c.pre[i];
+            sum[kSS] += s[i] * s[i];
+            sum[kSY] += s[i] * y[i];
         }
-        if (rows) {
+    }
+    if (a.post || a.gate_kind == ENTQ_GATE_TOKEN) {
+        double w[kP];
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
             const float b = act_of<TYPE>(r.b, i);
-            const double w = b * (c.post[i] * (a.gate_kind == ENTQ_GATE_FULL ? act_of<TYPE>(r.gate, i) : c.gate[i]));
+            w[i] = b * (c.post[i] * (FULL ? act_of<TYPE>(r.gate, i) : c.gate[i]));
             sum[kBB] += (double)b * (double)b;
-            sum[kBD] += w * (double)act_of<TYPE>(r.dout, i);
-            if (a.dy) {
-                sum[kBY] += w * y;
-                sum[kBS] += w * s;
+            sum[kBD] += w[i] * (double)act_of<TYPE>(r.dout, i);
+        }
+        if (a.dy) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i) {
+                sum[kBY] += w[i] * y[i];
+                sum[kBS] += w[i] * s[i];
             }
         }
     }
 }
 
 // A piece's gradients, and its part of the column sums.
-template <int TYPE>
+template <int TYPE, bool FULL>
 __device__ __forceinline__ void gradients(const NormArgs &a, const RowStats &r, uint64_t m, uint32_t p, float token,
                                           const RowPiece &v, const Columns<TYPE> &c, float (&c_pre)[kPer<TYPE>],
                                           float (&c_post)[kPer<TYPE>]) {
@@ -359,25 +383,43 @@ __device__ __forceinline__ void gradients(const NormArgs &a, const RowStats &r, 
             c_pre[i] += dy * unit;
         }
     }
-    if (a.dx) {
 #pragma unroll
-        for (int i = 0; i < kP; ++i) f[i] = a.alpha * D[i];
-        store_piece<TYPE>(const_cast<uint8_t *>(row_of<TYPE>(a.dx, a.lddx, m)), p, a.N, pack<TYPE>(f));
-    }
-    if (!a.branch) return;
-    const bool full = a.gate_kind == ENTQ_GATE_FULL;
+    for (int i = 0; i < kP; ++i) f[i] = a.alpha * D[i];
+    const v4i dx = pack<TYPE>(f);
+    v4i db = {0, 0, 0, 0}, dgate = {0, 0, 0, 0};
+    if (a.branch) {
+        float unit[kP];
+        const float bt = a.beta * token;
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-        const float b = act_of<TYPE>(v.b, i), unit = b * r.rho2;
-        const float row = full ? act_of<TYPE>(v.gate, i) : token;  // the gate's part that differs between tokens
-        const float dv = a.beta * (full ? row : token * c.gate[i]) * D[i];
-        c_post[i] += row * D[i] * unit;
-        f[i] = a.post ? r.rho2 * (c.post[i] * dv - unit * r.c2) : dv;
-        D[i] = a.beta * D[i] * (unit * c.post[i]);
+        for (int i = 0; i < kP; ++i) {
+            unit[i] = act_of<TYPE>(v.b, i) * r.rho2;
+            // (its first factor: the gate's part that differs between tokens)
+            c_post[i] += (FULL ? act_of<TYPE>(v.gate, i) : token) * D[i] * unit[i];
+            f[i] = FULL ? a.beta * act_of<TYPE>(v.gate, i) * D[i] : bt * c.gate[i] * D[i];
+        }
+        if (a.post) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i) f[i] = r.rho2 * (c.post[i] * f[i] - unit[i] * r.c2);
+        }
+        db = pack<TYPE>(f);
+        if (FULL) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i) f[i] = a.beta * D[i] * (unit[i] * c.post[i]);
+            dgate = pack<TYPE>(f);
+        }
     }
-    if (a.db) store_piece<TYPE>(const_cast<uint8_t *>(row_of<TYPE>(a.db, a.lddb, m)), p, a.N, pack<TYPE>(f));
-    if (a.dgate && full)
-        store_piece<TYPE>(const_cast<uint8_t *>(row_of<TYPE>(a.dgate, a.lddg, m)), p, a.N, pack<TYPE>(D));
+    uint8_t *to_dx = const_cast<uint8_t *>(row_of<TYPE>(a.dx, a.lddx, m)),
+            *to_db = const_cast<uint8_t *>(row_of<TYPE>(a.db, a.lddb, m)),
+            *to_dgate = const_cast<uint8_t *>(row_of<TYPE>(a.dgate, a.lddg, m));
+    if (whole_piece<TYPE>(p, a.N)) {
+        if (a.dx) store_whole(to_dx, p, dx);
+        if (a.db) store_whole(to_db, p, db);
+        if (FULL && a.dgate) store_whole(to_dgate, p, dgate);
+    } else {
+        if (a.dx) store_rest<TYPE>(to_dx, p, a.N, dx);
+        if (a.db) store_rest<TYPE>(to_db, p, a.N, db);
+        if (FULL && a.dgate) store_rest<TYPE>(to_dgate, p, a.N, dgate);
+    }
 }
 
 // The column sums of a piece into row `strip` of the partial sums.
@@ -398,7 +440,7 @@ __device__ __forceinline__ void store_columns(const NormArgs &a, uint64_t strip,
 // strips-th row, VECS pieces a thread, and keeps the columns' factors and sums
 // over all its rows. The next row's pieces are on their way while this one's
 // gradients are computed. One barrier a row, for its sums.
-template <int TYPE, int VECS, int WAVES>
+template <int TYPE, int VECS, int WAVES, bool FULL>
 __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_back_rows(NormArgs a) {
     constexpr int kThreads = 64 * WAVES, kRows = WAVES < 4 ? 4 / WAVES : 1;
     __shared__ double part[2][4 * WAVES][8];
@@ -413,17 +455,17 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_back_rows(N
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         load_columns<TYPE>(a, i * kThreads + t, columns[i]);
-        v[i] = load_row<TYPE>(a, strip, i * kThreads + t);
+        v[i] = load_row<TYPE, FULL>(a, strip, i * kThreads + t);
     }
     uint32_t turn = 0;
     for (uint64_t m = strip; m < a.M; m += a.strips, turn ^= 1) {
         double sum[kRowSums] = {};
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) add_sums<TYPE>(a, v[i], columns[i], sum);
+        for (int i = 0; i < VECS; ++i) add_sums<TYPE, FULL>(a, v[i], columns[i], sum);
         RowPiece next[VECS];
         const uint64_t after = m + a.strips < a.M ? m + a.strips : m;
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) next[i] = load_row<TYPE>(a, after, i * kThreads + t);
+        for (int i = 0; i < VECS; ++i) next[i] = load_row<TYPE, FULL>(a, after, i * kThreads + t);
         const float token = token_gate(a, m);
 #pragma unroll
         for (int i = 0; i < kRowSums; ++i) sum[i] = row16_sum(sum[i]);
@@ -454,7 +496,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_back_rows(N
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
             const uint32_t p = i * kThreads + t;
-            if (p < pieces) gradients<TYPE>(a, r, m, p, token, v[i], columns[i], c_pre[i], c_post[i]);
+            if (p < pieces) gradients<TYPE, FULL>(a, r, m, p, token, v[i], columns[i], c_pre[i], c_post[i]);
             v[i] = next[i];
         }
     }
@@ -464,7 +506,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_back_rows(N
 }
 
 // Rows of any length, in two launches: the rows' sums, one workgroup a row ...
-template <int TYPE>
+template <int TYPE, bool FULL>
 __global__ __launch_bounds__(512) void norm_back_sums(NormArgs a) {
     constexpr int kThreads = 512, kWaves = kThreads / 64;
     __shared__ double part[kRowSums][kWaves];
@@ -474,7 +516,7 @@ __global__ __launch_bounds__(512) void norm_back_sums(NormArgs a) {
         for (uint32_t p = threadIdx.x; p < pieces; p += kThreads) {
             Columns<TYPE> c;
             load_columns<TYPE>(a, p, c);
-            add_sums<TYPE>(a, load_row<TYPE>(a, m, p), c, sum);
+            add_sums<TYPE, FULL>(a, load_row<TYPE, FULL>(a, m, p), c, sum);
         }
 #pragma unroll
         for (int i = 0; i < kRowSums; ++i) {
@@ -498,7 +540,7 @@ __global__ __launch_bounds__(512) void norm_back_sums(NormArgs a) {
 
 // ... and the gradients: a thread keeps the column sums of one piece over a
 // strip of the rows.
-template <int TYPE>
+template <int TYPE, bool FULL>
 __global__ __launch_bounds__(256) void norm_back_apply(NormArgs a) {
     constexpr int kP = kPer<TYPE>;
     const uint32_t p = blockIdx.x * 256 + threadIdx.x;
@@ -508,8 +550,8 @@ __global__ __launch_bounds__(256) void norm_back_apply(NormArgs a) {
     load_columns<TYPE>(a, p, c);
     for (uint64_t m = blockIdx.y; m < a.M; m += a.strips) {
         const v4f st = *(const v4f *)(a.stats + m * 4);
-        gradients<TYPE>(a, RowStats{st[0], st[1], st[2], st[3], 0.0f}, m, p, token_gate(a, m), load_row<TYPE>(a, m, p),
-                        c, c_pre, c_post);
+        gradients<TYPE, FULL>(a, RowStats{st[0], st[1], st[2], st[3], 0.0f}, m, p, token_gate(a, m),
+                              load_row<TYPE, FULL>(a, m, p), c, c_pre, c_post);
     }
     store_columns<TYPE>(a, blockIdx.y, p, c_pre, c_post);
 }
@@ -644,17 +686,24 @@ Room room_of(const entq_norm &n) {
     return r;
 }
 
+template <int TYPE, bool FULL>
+void launch_back(const BackPlan &p, const NormArgs &a, hipStream_t s) {
+    if (p.waves == 1) norm_back_rows<TYPE, 1, 1, FULL><<<(a.strips + 3) / 4, 256, 0, s>>>(a);
+    if (p.waves == 4) norm_back_rows<TYPE, 1, 4, FULL><<<a.strips, 256, 0, s>>>(a);
+    if (p.waves == 8 && p.vecs == 1) norm_back_rows<TYPE, 1, 8, FULL><<<a.strips, 512, 0, s>>>(a);
+    if (p.waves == 8 && p.vecs == 2) norm_back_rows<TYPE, 2, 8, FULL><<<a.strips, 512, 0, s>>>(a);
+    if (!p.vecs) {
+        norm_back_sums<TYPE, FULL><<<std::min(a.M, 1u << 20), 512, 0, s>>>(a);
+        const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;
+        norm_back_apply<TYPE, FULL><<<dim3((pieces + 255) / 256, a.strips), 256, 0, s>>>(a);
+    }
+}
 template <int TYPE>
 int launch_back(const BackPlan &p, const NormArgs &a, hipStream_t s) {
-    if (p.waves == 1) norm_back_rows<TYPE, 1, 1><<<(a.strips + 3) / 4, 256, 0, s>>>(a);
-    if (p.waves == 4) norm_back_rows<TYPE, 1, 4><<<a.strips, 256, 0, s>>>(a);
-    if (p.waves == 8 && p.vecs == 1) norm_back_rows<TYPE, 1, 8><<<a.strips, 512, 0, s>>>(a);
-    if (p.waves == 8 && p.vecs == 2) norm_back_rows<TYPE, 2, 8><<<a.strips, 512, 0, s>>>(a);
-    if (!p.vecs) {
-        norm_back_sums<TYPE><<<std::min(a.M, 1u << 20), 512, 0, s>>>(a);
-        const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;
-        norm_back_apply<TYPE><<<dim3((pieces + 255) / 256, a.strips), 256, 0, s>>>(a);
-    }
+    if (a.gate_kind == ENTQ_GATE_FULL)
+        launch_back<TYPE, true>(p, a, s);
+    else
+        launch_back<TYPE, false>(p, a, s);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 

@@ -12,13 +12,24 @@ constexpr int kPer = TYPE == ENTQ_F32 ? 4 : 8;
 
 typedef v4i __attribute__((aligned(1))) any_v4i;
 
-// Piece p of a row of n values at any address, zeros past its end. (A row has
-// fewer than 2^32 bytes: offsets of 32 bits beside a base that is the same for
-// the wave take half the address registers.)
+// Whether piece p of a row of n values is whole.
 template <int TYPE>
-__device__ __forceinline__ v4i load_piece(const void *row, uint32_t p, uint32_t n) {
+__device__ __forceinline__ bool whole_piece(uint32_t p, uint32_t n) {
+    return (p + 1) * kPer<TYPE> <= n;
+}
+// A whole piece at any address. (A row has fewer than 2^32 bytes: offsets of 32
+// bits beside a base that is the same for the wave take half the address
+// registers.)
+__device__ __forceinline__ v4i load_whole(const void *row, uint32_t p) {
+    return ((const any16 *)((const uint8_t *)row + p * 16))->v;
+}
+__device__ __forceinline__ void store_whole(void *row, uint32_t p, v4i v) {
+    ((any16 *)((uint8_t *)row + p * 16))->v = v;
+}
+// A row's last piece, which it does not fill, or one behind it: zeros there.
+template <int TYPE>
+__device__ __forceinline__ v4i load_rest(const void *row, uint32_t p, uint32_t n) {
     const uint32_t c = p * kPer<TYPE>;
-    if (c + kPer<TYPE> <= n) return ((const any16 *)((const uint8_t *)row + p * 16))->v;
     v4i v = {0, 0, 0, 0};
     if (c >= n) return v;
 #pragma unroll
@@ -31,14 +42,9 @@ __device__ __forceinline__ v4i load_piece(const void *row, uint32_t p, uint32_t 
     }
     return v;
 }
-
 template <int TYPE>
-__device__ __forceinline__ void store_piece(void *row, uint32_t p, uint32_t n, v4i v) {
+__device__ __forceinline__ void store_rest(void *row, uint32_t p, uint32_t n, v4i v) {
     const uint32_t c = p * kPer<TYPE>;
-    if (c + kPer<TYPE> <= n) {
-        ((any16 *)((uint8_t *)row + p * 16))->v = v;
-        return;
-    }
 #pragma unroll
     for (int i = 0; i < kPer<TYPE> - 1; ++i) {
         if (c + i >= n) continue;
@@ -47,6 +53,17 @@ __device__ __forceinline__ void store_piece(void *row, uint32_t p, uint32_t n, v
         else
             ((uint16_t *)row)[c + i] = (uint16_t)((uint32_t)v[i / 2] >> (16 * (i % 2)));
     }
+}
+template <int TYPE>
+__device__ __forceinline__ v4i load_piece(const void *row, uint32_t p, uint32_t n) {
+    return whole_piece<TYPE>(p, n) ? load_whole(row, p) : load_rest<TYPE>(row, p, n);
+}
+template <int TYPE>
+__device__ __forceinline__ void store_piece(void *row, uint32_t p, uint32_t n, v4i v) {
+    if (whole_piece<TYPE>(p, n))
+        store_whole(row, p, v);
+    else
+        store_rest<TYPE>(row, p, n, v);
 }
 
 // The values rounded to the type, as a piece.
