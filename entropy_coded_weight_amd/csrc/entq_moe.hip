@@ -14,7 +14,7 @@ constexpr uint32_t kTokens = ENTQ_MOE_MAX_TOKENS, kMaxExperts = ENTQ_MOE_MAX_EXP
 struct MoeArgs {
     const void *x, *router;
     uint64_t ldx, ldr;
-    int x_type, router_type;
+    int router_type;
     uint32_t M, E, K, D, F, N;     // tokens, experts, chosen, width, hidden, results
     int act;
     bool normalize;
@@ -22,11 +22,12 @@ struct MoeArgs {
     const float *sw[3];
     uint64_t ldw[3], stride[3], sstride[3];
     // the workspace
+    uint64_t *tokens;              // [E]: a bit for each token that chose the expert
     int8_t *codes;                 // [M][ldc] of x
     float *sx;                     // [M]
     double *logits;                // [M][E]
-    int32_t *place;                // [E][M]: which of its token's choices the expert is, -1: none
-    float *share;                  // [E][M]
+    int8_t *place;                 // [E][M]: which of its token's choices the expert is, -1: none
+    float *share;                  // [M K]: the token's weight for its choice
     float *h;                      // [M K][F]
     int8_t *hcodes;                // [M K][ldh]
     float *sh;                     // [M K]
@@ -39,29 +40,88 @@ struct MoeArgs {
     float *weights;                // [M][K], or null
 };
 
-__device__ __forceinline__ float value(const void *p, int type, uint64_t at) {
-    return type == ENTQ_F32 ? ((const float *)p)[at] : from16(((const uint16_t *)p)[at], type == ENTQ_F16);
+// Values c..c+7 of a row of n values of any type, zeros past its end.
+template <int TYPE>
+__device__ __forceinline__ void load8(const void *row, uint32_t c, uint32_t n, float (&f)[8]) {
+#pragma unroll
+    for (int h = 0; h < 8 / kPer<TYPE>; ++h) {
+        const v4i v = load_piece<TYPE>(row, c / kPer<TYPE> + h, n);
+#pragma unroll
+        for (int i = 0; i < kPer<TYPE>; ++i) f[h * kPer<TYPE> + i] = act_of<TYPE>(v, i);
+    }
+}
+
+// A token's codes and scale (entq_quantize_rows), zeros up to ldc; one workgroup.
+template <int TYPE>
+__device__ __forceinline__ void quantize_token(const MoeArgs &a, uint32_t m) {
+    __shared__ uint32_t top[4];
+    const uint8_t *x = (const uint8_t *)a.x + m * a.ldx * (TYPE == ENTQ_F32 ? 4 : 2);
+    const uint32_t groups = (uint32_t)(a.ldc / 8);
+    uint32_t big = 0;
+    for (uint32_t g = threadIdx.x; g < groups; g += 256) {
+        float f[8];
+        load8<TYPE>(x, g * 8, a.D, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    }
+    big = wave_max(big);
+    if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) big = max(big, top[i]);
+    const Quantizer z(big);
+    if (threadIdx.x == 0) a.sx[m] = z.scale;
+    for (uint32_t g = threadIdx.x; g < groups; g += 256) {
+        float f[8];
+        load8<TYPE>(x, g * 8, a.D, f);
+        uint32_t q[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i / 4] |= z.code(f[i]) << (8 * (i % 4));
+        *(v2i *)(a.codes + m * a.ldc + g * 8) = v2i{(int)q[0], (int)q[1]};
+    }
 }
 
 // The router's logits, summed in 64 bits: which expert is chosen hangs on
-// their order. One workgroup per expert and 8 tokens.
+// their order. A workgroup takes one expert and up to 8 tokens; those after
+// them quantise a token each.
+constexpr uint32_t kRouteTokens = 8;
+template <int TYPE>
 __global__ __launch_bounds__(256) void moe_route(MoeArgs a) {
-    __shared__ double part[4][8];
-    const uint32_t e = blockIdx.x, m0 = blockIdx.y * 8, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    double sum[8] = {};
-    for (uint32_t c = threadIdx.x; c < a.D; c += 256) {
-        const double r = value(a.router, a.router_type, e * a.ldr + c);
+    const uint32_t groups = (a.M + kRouteTokens - 1) / kRouteTokens;
+    if (blockIdx.x >= a.E * groups) return quantize_token<TYPE>(a, blockIdx.x - a.E * groups);
+    __shared__ double part[4][kRouteTokens];
+    const uint32_t e = blockIdx.x / groups, m0 = blockIdx.x % groups * kRouteTokens;
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    if (m0 == 0 && threadIdx.x == 0) a.tokens[e] = 0;  // for the choice that comes next
+    double sum[kRouteTokens] = {};
+    const uint32_t all = (a.D + 7) / 8;
+    for (uint32_t g = threadIdx.x; g < all; g += 256) {
+        float r[8], x[kRouteTokens][8];
+        const uint8_t *row = (const uint8_t *)a.router + e * a.ldr * (a.router_type == ENTQ_F32 ? 4 : 2);
+        if (a.router_type == ENTQ_F32) load8<ENTQ_F32>(row, g * 8, a.D, r);
+        if (a.router_type == ENTQ_BF16) load8<ENTQ_BF16>(row, g * 8, a.D, r);
+        if (a.router_type == ENTQ_F16) load8<ENTQ_F16>(row, g * 8, a.D, r);
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i)
-            if (m0 + i < a.M) sum[i] += r * (double)value(a.x, a.x_type, (m0 + i) * a.ldx + c);
+        for (uint32_t i = 0; i < kRouteTokens; ++i)
+            if (m0 + i < a.M)
+                load8<TYPE>((const uint8_t *)a.x + (m0 + i) * a.ldx * (TYPE == ENTQ_F32 ? 4 : 2), g * 8, a.D, x[i]);
+#pragma unroll
+        for (uint32_t i = 0; i < kRouteTokens; ++i)
+            if (m0 + i < a.M) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) sum[i] += (double)r[c] * (double)x[i][c];
+            }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        sum[i] = wave_sum(sum[i]);
+    for (uint32_t i = 0; i < kRouteTokens; ++i) {
+        if (m0 + i >= a.M) continue;
+        sum[i] = row16_sum(sum[i]);
+        sum[i] += __shfl_xor(sum[i], 16);
+        sum[i] += __shfl_xor(sum[i], 32);
         if (lane == 0) part[wave][i] = sum[i];
     }
     __syncthreads();
-    if (threadIdx.x < 8 && m0 + threadIdx.x < a.M)
+    if (threadIdx.x < kRouteTokens && m0 + threadIdx.x < a.M)
         a.logits[(uint64_t)(m0 + threadIdx.x) * a.E + e] =
             part[0][threadIdx.x] + part[1][threadIdx.x] + part[2][threadIdx.x] + part[3][threadIdx.x];
 }
@@ -73,78 +133,122 @@ __device__ __forceinline__ uint64_t order_of(double v) {
     return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-// A token's choices, one workgroup a token: an expert's place is the number
-// of experts before it (greater logits, or equal ones of lower index).
-__global__ __launch_bounds__(256) void moe_choose(MoeArgs a) {
-    __shared__ uint64_t key[kMaxExperts];
-    __shared__ double part[4];
+// A token's choices, one workgroup a token and one thread an expert: its place
+// is the number of experts before it (greater logits, or equal ones of lower
+// index).
+__global__ __launch_bounds__(kMaxExperts) void moe_choose(MoeArgs a) {
+    __shared__ __attribute__((aligned(16))) uint64_t key[kMaxExperts];
+    __shared__ double part[kMaxExperts / 64], most;
     const uint32_t m = blockIdx.x, t = threadIdx.x;
-    const double *l = a.logits + (uint64_t)m * a.E;
-    const double mine = t < a.E ? l[t] : 0.0;
-    if (t < a.E) key[t] = order_of(mine);
+    const double mine = t < a.E ? a.logits[(uint64_t)m * a.E + t] : 0.0;
+    const uint64_t k = order_of(mine);
+    key[t] = t < a.E ? k : 0;  // (below every logit's)
     __syncthreads();
     uint32_t before = 0;
-    double most = -INFINITY;
-    for (uint32_t i = 0; i < a.E; ++i) {
-        if (t < a.E) before += key[i] > key[t] || (key[i] == key[t] && i < t);
-        const double v = l[i];
-        most = v > most || v != v ? v : most;
+    for (uint32_t i = 0; i < a.E; i += 8) {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+            const uint64_t other = key[i + j];
+            before += other > k || (other == k && i + j < t);
+        }
     }
+    if (t < a.E && before == 0) most = mine;
+    __syncthreads();
     const bool in = t < a.E && before < a.K;
-    const double p = t < a.E ? exp(mine - most) : 0.0;
-    double s = wave_sum(in || !a.normalize ? p : 0.0);
+    const double p = t < a.E && (in || !a.normalize) ? exp(mine - most) : 0.0;
+    double s = wave_sum(p);
     if (t % 64 == 0) part[t / 64] = s;
     __syncthreads();
-    s = part[0] + part[1] + part[2] + part[3];
+    s = 0.0;
+    for (uint32_t i = 0; i < (a.E + 63) / 64; ++i) s += part[i];
     if (t >= a.E) return;
-    const float w = (float)(p / s);
-    a.place[(uint64_t)t * a.M + m] = in ? (int32_t)before : -1;
-    a.share[(uint64_t)t * a.M + m] = in ? w : 0.0f;
+    a.place[(uint64_t)t * a.M + m] = in ? (int8_t)before : -1;
     if (!in) return;
+    const float w = (float)(p / s);
+    atomicOr((unsigned long long *)&a.tokens[t], 1ull << m);
+    a.share[m * a.K + before] = w;
     if (a.experts) a.experts[(uint64_t)m * a.K + before] = (int32_t)t;
     if (a.weights) a.weights[(uint64_t)m * a.K + before] = w;
 }
 
-// Codes k..k+15 (of a lane's row) of a block that may pass the row's end.
+// Codes k..k+15 of a row of K codes; `whole`: the row has them.
 __device__ __forceinline__ v4i load_codes(const int8_t *row, uint32_t k, uint32_t K, bool whole) {
     return whole ? ((const any16 *)(row + k))->v : load16_any(row, k, K);
 }
 
+// The expert that is the nth of those that some token chose, or E.
+__device__ __forceinline__ uint32_t nth_expert(const MoeArgs &a, uint32_t nth, uint32_t lane) {
+    for (uint32_t e = 0; e < a.E; e += 64) {
+        const uint64_t used = __ballot(e + lane < a.E && a.tokens[e + lane] != 0);
+        const uint32_t n = (uint32_t)__popcll(used);
+        if (nth < n) {
+            const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(used >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)used, 0));
+            return e + (uint32_t)__builtin_ctzll(__ballot((used >> lane & 1) && before == nth));
+        }
+        nth -= n;
+    }
+    return a.E;
+}
+
 // h = act(x gate^T) (x up^T) for the tokens of one expert: a workgroup takes
-// 16 of its channels, its waves blocks of 128 codes in turn. Every token has
-// its column of the matrix instruction; those that did not choose the expert
-// load nothing.
+// 16 of its channels, its waves blocks of 128 codes in turn, four of them (two
+// for many tokens) on their way. Every token has its column of the matrix
+// instruction; those that did not choose the expert load nothing.
 template <int MT>
 __global__ __launch_bounds__(64 * kWavesMoe) void moe_gated(MoeArgs a) {
+    constexpr int kDepth = MT > 1 ? 2 : 4;
     __shared__ v4i sums[kWavesMoe][2 * MT][64];
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const uint32_t e = blockIdx.y, n0 = blockIdx.x * 16, kc = lane / 16 * 32;
-    int32_t place[MT];
-    bool any = false;
+    const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32;
+    const uint32_t e = gridDim.y == a.E ? blockIdx.y : nth_expert(a, blockIdx.y, lane);
+    const uint64_t tokens = e < a.E ? a.tokens[e] : 0;
+    if (!tokens) return;
+    bool in[MT];
+    const int8_t *x[MT];
 #pragma unroll
     for (int g = 0; g < MT; ++g) {
-        const uint32_t m = g * 16 + lane % 16;
-        place[g] = m < a.M ? a.place[(uint64_t)e * a.M + m] : -1;
-        any |= place[g] >= 0;
+        in[g] = tokens >> (g * 16 + lane % 16) & 1;
+        x[g] = a.codes + (g * 16 + lane % 16) * a.ldc + kc;
     }
-    if (!__any(any)) return;
     const uint64_t row = min(n0 + lane % 16, a.F - 1);
-    const int8_t *wg = a.w[0] + e * a.stride[0] + row * a.ldw[0], *wu = a.w[1] + e * a.stride[1] + row * a.ldw[1];
+    const int8_t *w[2] = {a.w[0] + e * a.stride[0] + row * a.ldw[0], a.w[1] + e * a.stride[1] + row * a.ldw[1]};
     v4i acc[2][MT] = {};
-    const uint32_t blocks = (a.D + 127) / 128;
-    for (uint32_t b = wave; b < blocks; b += kWavesMoe) {
-        const bool whole = b * 128 + 128 <= a.D;
+    struct Block {
+        v4i w[2][2], x[MT][2];
+    };
+    const uint32_t blocks = (a.D + 127) / 128, mine = blocks > wave ? (blocks - wave + kWavesMoe - 1) / kWavesMoe : 0;
+    auto load = [&](Block &b, uint32_t i) {
+        const uint32_t k = (i * kWavesMoe + wave) * 128;
+        const bool whole = k + 128 <= a.D;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint32_t k = b * 128 + kc + 16 * half;
-            const v4i g0 = load_codes(wg, k, a.D, whole), u0 = load_codes(wu, k, a.D, whole);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) b.w[t][half] = load_codes(w[t], k + kc + 16 * half, a.D, whole);
 #pragma unroll
             for (int g = 0; g < MT; ++g) {
-                v4i xv = {0, 0, 0, 0};
-                if (place[g] >= 0) xv = *(const v4i *)(a.codes + (g * 16 + lane % 16) * a.ldc + k);
-                acc[0][g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(g0, xv, acc[0][g], 0, 0, 0);
-                acc[1][g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(u0, xv, acc[1][g], 0, 0, 0);
+                b.x[g][half] = v4i{0, 0, 0, 0};
+                if (in[g]) b.x[g][half] = *(const v4i *)(x[g] + k + 16 * half);
             }
+        }
+    };
+    auto multiply = [&](const Block &b) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int g = 0; g < MT; ++g)
+                    acc[t][g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b.w[t][half], b.x[g][half], acc[t][g], 0, 0, 0);
+    };
+    Block b[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+        if ((uint32_t)d < mine) load(b[d], d);
+    for (uint32_t i = 0; i < mine; i += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            if (i + d < mine) multiply(b[d]);
+            if (i + d + kDepth < mine) load(b[d], i + d + kDepth);
         }
     }
 #pragma unroll
@@ -160,95 +264,160 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_gated(MoeArgs a) {
         s1 += sums[v][MT + wave][lane];
     }
     const uint32_t m = wave * 16 + lane % 16, n = n0 + lane / 16 * 4;
-    const int32_t at = m < a.M ? a.place[(uint64_t)e * a.M + m] : -1;
-    if (at < 0 || n >= a.F) return;
+    if (!(tokens >> m & 1) || n >= a.F) return;
+    const int32_t place = a.place[(uint64_t)e * a.M + m];
     const float sx = a.sx[m];
     float g[4], u[4], r[4], none[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bool in = n + i < a.F;
-        g[i] = ((float)s0[i] * sx) * (in ? a.sw[0][e * a.sstride[0] + n + i] : 0.0f);
-        u[i] = ((float)s1[i] * sx) * (in ? a.sw[1][e * a.sstride[1] + n + i] : 0.0f);
+        const bool there = n + i < a.F;
+        g[i] = ((float)s0[i] * sx) * (there ? a.sw[0][e * a.sstride[0] + n + i] : 0.0f);
+        u[i] = ((float)s1[i] * sx) * (there ? a.sw[1][e * a.sstride[1] + n + i] : 0.0f);
     }
     activate4<false>(a.act, g, r, none);
-    float *h = a.h + ((uint64_t)m * a.K + at) * a.F + n;
+    float *h = a.h + ((uint64_t)m * a.K + place) * a.F + n;
+    if (n + 4 <= a.F) {
+        ((any16 *)h)->v = __builtin_bit_cast(v4i, v4f{r[0] * u[0], r[1] * u[1], r[2] * u[2], r[3] * u[3]});
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (n + i < a.F) h[i] = r[i] * u[i];
+        for (int i = 0; i < 3; ++i)
+            if (n + i < a.F) h[i] = r[i] * u[i];
+    }
 }
 
 // y = the sum over experts of share (h down^T): a workgroup takes 16 results
-// of every token and goes over the experts in use in their order.
+// of every token. The blocks of 128 codes of all experts in use are one list,
+// which its waves take in turn, so that the next expert's codes are on their
+// way while one's are multiplied; at an expert's end a wave scales its integer
+// sums and adds them to its own of fp32.
 template <int MT>
 __global__ __launch_bounds__(64 * kWavesMoe) void moe_down(MoeArgs a) {
-    __shared__ v4f sums[kWavesMoe][MT][64];
-    const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    constexpr int kDepth = MT > 1 ? 2 : 4;
+    extern __shared__ __attribute__((aligned(16))) uint8_t room[];
+    __shared__ uint8_t used[kMaxExperts];
+    const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), t = threadIdx.x;
     const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32, n = n0 + lane / 16 * 4;
-    const uint64_t row = min(n0 + lane % 16, a.N - 1);
-    float total[MT][4] = {};
-    const uint32_t blocks = (a.F + 127) / 128;
-    for (uint32_t e = 0; e < a.E; ++e) {
-        int32_t place[MT];
-        bool any = false;
+    // the experts in use, in their order
+    uint32_t count = 0;
+    for (uint32_t e = 0; e < a.E; e += 64) {
+        const bool some = e + lane < a.E && a.tokens[e + lane] != 0;
+        const uint64_t all = __ballot(some);
+        if (some && wave == 0)
+            used[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] =
+                (uint8_t)(e + lane);
+        count += (uint32_t)__popcll(all);
+    }
+    float *const factor = (float *)room;                  // [M K]
+    float *const scale = factor + (a.M * a.K + 3) / 4 * 4;  // [E in use][16]
+    int8_t *const place = (int8_t *)(scale + a.E * 16);   // [E][M]
+    for (uint32_t i = t; i < a.M * a.K; i += 64 * kWavesMoe) factor[i] = a.share[i] * a.sh[i];
+    for (uint32_t i = t; i < a.E * a.M; i += 64 * kWavesMoe) place[i] = a.place[i];
+    __syncthreads();
+    for (uint32_t i = t; i < count * 16; i += 64 * kWavesMoe)
+        scale[i] = n0 + i % 16 < a.N ? a.sw[2][used[i / 16] * a.sstride[2] + n0 + i % 16] : 0.0f;
+    __syncthreads();
+    const uint64_t row = min(n0 + lane % 16, a.N - 1) * a.ldw[2];
+    const uint32_t blocks = (a.F + 127) / 128, step_e = kWavesMoe / blocks, step_b = kWavesMoe % blocks;
+    struct Block {
+        v4i w[2], x[MT][2];
+        uint32_t at;  // in the list of experts
+    };
+    uint32_t at = wave / blocks, block = wave % blocks;  // the next to load
+    auto load = [&](Block &b) {
+        b.at = at;
+        const uint32_t e = __builtin_amdgcn_readfirstlane(used[at]), k = block * 128;
+        const bool whole = k + 128 <= a.F;
+        const int8_t *w = a.w[2] + e * a.stride[2] + row;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) b.w[half] = load_codes(w, k + kc + 16 * half, a.F, whole);
 #pragma unroll
         for (int g = 0; g < MT; ++g) {
             const uint32_t m = g * 16 + lane % 16;
-            place[g] = m < a.M ? a.place[(uint64_t)e * a.M + m] : -1;
-            any |= place[g] >= 0;
-        }
-        if (!__any(any)) continue;
-        const int8_t *w = a.w[2] + e * a.stride[2] + row * a.ldw[2];
-        v4i acc[MT] = {};
-        for (uint32_t b = wave; b < blocks; b += kWavesMoe) {
-            const bool whole = b * 128 + 128 <= a.F;
+            const int32_t p = m < a.M ? place[e * a.M + m] : -1;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const uint32_t k = b * 128 + kc + 16 * half;
-                const v4i wv = load_codes(w, k, a.F, whole);
-#pragma unroll
-                for (int g = 0; g < MT; ++g) {
-                    v4i hv = {0, 0, 0, 0};
-                    if (place[g] >= 0)
-                        hv = *(const v4i *)(a.hcodes + ((uint64_t)(g * 16 + lane % 16) * a.K + place[g]) * a.ldh + k);
-                    acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, hv, acc[g], 0, 0, 0);
-                }
+                b.x[g][half] = v4i{0, 0, 0, 0};
+                if (p >= 0) b.x[g][half] = *(const v4i *)(a.hcodes + ((uint64_t)m * a.K + p) * a.ldh + k + kc + 16 * half);
             }
         }
+        block += step_b;
+        at += step_e;
+        if (block >= blocks) {
+            block -= blocks;
+            ++at;
+        }
+    };
+    float total[MT][4] = {};
+    v4i acc[MT] = {};
+    auto finish = [&](uint32_t done) {
+        const uint32_t e = __builtin_amdgcn_readfirstlane(used[done]);
+        const v4f s = *(const v4f *)(scale + done * 16 + lane / 16 * 4);
 #pragma unroll
         for (int g = 0; g < MT; ++g) {
-            if (place[g] < 0) continue;
             const uint32_t m = g * 16 + lane % 16;
-            const float f = a.share[(uint64_t)e * a.M + m] * a.sh[(uint64_t)m * a.K + place[g]];
+            const int32_t p = m < a.M ? place[e * a.M + m] : -1;
+            if (p < 0) continue;
+            const float f = factor[m * a.K + p];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                total[g][i] += (float)acc[g][i] * f * (n + i < a.N ? a.sw[2][e * a.sstride[2] + n + i] : 0.0f);
+            for (int i = 0; i < 4; ++i) total[g][i] += (float)acc[g][i] * f * s[i];
+        }
+#pragma unroll
+        for (int g = 0; g < MT; ++g) acc[g] = v4i{0, 0, 0, 0};
+    };
+    Block b[kDepth];
+    uint32_t current = at;
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+        b[d].at = count;
+        if (at < count) load(b[d]);
+    }
+    while (b[0].at < count) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            if (b[d].at >= count) continue;
+            if (b[d].at != current) {
+                finish(current);
+                current = b[d].at;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int g = 0; g < MT; ++g)
+                    acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[d].w[half], b[d].x[g][half], acc[g], 0, 0, 0);
+            b[d].at = count;
+            if (at < count) load(b[d]);
         }
     }
+    if (current < count) finish(current);
+    __syncthreads();  // the tables are done with: their room holds the waves' sums
+    v4f *const sums = (v4f *)room;
 #pragma unroll
-    for (int g = 0; g < MT; ++g) sums[wave][g][lane] = v4f{total[g][0], total[g][1], total[g][2], total[g][3]};
+    for (int g = 0; g < MT; ++g)
+        sums[(wave * MT + g) * 64 + lane] = v4f{total[g][0], total[g][1], total[g][2], total[g][3]};
     __syncthreads();
     if (wave >= MT) return;
     v4f s = {0, 0, 0, 0};
 #pragma unroll
-    for (int v = 0; v < kWavesMoe; ++v) s += sums[v][wave][lane];
+    for (int v = 0; v < kWavesMoe; ++v) s += sums[(v * MT + wave) * 64 + lane];
     const uint32_t m = wave * 16 + lane % 16;
     if (m >= a.M) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (n + i >= a.N) continue;
-        const uint64_t at = m * a.ldy + n + i;
+        const uint64_t to = m * a.ldy + n + i;
         if (a.y_type == ENTQ_F32)
-            ((float *)a.y)[at] = s[i];
+            ((float *)a.y)[to] = s[i];
         else
-            ((uint16_t *)a.y)[at] = bits16(s[i], a.y_type == ENTQ_F16);
+            ((uint16_t *)a.y)[to] = bits16(s[i], a.y_type == ENTQ_F16);
     }
 }
 
 template <int MT>
 void launch_products(const MoeArgs &a, hipStream_t s) {
-    moe_gated<MT><<<dim3((a.F + 15) / 16, a.E), 64 * kWavesMoe, 0, s>>>(a);
+    moe_gated<MT><<<dim3((a.F + 15) / 16, std::min(a.E, a.M * a.K)), 64 * kWavesMoe, 0, s>>>(a);
     quantize_padded({a.h, a.F, nullptr, a.M * a.K, a.F, ENTQ_F32, 0}, a.hcodes, a.ldh, a.sh, s);
-    moe_down<MT><<<(a.N + 15) / 16, 64 * kWavesMoe, 0, s>>>(a);
+    const uint32_t lds = std::max((a.M * a.K + 3) / 4 * 16 + a.E * 64 + a.E * a.M, kWavesMoe * MT * 1024u);
+    moe_down<MT><<<(a.N + 15) / 16, 64 * kWavesMoe, lds, s>>>(a);
 }
 
 uint32_t bytes_of(int t) { return t == ENTQ_F32 ? 4 : 2; }
@@ -292,11 +461,12 @@ uint64_t lay_out(const entq_rows &x, const entq_experts &e, uint8_t *base, MoeAr
     const uint64_t M = x.rows, rows = M * e.top_k;
     a.ldc = (x.cols + 127ull) / 128 * 128;
     a.ldh = (e.hidden + 127ull) / 128 * 128;
+    take(a.tokens, e.experts);
     take(a.codes, M * a.ldc);
     take(a.sx, M);
     take(a.logits, M * e.experts);
     take(a.place, M * e.experts);
-    take(a.share, M * e.experts);
+    take(a.share, rows);
     take(a.h, rows * e.hidden);
     take(a.hcodes, rows * a.ldh);
     take(a.sh, rows);
@@ -329,7 +499,6 @@ entq_status entq_moe_few(const entq_rows *x, const entq_experts *e, void *d_y, i
     lay_out(*x, *e, (uint8_t *)d_workspace, a);
     a.x = x->d_data;
     a.ldx = x->ld;
-    a.x_type = x->type;
     a.router = e->d_router;
     a.ldr = e->ldrouter;
     a.router_type = e->router_type;
@@ -354,9 +523,11 @@ entq_status entq_moe_few(const entq_rows *x, const entq_experts *e, void *d_y, i
     a.experts = d_experts;
     a.weights = d_weights;
     const hipStream_t s = (hipStream_t)stream;
-    if ((st = quantize_padded(*x, a.codes, a.ldc, a.sx, s)) != ENTQ_OK) return st;
-    moe_route<<<dim3(a.E, (a.M + 7) / 8), 256, 0, s>>>(a);
-    moe_choose<<<a.M, 256, 0, s>>>(a);
+    const uint32_t route = a.E * ((a.M + kRouteTokens - 1) / kRouteTokens) + a.M;
+    if (x->type == ENTQ_BF16) moe_route<ENTQ_BF16><<<route, 256, 0, s>>>(a);
+    if (x->type == ENTQ_F16) moe_route<ENTQ_F16><<<route, 256, 0, s>>>(a);
+    if (x->type == ENTQ_F32) moe_route<ENTQ_F32><<<route, 256, 0, s>>>(a);
+    moe_choose<<<a.M, kMaxExperts, 0, s>>>(a);
     const uint32_t groups = (a.M + 15) / 16;
     if (groups == 1) launch_products<1>(a, s);
     if (groups == 2) launch_products<2>(a, s);
