@@ -8,13 +8,11 @@
 namespace entq {
 namespace {
 
-constexpr int kWavesMoe = 8;
 constexpr uint32_t kTokens = ENTQ_MOE_MAX_TOKENS, kMaxExperts = ENTQ_MOE_MAX_EXPERTS;
 
 struct MoeArgs {
     const void *x, *router;
     uint64_t ldx, ldr;
-    int router_type;
     uint32_t M, E, K, D, F, N;     // tokens, experts, chosen, width, hidden, results
     int act;
     bool normalize;
@@ -30,7 +28,7 @@ struct MoeArgs {
     float *share;                  // [M K]: the token's weight for its choice
     float *h;                      // [M K][F]
     int8_t *hcodes;                // [M K][ldh]
-    float *sh;                     // [M K]
+    float *factor;                 // [M K]: share times the scale of the codes
     uint64_t ldc, ldh;
     // the results
     void *y;
@@ -51,16 +49,42 @@ __device__ __forceinline__ void load8(const void *row, uint32_t c, uint32_t n, f
     }
 }
 
-// A token's codes and scale (entq_quantize_rows), zeros up to ldc; one workgroup.
+// Rows of codes as the products read them: in segments of 16, padded with
+// zeros to blocks of 128. Where a row of n codes ends inside a segment, that
+// segment holds its last 16 codes instead, zeros for those of the segment
+// before: then every lane can read 16 of a weight row's codes, from column
+// min(segment, n - 16), without a branch and within the row. (Rows of fewer
+// than 16 codes: one segment, read by load16_any.)
+//
+// 8 codes of such a row, from position `at` (a multiple of 8).
 template <int TYPE>
-__device__ __forceinline__ void quantize_token(const MoeArgs &a, uint32_t m) {
-    __shared__ uint32_t top[4];
-    const uint8_t *x = (const uint8_t *)a.x + m * a.ldx * (TYPE == ENTQ_F32 ? 4 : 2);
-    const uint32_t groups = (uint32_t)(a.ldc / 8);
+__device__ __forceinline__ v2i segment_codes(const Quantizer &z, const void *row, uint32_t at, uint32_t n) {
+    float f[8];
+    const uint32_t segment = at / 16 * 16;
+    if (segment + 16 <= n || n < 16 || segment >= n) {
+        load8<TYPE>(row, at, n, f);
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+            const uint32_t c = n - 16 + at % 16 + i;
+            f[i] = c >= segment ? load_act<TYPE>(row, c) : 0.0f;
+        }
+    }
+    uint32_t q[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i / 4] |= z.code(f[i]) << (8 * (i % 4));
+    return v2i{(int)q[0], (int)q[1]};
+}
+
+// The codes and the scale of one row (the values of entq_quantize_rows); one
+// workgroup.
+template <int TYPE, int THREADS>
+__device__ __forceinline__ float quantize_segments(const void *x, uint32_t n, int8_t *codes, uint32_t ldc) {
+    __shared__ uint32_t top[THREADS / 64];
     uint32_t big = 0;
-    for (uint32_t g = threadIdx.x; g < groups; g += 256) {
+    for (uint32_t c = threadIdx.x * 8; c < n; c += THREADS * 8) {
         float f[8];
-        load8<TYPE>(x, g * 8, a.D, f);
+        load8<TYPE>(x, c, n, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(f[i]) & 0x7FFFFFFFu);
     }
@@ -68,27 +92,36 @@ __device__ __forceinline__ void quantize_token(const MoeArgs &a, uint32_t m) {
     if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) big = max(big, top[i]);
+    for (int i = 0; i < THREADS / 64; ++i) big = max(big, top[i]);
     const Quantizer z(big);
-    if (threadIdx.x == 0) a.sx[m] = z.scale;
-    for (uint32_t g = threadIdx.x; g < groups; g += 256) {
-        float f[8];
-        load8<TYPE>(x, g * 8, a.D, f);
-        uint32_t q[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i / 4] |= z.code(f[i]) << (8 * (i % 4));
-        *(v2i *)(a.codes + m * a.ldc + g * 8) = v2i{(int)q[0], (int)q[1]};
-    }
+    for (uint32_t c = threadIdx.x * 8; c < ldc; c += THREADS * 8) *(v2i *)(codes + c) = segment_codes<TYPE>(z, x, c, n);
+    return z.scale;
+}
+
+// Codes of segment k of a weight row of n codes (TINY: of fewer than 16).
+template <bool TINY>
+__device__ __forceinline__ v4i weight_segment(const int8_t *row, uint32_t k, uint32_t n) {
+    if (TINY) return load16_any(row, k, n);
+    return ((const any16 *)(row + min(k, n - 16)))->v;
 }
 
 // The router's logits, summed in 64 bits: which expert is chosen hangs on
 // their order. A workgroup takes one expert and up to 8 tokens; those after
 // them quantise a token each.
+// (The router's type is a template's and not the loop's to look at: with the
+// three loads of it in one kernel the compiler shared a token's offset with
+// them and left it unset on the way of the third.)
 constexpr uint32_t kRouteTokens = 8;
-template <int TYPE>
+template <int TYPE, int ROUTER>
 __global__ __launch_bounds__(256) void moe_route(MoeArgs a) {
     const uint32_t groups = (a.M + kRouteTokens - 1) / kRouteTokens;
-    if (blockIdx.x >= a.E * groups) return quantize_token<TYPE>(a, blockIdx.x - a.E * groups);
+    if (blockIdx.x >= a.E * groups) {
+        const uint32_t m = blockIdx.x - a.E * groups;
+        const float s = quantize_segments<TYPE, 256>((const uint8_t *)a.x + m * a.ldx * (TYPE == ENTQ_F32 ? 4 : 2), a.D,
+                                                     a.codes + m * a.ldc, (uint32_t)a.ldc);
+        if (threadIdx.x == 0) a.sx[m] = s;
+        return;
+    }
     __shared__ double part[4][kRouteTokens];
     const uint32_t e = blockIdx.x / groups, m0 = blockIdx.x % groups * kRouteTokens;
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -97,10 +130,7 @@ __global__ __launch_bounds__(256) void moe_route(MoeArgs a) {
     const uint32_t all = (a.D + 7) / 8;
     for (uint32_t g = threadIdx.x; g < all; g += 256) {
         float r[8], x[kRouteTokens][8];
-        const uint8_t *row = (const uint8_t *)a.router + e * a.ldr * (a.router_type == ENTQ_F32 ? 4 : 2);
-        if (a.router_type == ENTQ_F32) load8<ENTQ_F32>(row, g * 8, a.D, r);
-        if (a.router_type == ENTQ_BF16) load8<ENTQ_BF16>(row, g * 8, a.D, r);
-        if (a.router_type == ENTQ_F16) load8<ENTQ_F16>(row, g * 8, a.D, r);
+        load8<ROUTER>((const uint8_t *)a.router + e * a.ldr * (ROUTER == ENTQ_F32 ? 4 : 2), g * 8, a.D, r);
 #pragma unroll
         for (uint32_t i = 0; i < kRouteTokens; ++i)
             if (m0 + i < a.M)
@@ -171,11 +201,6 @@ __global__ __launch_bounds__(kMaxExperts) void moe_choose(MoeArgs a) {
     if (a.weights) a.weights[(uint64_t)m * a.K + before] = w;
 }
 
-// Codes k..k+15 of a row of K codes; `whole`: the row has them.
-__device__ __forceinline__ v4i load_codes(const int8_t *row, uint32_t k, uint32_t K, bool whole) {
-    return whole ? ((const any16 *)(row + k))->v : load16_any(row, k, K);
-}
-
 // The expert that is the nth of those that some token chose, or E.
 __device__ __forceinline__ uint32_t nth_expert(const MoeArgs &a, uint32_t nth, uint32_t lane) {
     for (uint32_t e = 0; e < a.E; e += 64) {
@@ -191,24 +216,25 @@ __device__ __forceinline__ uint32_t nth_expert(const MoeArgs &a, uint32_t nth, u
 }
 
 // h = act(x gate^T) (x up^T) for the tokens of one expert: a workgroup takes
-// 16 of its channels, its waves blocks of 128 codes in turn, four of them (two
-// for many tokens) on their way. Every token has its column of the matrix
-// instruction; those that did not choose the expert load nothing.
-template <int MT>
-__global__ __launch_bounds__(64 * kWavesMoe) void moe_gated(MoeArgs a) {
+// 16 of its channels, its waves blocks of 128 codes in turn, DEPTH of them on
+// their way. Every token has its column of the matrix instruction; a token
+// that did not choose the expert reads with one that did (the same cache
+// lines, and no branch, so that no load waits for another), and its sums go
+// nowhere.
+template <int MT, int WAVES, bool TINY>
+__global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
     constexpr int kDepth = MT > 1 ? 2 : 4;
-    __shared__ v4i sums[kWavesMoe][2 * MT][64];
+    __shared__ v4i sums[WAVES][2 * MT][64];
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32;
     const uint32_t e = gridDim.y == a.E ? blockIdx.y : nth_expert(a, blockIdx.y, lane);
     const uint64_t tokens = e < a.E ? a.tokens[e] : 0;
     if (!tokens) return;
-    bool in[MT];
-    const int8_t *x[MT];
+    uint32_t x[MT];
 #pragma unroll
     for (int g = 0; g < MT; ++g) {
-        in[g] = tokens >> (g * 16 + lane % 16) & 1;
-        x[g] = a.codes + (g * 16 + lane % 16) * a.ldc + kc;
+        const uint32_t m = g * 16 + lane % 16;
+        x[g] = (uint32_t)((tokens >> m & 1 ? m : (uint32_t)__builtin_ctzll(tokens)) * a.ldc) + kc;
     }
     const uint64_t row = min(n0 + lane % 16, a.F - 1);
     const int8_t *w[2] = {a.w[0] + e * a.stride[0] + row * a.ldw[0], a.w[1] + e * a.stride[1] + row * a.ldw[1]};
@@ -216,19 +242,15 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_gated(MoeArgs a) {
     struct Block {
         v4i w[2][2], x[MT][2];
     };
-    const uint32_t blocks = (a.D + 127) / 128, mine = blocks > wave ? (blocks - wave + kWavesMoe - 1) / kWavesMoe : 0;
+    const uint32_t blocks = (a.D + 127) / 128, mine = blocks > wave ? (blocks - wave + WAVES - 1) / WAVES : 0;
     auto load = [&](Block &b, uint32_t i) {
-        const uint32_t k = (i * kWavesMoe + wave) * 128;
-        const bool whole = k + 128 <= a.D;
+        const uint32_t k = (i * WAVES + wave) * 128;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) b.w[t][half] = load_codes(w[t], k + kc + 16 * half, a.D, whole);
+            for (int t = 0; t < 2; ++t) b.w[t][half] = weight_segment<TINY>(w[t], k + kc + 16 * half, a.D);
 #pragma unroll
-            for (int g = 0; g < MT; ++g) {
-                b.x[g][half] = v4i{0, 0, 0, 0};
-                if (in[g]) b.x[g][half] = *(const v4i *)(x[g] + k + 16 * half);
-            }
+            for (int g = 0; g < MT; ++g) b.x[g][half] = *(const v4i *)(a.codes + (x[g] + k + 16 * half));
         }
     };
     auto multiply = [&](const Block &b) {
@@ -244,13 +266,22 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_gated(MoeArgs a) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)
         if ((uint32_t)d < mine) load(b[d], d);
-    for (uint32_t i = 0; i < mine; i += kDepth) {
+    uint32_t i = 0;
+    for (; i + 2 * kDepth <= mine; i += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            multiply(b[d]);
+            load(b[d], i + d + kDepth);
+        }
+    }
+    for (; i < mine; i += kDepth) {
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             if (i + d < mine) multiply(b[d]);
             if (i + d + kDepth < mine) load(b[d], i + d + kDepth);
         }
     }
+    static_assert(WAVES >= MT, "a wave for each group of tokens at the end");
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -259,7 +290,7 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_gated(MoeArgs a) {
     if (wave >= MT) return;
     v4i s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
 #pragma unroll
-    for (int v = 0; v < kWavesMoe; ++v) {
+    for (int v = 0; v < WAVES; ++v) {
         s0 += sums[v][wave][lane];
         s1 += sums[v][MT + wave][lane];
     }
@@ -285,16 +316,25 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_gated(MoeArgs a) {
     }
 }
 
+// The hidden values' codes, and what a row's products are scaled with: its
+// scale times the token's weight for the expert.
+__global__ __launch_bounds__(512) void moe_quantize(MoeArgs a) {
+    const uint32_t r = blockIdx.x;
+    const float s = quantize_segments<ENTQ_F32, 512>(a.h + (uint64_t)r * a.F, a.F, a.hcodes + r * a.ldh, (uint32_t)a.ldh);
+    if (threadIdx.x == 0) a.factor[r] = a.share[r] * s;
+}
+
 // y = the sum over experts of share (h down^T): a workgroup takes 16 results
 // of every token. The blocks of 128 codes of all experts in use are one list,
 // which its waves take in turn, so that the next expert's codes are on their
 // way while one's are multiplied; at an expert's end a wave scales its integer
 // sums and adds them to its own of fp32.
-template <int MT>
-__global__ __launch_bounds__(64 * kWavesMoe) void moe_down(MoeArgs a) {
+template <int MT, int WAVES, bool TINY>
+__global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a) {
     constexpr int kDepth = MT > 1 ? 2 : 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t room[];
     __shared__ uint8_t used[kMaxExperts];
+    __shared__ uint16_t rows[kMaxExperts];  // of an expert's first token
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), t = threadIdx.x;
     const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32, n = n0 + lane / 16 * 4;
     // the experts in use, in their order
@@ -310,14 +350,18 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_down(MoeArgs a) {
     float *const factor = (float *)room;                  // [M K]
     float *const scale = factor + (a.M * a.K + 3) / 4 * 4;  // [E in use][16]
     int8_t *const place = (int8_t *)(scale + a.E * 16);   // [E][M]
-    for (uint32_t i = t; i < a.M * a.K; i += 64 * kWavesMoe) factor[i] = a.share[i] * a.sh[i];
-    for (uint32_t i = t; i < a.E * a.M; i += 64 * kWavesMoe) place[i] = a.place[i];
+    for (uint32_t i = t; i < a.M * a.K; i += 64 * WAVES) factor[i] = a.factor[i];
+    for (uint32_t i = t; i < a.E * a.M; i += 64 * WAVES) place[i] = a.place[i];
     __syncthreads();
-    for (uint32_t i = t; i < count * 16; i += 64 * kWavesMoe)
+    if (t < count) {
+        const uint32_t e = used[t], m = (uint32_t)__builtin_ctzll(a.tokens[e]);
+        rows[t] = (uint16_t)(m * a.K + place[e * a.M + m]);
+    }
+    for (uint32_t i = t; i < count * 16; i += 64 * WAVES)
         scale[i] = n0 + i % 16 < a.N ? a.sw[2][used[i / 16] * a.sstride[2] + n0 + i % 16] : 0.0f;
     __syncthreads();
     const uint64_t row = min(n0 + lane % 16, a.N - 1) * a.ldw[2];
-    const uint32_t blocks = (a.F + 127) / 128, step_e = kWavesMoe / blocks, step_b = kWavesMoe % blocks;
+    const uint32_t blocks = (a.F + 127) / 128, step_e = WAVES / blocks, step_b = WAVES % blocks;
     struct Block {
         v4i w[2], x[MT][2];
         uint32_t at;  // in the list of experts
@@ -325,20 +369,19 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_down(MoeArgs a) {
     uint32_t at = wave / blocks, block = wave % blocks;  // the next to load
     auto load = [&](Block &b) {
         b.at = at;
-        const uint32_t e = __builtin_amdgcn_readfirstlane(used[at]), k = block * 128;
-        const bool whole = k + 128 <= a.F;
+        const uint32_t e = __builtin_amdgcn_readfirstlane(used[at]), k = block * 128 + kc;
         const int8_t *w = a.w[2] + e * a.stride[2] + row;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) b.w[half] = load_codes(w, k + kc + 16 * half, a.F, whole);
+        for (int half = 0; half < 2; ++half) b.w[half] = weight_segment<TINY>(w, k + 16 * half, a.F);
+        // (a token without the expert reads with its first one, as in moe_gated)
+        const uint32_t first = __builtin_amdgcn_readfirstlane(rows[at]);
 #pragma unroll
         for (int g = 0; g < MT; ++g) {
             const uint32_t m = g * 16 + lane % 16;
             const int32_t p = m < a.M ? place[e * a.M + m] : -1;
+            const int8_t *x = a.hcodes + (uint64_t)(p < 0 ? first : m * a.K + p) * a.ldh + k;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                b.x[g][half] = v4i{0, 0, 0, 0};
-                if (p >= 0) b.x[g][half] = *(const v4i *)(a.hcodes + ((uint64_t)m * a.K + p) * a.ldh + k + kc + 16 * half);
-            }
+            for (int half = 0; half < 2; ++half) b.x[g][half] = *(const v4i *)(x + 16 * half);
         }
         block += step_b;
         at += step_e;
@@ -398,7 +441,7 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_down(MoeArgs a) {
     if (wave >= MT) return;
     v4f s = {0, 0, 0, 0};
 #pragma unroll
-    for (int v = 0; v < kWavesMoe; ++v) s += sums[(v * MT + wave) * 64 + lane];
+    for (int v = 0; v < WAVES; ++v) s += sums[(v * MT + wave) * 64 + lane];
     const uint32_t m = wave * 16 + lane % 16;
     if (m >= a.M) return;
 #pragma unroll
@@ -414,10 +457,18 @@ __global__ __launch_bounds__(64 * kWavesMoe) void moe_down(MoeArgs a) {
 
 template <int MT>
 void launch_products(const MoeArgs &a, hipStream_t s) {
-    moe_gated<MT><<<dim3((a.F + 15) / 16, std::min(a.E, a.M * a.K)), 64 * kWavesMoe, 0, s>>>(a);
-    quantize_padded({a.h, a.F, nullptr, a.M * a.K, a.F, ENTQ_F32, 0}, a.hcodes, a.ldh, a.sh, s);
-    const uint32_t lds = std::max((a.M * a.K + 3) / 4 * 16 + a.E * 64 + a.E * a.M, kWavesMoe * MT * 1024u);
-    moe_down<MT><<<(a.N + 15) / 16, 64 * kWavesMoe, lds, s>>>(a);
+    constexpr int W = 8, WG = 4;
+    const dim3 grid((a.F + 15) / 16, std::min(a.E, a.M * a.K));
+    if (a.D < 16)
+        moe_gated<MT, WG, true><<<grid, 64 * WG, 0, s>>>(a);
+    else
+        moe_gated<MT, WG, false><<<grid, 64 * WG, 0, s>>>(a);
+    moe_quantize<<<a.M * a.K, 512, 0, s>>>(a);
+    const uint32_t lds = std::max((a.M * a.K + 3) / 4 * 16 + a.E * 64 + a.E * a.M, W * MT * 1024u);
+    if (a.F < 16)
+        moe_down<MT, W, true><<<(a.N + 15) / 16, 64 * W, lds, s>>>(a);
+    else
+        moe_down<MT, W, false><<<(a.N + 15) / 16, 64 * W, lds, s>>>(a);
 }
 
 uint32_t bytes_of(int t) { return t == ENTQ_F32 ? 4 : 2; }
@@ -469,7 +520,7 @@ uint64_t lay_out(const entq_rows &x, const entq_experts &e, uint8_t *base, MoeAr
     take(a.share, rows);
     take(a.h, rows * e.hidden);
     take(a.hcodes, rows * a.ldh);
-    take(a.sh, rows);
+    take(a.factor, rows);
     return used;
 }
 
@@ -501,7 +552,6 @@ entq_status entq_moe_few(const entq_rows *x, const entq_experts *e, void *d_y, i
     a.ldx = x->ld;
     a.router = e->d_router;
     a.ldr = e->ldrouter;
-    a.router_type = e->router_type;
     a.M = x->rows;
     a.E = e->experts;
     a.K = e->top_k;
@@ -524,9 +574,15 @@ entq_status entq_moe_few(const entq_rows *x, const entq_experts *e, void *d_y, i
     a.weights = d_weights;
     const hipStream_t s = (hipStream_t)stream;
     const uint32_t route = a.E * ((a.M + kRouteTokens - 1) / kRouteTokens) + a.M;
-    if (x->type == ENTQ_BF16) moe_route<ENTQ_BF16><<<route, 256, 0, s>>>(a);
-    if (x->type == ENTQ_F16) moe_route<ENTQ_F16><<<route, 256, 0, s>>>(a);
-    if (x->type == ENTQ_F32) moe_route<ENTQ_F32><<<route, 256, 0, s>>>(a);
+    const auto go = [&](auto type) {
+        constexpr int T = decltype(type)::value;
+        if (e->router_type == ENTQ_BF16) moe_route<T, ENTQ_BF16><<<route, 256, 0, s>>>(a);
+        if (e->router_type == ENTQ_F16) moe_route<T, ENTQ_F16><<<route, 256, 0, s>>>(a);
+        if (e->router_type == ENTQ_F32) moe_route<T, ENTQ_F32><<<route, 256, 0, s>>>(a);
+    };
+    if (x->type == ENTQ_BF16) go(std::integral_constant<int, ENTQ_BF16>());
+    if (x->type == ENTQ_F16) go(std::integral_constant<int, ENTQ_F16>());
+    if (x->type == ENTQ_F32) go(std::integral_constant<int, ENTQ_F32>());
     moe_choose<<<a.M, kMaxExperts, 0, s>>>(a);
     const uint32_t groups = (a.M + 15) / 16;
     if (groups == 1) launch_products<1>(a, s);

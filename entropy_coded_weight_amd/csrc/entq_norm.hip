@@ -295,9 +295,16 @@ template <int TYPE>
 __device__ __forceinline__ void load_columns(const NormArgs &a, uint32_t p, Columns<TYPE> &c) {
 #pragma unroll
     for (int i = 0; i < kPer<TYPE>; ++i) c.pre[i] = c.post[i] = c.gate[i] = 1.0f;
-    if (a.pre) load_floats<TYPE>(a.pre, p, a.N, c.pre);
-    if (a.post) load_floats<TYPE>(a.post, p, a.N, c.post);
-    if (a.gate_kind == ENTQ_GATE_CHANNEL) load_floats<TYPE>((const float *)a.gate, p, a.N, c.gate);
+    // (each with an offset of its own: none is left for the compiler to share
+    // between branches of which a call takes some)
+    auto read = [&](const float *w, float (&f)[kPer<TYPE>]) {
+        uint32_t q = p;
+        asm("" : "+v"(q));
+        load_floats<TYPE>(w, q, a.N, f);
+    };
+    if (a.pre) read(a.pre, c.pre);
+    if (a.post) read(a.post, c.post);
+    if (a.gate_kind == ENTQ_GATE_CHANNEL) read((const float *)a.gate, c.gate);
 }
 
 // A piece of each of a row's matrices, zeros for those that are absent or not
