@@ -30,6 +30,10 @@ struct MoeArgs {
     int8_t *hcodes;                // [M K][ldh]
     float *factor;                 // [M K]: share times the scale of the codes
     uint64_t ldc, ldh;
+    uint16_t *list;                // the experts in use, and the row of each one's first token: [2][E]
+    uint32_t *count;               // of them
+    float *part;                   // [splits][M][N rounded up to 4]: sums of a part of the list
+    uint32_t splits;
     // the results
     void *y;
     int y_type;
@@ -317,46 +321,69 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
 }
 
 // The hidden values' codes, and what a row's products are scaled with: its
-// scale times the token's weight for the expert.
+// scale times the token's weight for the expert. And once, for the down
+// products, the list of the experts in use, in their order.
 __global__ __launch_bounds__(512) void moe_quantize(MoeArgs a) {
     const uint32_t r = blockIdx.x;
     const float s = quantize_segments<ENTQ_F32, 512>(a.h + (uint64_t)r * a.F, a.F, a.hcodes + r * a.ldh, (uint32_t)a.ldh);
     if (threadIdx.x == 0) a.factor[r] = a.share[r] * s;
+    if (r || threadIdx.x >= 64) return;
+    uint32_t count = 0;
+    for (uint32_t e = 0; e < a.E; e += 64) {
+        const uint32_t mine = e + threadIdx.x;
+        const uint64_t tokens = mine < a.E ? a.tokens[mine] : 0, all = __ballot(tokens != 0);
+        if (tokens) {
+            const uint32_t m = (uint32_t)__builtin_ctzll(tokens);
+            const uint32_t at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+            a.list[at] = (uint16_t)mine;
+            a.list[a.E + at] = (uint16_t)(m * a.K + a.place[mine * a.M + m]);
+        }
+        count += (uint32_t)__popcll(all);
+    }
+    if (threadIdx.x == 0) *a.count = count;
+}
+
+// Results n..n+3 of token m.
+__device__ __forceinline__ void store_result(const MoeArgs &a, uint32_t m, uint32_t n, v4f s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= a.N) continue;
+        const uint64_t to = m * a.ldy + n + i;
+        if (a.y_type == ENTQ_F32)
+            ((float *)a.y)[to] = s[i];
+        else
+            ((uint16_t *)a.y)[to] = bits16(s[i], a.y_type == ENTQ_F16);
+    }
 }
 
 // y = the sum over experts of share (h down^T): a workgroup takes 16 results
-// of every token. The blocks of 128 codes of all experts in use are one list,
-// which its waves take in turn, so that the next expert's codes are on their
-// way while one's are multiplied; at an expert's end a wave scales its integer
-// sums and adds them to its own of fp32.
+// of every token, and its part of a list of the blocks of 128 codes of all
+// experts in use, which its waves take in turn, so that the next expert's
+// codes are on their way while one's are multiplied; at an expert's end a wave
+// scales its integer sums and adds them to its own of fp32. The list is split
+// over workgroups (blockIdx.y), so that there are some for every CU, and
+// moe_join adds the parts up. (Left to the workgroup that ends last it took
+// 297 .. 583 us where all of one token takes 107: the fences that order it
+// write back an XCD's whole L2.)
 template <int MT, int WAVES, bool TINY>
 __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a) {
     constexpr int kDepth = MT > 1 ? 2 : 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t room[];
-    __shared__ uint8_t used[kMaxExperts];
+    __shared__ uint16_t used[kMaxExperts];
     __shared__ uint16_t rows[kMaxExperts];  // of an expert's first token
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), t = threadIdx.x;
     const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32, n = n0 + lane / 16 * 4;
-    // the experts in use, in their order
-    uint32_t count = 0;
-    for (uint32_t e = 0; e < a.E; e += 64) {
-        const bool some = e + lane < a.E && a.tokens[e + lane] != 0;
-        const uint64_t all = __ballot(some);
-        if (some && wave == 0)
-            used[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] =
-                (uint8_t)(e + lane);
-        count += (uint32_t)__popcll(all);
-    }
     float *const factor = (float *)room;                  // [M K]
     float *const scale = factor + (a.M * a.K + 3) / 4 * 4;  // [E in use][16]
     int8_t *const place = (int8_t *)(scale + a.E * 16);   // [E][M]
+    const uint32_t count = *a.count;
+    for (uint32_t i = t; i < a.E; i += 64 * WAVES) {
+        used[i] = i < count ? a.list[i] : 0;
+        rows[i] = i < count ? a.list[a.E + i] : 0;
+    }
     for (uint32_t i = t; i < a.M * a.K; i += 64 * WAVES) factor[i] = a.factor[i];
     for (uint32_t i = t; i < a.E * a.M; i += 64 * WAVES) place[i] = a.place[i];
     __syncthreads();
-    if (t < count) {
-        const uint32_t e = used[t], m = (uint32_t)__builtin_ctzll(a.tokens[e]);
-        rows[t] = (uint16_t)(m * a.K + place[e * a.M + m]);
-    }
     for (uint32_t i = t; i < count * 16; i += 64 * WAVES)
         scale[i] = n0 + i % 16 < a.N ? a.sw[2][used[i / 16] * a.sstride[2] + n0 + i % 16] : 0.0f;
     __syncthreads();
@@ -366,7 +393,10 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a) {
         v4i w[2], x[MT][2];
         uint32_t at;  // in the list of experts
     };
-    uint32_t at = wave / blocks, block = wave % blocks;  // the next to load
+    // this workgroup's items of the list; the next to load, and its place
+    const uint32_t items = count * blocks, end = (uint32_t)((uint64_t)items * (blockIdx.y + 1) / a.splits);
+    uint32_t item = (uint32_t)((uint64_t)items * blockIdx.y / a.splits) + wave;
+    uint32_t at = item / blocks, block = item % blocks;
     auto load = [&](Block &b) {
         b.at = at;
         const uint32_t e = __builtin_amdgcn_readfirstlane(used[at]), k = block * 128 + kc;
@@ -383,6 +413,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) b.x[g][half] = *(const v4i *)(x + 16 * half);
         }
+        item += WAVES;
         block += step_b;
         at += step_e;
         if (block >= blocks) {
@@ -408,11 +439,11 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a) {
         for (int g = 0; g < MT; ++g) acc[g] = v4i{0, 0, 0, 0};
     };
     Block b[kDepth];
-    uint32_t current = at;
+    uint32_t current = item < end ? at : count;
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
         b[d].at = count;
-        if (at < count) load(b[d]);
+        if (item < end) load(b[d]);
     }
     while (b[0].at < count) {
 #pragma unroll
@@ -428,7 +459,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a) {
                 for (int g = 0; g < MT; ++g)
                     acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[d].w[half], b[d].x[g][half], acc[g], 0, 0, 0);
             b[d].at = count;
-            if (at < count) load(b[d]);
+            if (item < end) load(b[d]);
         }
     }
     if (current < count) finish(current);
@@ -438,37 +469,50 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a) {
     for (int g = 0; g < MT; ++g)
         sums[(wave * MT + g) * 64 + lane] = v4f{total[g][0], total[g][1], total[g][2], total[g][3]};
     __syncthreads();
-    if (wave >= MT) return;
-    v4f s = {0, 0, 0, 0};
-#pragma unroll
-    for (int v = 0; v < WAVES; ++v) s += sums[(v * MT + wave) * 64 + lane];
     const uint32_t m = wave * 16 + lane % 16;
-    if (m >= a.M) return;
+    v4f s = {0, 0, 0, 0};
+    if (wave < MT) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i >= a.N) continue;
-        const uint64_t to = m * a.ldy + n + i;
-        if (a.y_type == ENTQ_F32)
-            ((float *)a.y)[to] = s[i];
-        else
-            ((uint16_t *)a.y)[to] = bits16(s[i], a.y_type == ENTQ_F16);
+        for (int v = 0; v < WAVES; ++v) s += sums[(v * MT + wave) * 64 + lane];
     }
+    if (wave >= MT || m >= a.M || n >= a.N) return;
+    if (a.splits > 1)
+        *(v4f *)(a.part + ((uint64_t)blockIdx.y * a.M + m) * ((a.N + 3) / 4 * 4) + n) = s;
+    else
+        store_result(a, m, n, s);
 }
+
+// The results out of the parts' sums, in the order of the parts; four a thread.
+__global__ __launch_bounds__(256) void moe_join(MoeArgs a) {
+    const uint32_t n = 4 * (blockIdx.x * 256 + threadIdx.x), m = blockIdx.y;
+    if (n >= a.N) return;
+    const uint64_t step = (uint64_t)a.M * ((a.N + 3) / 4 * 4);
+    const float *p = a.part + (uint64_t)m * ((a.N + 3) / 4 * 4) + n;
+    v4f s = {0, 0, 0, 0};
+#pragma unroll 4
+    for (uint32_t i = 0; i < a.splits; ++i) s += *(const v4f *)(p + i * step);
+    store_result(a, m, n, s);
+}
+
+// Parts of the list of blocks: some 5 workgroups for each of 256 CUs.
+uint32_t splits_of(uint32_t results) { return std::max(1u, std::min(8u, 1280 / ((results + 15) / 16))); }
 
 template <int MT>
 void launch_products(const MoeArgs &a, hipStream_t s) {
-    constexpr int W = 8, WG = 4;
+    constexpr int W = 4, WG = 4;
     const dim3 grid((a.F + 15) / 16, std::min(a.E, a.M * a.K));
     if (a.D < 16)
         moe_gated<MT, WG, true><<<grid, 64 * WG, 0, s>>>(a);
     else
         moe_gated<MT, WG, false><<<grid, 64 * WG, 0, s>>>(a);
     moe_quantize<<<a.M * a.K, 512, 0, s>>>(a);
+    const dim3 down((a.N + 15) / 16, a.splits);
     const uint32_t lds = std::max((a.M * a.K + 3) / 4 * 16 + a.E * 64 + a.E * a.M, W * MT * 1024u);
     if (a.F < 16)
-        moe_down<MT, W, true><<<(a.N + 15) / 16, 64 * W, lds, s>>>(a);
+        moe_down<MT, W, true><<<down, 64 * W, lds, s>>>(a);
     else
-        moe_down<MT, W, false><<<(a.N + 15) / 16, 64 * W, lds, s>>>(a);
+        moe_down<MT, W, false><<<down, 64 * W, lds, s>>>(a);
+    if (a.splits > 1) moe_join<<<dim3((a.N + 1023) / 1024, a.M), 256, 0, s>>>(a);
 }
 
 uint32_t bytes_of(int t) { return t == ENTQ_F32 ? 4 : 2; }
@@ -521,6 +565,10 @@ uint64_t lay_out(const entq_rows &x, const entq_experts &e, uint8_t *base, MoeAr
     take(a.h, rows * e.hidden);
     take(a.hcodes, rows * a.ldh);
     take(a.factor, rows);
+    a.splits = splits_of(e.out);
+    take(a.list, 2 * e.experts);
+    take(a.count, 1);
+    take(a.part, a.splits > 1 ? a.splits * M * ((e.out + 3) / 4 * 4) : 0);
     return used;
 }
 
