@@ -25,13 +25,15 @@ struct MoeArgs {
     float *sx;                     // [M]
     double *logits;                // [M][E]
     int8_t *place;                 // [E][M]: which of its token's choices the expert is, -1: none
+    uint16_t *chosen;              // [M K]: a choice's expert
     float *share;                  // [M K]: the token's weight for its choice
     float *h;                      // [M K][F]
     int8_t *hcodes;                // [M K][ldh]
     float *factor;                 // [M K]: share times the scale of the codes
     uint64_t ldc, ldh;
-    uint16_t *list;                // the experts in use, and the row of each one's first token: [2][E]
-    uint32_t *count;               // of them
+    uint16_t *jobs;                // [most jobs][2 + columns]: expert, tokens, their rows
+    uint32_t *count;               // of jobs
+    uint32_t most;                 // of jobs there can be
     float *part;                   // [splits][M][N rounded up to 4]: sums of a part of the list
     uint32_t splits;
     // the results
@@ -201,44 +203,82 @@ __global__ __launch_bounds__(kMaxExperts) void moe_choose(MoeArgs a) {
     const float w = (float)(p / s);
     atomicOr((unsigned long long *)&a.tokens[t], 1ull << m);
     a.share[m * a.K + before] = w;
+    a.chosen[m * a.K + before] = (uint16_t)t;
     if (a.experts) a.experts[(uint64_t)m * a.K + before] = (int32_t)t;
     if (a.weights) a.weights[(uint64_t)m * a.K + before] = w;
 }
 
-// The expert that is the nth of those that some token chose, or E.
-__device__ __forceinline__ uint32_t nth_expert(const MoeArgs &a, uint32_t nth, uint32_t lane) {
-    for (uint32_t e = 0; e < a.E; e += 64) {
-        const uint64_t used = __ballot(e + lane < a.E && a.tokens[e + lane] != 0);
-        const uint32_t n = (uint32_t)__popcll(used);
-        if (nth < n) {
-            const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(used >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)used, 0));
-            return e + (uint32_t)__builtin_ctzll(__ballot((used >> lane & 1) && before == nth));
-        }
-        nth -= n;
+// The products go by jobs: an expert and up to COLS of its tokens, in their
+// order, each a column of the matrix instructions. (Most experts of a batch
+// have a few of its tokens: with a column for every token the codes of x and h
+// were two thirds of all loads, and 48 tokens took 428 us.)
+//
+// The jobs of the experts before each lane's (of 64 from e0), and their sum.
+template <int COLS>
+__device__ __forceinline__ uint32_t jobs_before(uint64_t tokens, uint32_t lane, uint32_t &all) {
+    const uint32_t mine = ((uint32_t)__popcll(tokens) + COLS - 1) / COLS;
+    uint32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+        const uint32_t v = (uint32_t)__shfl_up((int)sum, o);
+        if (lane >= (uint32_t)o) sum += v;
     }
-    return a.E;
+    all = (uint32_t)__shfl((int)sum, 63);
+    return sum - mine;
 }
 
-// h = act(x gate^T) (x up^T) for the tokens of one expert: a workgroup takes
-// 16 of its channels, its waves blocks of 128 codes in turn, DEPTH of them on
-// their way. Every token has its column of the matrix instruction; a token
-// that did not choose the expert reads with one that did (the same cache
-// lines, and no branch, so that no load waits for another), and its sums go
+struct Job {
+    uint32_t expert;        // E: there is none
+    uint32_t first;         // of the expert's tokens
+    uint64_t tokens;        // of the expert
+};
+template <int COLS>
+__device__ __forceinline__ Job nth_job(const MoeArgs &a, uint32_t nth, uint32_t lane) {
+    for (uint32_t e = 0; e < a.E; e += 64) {
+        const uint64_t tokens = e + lane < a.E ? a.tokens[e + lane] : 0;
+        uint32_t all;
+        const uint32_t before = jobs_before<COLS>(tokens, lane, all);
+        if (nth < all) {
+            const bool here = tokens && before <= nth && nth - before < ((uint32_t)__popcll(tokens) + COLS - 1) / COLS;
+            const int at = __builtin_ctzll(__ballot(here));
+            const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)tokens, at);
+            const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(tokens >> 32), at);
+            return {e + at, (nth - __builtin_amdgcn_readlane(before, at)) * COLS, (uint64_t)hi << 32 | lo};
+        }
+        nth -= all;
+    }
+    return {a.E, 0, 0};
+}
+
+// The token at a place of the set (its last one for places beyond).
+__device__ __forceinline__ uint32_t token_at(uint64_t tokens, uint32_t place, uint32_t lane) {
+    const uint32_t n = (uint32_t)__popcll(tokens);
+    const uint32_t rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(tokens >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)tokens, 0));
+    // lane r gets the rth token (the others' lanes are past the last one)
+    const uint32_t to = tokens >> lane & 1 ? rank : n + (lane - rank);
+    const int mine = __builtin_amdgcn_ds_permute((int)(to * 4), (int)lane);
+    return (uint32_t)__shfl(mine, (int)min(place, n - 1));
+}
+
+// h = act(x gate^T) (x up^T) for a job: a workgroup takes 16 of the expert's
+// channels, its waves blocks of 128 codes in turn, some of them on their way.
+// Columns beyond the job's tokens read with its last one (the same cache
+// lines, and no branch, so that no load waits for another); their sums go
 // nowhere.
 template <int MT, int WAVES, bool TINY>
 __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
-    constexpr int kDepth = MT > 1 ? 2 : 4;
+    constexpr int kDepth = MT > 1 ? 2 : 4, kCols = 16 * MT;
     __shared__ v4i sums[WAVES][2 * MT][64];
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32;
-    const uint32_t e = gridDim.y == a.E ? blockIdx.y : nth_expert(a, blockIdx.y, lane);
-    const uint64_t tokens = e < a.E ? a.tokens[e] : 0;
-    if (!tokens) return;
-    uint32_t x[MT];
+    const Job job = nth_job<kCols>(a, blockIdx.y, lane);
+    const uint32_t e = job.expert;
+    if (e >= a.E) return;
+    uint32_t x[MT], token[MT];
 #pragma unroll
     for (int g = 0; g < MT; ++g) {
-        const uint32_t m = g * 16 + lane % 16;
-        x[g] = (uint32_t)((tokens >> m & 1 ? m : (uint32_t)__builtin_ctzll(tokens)) * a.ldc) + kc;
+        token[g] = token_at(job.tokens, job.first + g * 16 + lane % 16, lane);
+        x[g] = (uint32_t)(token[g] * a.ldc) + kc;
     }
     const uint64_t row = min(n0 + lane % 16, a.F - 1);
     const int8_t *w[2] = {a.w[0] + e * a.stride[0] + row * a.ldw[0], a.w[1] + e * a.stride[1] + row * a.ldw[1]};
@@ -285,7 +325,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
             if (i + d + kDepth < mine) load(b[d], i + d + kDepth);
         }
     }
-    static_assert(WAVES >= MT, "a wave for each group of tokens at the end");
+    static_assert(WAVES >= MT, "a wave for each 16 columns at the end");
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -298,8 +338,11 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
         s0 += sums[v][wave][lane];
         s1 += sums[v][MT + wave][lane];
     }
-    const uint32_t m = wave * 16 + lane % 16, n = n0 + lane / 16 * 4;
-    if (!(tokens >> m & 1) || n >= a.F) return;
+    uint32_t m = token[0];
+#pragma unroll
+    for (int g = 1; g < MT; ++g) m = wave == (uint32_t)g ? token[g] : m;
+    const uint32_t n = n0 + lane / 16 * 4;
+    if (job.first + wave * 16 + lane % 16 >= (uint32_t)__popcll(job.tokens) || n >= a.F) return;
     const int32_t place = a.place[(uint64_t)e * a.M + m];
     const float sx = a.sx[m];
     float g[4], u[4], r[4], none[4];
@@ -321,26 +364,33 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
 }
 
 // The hidden values' codes, and what a row's products are scaled with: its
-// scale times the token's weight for the expert. And once, for the down
-// products, the list of the experts in use, in their order.
+// scale times the token's weight for the expert. Each row also enters itself
+// into its job.
+template <int COLS>
 __global__ __launch_bounds__(512) void moe_quantize(MoeArgs a) {
     const uint32_t r = blockIdx.x;
     const float s = quantize_segments<ENTQ_F32, 512>(a.h + (uint64_t)r * a.F, a.F, a.hcodes + r * a.ldh, (uint32_t)a.ldh);
     if (threadIdx.x == 0) a.factor[r] = a.share[r] * s;
-    if (r || threadIdx.x >= 64) return;
-    uint32_t count = 0;
+    if (threadIdx.x >= 64) return;
+    const uint32_t lane = threadIdx.x, expert = a.chosen[r], m = r / a.K;
+    uint32_t base = 0, job = 0;
     for (uint32_t e = 0; e < a.E; e += 64) {
-        const uint32_t mine = e + threadIdx.x;
-        const uint64_t tokens = mine < a.E ? a.tokens[mine] : 0, all = __ballot(tokens != 0);
-        if (tokens) {
-            const uint32_t m = (uint32_t)__builtin_ctzll(tokens);
-            const uint32_t at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
-            a.list[at] = (uint16_t)mine;
-            a.list[a.E + at] = (uint16_t)(m * a.K + a.place[mine * a.M + m]);
-        }
-        count += (uint32_t)__popcll(all);
+        const uint64_t tokens = e + lane < a.E ? a.tokens[e + lane] : 0;
+        uint32_t all;
+        const uint32_t before = jobs_before<COLS>(tokens, lane, all);
+        if (expert - e < 64) job = base + (uint32_t)__shfl((int)before, (int)(expert - e));
+        base += all;
     }
-    if (threadIdx.x == 0) *a.count = count;
+    if (lane) return;
+    if (r == 0) *a.count = base;
+    const uint64_t tokens = a.tokens[expert];
+    const uint32_t place = (uint32_t)__popcll(tokens & ((1ull << m) - 1)), n = (uint32_t)__popcll(tokens);
+    uint16_t *entry = a.jobs + (job + place / COLS) * (2 + COLS);
+    entry[2 + place % COLS] = (uint16_t)r;
+    if (place % COLS == 0) {
+        entry[0] = (uint16_t)expert;
+        entry[1] = (uint16_t)min((uint32_t)COLS, n - place);
+    }
 }
 
 // Results n..n+3 of token m.
@@ -358,128 +408,125 @@ __device__ __forceinline__ void store_result(const MoeArgs &a, uint32_t m, uint3
 
 // y = the sum over experts of share (h down^T): a workgroup takes 16 results
 // of every token, and its part of a list of the blocks of 128 codes of all
-// experts in use, which its waves take in turn, so that the next expert's
-// codes are on their way while one's are multiplied; at an expert's end a wave
-// scales its integer sums and adds them to its own of fp32. The list is split
-// over workgroups (blockIdx.y), so that there are some for every CU, and
-// moe_join adds the parts up. (Left to the workgroup that ends last it took
-// 297 .. 583 us where all of one token takes 107: the fences that order it
-// write back an XCD's whole L2.)
+// jobs, which its waves take in turn, so that the next job's codes are on their
+// way while one's are multiplied; at a job's end a wave scales its integer sums
+// and adds them to its tokens' fp32 sums in LDS. The list is split over
+// workgroups (blockIdx.y), so that there are some for every CU, and moe_join
+// adds the parts up. (Left to the workgroup that ends last it took 297 .. 583
+// us where all of one token took 107: the fences that order it write back an
+// XCD's whole L2.)
+constexpr uint32_t kMostJobs = 64;  // of a part of the list
 template <int MT, int WAVES, bool TINY>
 __global__ __launch_bounds__(64 * WAVES) void moe_down(MoeArgs a) {
-    constexpr int kDepth = MT > 1 ? 2 : 4;
+    constexpr int kDepth = MT > 1 ? 2 : 4, kCols = 16 * MT;
     extern __shared__ __attribute__((aligned(16))) uint8_t room[];
-    __shared__ uint16_t used[kMaxExperts];
-    __shared__ uint16_t rows[kMaxExperts];  // of an expert's first token
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), t = threadIdx.x;
-    const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32, n = n0 + lane / 16 * 4;
-    float *const factor = (float *)room;                  // [M K]
-    float *const scale = factor + (a.M * a.K + 3) / 4 * 4;  // [E in use][16]
-    int8_t *const place = (int8_t *)(scale + a.E * 16);   // [E][M]
-    const uint32_t count = *a.count;
-    for (uint32_t i = t; i < a.E; i += 64 * WAVES) {
-        used[i] = i < count ? a.list[i] : 0;
-        rows[i] = i < count ? a.list[a.E + i] : 0;
+    const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32;
+    const uint32_t count = *a.count, blocks = (a.F + 127) / 128;
+    // this workgroup's items of the list, and their jobs
+    const uint32_t items = count * blocks, end = (uint32_t)((uint64_t)items * (blockIdx.y + 1) / a.splits);
+    uint32_t item = (uint32_t)((uint64_t)items * blockIdx.y / a.splits);
+    const uint32_t job0 = item / blocks, n_jobs = (end + blocks - 1) / blocks - job0;
+    float *const sums = (float *)room;                              // [WAVES][M][16]
+    float *const scale = sums + WAVES * a.M * 16;                   // [jobs][16]
+    float *const factor = scale + kMostJobs * 16;                   // [jobs][columns]; 0 beyond the tokens
+    uint16_t *const rows = (uint16_t *)(factor + kMostJobs * kCols);  // [jobs][columns]
+    uint16_t *const expert = rows + kMostJobs * kCols;              // [jobs]
+    for (uint32_t i = t; i < WAVES * a.M * 16; i += 64 * WAVES) sums[i] = 0.0f;
+    for (uint32_t i = t; i < n_jobs * kCols; i += 64 * WAVES) {
+        const uint16_t *entry = a.jobs + (job0 + i / kCols) * (2 + kCols);
+        const uint32_t c = i % kCols, tokens = entry[1];
+        rows[i] = entry[2 + min(c, tokens - 1)];
+        factor[i] = c < tokens ? a.factor[rows[i]] : 0.0f;
+        if (c == 0) expert[i / kCols] = entry[0];
     }
-    for (uint32_t i = t; i < a.M * a.K; i += 64 * WAVES) factor[i] = a.factor[i];
-    for (uint32_t i = t; i < a.E * a.M; i += 64 * WAVES) place[i] = a.place[i];
-    __syncthreads();
-    for (uint32_t i = t; i < count * 16; i += 64 * WAVES)
-        scale[i] = n0 + i % 16 < a.N ? a.sw[2][used[i / 16] * a.sstride[2] + n0 + i % 16] : 0.0f;
+    for (uint32_t i = t; i < n_jobs * 16; i += 64 * WAVES) {
+        const uint32_t e = a.jobs[(job0 + i / 16) * (2 + kCols)];
+        scale[i] = n0 + i % 16 < a.N ? a.sw[2][e * a.sstride[2] + n0 + i % 16] : 0.0f;
+    }
     __syncthreads();
     const uint64_t row = min(n0 + lane % 16, a.N - 1) * a.ldw[2];
-    const uint32_t blocks = (a.F + 127) / 128, step_e = WAVES / blocks, step_b = WAVES % blocks;
+    const uint32_t step_j = WAVES / blocks, step_b = WAVES % blocks;
     struct Block {
         v4i w[2], x[MT][2];
-        uint32_t at;  // in the list of experts
+        uint32_t job;
     };
-    // this workgroup's items of the list; the next to load, and its place
-    const uint32_t items = count * blocks, end = (uint32_t)((uint64_t)items * (blockIdx.y + 1) / a.splits);
-    uint32_t item = (uint32_t)((uint64_t)items * blockIdx.y / a.splits) + wave;
-    uint32_t at = item / blocks, block = item % blocks;
+    item += wave;
+    uint32_t job = item / blocks - job0, block = item % blocks;  // the next to load
     auto load = [&](Block &b) {
-        b.at = at;
-        const uint32_t e = __builtin_amdgcn_readfirstlane(used[at]), k = block * 128 + kc;
+        b.job = job;
+        const uint32_t e = __builtin_amdgcn_readfirstlane(expert[job]), k = block * 128 + kc;
         const int8_t *w = a.w[2] + e * a.stride[2] + row;
 #pragma unroll
         for (int half = 0; half < 2; ++half) b.w[half] = weight_segment<TINY>(w, k + 16 * half, a.F);
-        // (a token without the expert reads with its first one, as in moe_gated)
-        const uint32_t first = __builtin_amdgcn_readfirstlane(rows[at]);
 #pragma unroll
         for (int g = 0; g < MT; ++g) {
-            const uint32_t m = g * 16 + lane % 16;
-            const int32_t p = m < a.M ? place[e * a.M + m] : -1;
-            const int8_t *x = a.hcodes + (uint64_t)(p < 0 ? first : m * a.K + p) * a.ldh + k;
+            const int8_t *x = a.hcodes + rows[job * kCols + g * 16 + lane % 16] * a.ldh + k;
 #pragma unroll
             for (int half = 0; half < 2; ++half) b.x[g][half] = *(const v4i *)(x + 16 * half);
         }
         item += WAVES;
         block += step_b;
-        at += step_e;
+        job += step_j;
         if (block >= blocks) {
             block -= blocks;
-            ++at;
+            ++job;
         }
     };
-    float total[MT][4] = {};
     v4i acc[MT] = {};
     auto finish = [&](uint32_t done) {
-        const uint32_t e = __builtin_amdgcn_readfirstlane(used[done]);
         const v4f s = *(const v4f *)(scale + done * 16 + lane / 16 * 4);
 #pragma unroll
         for (int g = 0; g < MT; ++g) {
-            const uint32_t m = g * 16 + lane % 16;
-            const int32_t p = m < a.M ? place[e * a.M + m] : -1;
-            if (p < 0) continue;
-            const float f = factor[m * a.K + p];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) total[g][i] += (float)acc[g][i] * f * s[i];
+            const uint32_t c = done * kCols + g * 16 + lane % 16;
+            const float f = factor[c];
+            const bool last = g * 16 + lane % 16 > 0 && rows[c] == rows[c - 1];  // (beyond the tokens)
+            if (!last) {
+                v4f *to = (v4f *)(sums + (wave * a.M + rows[c] / a.K) * 16 + lane / 16 * 4);
+                *to += v4f{(float)acc[g][0] * f * s[0], (float)acc[g][1] * f * s[1], (float)acc[g][2] * f * s[2],
+                           (float)acc[g][3] * f * s[3]};
+            }
+            acc[g] = v4i{0, 0, 0, 0};
         }
-#pragma unroll
-        for (int g = 0; g < MT; ++g) acc[g] = v4i{0, 0, 0, 0};
     };
     Block b[kDepth];
-    uint32_t current = item < end ? at : count;
+    constexpr uint32_t kNone = 0xFFFFFFFFu;
+    uint32_t current = item < end ? job : kNone;
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-        b[d].at = count;
+        b[d].job = kNone;
         if (item < end) load(b[d]);
     }
-    while (b[0].at < count) {
+    while (b[0].job != kNone) {
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
-            if (b[d].at >= count) continue;
-            if (b[d].at != current) {
+            if (b[d].job == kNone) continue;
+            if (b[d].job != current) {
                 finish(current);
-                current = b[d].at;
+                current = b[d].job;
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int g = 0; g < MT; ++g)
                     acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[d].w[half], b[d].x[g][half], acc[g], 0, 0, 0);
-            b[d].at = count;
+            b[d].job = kNone;
             if (item < end) load(b[d]);
         }
     }
-    if (current < count) finish(current);
-    __syncthreads();  // the tables are done with: their room holds the waves' sums
-    v4f *const sums = (v4f *)room;
-#pragma unroll
-    for (int g = 0; g < MT; ++g)
-        sums[(wave * MT + g) * 64 + lane] = v4f{total[g][0], total[g][1], total[g][2], total[g][3]};
+    if (current != kNone) finish(current);
     __syncthreads();
-    const uint32_t m = wave * 16 + lane % 16;
-    v4f s = {0, 0, 0, 0};
-    if (wave < MT) {
+    for (uint32_t i = t; i < a.M * 4; i += 64 * WAVES) {
+        v4f s = {0, 0, 0, 0};
 #pragma unroll
-        for (int v = 0; v < WAVES; ++v) s += sums[(v * MT + wave) * 64 + lane];
+        for (int v = 0; v < WAVES; ++v) s += *(const v4f *)(sums + (v * a.M * 4 + i) * 4);
+        const uint32_t m = i / 4, at = n0 + i % 4 * 4;
+        if (at >= a.N) continue;
+        if (a.splits > 1)
+            *(v4f *)(a.part + ((uint64_t)blockIdx.y * a.M + m) * ((a.N + 3) / 4 * 4) + at) = s;
+        else
+            store_result(a, m, at, s);
     }
-    if (wave >= MT || m >= a.M || n >= a.N) return;
-    if (a.splits > 1)
-        *(v4f *)(a.part + ((uint64_t)blockIdx.y * a.M + m) * ((a.N + 3) / 4 * 4) + n) = s;
-    else
-        store_result(a, m, n, s);
 }
 
 // The results out of the parts' sums, in the order of the parts; four a thread.
@@ -494,20 +541,33 @@ __global__ __launch_bounds__(256) void moe_join(MoeArgs a) {
     store_result(a, m, n, s);
 }
 
-// Parts of the list of blocks: some 5 workgroups for each of 256 CUs.
-uint32_t splits_of(uint32_t results) { return std::max(1u, std::min(8u, 1280 / ((results + 15) / 16))); }
+// Parts of the list of blocks: some 5 workgroups for each of 256 CUs, and the
+// jobs of a part (one more than its share, where it begins inside one) in LDS.
+uint32_t splits_of(uint32_t results, uint32_t most) {
+    const uint32_t fill = std::min(8u, 1280 / ((results + 15) / 16));
+    return std::max(std::max(1u, fill), (most + kMostJobs - 3) / (kMostJobs - 2));
+}
+
+// Columns of a job: as many as the experts have tokens on average, times two.
+uint32_t columns_of(uint32_t tokens, uint32_t top_k, uint32_t experts) {
+    const uint32_t average = tokens * top_k / experts;
+    return tokens <= 16 || average <= 8 ? 16 : tokens <= 32 || average <= 16 ? 32 : 64;
+}
+uint32_t most_jobs(uint32_t tokens, uint32_t top_k, uint32_t experts, uint32_t columns) {
+    const uint32_t rows = tokens * top_k;
+    return std::min(rows, std::min(experts, rows) + rows / columns);
+}
 
 template <int MT>
 void launch_products(const MoeArgs &a, hipStream_t s) {
-    constexpr int W = 4, WG = 4;
-    const dim3 grid((a.F + 15) / 16, std::min(a.E, a.M * a.K));
+    constexpr int W = 4;
+    const dim3 grid((a.F + 15) / 16, a.most), down((a.N + 15) / 16, a.splits);
     if (a.D < 16)
-        moe_gated<MT, WG, true><<<grid, 64 * WG, 0, s>>>(a);
+        moe_gated<MT, W, true><<<grid, 64 * W, 0, s>>>(a);
     else
-        moe_gated<MT, WG, false><<<grid, 64 * WG, 0, s>>>(a);
-    moe_quantize<<<a.M * a.K, 512, 0, s>>>(a);
-    const dim3 down((a.N + 15) / 16, a.splits);
-    const uint32_t lds = std::max((a.M * a.K + 3) / 4 * 16 + a.E * 64 + a.E * a.M, W * MT * 1024u);
+        moe_gated<MT, W, false><<<grid, 64 * W, 0, s>>>(a);
+    moe_quantize<16 * MT><<<a.M * a.K, 512, 0, s>>>(a);
+    const uint32_t lds = W * a.M * 64 + kMostJobs * (64 + 16 * MT * 6 + 2);
     if (a.F < 16)
         moe_down<MT, W, true><<<down, 64 * W, lds, s>>>(a);
     else
@@ -561,12 +621,15 @@ uint64_t lay_out(const entq_rows &x, const entq_experts &e, uint8_t *base, MoeAr
     take(a.sx, M);
     take(a.logits, M * e.experts);
     take(a.place, M * e.experts);
+    take(a.chosen, rows);
     take(a.share, rows);
     take(a.h, rows * e.hidden);
     take(a.hcodes, rows * a.ldh);
     take(a.factor, rows);
-    a.splits = splits_of(e.out);
-    take(a.list, 2 * e.experts);
+    const uint32_t columns = columns_of(x.rows, e.top_k, e.experts);
+    a.most = most_jobs(x.rows, e.top_k, e.experts, columns);
+    a.splits = splits_of(e.out, a.most);
+    take(a.jobs, a.most * (2 + columns));
     take(a.count, 1);
     take(a.part, a.splits > 1 ? a.splits * M * ((e.out + 3) / 4 * 4) : 0);
     return used;
@@ -632,10 +695,10 @@ entq_status entq_moe_few(const entq_rows *x, const entq_experts *e, void *d_y, i
     if (x->type == ENTQ_F16) go(std::integral_constant<int, ENTQ_F16>());
     if (x->type == ENTQ_F32) go(std::integral_constant<int, ENTQ_F32>());
     moe_choose<<<a.M, kMaxExperts, 0, s>>>(a);
-    const uint32_t groups = (a.M + 15) / 16;
-    if (groups == 1) launch_products<1>(a, s);
-    if (groups == 2) launch_products<2>(a, s);
-    if (groups > 2) launch_products<4>(a, s);
+    const uint32_t columns = columns_of(a.M, a.K, a.E);
+    if (columns == 16) launch_products<1>(a, s);
+    if (columns == 32) launch_products<2>(a, s);
+    if (columns == 64) launch_products<4>(a, s);
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
