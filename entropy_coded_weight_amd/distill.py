@@ -50,7 +50,12 @@ def _describe(logits, index, teacher, teacher_lse, weight, temperature):
     dev = _gpu("logits", logits)
     kind, ld = _matrix("logits", logits, dev, _FLOATS)
     _no_graph("logits", logits)
-    m, v = logits.shape
+    return dev, _entries(dev, *logits.shape, kind, logits.data_ptr(), ld, index, teacher,
+                         teacher_lse, weight, temperature)
+
+
+def _entries(dev, m, v, kind, z, ld, index, teacher, teacher_lse, weight, temperature):
+    """The call for m x v logits of type ``kind`` at z."""
     if not 1 <= v <= MAX_CLASSES:
         raise EntqError(EINVAL, f"{v} classes, 1 to {MAX_CLASSES} are taken")
     if not isinstance(teacher, torch.Tensor) or teacher.dim() != 2 or teacher.shape[0] != m:
@@ -66,8 +71,8 @@ def _describe(logits, index, teacher, teacher_lse, weight, temperature):
     t = _number("temperature", temperature)
     if not 1e-4 <= t <= 1e4:
         raise EntqError(EINVAL, f"temperature {t}: 1e-4 to 1e4 is taken")
-    return dev, Distill(m, v, k, kind, tkind, size, t, 0, logits.data_ptr(), index.data_ptr(),
-                        teacher.data_ptr(), ld, ldi, ldt, lse, w)
+    return Distill(m, v, k, kind, tkind, size, t, 0, z, index.data_ptr(), teacher.data_ptr(), ld,
+                   ldi, ldt, lse, w)
 
 
 def loss(logits, index, teacher, loss, teacher_lse=None, weight=None, temperature=1.0,

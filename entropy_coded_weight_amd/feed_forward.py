@@ -11,6 +11,13 @@ quantised again for the last product. The backward pass gives the gradients
 of x and of every row scale; the codes are constants. Neither records an
 autograd graph, and an x or dy that would need one is refused: a
 torch.autograd.Function calls ``forward`` and ``backward`` for it.
+
+``residual`` is the block between its norms, as it stands in a transformer,
+
+    out = alpha x + beta gate norm(block(norm(x) pre)) post
+
+with the first norm written as the codes that the products take and the rest in
+one kernel; ``residual_backward`` gives its gradients.
 """
 from __future__ import annotations
 
@@ -19,7 +26,7 @@ import weakref
 
 import torch
 
-from . import EINVAL, KIND_INT8, OUT_CODES, EntqError, Plan, _device_buffer, decode, int8
+from . import EINVAL, KIND_INT8, OUT_CODES, EntqError, Plan, _device_buffer, decode, int8, norm
 
 
 def _on(stream, device):
@@ -161,14 +168,100 @@ class FeedForward(DecodedCodes):
             _device_buffer(self.plan, "dscales", dscales, self.plan.scale_rows,
                            dtypes=(torch.float32,))
         with self._using_codes(stream):
-            new = lambda n, t: torch.empty(m, n, dtype=t, device=x.device)  # noqa: E731
-            h = new(self.hidden, self.hidden_type or x.dtype)
-            q, qh = new(self.width, torch.int8), new(self.hidden, torch.int8)
-            sx, sh = (torch.empty(m, dtype=torch.float32, device=x.device) for _ in range(2))
-            dh = new(self.hidden, dy.dtype)
+            q = torch.empty(m, self.width, dtype=torch.int8, device=x.device)
+            sx = torch.empty(m, dtype=torch.float32, device=x.device)
             int8.quantize_rows(x, q, sx)
+            h = self._hidden(q, sx, x.dtype)
+            self._backward(dy, q, sx, *h, dx, dscales)
+
+    def _hidden(self, q, sx, dtype):
+        """The hidden values' codes and scales."""
+        m = q.shape[0]
+        h = torch.empty(m, self.hidden, dtype=self.hidden_type or dtype, device=q.device)
+        qh = torch.empty(m, self.hidden, dtype=torch.int8, device=q.device)
+        sh = torch.empty(m, dtype=torch.float32, device=q.device)
+        int8.gated(q, sx, *self._w[:4], h, self.activation)
+        int8.quantize_rows(h, qh, sh)
+        return qh, sh
+
+    def _backward(self, dy, q, sx, qh, sh, dx, dscales):
+        dh = torch.empty(q.shape[0], self.hidden, dtype=dy.dtype, device=dy.device)
+        dg, du, dd = (dscales.view(-1)[s] if dscales is not None else None for s in self._at)
+        int8.gemm_backward(dy, qh, sh, *self._w[4:], dh, dd)
+        int8.gated_backward(dh, q, sx, *self._w[:4], dx, dg, du, self.activation)
+
+    def _check_residual(self, x, pre, post, gate, alpha, beta, eps):
+        if self.out != self.width:
+            raise EntqError(EINVAL, f"a residual block has as many results as columns, this one "
+                                    f"{self.out} and {self.width}")
+        index = self.plan.device.index
+        int8._check_activations("x", x, index, self.width)
+        # (x in the place of the block's result, which has its shape and type)
+        if pre is None:
+            raise EntqError(EINVAL, "pre is required")
+        return norm._describe(x, x, post, gate, pre, alpha, beta, eps)
+
+    def residual(self, x, out, pre, post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6,
+                 stream=None):
+        """out = alpha x + beta gate norm(block(norm(x) pre)) post: x and out
+        bfloat16, float16 or float32 [m, D] of one type (out may be x), the
+        rest as in ``norm.block``; without post the block's result is not
+        normalised."""
+        index, a = self._check_residual(x, pre, post, gate, alpha, beta, eps)
+        int8._matrix("out", out, index, (a.type,), x.shape)
+        with self._using_codes(stream):
+            q, sx = self._normed(x, pre, eps)
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            h = torch.empty(x.shape[0], self.hidden, dtype=self.hidden_type or x.dtype,
+                            device=x.device)
             int8.gated(q, sx, *self._w[:4], h, self.activation)
-            int8.quantize_rows(h, qh, sh)
-            dg, du, dd = (dscales.view(-1)[s] if dscales is not None else None for s in self._at)
-            int8.gemm_backward(dy, qh, sh, *self._w[4:], dh, dd)
-            int8.gated_backward(dh, q, sx, *self._w[:4], dx, dg, du, self.activation)
+            int8.gemm(h, None, *self._w[4:], y)
+            norm.block(x, y, out, post, gate, alpha=alpha, beta=beta, eps=eps)
+
+    def _normed(self, x, pre, eps):
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        sx = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        norm.block(x, pre=pre, y=q, y_scales=sx, eps=eps)
+        return q, sx
+
+    def residual_backward(self, dout, x, pre, post=None, gate=None, dx=None, dscales=None,
+                          dpre=None, dpost=None, dgate=None, alpha=1.0, beta=1.0, eps=1e-6,
+                          stream=None):
+        """Gradients of ``residual`` for dout = dL/dout (bfloat16 or float16
+        [m, D], x's type): dx (that type), dscales (float32 [scale_rows]),
+        dpre, dpost (float32 [D]) and dgate (as the gate); None: not computed.
+        The forward pass is done again from x. Where alpha is not 1, alpha dout
+        is rounded to dout's type before the rest of dx is added."""
+        index, a = self._check_residual(x, pre, post, gate, alpha, beta, eps)
+        int8._matrix("x", x, index, (int8._BF16, int8._F16))
+        int8._grad_rows("dout", dout, index, *x.shape)
+        if x.dtype != dout.dtype:
+            raise EntqError(EINVAL, f"dout has dtype {dout.dtype}, x {x.dtype}")
+        if dx is not None:
+            int8._matrix("dx", dx, index, (a.type,), x.shape)
+        if dscales is not None:
+            _device_buffer(self.plan, "dscales", dscales, self.plan.scale_rows,
+                           dtypes=(torch.float32,))
+        for name, t, of in (("dpre", dpre, pre), ("dpost", dpost, post)):
+            if t is not None:
+                if of is None:
+                    raise EntqError(EINVAL, f"{name} without {name[1:]}")
+                int8._vector(name, t, index, self.width)
+        if dgate is not None:
+            if gate is None or norm._gate("dgate", dgate, a.type, index, *x.shape)[0] != a.gate_kind:
+                raise EntqError(EINVAL, "dgate goes with a gate of its shape")
+        with self._using_codes(stream):
+            q, sx = self._normed(x, pre, eps)
+            h = self._hidden(q, sx, x.dtype)
+            new = lambda: torch.empty(x.shape, dtype=x.dtype, device=x.device)  # noqa: E731
+            y, dy, dn = new(), new(), new()
+            int8.gemm(*h, *self._w[4:], y)
+            rest = dout if alpha == 1 else new()
+            norm.block_backward(x, dout, None, y, post, gate, None, None if alpha == 1 else rest,
+                                dy, dgate, None, dpost, alpha, beta, eps)
+            if dx is None and dpre is None and dscales is None:
+                return
+            wanted = dx is not None or dpre is not None
+            self._backward(dy, q, sx, *h, dn if wanted else None, dscales)
+            if wanted:
+                norm.block_backward(x, rest, dn, pre=pre, dx=dx, dpre=dpre, eps=eps)

@@ -98,3 +98,74 @@ def linear_int8(p: Plan, compressed, scales, xs, ys, codes=None, chunk_status=No
             rows, cols = int(r["rows"]), int(r["cols"])
             o, s = int(r["out_elem_offset"]), int(r["scale_row_offset"])
             int8.gemm(xs[t], None, codes[o:o + rows * cols].view(rows, cols), scales[s:s + rows], ys[t])
+
+
+def distill_int8(p: Plan, compressed, scales, x, index, teacher, loss, dx=None, dscales=None,
+                 dloss=None, teacher_lse=None, weight=None, temperature=1.0, codes=None,
+                 tokens=1024, chunk_status=None, stream=None):
+    """The distillation loss of a compressed output projection and its
+    gradients, for any number of tokens: the plan's one Int8 tensor W [V, D]
+    is decoded to codes; then, ``tokens`` tokens at a time, the fp32 logits
+    x . W^T (int8.gemm), the losses with the logits' gradient in x's type
+    (distill.loss_backward), and the gradients of x and of the row scales
+    (int8.gemm_backward). The logits of all tokens are never in memory.
+
+    x: device bfloat16 or float16 [m, D]; loss: float32 [m]; dx: x's type [m, D];
+    dscales: float32 [V], the sum over all tokens in fp32; None: not computed
+    (both None: the losses alone). index, teacher, dloss, teacher_lse, weight and
+    temperature as in ``distill.loss_backward`` (a float16 gradient below 6e-8
+    is 0, which a larger dloss mends); codes and stream as in ``linear_int8``."""
+    import torch
+
+    from . import distill, int8
+    from .feed_forward import _on
+    if p.n_tensors != 1 or (int(p.tensors[0]["kind"]) & 0xFF) != KIND_INT8:
+        raise EntqError(EINVAL, "distill_int8 takes a plan of one Int8 tensor")
+    v, d = int(p.tensors[0]["rows"]), int(p.tensors[0]["cols"])
+    _device_buffer(p, "scales", scales, p.scale_rows, dtypes=(torch.float32,))
+    if codes is not None:
+        _device_buffer(p, "codes", codes, p.out_elems, dtypes=(torch.int8,))
+    if not isinstance(tokens, int) or tokens < 1:
+        raise EntqError(EINVAL, f"tokens is {tokens!r}: a positive number is required")
+    at = p.device.index
+    m = int8._check_activations("x", x, at, d, (int8._BF16, int8._F16))
+    distill._entries(at, m, v, int8._F32, 0, v, index, teacher, teacher_lse, weight, temperature)
+    int8._vector("loss", loss, at, m)
+    if dloss is not None:
+        int8._vector("dloss", dloss, at, m)
+    if dx is not None:
+        int8._matrix("dx", dx, at, (int8._TYPES[x.dtype],), x.shape)
+    if dscales is not None:
+        _device_buffer(p, "dscales", dscales, p.scale_rows, dtypes=(torch.float32,))
+    with _on(stream, p.device):
+        new = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=p.device)  # noqa: E731
+        if codes is None:
+            codes = new(p.out_elems, t=torch.int8)
+        decode(p, compressed, codes, OUT_CODES, None, chunk_status)
+        r = p.tensors[0]
+        o, s = int(r["out_elem_offset"]), int(r["scale_row_offset"])
+        w, ws = codes.view(-1)[o:o + v * d].view(v, d), scales.view(-1)[s:s + v]
+        n = min(m, tokens)
+        q, sx, logits = new(n, d, t=torch.int8), new(n), new(n, v)
+        if dx is not None or dscales is not None:
+            dlogits = new(n, v, t=x.dtype)
+        if dscales is not None:
+            sums, part = dscales.view(-1)[s:s + v].zero_(), new(v)
+        for i in range(0, m, tokens):
+            k = min(m - i, tokens)
+            cut = lambda t: None if t is None else t[i:i + k]  # noqa: B023, E731
+            entries = dict(teacher_lse=cut(teacher_lse), weight=cut(weight),
+                           temperature=temperature)
+            int8.quantize_rows(cut(x), q[:k], sx[:k])
+            int8.gemm(q[:k], sx[:k], w, ws, logits[:k])
+            if dx is None and dscales is None:
+                distill.loss(logits[:k], cut(index), cut(teacher), cut(loss), **entries)
+                continue
+            distill.loss_backward(logits[:k], cut(index), cut(teacher), dlogits[:k], cut(dloss),
+                                  cut(loss), **entries)
+            # (a token that is not finite but has no weight takes no part in dscales)
+            sx[:k].nan_to_num_()
+            int8.gemm_backward(dlogits[:k], q[:k], sx[:k], w, ws, cut(dx),
+                               part if dscales is not None else None)
+            if dscales is not None:
+                sums.add_(part)
