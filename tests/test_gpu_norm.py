@@ -152,6 +152,22 @@ def test_backward_of_one_incoming_gradient_or_no_branch(N, m, n, kind):
         close(v, *want[name], name)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n", [(1, 1), (5, 7), (3, 513), (3, 2049), (7, 4100), (3, 8192), (2, 8200), (600, 200)])
+def test_backward_of_a_full_gate_without_norms(N, m, n, kind):
+    """branch and gate alone (a sum of products), with either incoming gradient."""
+    s, b, d, g = (matrix(m, n, kind, i, 1, i) for i in range(4))
+    pre = vector(n, 5)
+    for dy in (None, matrix(m, n, kind, 9)):
+        got = {name: matrix(m, n, kind, 7, 2, 3) for name in ("dx", "dbranch", "dgate")}
+        N.block_backward(s, d, dy, b, None, g, pre if dy is not None else None, alpha=-2.0, beta=0.5, **got)
+        want = R.gradients(s, d, dy, b, None, g, pre, -2.0, 0.5, 1e-6, kind)
+        for name, v in got.items():
+            close(v, *want[name], name)
+            tail = v.as_strided((m - 1, 2), (n + 2, 1), v.storage_offset() + n)
+            assert bool((tail == 7).all()), name
+
+
 @pytest.mark.parametrize("n", [24, 3000, 33000])
 def test_large_and_small_values(N, n):
     """fp32 rows whose squares leave fp32's range; zero rows."""
