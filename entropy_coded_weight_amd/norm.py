@@ -23,12 +23,15 @@ import math
 import torch
 
 from . import EINVAL, EntqError, Norm, lib
-from .int8 import (_F32, _I8, _TYPES, MAX_COLS, _enqueue, _gpu, _matrix, _no_graph, _vector)
+from .int8 import (_BF16, _F16, _F32, _I8, MAX_COLS, _enqueue, _gpu, _matrix, _no_graph, _vector)
 
 _NONE, _CHANNEL, _TOKEN, _FULL = 0, 1, 2, 3
+_FLOATS = (_BF16, _F16, _F32)
 
 
 def _number(name, v):
+    if type(v) is float and -3e38 <= v <= 3e38:
+        return v
     if not isinstance(v, (int, float)) or not math.isfinite(v) or abs(v) > 3e38:
         raise EntqError(EINVAL, f"{name} is {v!r}: a finite number is required")
     return float(v)
@@ -53,30 +56,33 @@ def _gate(name, t, kind, index, m, n):
 
 def _describe(x, branch, post, gate, pre, alpha, beta, eps, what="x"):
     index = _gpu(what, x)
-    kind, ldx = _matrix(what, x, index, tuple(v for v in _TYPES.values() if v != _I8))
+    kind, ldx = _matrix(what, x, index, _FLOATS)
     _no_graph(what, x)
-    m, n = x.shape
+    m, n = shape = x.shape
     if n > MAX_COLS:
         raise EntqError(EINVAL, f"{what} has {n} columns, at most {MAX_COLS} are taken")
-    if branch is None and (post is not None or gate is not None or alpha != 1 or beta != 1):
-        raise EntqError(EINVAL, "post, gate, alpha and beta belong to a branch")
-    a = Norm(m, n, kind, _NONE, x.data_ptr(), 0, 0, ldx, n, n, 0, 0, _number("alpha", alpha),
-             _number("beta", beta), _number("eps", eps), 0)
-    if not a.eps > 0:
-        raise EntqError(EINVAL, f"eps is {eps!r}: a positive number is required")
+    b = p = g = w = 0
+    ldb = ldg = n
+    gate_kind = _NONE
     if branch is not None:
-        _, a.ldbranch = _matrix("branch", branch, index, (kind,), (m, n))
+        _, ldb = _matrix("branch", branch, index, (kind,), shape)
         _no_graph("branch", branch)
-        a.branch = branch.data_ptr()
+        b = branch.data_ptr()
+    elif post is not None or gate is not None or alpha != 1 or beta != 1:
+        raise EntqError(EINVAL, "post, gate, alpha and beta belong to a branch")
     if post is not None:
-        a.post = _vector("post", post, index, n)
+        p = _vector("post", post, index, n)
     if pre is not None:
-        a.pre = _vector("pre", pre, index, n)
+        w = _vector("pre", pre, index, n)
     if gate is not None:
-        a.gate_kind, a.ldgate = _gate("gate", gate, kind, index, m, n)
-        if a.gate_kind == _FULL:
+        gate_kind, ldg = _gate("gate", gate, kind, index, m, n)
+        if gate_kind == _FULL:
             _no_graph("gate", gate)
-        a.gate = gate.data_ptr()
+        g = gate.data_ptr()
+    a = Norm(m, n, kind, gate_kind, x.data_ptr(), b, g, ldx, ldb, ldg, p, w,
+             _number("alpha", alpha), _number("beta", beta), _number("eps", eps), 0)
+    if not a.eps > 0:  # (of the fp32 number)
+        raise EntqError(EINVAL, f"eps is {eps!r}: a positive number is required")
     return index, a
 
 
@@ -87,18 +93,18 @@ def block(x, branch=None, out=None, post=None, gate=None, pre=None, y=None, y_sc
     with ``y_scales`` (float32 [M]). Without a branch the state is x and only y
     is written. y None: no norm (pre is then None too)."""
     index, a = _describe(x, branch, post, gate, pre, alpha, beta, eps)
-    shape = x.shape
+    shape, kind, n = x.shape, a.type, a.cols
     if (branch is None) != (out is None):
         raise EntqError(EINVAL, "out is required with a branch and takes nothing without one")
     if branch is None and y is None:
         raise EntqError(EINVAL, "neither a branch nor y: there is nothing to do")
     if (y is None) != (pre is None):
         raise EntqError(EINVAL, "y and pre go together")
-    ldo, ldy, y_type, yp, sp, op = a.cols, a.cols, a.type, 0, 0, 0
+    ldo, ldy, y_type, yp, sp, op = n, n, kind, 0, 0, 0
     if out is not None:
-        ldo, op = _matrix("out", out, index, (a.type,), shape)[1], out.data_ptr()
+        ldo, op = _matrix("out", out, index, (kind,), shape)[1], out.data_ptr()
     if y is not None:
-        y_type, ldy = _matrix("y", y, index, (a.type, _I8), shape)
+        y_type, ldy = _matrix("y", y, index, (kind, _I8), shape)
         yp = y.data_ptr()
     if (y_type == _I8) != (y_scales is not None):
         raise EntqError(EINVAL, "y_scales go with int8 codes in y")
