@@ -470,9 +470,6 @@ bool few_quantizes(uint32_t M, uint32_t K);
 int launch_int8_few(Int8Mode mode, const Int8Args &a, hipStream_t s);
 int launch_int8_product(Int8Mode mode, const Int8Plan &p, const Int8Args &a, hipStream_t s);
 
-// entq_quantize_rows without its checks, with zeros in columns K..ldc-1.
-entq_status quantize_padded(const entq_rows &x, int8_t *codes, uint64_t ldc, float *scales, hipStream_t s);
-
 struct GradPlan {
     int kind;               // of tile
     uint32_t splits;

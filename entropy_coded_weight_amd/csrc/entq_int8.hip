@@ -521,11 +521,6 @@ bool bad_act(int act) { return act < ENTQ_ACT_SILU || act > ENTQ_ACT_RELU; }
 
 }  // namespace
 
-entq_status quantize_padded(const entq_rows &x, int8_t *codes, uint64_t ldc, float *scales, hipStream_t s) {
-    Aligner none;
-    return (entq_status)launch_quantize(x, codes, ldc, (uint32_t)ldc, scales, none, s);
-}
-
 }  // namespace entq
 
 using entq::describe;

@@ -94,6 +94,36 @@ def test_equal_logits_go_to_the_lowest_index(M):
     assert torch.isfinite(y).all()
 
 
+@pytest.mark.parametrize("m,e,k,d,f,n", [(4, 64, 32, 64, 48, 20), (4, 65, 32, 64, 48, 20), (5, 64, 32, 64, 48, 20), (2, 64, 64 // 2, 15, 520, 5),
+                                         (3, 40, 9, 200, 15, 4100), (1, 33, 1, 100, 511, 3), (4, 7, 7, 33, 513, 9000),
+                                         (4, 64, 8, 300, 16, 1)])
+def test_few_tokens(M, m, e, k, d, f, n):
+    for kind in ("bf16", "f32"):
+        x, router, w = layer(m, e, d, f, n, kind, "f32", 17, 1)
+        check(M, x, router, w, k, "silu", True, kind)
+
+
+@pytest.mark.parametrize("m", [3, 9])
+def test_choices_of_nearly_equal_logits(M, m):
+    """Logits that are equal in 32 bits and differ in 64, in no order of their
+    experts, beside exactly equal ones and NaN."""
+    e, d = 48, 64
+    x, router, w = layer(m, e, d, 32, 24, "f32", "f32", 8)
+    x[:, :3] = torch.tensor([1.0, 2.0 ** -20, 2.0 ** -20], device="cuda")
+    router.zero_()
+    router[:, 0] = 1.0
+    g = torch.Generator(device="cuda").manual_seed(1)
+    router[:, 1] = (torch.randperm(e, device="cuda", generator=g) // 2) * 2.0 ** -20
+    router[5, 2] = router[5, 1]
+    check(M, x, router, w, 12, "silu", True, "f32")
+    check(M, x, router, w, 12, "silu", False, "f32")
+    router[7, 0] = float("nan")  # of every token
+    experts, y = torch.empty(m, 12, dtype=torch.int32, device="cuda"), torch.empty(m, 24, device="cuda")
+    p = torch.empty(m, 12, device="cuda")
+    M.few(x, router, *w, y, 12, experts=experts, weights=p)
+    assert torch.equal(experts.long(), R.choose(x, router, 12, True)[0]) and p.isnan().all() and bool((experts[:, 0] == 7).all())
+
+
 def test_rows_that_are_not_finite(M):
     x, router, w = layer(6, 8, 200, 90, 50, "bf16", "f32", 5)
     good, y = x.clone(), torch.empty(6, 50, device="cuda")
