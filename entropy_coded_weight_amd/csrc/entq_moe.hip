@@ -94,7 +94,7 @@ __device__ __forceinline__ float quantize_segments(const void *x, uint32_t n, in
 #pragma unroll
         for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(f[i]) & 0x7FFFFFFFu);
     }
-    big = wave_max(big);
+    big = greatest(big);
     if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
     __syncthreads();
 #pragma unroll
@@ -226,16 +226,6 @@ struct Choice {
     uint64_t experts[kFewTokens];              // a bit for each of the token's
     int8_t place[kFewTokens][kFewExperts];
 };
-template <int CTRL>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
-}
-__device__ __forceinline__ uint32_t greatest(uint32_t v) {
-    v = max_dpp<0x140>(max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(v))));
-    const uint32_t r[4] = {(uint32_t)__builtin_amdgcn_readlane(v, 0), (uint32_t)__builtin_amdgcn_readlane(v, 16),
-                           (uint32_t)__builtin_amdgcn_readlane(v, 32), (uint32_t)__builtin_amdgcn_readlane(v, 48)};
-    return max(max(r[0], r[1]), max(r[2], r[3]));
-}
 __device__ __forceinline__ void choose_few(const MoeArgs &a, uint32_t lane, uint32_t m, bool write, Choice &c) {
     const bool real = lane < a.E;
     const double mine = real ? a.logits[m * a.E + lane] : 0.0;

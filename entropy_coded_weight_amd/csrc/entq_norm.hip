@@ -167,7 +167,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_rows(NormAr
         }
     }
     if (codes) {
-        big = wave_max(big);
+        big = greatest(big);
         if (WAVES > 1 && threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
     }
     const float rho = rsqrt64(row_sum<WAVES>(ss, part[1]) / a.N + (double)a.eps);

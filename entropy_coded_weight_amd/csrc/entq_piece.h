@@ -97,12 +97,6 @@ __device__ __forceinline__ void load_floats(const float *w, uint32_t p, uint32_t
     for (int i = 0; i < kPer<TYPE>; ++i) f[i] = c + i < n ? w[c + i] : 0.0f;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int o = 32; o; o /= 2) v += __shfl_xor(v, o);
-    return v;
-}
-
 // A lane's value plus that of the lane that CTRL names in its row of 16.
 template <int CTRL>
 __device__ __forceinline__ double add_dpp(double v) {
@@ -118,6 +112,26 @@ __device__ __forceinline__ double row16_sum(double v) {
     v = add_dpp<0x4E>(v);
     v = add_dpp<0x141>(v);
     return add_dpp<0x140>(v);
+}
+
+// The sum of a wave's lanes, in all of them.
+__device__ __forceinline__ double wave_sum(double v) {
+    v = row16_sum(v);
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// The greatest of a wave's values, all lanes active: as row16_sum, then the
+// rows' own.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t greatest(uint32_t v) {
+    v = max_dpp<0x140>(max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(v))));
+    const uint32_t r[4] = {(uint32_t)__builtin_amdgcn_readlane(v, 0), (uint32_t)__builtin_amdgcn_readlane(v, 16),
+                           (uint32_t)__builtin_amdgcn_readlane(v, 32), (uint32_t)__builtin_amdgcn_readlane(v, 48)};
+    return max(max(r[0], r[1]), max(r[2], r[3]));
 }
 
 // 1 / sqrt(v) of a positive 64-bit value, rounded to fp32 (0 for an infinity):
