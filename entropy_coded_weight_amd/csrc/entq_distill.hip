@@ -44,10 +44,14 @@ __device__ __forceinline__ float wave_maxf(float v) {
     for (int o = 32; o; o /= 2) v = fmaxf(v, __shfl_xor(v, o));
     return v;
 }
-__device__ __forceinline__ float wave_sumf(float v) {
-#pragma unroll
-    for (int o = 32; o; o /= 2) v += __shfl_xor(v, o);
-    return v;
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ float scalar(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
+}
+__device__ __forceinline__ double scalar(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
 // (a NaN wins)
 __device__ __forceinline__ double wave_max64(double v) {
@@ -173,27 +177,33 @@ __device__ __forceinline__ Entries sum_entries(const DistillArgs &a, uint64_t m,
 // that a row is read once for the loss and its gradient; VECS 0: any length,
 // read two or three times, again out of the caches.
 //
-// The exponentials are the hardware's 2^x of one fused multiply-add, x scale +
-// c, with c = 64 - (the largest logit) scale: differences from the largest, so
-// that the logits' own size does not blur them (what rounding scale and c does
-// to all of them alike is put right in 64 bits), and 2^64 above the smallest
-// exponents that the hardware flushes, so that the gradients have theirs.
+// The exponentials are the hardware's 2^x of one fused multiply-add. Of the
+// sum: x scale + c with c = - (the largest logit) scale, differences from the
+// largest, so that the exponents that count are small and have their bits, and
+// its logarithm in 64 bits: the loss is a small difference of that, and off by
+// 1e-7 of a loss of 0.01 (5e-6 with exponents from 64 down and the hardware's
+// logarithm, and no faster). What rounding scale and c does to all of them
+// alike is put right in 64 bits. Of the gradients: x scale + c + 64, 2^64 above
+// the smallest exponents that the hardware flushes, so that small ones are
+// there, to 1e-6 of their values.
 //
-// Bound by memory: 4096 x 32000 bf16 in 47.8 us (5.5 TB/s read), with the
-// gradient 107.4 us (4.9 TB/s; a copy reaches 5.1), 515 x 50021 f16 with it in
-// 24.8 us. What carries that are waves: a workgroup has a multiple of 4 (with
+// Bound by memory: 4096 x 32000 bf16 in 47.1 us (5.6 TB/s read), with the
+// gradient 107.7 us (4.9 TB/s; a copy reaches 5.1), 515 x 50021 f16 with it in
+// 25.4 us. What carries that are waves: a workgroup has a multiple of 4 (with
 // 9, one SIMD's three decide, and the first took 107 us), the entries have a
 // wave to themselves (in a wave of the row their 64-bit registers come on top
 // of the row's: 54.7 and 127.4 us), and the registers are held to 80 and 64
-// for 3 and 4 waves more on a SIMD (the third at 78: 28.8 us). Without the row
-// in registers the first two took 130 and 305 us.
+// for 3 and 4 waves more on a SIMD (the third at 78: 29.3 us); a row's own
+// numbers are kept in scalar registers for that (29.2 us without). Without the
+// row in registers the first two took 130 and 305 us.
 template <int VECS, int WAVES>
 constexpr int kResident = WAVES == 7 ? 6 : VECS == 7 ? 8 : 1;  // waves on a SIMD, at least
 template <int TYPE, int GRAD, int VECS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void distill_rows(DistillArgs a, uint32_t row0) {
     constexpr int kP = kPer<TYPE>, kThreads = 64 * WAVES;
     extern __shared__ uint32_t marks[];  // a bit for each class of the entries
-    __shared__ float part[2][WAVES];
+    __shared__ float part[WAVES];
+    __shared__ double sums[WAVES];
     __shared__ EntryTable entries;
     __shared__ Entries found;
     const uint64_t m = (uint64_t)row0 + blockIdx.x;
@@ -242,7 +252,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         __syncthreads();  // the largest logit
         __syncthreads();  // the sum
     }
-    float top = -INFINITY, sum = 0.0f, c;
+    float top = -INFINITY, c;
     const bool tail = a.lse != nullptr;
     auto piece = [&](uint32_t p) {
         v4i v = load_piece<TYPE>(row, p, a.V);
@@ -271,10 +281,10 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
 #pragma unroll
         for (int i = 0; i < kP; ++i) top = fmaxf(top, act_of<TYPE>(v, i));
     };
-    auto power = [&](v4i v, int i) { return __builtin_amdgcn_exp2f(__builtin_fmaf(act_of<TYPE>(v, i), a.scale, c)); };
+    float own = 0.0f;
     auto add = [&](v4i v) {
 #pragma unroll
-        for (int i = 0; i < kP; ++i) sum += power(v, i);
+        for (int i = 0; i < kP; ++i) own += __builtin_amdgcn_exp2f(__builtin_fmaf(act_of<TYPE>(v, i), a.scale, c));
     };
     v4i held[VECS ? VECS : 1];
     // (between two passes: values unpacked in one are not kept for the next,
@@ -303,13 +313,13 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
             for (uint32_t p = t; p < pieces; p += kThreads) raise(again(p));
         }
         top = wave_maxf(top);
-        if (lane == 0) part[0][wave] = top;
+        if (lane == 0) part[wave] = top;
         __syncthreads();
     }
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[0][w]);
-    const float from = top == -INFINITY ? 0.0f : top;
-    c = (float)(64.0 - (double)from * a.scale);
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[w]);
+    const float from = scalar(top == -INFINITY ? 0.0f : top);
+    c = scalar((float)(-(double)from * a.scale));
     if (wave < WAVES) {
         if (VECS) {
 #pragma unroll
@@ -318,30 +328,30 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         } else {
             for (uint32_t p = t; p < pieces; p += kThreads) add(again(p));
         }
-        sum = wave_sumf(sum);
-        if (lane == 0) part[1][wave] = sum;
+        const double all = wave_sum((double)own);
+        if (lane == 0) sums[wave] = all;
         __syncthreads();
     }
-    sum = 0.0f;
+    double sum = 0.0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += part[1][w];
-    // log2 of the sum: its exponent, and the logarithm of a number in [1/2, 1)
+    for (int w = 0; w < WAVES; ++w) sum += sums[w];
+    sum = scalar(sum);
     const Entries f = found;
-    const double out2 = (double)__builtin_amdgcn_frexp_expf(sum) +
-                        (double)__builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(sum)) - (double)c +
-                        (double)from * (a.scale64 - (double)a.scale);
-    double all2 = sum == 0.0f ? -INFINITY : out2;
-    float factor = 1.0f;  // of the powers in the gradient, times their sum
-    double pt = 0.0;
-    const double lo2 = all2;
-    if (tail) {
-        // the entries' classes and the others together
-        const float d = (float)(f.top2 - lo2), u = __builtin_amdgcn_exp2f(-fabsf(d));
-        const float more = __builtin_amdgcn_logf(1.0f + u), inv = 1.0f / (1.0f + u);
-        all2 = (f.top2 > lo2 ? f.top2 : lo2) + more;
-        const float qt = d > 0.0f ? u * inv : inv;
-        pt = f.distinct == a.V ? 0.0 : fmax(0.0, 1.0 - f.mass);
-        factor = (float)((double)qt - pt);
+    const double pt = !tail || f.distinct == a.V ? 0.0 : fmax(0.0, 1.0 - f.mass);
+    // log2 of the sums over the classes outside the entries (lo2; of all classes
+    // without a tail) and over all (all2), and what a power in the gradient is
+    // multiplied by, times their sum
+    double lo2, all2;
+    float factor = 1.0f;
+    auto shift = [&] { return (double)from * (a.scale64 - (double)a.scale) - (double)c; };
+    if (wave == WAVES) {
+        lo2 = all2 = sum == 0.0 ? -INFINITY : log2(sum) + shift();
+        if (tail) all2 = fmax(f.top2, lo2) + log2(1.0 + exp2(-fabs(f.top2 - lo2)));
+    } else if (tail) {
+        lo2 = sum == 0.0 ? -INFINITY : (double)__builtin_amdgcn_frexp_exp(sum) +
+                                           (double)__builtin_amdgcn_logf((float)__builtin_amdgcn_frexp_mant(sum)) + shift();
+        const float d = (float)(f.top2 - lo2), u = __builtin_amdgcn_exp2f(-fabsf(d)), inv = 1.0f / (1.0f + u);
+        factor = (float)((double)(d > 0.0f ? u * inv : inv) - pt);
     }
     if (!f.any) factor = 0.0f;
     if (f.bad) factor = NAN;
@@ -351,9 +361,13 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         a.loss[m] = f.bad ? NAN : (float)(loss * weight);
     }
     if (!a.dlogits) return;
-    const double by = (double)weight * (a.dloss ? a.dloss[m] : 1.0f) * a.inv_t;
+    const double by = scalar((double)weight * (a.dloss ? a.dloss[m] : 1.0f) * a.inv_t);
     if (wave < WAVES) {
-        factor = factor == 0.0f ? 0.0f : (float)((double)factor / sum * by);
+        // (2^64 of the powers and both constants' roundings out of them again)
+        const float c64 = scalar((float)(64.0 - (double)from * a.scale));
+        const double back = (double)c - (double)c64 + 64.0;
+        factor = scalar(factor == 0.0f ? 0.0f : (float)((double)factor / sum * by * __builtin_amdgcn_exp2f((float)back) * 0x1p-64));
+        auto power = [&](v4i v, int i) { return __builtin_amdgcn_exp2f(__builtin_fmaf(act_of<TYPE>(v, i), a.scale, c64)); };
         auto write = [&](uint32_t p, v4i v) {
             float g[kP];
 #pragma unroll
