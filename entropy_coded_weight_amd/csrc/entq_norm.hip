@@ -15,6 +15,7 @@ struct NormArgs {
     uint32_t M, N;
     int gate_kind;
     float alpha, beta, eps;
+    double per;             // 1 / N
     // forward
     void *out, *y;
     float *scales;          // of codes in y, or null: y has the type
@@ -70,7 +71,10 @@ __device__ __forceinline__ double row_sum(double v, double *part) {
 // norm. VECS pieces a thread stay in registers; VECS 0: any length, the
 // branch and the state read again (the thread's own pieces, out of the L2).
 // Row sums are in 64 bits: no sum of squares of fp32 values overflows, and the
-// result hardly depends on their order.
+// result hardly depends on their order. Bound by memory: 4096 x 8192 bf16 with a
+// channel's gate 57.6 us (4.7 TB/s; a copy reaches 5.1), by latency for few
+// rows: one of 8192 into codes 5.1 us, 333 of 5121 f16 10.2. (Loading the
+// factors with the row, before its first sum: 60.1, and no gain for few rows.)
 template <int TYPE, int VECS, int WAVES>
 __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_rows(NormArgs a, uint32_t row0) {
     constexpr int kP = kPer<TYPE>, kThreads = 64 * WAVES, kRows = WAVES < 4 ? 4 / WAVES : 1;
@@ -123,7 +127,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_rows(NormAr
             } else {
                 for (uint32_t p = t; p < pieces; p += kThreads) add(load_piece<TYPE>(b, p, a.N));
             }
-            rho = rsqrt64(row_sum<WAVES>(sb, part[0]) / a.N + (double)a.eps);
+            rho = rsqrt64(row_sum<WAVES>(sb, part[0]) * a.per + (double)a.eps);
         }
         auto join = [&](uint32_t p, v4i xv, v4i bv) {
             float g[kP], w[kP], s[kP];
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_rows(NormAr
         big = greatest(big);
         if (WAVES > 1 && threadIdx.x % 64 == 0) top[threadIdx.x / 64] = big;
     }
-    const float rho = rsqrt64(row_sum<WAVES>(ss, part[1]) / a.N + (double)a.eps);
+    const float rho = rsqrt64(row_sum<WAVES>(ss, part[1]) * a.per + (double)a.eps);
     if (codes) {
         if (WAVES > 1) {
 #pragma unroll
@@ -234,12 +238,18 @@ int launch_norm(const NormArgs &a, hipStream_t s) {
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
+// As few waves as hold a row with one or two pieces a thread: more of them only
+// wait for each other, fewer leave too few on a CU. 4096 rows of bf16, us with
+// the next smaller row's choice or the next larger one's for this: 2048 values
+// 15.1 (two pieces in 8 waves 18.1), 4096 31.8 and 8192 57.6 (four in 16: 40.1
+// and 62.1), 16384 112.6 (146.8).
 template <int TYPE>
 int launch_norm_typed(const NormArgs &a, hipStream_t s) {
     const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;
     if (pieces <= 64) return launch_norm<TYPE, 1, 1>(a, s);
     if (pieces <= 256) return launch_norm<TYPE, 1, 4>(a, s);
     if (pieces <= 1024) return launch_norm<TYPE, 2, 8>(a, s);
+    if (pieces <= 2048) return launch_norm<TYPE, 2, 16>(a, s);
     if (pieces <= 4096) return launch_norm<TYPE, 4, 16>(a, s);
     return launch_norm<TYPE, 0, 16>(a, s);
 }
@@ -272,15 +282,15 @@ __device__ __forceinline__ RowStats row_stats(const NormArgs &a, const double (&
     RowStats r{0.0f, 0.0f, 1.0f, 0.0f, 0.0f};
     double d = sum[kBD];
     if (a.dy) {
-        r.rho1 = rsqrt64(sum[kSS] / a.N + (double)a.eps);
-        const double c1 = r.rho1 * (sum[kSY] / a.N);
+        r.rho1 = rsqrt64(sum[kSS] * a.per + (double)a.eps);
+        const double c1 = r.rho1 * (sum[kSY] * a.per);
         r.c1 = (float)c1;
         d += r.rho1 * (sum[kBY] - c1 * (r.rho1 * sum[kBS]));
     }
     if (a.post) {
-        r.rho2 = rsqrt64(sum[kBB] / a.N + (double)a.eps);
+        r.rho2 = rsqrt64(sum[kBB] * a.per + (double)a.eps);
         // (a token's gate is not in the sums)
-        r.c2 = (float)(r.rho2 * (a.beta * d / a.N) * token);
+        r.c2 = (float)(r.rho2 * (a.beta * d * a.per) * token);
     }
     r.dgate = (float)(a.beta * (double)r.rho2 * d);
     return r;
@@ -446,10 +456,14 @@ __device__ __forceinline__ void store_columns(const NormArgs &a, uint64_t strip,
 // Rows that fit the registers, in one pass: a group of WAVES waves takes every
 // strips-th row, VECS pieces a thread, and keeps the columns' factors and sums
 // over all its rows. The next row's pieces are on their way while this one's
-// gradients are computed. One barrier a row, for its sums.
+// gradients are computed. One barrier a row, for its sums. (16 waves have half
+// the registers: there the factors are read again, and rows come one by one.) Bound by memory: 4096 x
+// 8192 bf16 91.2 us with the columns' 4 (4.4 TB/s), by one row's latency for
+// few: 96 x 5120 f16 13.2 us and 3.
 template <int TYPE, int VECS, int WAVES, bool FULL>
 __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_back_rows(NormArgs a) {
     constexpr int kThreads = 64 * WAVES, kRows = WAVES < 4 ? 4 / WAVES : 1;
+    constexpr bool kLean = WAVES == 16;
     __shared__ double part[2][4 * WAVES][8];
     const uint32_t lane = threadIdx.x % 64, t = WAVES < 4 ? threadIdx.x % kThreads : threadIdx.x;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -457,22 +471,32 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_back_rows(N
     if (strip >= a.strips) return;  // (a whole wave, where rows are waves)
     const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;
     float c_pre[VECS][kPer<TYPE>] = {}, c_post[VECS][kPer<TYPE>] = {};
-    Columns<TYPE> columns[VECS];
+    Columns<TYPE> columns[kLean ? 1 : VECS];
     RowPiece v[VECS];
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
+        if (kLean) continue;
         load_columns<TYPE>(a, i * kThreads + t, columns[i]);
         v[i] = load_row<TYPE, FULL>(a, strip, i * kThreads + t);
     }
     uint32_t turn = 0;
     for (uint64_t m = strip; m < a.M; m += a.strips, turn ^= 1) {
         double sum[kRowSums] = {};
+        if (kLean) {
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) add_sums<TYPE, FULL>(a, v[i], columns[i], sum);
-        RowPiece next[VECS];
-        const uint64_t after = m + a.strips < a.M ? m + a.strips : m;
+            for (int i = 0; i < VECS; ++i) v[i] = load_row<TYPE, FULL>(a, m, i * kThreads + t);
+        }
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) next[i] = load_row<TYPE, FULL>(a, after, i * kThreads + t);
+        for (int i = 0; i < VECS; ++i) {
+            if (kLean) load_columns<TYPE>(a, i * kThreads + t, columns[0]);
+            add_sums<TYPE, FULL>(a, v[i], columns[kLean ? 0 : i], sum);
+        }
+        RowPiece next[kLean ? 1 : VECS];
+        if constexpr (!kLean) {
+            const uint64_t after = m + a.strips < a.M ? m + a.strips : m;
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) next[i] = load_row<TYPE, FULL>(a, after, i * kThreads + t);
+        }
         const float token = token_gate(a, m);
 #pragma unroll
         for (int i = 0; i < kRowSums; ++i) sum[i] = row16_sum(sum[i]);
@@ -503,8 +527,9 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void norm_back_rows(N
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
             const uint32_t p = i * kThreads + t;
-            if (p < pieces) gradients<TYPE, FULL>(a, r, m, p, token, v[i], columns[i], c_pre[i], c_post[i]);
-            v[i] = next[i];
+            if (kLean) load_columns<TYPE>(a, p, columns[0]);
+            if (p < pieces) gradients<TYPE, FULL>(a, r, m, p, token, v[i], columns[kLean ? 0 : i], c_pre[i], c_post[i]);
+            if constexpr (!kLean) v[i] = next[i];
         }
     }
 #pragma unroll
@@ -571,7 +596,7 @@ struct ColumnArgs {
     float beta;
     uint32_t strips, N;
 };
-constexpr uint32_t kColumnGroups = 8;  // of strips, side by side in a workgroup
+constexpr uint32_t kColumnGroups = 32;  // of strips, side by side in a workgroup
 __global__ __launch_bounds__(32 * kColumnGroups) void norm_columns(ColumnArgs a) {
     __shared__ double part[kColumnGroups][32];
     const uint32_t c = threadIdx.x % 32, group = threadIdx.x / 32, n = blockIdx.x * 32 + c;
@@ -649,6 +674,7 @@ NormArgs args_of(const entq_norm &n) {
     a.ldg = n.ldgate;
     a.M = n.rows;
     a.N = n.cols;
+    a.per = n.cols ? 1.0 / n.cols : 0.0;
     a.gate_kind = n.gate;
     a.alpha = n.alpha;
     a.beta = n.beta;
@@ -666,7 +692,12 @@ void zero(float *p, uint64_t ld, uint32_t n, hipStream_t s) {
 
 // How the backward pass runs: rows in the registers of `waves` waves, `vecs`
 // pieces a thread, or (vecs 0) in two launches; and its strips of rows, each
-// with column sums of its own.
+// with column sums of its own, as many as the chip holds at a time. 4096 rows
+// of bf16, us: 512 values 18.4 (512 strips 21.8; four waves a row 26.6), 2048
+// 34.5 (256 strips 40.9, 1024 41.7; one piece in 8 waves 48.3), 4096 56.7 (512
+// strips 64.0, two pieces in 8 waves 75), 8192 91.2 (in two launches 147). Rows
+// of 16 waves keep no next row and no columns' factors: 2048 x 8192 fp32 101
+// us (in two launches 136); of 16 bits they spill (210 us for 151).
 struct BackPlan {
     uint32_t vecs, waves, strips;
 };
@@ -674,8 +705,9 @@ BackPlan back_plan(const entq_norm &n) {
     const uint32_t per = n.type == ENTQ_F32 ? 4 : 8, pieces = (n.cols + per - 1) / per;
     const BackPlan p = pieces <= 64     ? BackPlan{1, 1, 1024}
                        : pieces <= 256  ? BackPlan{1, 4, 512}
-                       : pieces <= 512  ? BackPlan{1, 8, 512}
+                       : pieces <= 512  ? BackPlan{1, 8, 256}
                        : pieces <= 1024 ? BackPlan{2, 8, 256}
+                       : pieces <= 2048 && per == 4 ? BackPlan{2, 16, 256}
                                         : BackPlan{0, 8, std::max(1u, 1024 / ((n.cols + 2047) / 2048))};
     return {p.vecs, p.waves, std::max(1u, std::min(n.rows, p.strips))};
 }
@@ -699,6 +731,9 @@ void launch_back(const BackPlan &p, const NormArgs &a, hipStream_t s) {
     if (p.waves == 4) norm_back_rows<TYPE, 1, 4, FULL><<<a.strips, 256, 0, s>>>(a);
     if (p.waves == 8 && p.vecs == 1) norm_back_rows<TYPE, 1, 8, FULL><<<a.strips, 512, 0, s>>>(a);
     if (p.waves == 8 && p.vecs == 2) norm_back_rows<TYPE, 2, 8, FULL><<<a.strips, 512, 0, s>>>(a);
+    if constexpr (kPer<TYPE> == 4) {
+        if (p.waves == 16) norm_back_rows<TYPE, 2, 16, FULL><<<a.strips, 1024, 0, s>>>(a);
+    }
     if (!p.vecs) {
         norm_back_sums<TYPE, FULL><<<std::min(a.M, 1u << 20), 512, 0, s>>>(a);
         const uint32_t pieces = (a.N + kPer<TYPE> - 1) / kPer<TYPE>;

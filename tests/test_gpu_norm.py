@@ -97,7 +97,8 @@ def test_forward(N, m, n, kind):
 
 
 BACK = [(1, 1), (5, 7), (4, 64), (9, 255), (2, 512), (3, 513), (70, 2048), (3, 2049), (5, 4100), (3, 8192), (3, 8200),
-        (2, 16384), (2, 16400), (2, 40001), (1100, 96), (2600, 40), (600, 4096)]
+        (2, 16384), (2, 16400), (2, 40001), (1100, 96), (2600, 40), (600, 4096),
+        (300, 4500)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
