@@ -74,7 +74,7 @@ __device__ __forceinline__ void remove(v4i &v, int i) {
     }
 }
 
-// What the entries of a row come to, whatever the classes outside them.
+// What the entries of a row come to. Logits count from the row's largest.
 struct Entries {
     double terms;           // sum p (log p - z)
     double mass;            // sum p
@@ -92,7 +92,9 @@ struct EntryTable {
 constexpr int kOwn = kMaxTop / 64;
 struct OwnEntries {
     int32_t at[kOwn];       // the class, -1: none, -2: beyond the classes
-    float teacher[kOwn];
+    float teacher[kOwn], logit[kOwn];
+    double p[kOwn];
+    bool first[kOwn];       // of its class
 };
 #define ENTQ_OWN_ENTRIES(i, j) \
     _Pragma("unroll") for (int i = 0; i < kOwn; ++i) if (const uint32_t j = i * 64 + lane; j < a.K)
@@ -105,70 +107,80 @@ __device__ __forceinline__ void load_entries(const DistillArgs &a, uint64_t m, u
     }
 }
 
-// A row's entries: their classes, marked in `marks`, and their sums, in 64
-// bits; one wave. The marks are set when `marked` is called.
+// A row's entries, in 64 bits; one wave. First their classes, marked in `marks`
+// when `marked` is called, and the teacher's side ...
 template <int TYPE, class Marked>
-__device__ __forceinline__ Entries sum_entries(const DistillArgs &a, uint64_t m, const void *row, uint32_t lane,
-                                               const OwnEntries &o, EntryTable &e, uint32_t *marks, Marked marked) {
+__device__ __forceinline__ Entries teacher_side(const DistillArgs &a, uint64_t m, const void *row, uint32_t lane,
+                                                OwnEntries &o, EntryTable &e, uint32_t *marks, Marked marked) {
     Entries f{};
-    bool in[kOwn], first[kOwn];
-    float logit[kOwn];
     ENTQ_OWN_ENTRIES(i, j) {
-        in[i] = o.at[i] >= 0;
+        const bool in = o.at[i] >= 0;
         f.bad |= o.at[i] == -2;
-        f.any |= in[i];
+        f.any |= in;
         e.where[j] = o.at[i];
-        logit[i] = in[i] ? load_act<TYPE>(row, (uint32_t)o.at[i]) : 0.0f;
+        o.logit[i] = in ? load_act<TYPE>(row, (uint32_t)o.at[i]) : 0.0f;
         const uint32_t c = (uint32_t)o.at[i];
-        if (in[i]) f.twice |= atomicOr(&marks[c / 32], 1u << (c % 32)) >> (c % 32) & 1;
+        if (in) f.twice |= atomicOr(&marks[c / 32], 1u << (c % 32)) >> (c % 32) & 1;
     }
     f.bad = __any(f.bad);
     f.any = __any(f.any);
     f.twice = __any(f.twice);
     marked();
-    double most = -INFINITY, peak = -INFINITY;
+    double most = -INFINITY;
     ENTQ_OWN_ENTRIES(i, j) {
-        first[i] = in[i];
+        o.first[i] = o.at[i] >= 0;
         if (f.twice) {
-            for (uint32_t k = 0; k < j; ++k) first[i] &= e.where[k] != o.at[i];
+            for (uint32_t k = 0; k < j; ++k) o.first[i] &= e.where[k] != o.at[i];
         }
-        e.later[j] = !first[i];
-        const double v = in[i] ? o.teacher[i] * a.inv_t : -INFINITY, z = in[i] ? logit[i] * a.scale64 : -INFINITY;
-        e.z2[j] = z;
+        e.later[j] = !o.first[i];
+        f.distinct += o.first[i];
+        const double v = o.at[i] >= 0 ? o.teacher[i] * a.inv_t : -INFINITY;
         most = v > most || v != v ? v : most;
-        peak = z > peak || z != z ? z : peak;
     }
+#pragma unroll
+    for (int w = 32; w; w /= 2) f.distinct += __shfl_xor(f.distinct, w);
     double lse;
     if (a.lse) {
         lse = a.lse[m];
-        peak = wave_max64(peak);
-        double s = 0.0;
-        ENTQ_OWN_ENTRIES(i, j) {
-            if (!first[i]) continue;
-            ++f.distinct;
-            s += exp2(logit[i] * a.scale64 - peak);
-        }
-        f.top2 = peak + log2(wave_sum(s));
-#pragma unroll
-        for (int o2 = 32; o2; o2 /= 2) f.distinct += __shfl_xor(f.distinct, o2);
     } else {
         most = wave_max64(most);
         double s = 0.0;
         ENTQ_OWN_ENTRIES(i, j) {
-            if (in[i]) s += exp(o.teacher[i] * a.inv_t - most);
+            if (o.at[i] >= 0) s += exp(o.teacher[i] * a.inv_t - most);
         }
         lse = most + log(wave_sum(s));
     }
     ENTQ_OWN_ENTRIES(i, j) {
-        if (!in[i]) continue;
-        const double logp = o.teacher[i] * a.inv_t - lse, p = exp(logp);
-        e.mass[j] = (float)p;
-        f.mass += p;
-        if (!(p == 0.0)) f.terms += p * (logp - logit[i] * a.scale64 * kLn2);
+        if (o.at[i] < 0) continue;
+        const double logp = o.teacher[i] * a.inv_t - lse;
+        o.p[i] = exp(logp);
+        e.mass[j] = (float)o.p[i];
+        f.mass += o.p[i];
+        if (!(o.p[i] == 0.0)) f.terms += o.p[i] * logp;
     }
     f.mass = wave_sum(f.mass);
     f.terms = wave_sum(f.terms);
     return f;
+}
+
+// ... then the student's, its logits counted from `from`.
+__device__ __forceinline__ void student_side(const DistillArgs &a, uint32_t lane, double from, const OwnEntries &o,
+                                             EntryTable &e, Entries &f) {
+    double peak = -INFINITY, s = 0.0;
+    ENTQ_OWN_ENTRIES(i, j) {
+        const double z = o.at[i] >= 0 ? (o.logit[i] - from) * a.scale64 : -INFINITY;
+        e.z2[j] = z;
+        peak = z > peak || z != z ? z : peak;
+        if (o.at[i] >= 0 && !(o.p[i] == 0.0)) s += o.p[i] * z;
+    }
+    f.terms -= wave_sum(s) * kLn2;
+    if (!a.lse) return;
+    peak = wave_max64(peak);
+    s = 0.0;
+    ENTQ_OWN_ENTRIES(i, j) {
+        if (o.first[i]) s += exp2((o.logit[i] - from) * a.scale64 - peak);
+    }
+    f.top2 = peak == -INFINITY ? peak : peak + log2(wave_sum(s));
 }
 
 // One workgroup per token: WAVES waves for the row, and one for the entries,
@@ -182,14 +194,14 @@ __device__ __forceinline__ Entries sum_entries(const DistillArgs &a, uint64_t m,
 // largest, so that the exponents that count are small and have their bits, and
 // its logarithm in 64 bits: the loss is a small difference of that, and off by
 // 1e-7 of a loss of 0.01 (5e-6 with exponents from 64 down and the hardware's
-// logarithm, and no faster). What rounding scale and c does to all of them
-// alike is put right in 64 bits. Of the gradients: x scale + c + 64, 2^64 above
+// logarithm, and no faster). What rounding c does to all of them alike is put
+// right in 64 bits. Of the gradients: x scale + c + 64, 2^64 above
 // the smallest exponents that the hardware flushes, so that small ones are
 // there, to 1e-6 of their values.
 //
-// Bound by memory: 4096 x 32000 bf16 in 47.1 us (5.6 TB/s read), with the
-// gradient 107.7 us (4.9 TB/s; a copy reaches 5.1), 515 x 50021 f16 with it in
-// 25.4 us. What carries that are waves: a workgroup has a multiple of 4 (with
+// Bound by memory: 4096 x 32000 bf16 in 46.6 us (5.6 TB/s read), with the
+// gradient 108 us (4.9 TB/s; a copy reaches 5.1), 515 x 50021 f16 with it in
+// 24.8 us. What carries that are waves: a workgroup has a multiple of 4 (with
 // 9, one SIMD's three decide, and the first took 107 us), the entries have a
 // wave to themselves (in a wave of the row their 64-bit registers come on top
 // of the row's: 54.7 and 127.4 us), and the registers are held to 80 and 64
@@ -204,6 +216,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     extern __shared__ uint32_t marks[];  // a bit for each class of the entries
     __shared__ float part[WAVES];
     __shared__ double sums[WAVES];
+    __shared__ float of_entries;  // their largest logit
     __shared__ EntryTable entries;
     __shared__ Entries found;
     const uint64_t m = (uint64_t)row0 + blockIdx.x;
@@ -243,16 +256,8 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         }
         return;
     }
-    if (wave == WAVES) {
-        OwnEntries own;
-        load_entries(a, m, lane, own);
-        __syncthreads();  // the marks are clear
-        const Entries f = sum_entries<TYPE>(a, m, row, lane, own, entries, marks, [] { __syncthreads(); });
-        if (lane == 0) found = f;
-        __syncthreads();  // the largest logit
-        __syncthreads();  // the sum
-    }
-    float top = -INFINITY, c;
+    float top = -INFINITY, from, all_from, c;
+    bool far;
     const bool tail = a.lse != nullptr;
     auto piece = [&](uint32_t p) {
         v4i v = load_piece<TYPE>(row, p, a.V);
@@ -272,10 +277,35 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
                 if (out >> i & 1) remove<TYPE>(v, i);
         }
     };
-    auto again = [&](uint32_t p) {
+    // A row whose largest logit is some 2^24 T or more in size (what a mask of the
+    // type's lowest value leaves of a row, say) is replaced by its differences from
+    // it: exact where they count.
+    auto nearer = [&](v4i &v) {
+        float d[kP];
+#pragma unroll
+        for (int i = 0; i < kP; ++i) d[i] = act_of<TYPE>(v, i) - from;
+        v = pack<TYPE>(d);
+    };
+    auto masked = [&](uint32_t p) {
         v4i v = piece(p);
         if (tail) outside(v, p);
         return v;
+    };
+    auto again = [&](uint32_t p) {
+        v4i v = masked(p);
+        if (far) nearer(v);
+        return v;
+    };
+    // The largest logit is there: `from` that of the classes in the sum,
+    // `all_from` of all.
+    auto refer = [&] {
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[w]);
+        const float most = fmaxf(top, of_entries);
+        from = scalar(top == -INFINITY ? 0.0f : top);
+        all_from = scalar(most == -INFINITY ? 0.0f : most);
+        far = fabs((double)from * a.scale64) >= 0x1p24;
+        c = scalar(far ? 0.0f : (float)(-(double)from * a.scale));
     };
     auto raise = [&](v4i v) {
 #pragma unroll
@@ -310,17 +340,16 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
             for (int i = 0; i < VECS; ++i) raise(held[i]);
             forget();
         } else {
-            for (uint32_t p = t; p < pieces; p += kThreads) raise(again(p));
+            for (uint32_t p = t; p < pieces; p += kThreads) raise(masked(p));
         }
         top = wave_maxf(top);
         if (lane == 0) part[wave] = top;
         __syncthreads();
-    }
+        refer();
+        if (VECS && far) {
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[w]);
-    const float from = scalar(top == -INFINITY ? 0.0f : top);
-    c = scalar((float)(-(double)from * a.scale));
-    if (wave < WAVES) {
+            for (int i = 0; i < VECS; ++i) nearer(held[i]);
+        }
         if (VECS) {
 #pragma unroll
             for (int i = 0; i < VECS; ++i) add(held[i]);
@@ -331,6 +360,22 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         const double all = wave_sum((double)own);
         if (lane == 0) sums[wave] = all;
         __syncthreads();
+    } else {
+        OwnEntries own;
+        load_entries(a, m, lane, own);
+        __syncthreads();  // the marks are clear
+        Entries f = teacher_side<TYPE>(a, m, row, lane, own, entries, marks, [] { __syncthreads(); });
+        float most = -INFINITY;
+        ENTQ_OWN_ENTRIES(i, j) {
+            if (own.at[i] >= 0) most = fmaxf(most, own.logit[i]);
+        }
+        most = wave_maxf(most);
+        if (lane == 0) of_entries = most;
+        __syncthreads();  // the largest logit
+        refer();
+        student_side(a, lane, all_from, own, entries, f);
+        if (lane == 0) found = f;
+        __syncthreads();  // the sum
     }
     double sum = 0.0;
 #pragma unroll
@@ -343,7 +388,10 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     // multiplied by, times their sum
     double lo2, all2;
     float factor = 1.0f;
-    auto shift = [&] { return (double)from * (a.scale64 - (double)a.scale) - (double)c; };
+    // (from all_from, and c's rounding out of all exponents)
+    auto shift = [&] {
+        return ((double)from - all_from) * a.scale64 - (far ? 0.0 : (double)c + (double)from * (double)a.scale);
+    };
     if (wave == WAVES) {
         lo2 = all2 = sum == 0.0 ? -INFINITY : log2(sum) + shift();
         if (tail) all2 = fmax(f.top2, lo2) + log2(1.0 + exp2(-fabs(f.top2 - lo2)));
@@ -351,7 +399,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         lo2 = sum == 0.0 ? -INFINITY : (double)__builtin_amdgcn_frexp_exp(sum) +
                                            (double)__builtin_amdgcn_logf((float)__builtin_amdgcn_frexp_mant(sum)) + shift();
         const float d = (float)(f.top2 - lo2), u = __builtin_amdgcn_exp2f(-fabsf(d)), inv = 1.0f / (1.0f + u);
-        factor = (float)((double)(d > 0.0f ? u * inv : inv) - pt);
+        factor = sum == 0.0 ? 0.0f : (float)((double)(d > 0.0f ? u * inv : inv) - pt);  // (0: none of them has a q)
     }
     if (!f.any) factor = 0.0f;
     if (f.bad) factor = NAN;
@@ -364,7 +412,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     const double by = scalar((double)weight * (a.dloss ? a.dloss[m] : 1.0f) * a.inv_t);
     if (wave < WAVES) {
         // (2^64 of the powers and both constants' roundings out of them again)
-        const float c64 = scalar((float)(64.0 - (double)from * a.scale));
+        const float c64 = scalar(far ? 64.0f : (float)(64.0 - (double)from * a.scale));
         const double back = (double)c - (double)c64 + 64.0;
         factor = scalar(factor == 0.0f ? 0.0f : (float)((double)factor / sum * by * __builtin_amdgcn_exp2f((float)back) * 0x1p-64));
         auto power = [&](v4i v, int i) { return __builtin_amdgcn_exp2f(__builtin_fmaf(act_of<TYPE>(v, i), a.scale, c64)); };

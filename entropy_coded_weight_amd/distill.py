@@ -11,7 +11,8 @@ the classes index[m]:
 p is the softmax of teacher[m] / T over the token's entries, or, with
 ``teacher_lse`` (the logsumexp of all the teacher's logits / T), exp(teacher /
 T - lse), and the mass outside the entries is compared with the student's mass
-there as one more class. An index below 0 is no entry.
+there as one more class. An index below 0 is no entry; a row of weight 0 may
+hold anything. Masks may be the type's lowest value or -infinity.
 
 logits: bfloat16, float16 or float32 [M, V]; index: int32 or int64 [M, K], K
 up to MAX_TOP; teacher: any of the logits' types [M, K] (unit stride along the
@@ -88,8 +89,8 @@ def loss_backward(logits, index, teacher, dlogits, dloss=None, loss=None, teache
                   weight=None, temperature=1.0, stream=None):
     """The gradient of sum(dloss * loss) (dloss float32 [M]; None: all 1) into
     ``dlogits`` (the logits' type [M, V], or of float32 logits any of the
-    types, as ``int8.gemm_backward`` takes 16 bits), and, unless None, the losses into
-    ``loss``: a training step needs no call of ``loss`` before, and the logits
+    types, as ``int8.gemm_backward`` takes 16 bits; it overlaps nothing), and,
+    unless None, the losses into ``loss``: a training step needs no call of ``loss`` before, and the logits
     are read once for both."""
     dev, d = _describe(logits, index, teacher, teacher_lse, weight, temperature)
     kind, ld = _matrix("dlogits", dlogits, dev, _FLOATS if d.type == _F32 else (d.type,),

@@ -786,8 +786,13 @@ entq_status entq_norm_block_backward(const entq_norm *n, const void *d_dout, uin
  * times the row's weight. An entry with a negative index is none; a row
  * without entries has loss and gradient 0, and so has one of weight 0,
  * whatever its logits hold. Entries of one class count each (their p add up).
- * An index of classes and beyond makes the row's loss and gradient NaN. The
- * entries' terms are in 64 bits, the sums over classes in fp32. */
+ * An index of classes and beyond makes the row's loss and gradient NaN. Logits
+ * count by their differences from the row's largest, whatever its size: a mask
+ * may be of the type's lowest value or -infinity, and a row of the lowest value
+ * alone is uniform (one of -infinity alone NaN). Where the student gives a class
+ * that p has no mass at all, the loss is infinite. The entries' terms and the
+ * logarithms are in 64 bits, the sums over classes in fp32 for each of a row's
+ * threads. */
 #define ENTQ_DISTILL_MAX_TOP 256u
 #define ENTQ_DISTILL_MAX_CLASSES 262144u
 
@@ -807,8 +812,8 @@ typedef struct {
 entq_status entq_distill_loss(const entq_distill *d, float *d_loss, void *stream);
 
 /* d_dlogits ([rows][lddlogits >= classes] of dlogits_type: the logits' type, or
- * of fp32 logits any; no overlap with anything) = the gradient of sum_r d_dloss[r] loss[r] (d_dloss NULL: of their
- * sum). The logits are read as the loss reads them; d_loss, if not NULL, gets
+ * of fp32 logits any; no overlap with anything) = the gradient of sum_r
+ * d_dloss[r] loss[r] (d_dloss NULL: of their sum). The logits are read as the loss reads them; d_loss, if not NULL, gets
  * the loss too. */
 entq_status entq_distill_backward(const entq_distill *d, const float *d_dloss, void *d_dlogits,
                                   int dlogits_type, uint64_t lddlogits, float *d_loss,

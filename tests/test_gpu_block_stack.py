@@ -130,6 +130,15 @@ def test_residual_gradients(E, m, d, f, alpha, gate, post):
         assert torch.equal(alone, t), name
 
 
+def test_residual_of_no_tokens(E):
+    block, _, scales, _ = residual_setup(E, 1, 256, 352, "f16")
+    x, pre, post = torch.empty(0, 256, device="cuda").half(), vector(256, 1), vector(256, 2)
+    block.residual(x, x.clone(), pre, post, vector(256, 3))
+    got = [torch.ones_like(scales)] + [torch.ones(256, device="cuda") for _ in range(3)]
+    block.residual_backward(x, x, pre, post, vector(256, 3), x.clone(), *got)
+    assert not any(bool(t.any()) for t in got)
+
+
 def head_inputs(m, v, d, k, kind, tail, seed=3):
     torch.manual_seed(seed)
     x = torch.randn(m, d, device="cuda").to(TYPES[kind])

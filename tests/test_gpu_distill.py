@@ -129,6 +129,56 @@ def test_large_logits(D):
     check(D, logits, index, teacher, None, None, "f32", T=1.0)
 
 
+@pytest.mark.parametrize("v", [300, 9000, 33000, 60000, 150000])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("kind", KINDS)
+def test_masks_of_the_lowest_value(D, v, tail, kind):
+    """Rows of which a mask of the type's lowest value, or of -inf, leaves some
+    classes, one, or none; rows of large logits of either sign. Differences of
+    logits are what counts: the reference's are exact in 64 bits."""
+    logits, index, teacher, lse, _ = inputs(8, v, 8, kind, 4, tail)
+    low = torch.finfo(logits.dtype).min
+    logits[1, v // 3:] = low
+    logits[2] = low                                     # nothing left: all alike
+    logits[3] = low
+    logits[3, index[3, 0].long()] = 1.5
+    logits[4] = -logits[4].abs() * (3e4 if kind != "f16" else 3e3)
+    logits[5, 7:] = float("-inf")
+    index[5] = torch.arange(8, dtype=torch.int32, device="cuda") % 7
+    logits[6] = float("-inf")
+    logits[6, index[6].long()] = 0.5 * teacher[6].to(logits.dtype)
+    logits[7] = -low
+    logits[7, 3] = low
+    index[7] = torch.arange(10, 18, dtype=torch.int32, device="cuda")
+    if tail:
+        lse[2] = lse[3] = torch.logsumexp(teacher[2].double() / 1.25, 0).float() + 3
+        teacher[3] = teacher[2]
+    T = 1.25
+    loss, grad = torch.empty(8, device="cuda"), torch.empty_like(logits)
+    D.loss_backward(logits, index, teacher, grad, None, loss, lse, None, T)
+    # in 64 bits from each row's largest
+    z = logits.double()
+    z = (z - z.amax(1, keepdim=True)) / T
+    want = R.distill(z * T, index, teacher, lse, None, T, None, kind)
+    ok = [0, 1, 2, 4, 7]
+    assert torch.isfinite(want[0][0][ok]).all()
+    close(loss[ok], want[0][0][ok], want[0][1][ok], "loss")
+    close(grad[ok], want[1][0][ok], want[1][1][ok], "gradient")
+    assert loss[5:7].isinf().tolist() == want[0][0][5:7].isinf().tolist()  # (what the student rules out)
+    for r in (5, 6):
+        if torch.isfinite(want[1][0][r]).all():
+            close(grad[r:r + 1], want[1][0][r:r + 1], want[1][1][r:r + 1], r)
+    # row 3's classes outside the entries are alike, and far from the one that is
+    # left: 64 bits hold no 2.7e38 + log v, so its gradient is written out here
+    hit = torch.zeros(v, dtype=torch.bool, device="cuda").scatter_(0, index[3].long(), True)
+    p = torch.exp(teacher[3].double() / T - lse[3].double()) if tail else torch.softmax(teacher[3].double() / T, 0)
+    g = torch.full((v,), -(1 - float(p.sum())) / (v - int(hit.sum())) if tail else 0.0, dtype=torch.float64, device="cuda")
+    g[index[3].long()] = -p
+    g[index[3, 0].long()] += 1
+    g = g / T
+    close(grad[3], g, (R.ROUND[kind] + 64 * R.EPS) * g.abs() + 64 * R.EPS * hit + R.TINY[kind], "gradient of row 3")
+
+
 @pytest.mark.parametrize("v", [300, 33000, 150000])
 @pytest.mark.parametrize("tail", [False, True])
 def test_masked_and_broken_rows(D, v, tail):
