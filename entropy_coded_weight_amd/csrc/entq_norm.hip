@@ -25,7 +25,7 @@ struct NormArgs {
     uint64_t lddo, lddy;
     void *dx, *db, *dgate;  // dgate: of every kind but CHANNEL (which finishes with dpost)
     uint64_t lddx, lddb, lddg;
-    float *stats;           // [M][4]
+    float *stats;           // [M][4], of the two launches
     float *part_pre, *part_post;  // [strips][N], or null
     uint32_t strips;
 };
@@ -718,7 +718,7 @@ struct Room {
 Room room_of(const entq_norm &n) {
     const auto up = [](uint64_t b) { return (b + 255) / 256 * 256; };
     Room r{};
-    r.pre = up((uint64_t)n.rows * 16);
+    r.pre = back_plan(n).vecs ? 0 : up((uint64_t)n.rows * 16);
     const uint64_t one = up((uint64_t)back_plan(n).strips * n.cols * 4);
     r.post = r.pre + one;
     r.all = r.post + one;

@@ -205,6 +205,20 @@ def test_masked_and_broken_rows(D, v, tail):
     close(grad[:1], *want[1], "gradient")
 
 
+def test_rows_beyond_32_bits(D):
+    """Row strides whose offsets, in elements and in bytes, pass 2^32."""
+    v, ld = 3001, 1_500_000_011
+    logits, index, teacher, lse, _ = inputs(4, v, 9, "f16", 6, True)
+    room = torch.empty(3 * ld + 4 * v, dtype=torch.float16, device="cuda")
+    far, grad = room.as_strided((4, v), (ld, 1)), room[2 * v:].as_strided((4, v), (ld, 1))
+    far.copy_(logits)
+    loss = torch.empty(4, device="cuda")
+    D.loss_backward(far, index, teacher, grad, None, loss, lse, None, 1.25)
+    want = R.distill(logits, index, teacher, lse, None, 1.25, None, "f16")
+    close(loss, *want[0], "loss")
+    close(grad, *want[1], "gradient")
+
+
 def test_empty(D):
     x = torch.empty(0, 10, device="cuda")
     D.loss(x, torch.empty(0, 3, dtype=torch.int64, device="cuda"), torch.empty(0, 3, device="cuda"), torch.empty(0, device="cuda"))

@@ -222,6 +222,24 @@ def test_state_in_place(N, n, kind):
     assert torch.equal(x, out) and torch.equal(y, y2)
 
 
+def test_rows_beyond_32_bits(N):
+    """Row strides whose offsets, in elements and in bytes, pass 2^32."""
+    n, ld = 700, 1_500_000_011
+    room = torch.empty(3 * ld + 5000, dtype=torch.bfloat16, device="cuda")
+    at = lambda i: room[i * 1000:].as_strided((4, n), (ld, 1))  # noqa: E731
+    x, out, y = at(0), at(1), at(2)
+    x.copy_(matrix(4, n, "bf16", 1))
+    b, w = matrix(4, n, "bf16", 2), vector(n, 3)
+    N.block(x, b, out, w, None, w, y)
+    close(out, *R.state(x, b, w, None, 1, 1, 1e-6, "bf16"), "out")
+    close(y, *R.normed(out, w, 1e-6, "bf16"), "y")
+    dx, db, dpre = at(3), at(4), torch.empty(n, device="cuda")
+    N.block_backward(out, y, b, b, w, None, w, dx, db, None, dpre)
+    want = R.gradients(out, y, b, b, w, None, w, 1, 1, 1e-6, "bf16")
+    for name, t in (("dx", dx), ("dbranch", db), ("dpre", dpre)):
+        close(t, *want[name], name)
+
+
 def test_empty(N):
     for m, n in ((0, 16), (3, 0), (0, 0)):
         x = torch.empty(m, n, device="cuda")
