@@ -520,7 +520,6 @@ entq_status backward(const Call &c, int act, void *dx, uint64_t lddx, float *ds0
 bool bad_act(int act) { return act < ENTQ_ACT_SILU || act > ENTQ_ACT_RELU; }
 
 }  // namespace
-
 }  // namespace entq
 
 using entq::describe;
