@@ -327,14 +327,20 @@ __device__ __forceinline__ uint32_t token_at(uint64_t tokens, uint32_t place, ui
 // channels, its waves blocks of 128 codes in turn, some of them on their way.
 // Columns beyond the job's tokens read with its last one (the same cache
 // lines, and no branch, so that no load waits for another); their sums go
-// nowhere.
-template <int MT, int WAVES, bool TINY, bool FEW>
+// nowhere. WIDE, for more than 16 columns: each wave has 16 channels of its own
+// and takes all blocks, so that a workgroup's way to its job is paid once for
+// four times the channels, and its waves read the same codes of x.
+// Bound by memory: one token, 2 experts of 5120 x 13824, in 57 us (5.0 TB/s), 48
+// tokens, 64 experts of 5120 x 1728, 231 us (4.9 TB/s); with more columns an
+// expert by the waits of a wave's blocks for each other (64 tokens, 4 experts of
+// 4096 x 8192: 81 us, 3.3 TB/s).
+template <int MT, int WAVES, bool TINY, bool FEW, bool WIDE>
 __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
-    constexpr int kDepth = MT > 1 ? 2 : 4, kCols = 16 * MT;
-    __shared__ v4i sums[WAVES][2 * MT][64];
+    constexpr int kDepth = MT > 1 ? 2 : 4, kCols = 16 * MT, kSteps = WIDE ? 1 : WAVES;
+    __shared__ v4i sums[WIDE ? 1 : WAVES][2 * MT][64];
     __shared__ Choice choice;
     const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const uint32_t n0 = blockIdx.x * 16, kc = lane / 16 * 32;
+    const uint32_t n0 = WIDE ? (blockIdx.x * WAVES + wave) * 16 : blockIdx.x * 16, kc = lane / 16 * 32;
     Job job;
     if constexpr (FEW) {
         static_assert(!FEW || WAVES == kFewTokens, "a wave for each token");
@@ -351,7 +357,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
         job = nth_job<kCols>(a, blockIdx.y, lane);
     }
     const uint32_t e = job.expert;
-    if (e >= a.E) return;
+    if (e >= a.E || (WIDE && n0 >= a.F)) return;
     uint32_t x[MT], token[MT];
 #pragma unroll
     for (int g = 0; g < MT; ++g) {
@@ -364,9 +370,10 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
     struct Block {
         v4i w[2][2], x[MT][2];
     };
-    const uint32_t blocks = (a.D + 127) / 128, mine = blocks > wave ? (blocks - wave + WAVES - 1) / WAVES : 0;
+    const uint32_t blocks = (a.D + 127) / 128, first = WIDE ? 0 : wave,
+                   mine = blocks > first ? (blocks - first + kSteps - 1) / kSteps : 0;
     auto load = [&](Block &b, uint32_t i) {
-        const uint32_t k = (i * WAVES + wave) * 128;
+        const uint32_t k = (i * kSteps + first) * 128;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -403,41 +410,50 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gated(MoeArgs a) {
             if (i + d + kDepth < mine) load(b[d], i + d + kDepth);
         }
     }
-    static_assert(WAVES >= MT, "a wave for each 16 columns at the end");
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int g = 0; g < MT; ++g) sums[wave][t * MT + g][lane] = acc[t][g];
-    __syncthreads();
-    if (wave >= MT) return;
-    v4i s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
-#pragma unroll
-    for (int v = 0; v < WAVES; ++v) {
-        s0 += sums[v][wave][lane];
-        s1 += sums[v][MT + wave][lane];
-    }
-    uint32_t m = token[0];
-#pragma unroll
-    for (int g = 1; g < MT; ++g) m = wave == (uint32_t)g ? token[g] : m;
+    // 16 channels of 16 columns: their hidden values
     const uint32_t n = n0 + lane / 16 * 4;
-    if (job.first + wave * 16 + lane % 16 >= (uint32_t)__popcll(job.tokens) || n >= a.F) return;
-    const int32_t place = FEW ? choice.place[m][e] : a.place[(uint64_t)e * a.M + m];
-    const float sx = a.sx[m];
-    float g[4], u[4], r[4], none[4];
+    auto finish = [&](v4i s0, v4i s1, uint32_t group, uint32_t m) {
+        if (job.first + group * 16 + lane % 16 >= (uint32_t)__popcll(job.tokens) || n >= a.F) return;
+        const int32_t place = FEW ? choice.place[m][e] : a.place[(uint64_t)e * a.M + m];
+        const float sx = a.sx[m];
+        float g[4], u[4], r[4], none[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool there = n + i < a.F;
-        g[i] = ((float)s0[i] * sx) * (there ? a.sw[0][e * a.sstride[0] + n + i] : 0.0f);
-        u[i] = ((float)s1[i] * sx) * (there ? a.sw[1][e * a.sstride[1] + n + i] : 0.0f);
-    }
-    activate4<false>(a.act, g, r, none);
-    float *h = a.h + ((uint64_t)m * a.K + place) * a.F + n;
-    if (n + 4 <= a.F) {
-        ((any16 *)h)->v = __builtin_bit_cast(v4i, v4f{r[0] * u[0], r[1] * u[1], r[2] * u[2], r[3] * u[3]});
+        for (int i = 0; i < 4; ++i) {
+            const bool there = n + i < a.F;
+            g[i] = ((float)s0[i] * sx) * (there ? a.sw[0][e * a.sstride[0] + n + i] : 0.0f);
+            u[i] = ((float)s1[i] * sx) * (there ? a.sw[1][e * a.sstride[1] + n + i] : 0.0f);
+        }
+        activate4<false>(a.act, g, r, none);
+        float *h = a.h + ((uint64_t)m * a.K + place) * a.F + n;
+        if (n + 4 <= a.F) {
+            ((any16 *)h)->v = __builtin_bit_cast(v4i, v4f{r[0] * u[0], r[1] * u[1], r[2] * u[2], r[3] * u[3]});
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (n + i < a.F) h[i] = r[i] * u[i];
+        }
+    };
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int g = 0; g < MT; ++g) finish(acc[0][g], acc[1][g], g, token[g]);
     } else {
+        static_assert(WAVES >= MT, "a wave for each 16 columns at the end");
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (n + i < a.F) h[i] = r[i] * u[i];
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int g = 0; g < MT; ++g) sums[wave][t * MT + g][lane] = acc[t][g];
+        __syncthreads();
+        if (wave >= MT) return;
+        v4i s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
+#pragma unroll
+        for (int v = 0; v < WAVES; ++v) {
+            s0 += sums[v][wave][lane];
+            s1 += sums[v][MT + wave][lane];
+        }
+        uint32_t m = token[0];
+#pragma unroll
+        for (int g = 1; g < MT; ++g) m = wave == (uint32_t)g ? token[g] : m;
+        finish(s0, s1, wave, m);
     }
 }
 
@@ -636,20 +652,27 @@ uint32_t most_jobs(uint32_t tokens, uint32_t top_k, uint32_t experts, uint32_t c
     return std::min(rows, std::min(experts, rows) + rows / columns);
 }
 
+// Workgroups from which WIDE pays, 64 tokens, us with it and without: 8 experts of
+// 4096 x 8192 215 and 224, 4096 x 4096 122 and 127, 4096 x 2048 (256 of them) 80.6
+// and 80.8, 4 of 4096 x 1024 (64) 70 and 46.
+constexpr uint32_t kWideGroups = 512;
 template <int MT>
 void launch_products(const MoeArgs &a, hipStream_t s) {
     constexpr int W = 4;
     const dim3 grid((a.F + 15) / 16, a.most), down((a.N + 15) / 16, a.splits);
     const bool few = a.M <= kFewTokens && a.E <= kFewExperts;
     if (!few) moe_choose<<<a.M, kMaxExperts, 0, s>>>(a);
+    const dim3 wide((a.F + 16 * W - 1) / (16 * W), a.most);
     if (MT == 1 && few && a.D >= 16)
-        moe_gated<1, W, false, true><<<grid, 64 * W, 0, s>>>(a);
+        moe_gated<1, W, false, true, false><<<grid, 64 * W, 0, s>>>(a);
     else if (MT == 1 && few)
-        moe_gated<1, W, true, true><<<grid, 64 * W, 0, s>>>(a);
+        moe_gated<1, W, true, true, false><<<grid, 64 * W, 0, s>>>(a);
+    else if (MT > 1 && a.D >= 16 && wide.x * std::min(a.E, a.most) >= kWideGroups)
+        moe_gated<MT, W, false, false, (MT > 1)><<<wide, 64 * W, 0, s>>>(a);
     else if (a.D >= 16)
-        moe_gated<MT, W, false, false><<<grid, 64 * W, 0, s>>>(a);
+        moe_gated<MT, W, false, false, false><<<grid, 64 * W, 0, s>>>(a);
     else
-        moe_gated<MT, W, true, false><<<grid, 64 * W, 0, s>>>(a);
+        moe_gated<MT, W, true, false, false><<<grid, 64 * W, 0, s>>>(a);
     moe_quantize<16 * MT><<<a.M * a.K, 1024, 0, s>>>(a);
     const uint32_t lds = W * a.M * 64 + kMostJobs * (64 + 16 * MT * 6 + 2);
     if (a.F < 16)

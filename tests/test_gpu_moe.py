@@ -103,6 +103,13 @@ def test_few_tokens(M, m, e, k, d, f, n):
         check(M, x, router, w, k, "silu", True, kind)
 
 
+@pytest.mark.parametrize("m,e,k,d,f,n", [(64, 2, 2, 64, 16384 + 33, 5), (40, 4, 2, 70, 8200, 17), (33, 8, 4, 129, 4096, 16)])
+def test_many_channels_and_tokens(M, m, e, k, d, f, n):
+    """Enough of both for workgroups of 64 channels, some of them beyond the last."""
+    x, router, w = layer(m, e, d, f, n, "f16", "f32", 23, 3)
+    check(M, x, router, w, k, "silu", False, "f16")
+
+
 @pytest.mark.parametrize("m", [3, 9])
 def test_choices_of_nearly_equal_logits(M, m):
     """Logits that are equal in 32 bits and differ in 64, in no order of their
