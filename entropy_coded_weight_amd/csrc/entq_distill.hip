@@ -382,7 +382,9 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     for (int w = 0; w < WAVES; ++w) sum += sums[w];
     sum = scalar(sum);
     const Entries f = found;
-    const double pt = !tail || f.distinct == a.V ? 0.0 : fmax(0.0, 1.0 - f.mass);
+    const double rest = 1.0 - f.mass, pt = !tail || f.distinct == a.V || rest < 0.0 ? 0.0 : rest;
+    // (a NaN of the teacher is in L's coefficient: it reaches every class)
+    const bool broken = f.bad || f.mass != f.mass;
     // log2 of the sums over the classes outside the entries (lo2; of all classes
     // without a tail) and over all (all2), and what a power in the gradient is
     // multiplied by, times their sum
@@ -402,7 +404,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         factor = sum == 0.0 ? 0.0f : (float)((double)(d > 0.0f ? u * inv : inv) - pt);  // (0: none of them has a q)
     }
     if (!f.any) factor = 0.0f;
-    if (f.bad) factor = NAN;
+    if (broken) factor = NAN;
     if (a.loss && wave == WAVES && lane == 0) {
         double loss = f.any ? f.terms + f.mass * (all2 * kLn2) : 0.0;
         if (f.any && pt > 0.0) loss += pt * (log(pt) + (all2 - lo2) * kLn2);
@@ -441,7 +443,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
             for (uint32_t i = j + 1; i < a.K; ++i)
                 if (entries.where[i] == entries.where[j]) p += entries.mass[i];
         }
-        const float g = f.bad ? NAN : (float)by * ((float)exp2(entries.z2[j] - all2) - p);
+        const float g = broken ? NAN : (float)by * ((float)exp2(entries.z2[j] - all2) - p);
         if (GRAD == ENTQ_F32)
             ((float *)grad)[entries.where[j]] = g;
         else

@@ -786,11 +786,13 @@ entq_status entq_norm_block_backward(const entq_norm *n, const void *d_dout, uin
  * times the row's weight. An entry with a negative index is none; a row
  * without entries has loss and gradient 0, and so has one of weight 0,
  * whatever its logits hold. Entries of one class count each (their p add up).
- * An index of classes and beyond makes the row's loss and gradient NaN. Logits
- * count by their differences from the row's largest, whatever its size: a mask
- * may be of the type's lowest value or -infinity, and a row of the lowest value
- * alone is uniform (one of -infinity alone NaN). Where the student gives a class
- * that p has no mass at all, the loss is infinite. The entries' terms and the
+ * An index of classes and beyond, or p that are no numbers (a NaN among the
+ * teacher's entries or in its log-sum; without d_lse also entries of -infinity
+ * alone), make the row's loss and gradient NaN. Logits count by their
+ * differences from the row's largest, whatever its size: a mask may be of the
+ * type's lowest value or -infinity, and a row of the lowest value alone is
+ * uniform (one of -infinity alone NaN). Where the student gives a class that p
+ * has no mass at all, the loss is infinite. The entries' terms and the
  * logarithms are in 64 bits, the sums over classes in fp32 for each of a row's
  * threads. */
 #define ENTQ_DISTILL_MAX_TOP 256u
