@@ -12,12 +12,14 @@ namespace {
 // entries (their softmax; or, with the log-sum lse over all its classes, p_j =
 // exp(t_j / T - lse), the rest pt = max(0, 1 - sum p) being the tail's):
 //   loss = sum_j p_j (log p_j - z_j + L)  [+ pt (log pt - Lt + L)]
-//   dL/dz_v = q_v - sum_{j of v} p_j,   q_v = exp(z_v - L)
-// Lt is the log-sum over the classes outside the top entries, whose gradient
-// with a tail is q_v - pt exp(z_v - Lt) = exp(z_v - Lt) (qt - pt), qt = exp(Lt
-// - L). Lt comes from a sum over those classes alone (a bit for each class
-// marks the others): L minus the top entries would lose it to cancellation
-// where the student is sure.
+//   dloss/dz_v = all q_v - sum_{j of v} p_j,   q_v = exp(z_v - L),   all = sum p [+ pt]
+// (all is 1 unless sum p is above 1, or below it with entries that cover every
+// class: what a rounded lse or teacher and a class with two entries leave.) Lt
+// is the log-sum over the classes outside the top entries, whose gradient with
+// a tail is all q_v - pt exp(z_v - Lt) = exp(z_v - Lt) (all qt - pt), qt =
+// exp(Lt - L). Lt comes from a sum over those classes alone (a bit for each
+// class marks the others): L minus the top entries would lose it to
+// cancellation where the student is sure.
 struct DistillArgs {
     const void *logits, *teacher, *index;
     const float *lse, *weight, *dloss;
@@ -383,13 +385,13 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     sum = scalar(sum);
     const Entries f = found;
     const double rest = 1.0 - f.mass, pt = !tail || f.distinct == a.V || rest < 0.0 ? 0.0 : rest;
-    // (a NaN of the teacher is in L's coefficient: it reaches every class)
-    const bool broken = f.bad || f.mass != f.mass;
+    const double total = f.mass + pt;  // L's coefficient: a NaN of the teacher reaches every class
+    const bool broken = f.bad || total != total;
     // log2 of the sums over the classes outside the entries (lo2; of all classes
     // without a tail) and over all (all2), and what a power in the gradient is
     // multiplied by, times their sum
     double lo2, all2;
-    float factor = 1.0f;
+    float factor = (float)total;
     // (from all_from, and c's rounding out of all exponents)
     auto shift = [&] {
         return ((double)from - all_from) * a.scale64 - (far ? 0.0 : (double)c + (double)from * (double)a.scale);
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         lo2 = sum == 0.0 ? -INFINITY : (double)__builtin_amdgcn_frexp_exp(sum) +
                                            (double)__builtin_amdgcn_logf((float)__builtin_amdgcn_frexp_mant(sum)) + shift();
         const float d = (float)(f.top2 - lo2), u = __builtin_amdgcn_exp2f(-fabsf(d)), inv = 1.0f / (1.0f + u);
-        factor = sum == 0.0 ? 0.0f : (float)((double)(d > 0.0f ? u * inv : inv) - pt);  // (0: none of them has a q)
+        factor = sum == 0.0 ? 0.0f : (float)(total * (double)(d > 0.0f ? u * inv : inv) - pt);  // (0: none of them has a q)
     }
     if (!f.any) factor = 0.0f;
     if (broken) factor = NAN;
@@ -443,7 +445,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
             for (uint32_t i = j + 1; i < a.K; ++i)
                 if (entries.where[i] == entries.where[j]) p += entries.mass[i];
         }
-        const float g = broken ? NAN : (float)by * ((float)exp2(entries.z2[j] - all2) - p);
+        const float g = broken ? NAN : (float)by * ((float)(total * exp2(entries.z2[j] - all2)) - p);
         if (GRAD == ENTQ_F32)
             ((float *)grad)[entries.where[j]] = g;
         else

@@ -36,14 +36,19 @@ def distill(logits, index, teacher, lse=None, weight=None, temperature=1.0, dlos
     eL = (share * torch.where(share > 0, r, 0)).sum(1, keepdim=True) + (v / 512 + 24) * EPS
     terms = torch.where(p > 0, p * (torch.where(p > 0, logp, 0) - z.gather(1, at) + L), 0)
     loss, q = terms.sum(1), torch.exp(z - L)
-    g = q - mass
-    size = q + mass
+    # (L has the coefficient sum p, and pt with a tail: not 1 where sum p is above
+    # 1, or below it with entries that cover every class)
+    total = p.sum(1, keepdim=True)
     any_ = inside.any(1)
     if lse is not None:
         pt = (1 - p.sum(1)).clamp_min(0)
         pt = torch.where(hit.all(1), 0, pt)[:, None]
+        total = total + pt
+    g = total * q - mass
+    size = total * q + mass
+    if lse is not None:
         loss = loss + torch.where(pt > 0, pt * (pt.clamp_min(1e-300).log() - Lt + L), 0)[:, 0]
-        g = torch.where(hit, g, q - pt * share)
+        g = torch.where(hit, g, total * q - pt * share)
         size = size + pt * share
     g, size = (torch.where(any_[:, None], x, 0) for x in (g, size))
     loss = torch.where(any_ & (w != 0), loss * w, 0)

@@ -34,3 +34,56 @@ def test_a_nan_of_the_teacher_reaches_every_class(D, v, tail):  # noqa: F811
     close(loss[:1], *want[0], "loss")
     close(grad[:1], *want[1], "gradient")
     assert torch.isfinite(loss[2]) and torch.isfinite(grad[2]).all()
+
+
+def exact(logits, index, teacher, lse, weight, T, dloss=None):
+    """Loss and gradient by autograd in 64 bits, from the loss's definition."""
+    T = float(torch.tensor(T, dtype=torch.float32))
+    z = (logits.double() / T).requires_grad_()
+    inside, at = index >= 0, index.clamp_min(0).long()
+    t = torch.where(inside, teacher.double() / T, -float("inf"))
+    logp = torch.log_softmax(t, 1) if lse is None else t - lse.double()[:, None]
+    p = torch.where(inside, logp.exp(), 0)
+    L = torch.logsumexp(z, 1)
+    loss = torch.where(p > 0, p * (torch.where(p > 0, logp, 0) - z.gather(1, at) + L[:, None]), 0).sum(1)
+    if lse is not None:
+        hit = torch.zeros_like(z).detach().scatter_add_(1, at, inside.double()) > 0
+        pt = torch.where(hit.all(1), 0, (1 - p.sum(1)).clamp_min(0))
+        Lt = torch.logsumexp(z.masked_fill(hit, -float("inf")), 1)
+        loss = loss + torch.where(pt > 0, pt * (pt.clamp_min(1e-300).log() - Lt + L), 0)
+    if weight is not None:
+        loss = loss * weight.double()
+    by = torch.ones_like(loss) if dloss is None else dloss.double()
+    return loss.detach(), torch.autograd.grad((loss * by).sum(), z)[0] / T
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("v", [64, 1001, 9000, 33001, 150000])
+def test_a_mass_that_is_not_one(D, v, kind):  # noqa: F811
+    """The teacher's masses sum to more than 1, or the entries cover every class
+    and sum to less: L counts with their sum."""
+    logits, index, teacher, lse, _ = inputs(6, v, 20, kind, 7, True)
+    teacher[0] += 0.05                          # as 16-bit logits beside the sum of the unrounded ones
+    teacher[0, 0] += 9
+    logits[0, int(index[0, 0])] += 9
+    lse[0] = torch.logsumexp(teacher[0].double() / 1.25, 0).float() - 0.05
+    index[1, 10:] = index[1, :10].clone()       # every entry twice
+    teacher[1, 10:] = teacher[1, :10].clone()
+    lse[1] = torch.logsumexp(teacher[1].double() / 1.25, 0).float() - 0.3
+    lse[2] = torch.logsumexp(teacher[2].double() / 1.25, 0).float() - 1e-3
+    lse[3] -= 4
+    dloss = torch.tensor([1.0, -2.0, 0.5, 3.0, 1.0, 1.0], device="cuda")
+    sets = [(logits, index, teacher, lse)]
+    if v == 64:
+        all_, every = inputs(6, v, v, kind, 8, True)[:4], torch.tensor([1e-3, -1e-3, 0.4, -0.4, 0.0, 2.0], device="cuda")
+        sets.append((*all_[:3], all_[3] + every))
+    for logits, index, teacher, lse in sets:
+        for t in (teacher, teacher.bfloat16()):
+            loss, grad = torch.empty(6, device="cuda"), torch.empty_like(logits)
+            D.loss_backward(logits, index, t, grad, dloss, loss, lse, None, 1.25)
+            want = exact(logits, index, t, lse, None, 1.25, dloss)
+            bounds = R.distill(logits, index, t, lse, None, 1.25, dloss, kind)
+            close(loss, want[0], bounds[0][1], "loss")
+            close(grad, want[1], bounds[1][1], "gradient")
+            # L moves all logits alike: a row's gradients sum to 0
+            assert (grad.double().sum(1).abs() <= bounds[1][1].sum(1)).all()
