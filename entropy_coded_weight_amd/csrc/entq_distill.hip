@@ -80,7 +80,8 @@ __device__ __forceinline__ void remove(v4i &v, int i) {
 struct Entries {
     double terms;           // sum p (log p - z)
     double mass;            // sum p
-    double top2;            // with a tail: log2 of the student's sum over the entries' classes
+    double top2;            // with a tail: log2 of the student's sum over the entries' classes,
+    double top;             // and the sum as the row's waves' sums count (an infinity beyond 64 bits)
     uint32_t distinct;      // of these classes
     bool any, bad, twice;   // an entry, an index beyond the classes, a class with two entries
 };
@@ -309,6 +310,11 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         far = fabs((double)from * a.scale64) >= 0x1p24;
         c = scalar(far ? 0.0f : (float)(-(double)from * a.scale));
     };
+    // What is added to log2 of the row's waves' sum: from all_from, and c's rounding
+    // out of all exponents.
+    auto shift = [&] {
+        return ((double)from - all_from) * a.scale64 - (far ? 0.0 : (double)c + (double)from * (double)a.scale);
+    };
     auto raise = [&](v4i v) {
 #pragma unroll
         for (int i = 0; i < kP; ++i) top = fmaxf(top, act_of<TYPE>(v, i));
@@ -376,6 +382,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         __syncthreads();  // the largest logit
         refer();
         student_side(a, lane, all_from, own, entries, f);
+        if (tail) f.top = exp2(f.top2 - shift());
         if (lane == 0) found = f;
         __syncthreads();  // the sum
     }
@@ -387,26 +394,19 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     const double rest = 1.0 - f.mass, pt = !tail || f.distinct == a.V || rest < 0.0 ? 0.0 : rest;
     const double total = f.mass + pt;  // L's coefficient: a NaN of the teacher reaches every class
     const bool broken = f.bad || total != total;
+    // What a power in the gradient is multiplied by, times their sum. In 64 bits,
+    // since qt - pt may be far below both.
+    double factor = total;
+    if (tail) factor = sum == 0.0 ? 0.0 : total * (sum / (sum + f.top)) - pt;  // (0: none of them has a q)
+    if (!f.any) factor = 0.0;
+    if (broken) factor = NAN;
     // log2 of the sums over the classes outside the entries (lo2; of all classes
-    // without a tail) and over all (all2), and what a power in the gradient is
-    // multiplied by, times their sum
+    // without a tail) and over all (all2)
     double lo2, all2;
-    float factor = (float)total;
-    // (from all_from, and c's rounding out of all exponents)
-    auto shift = [&] {
-        return ((double)from - all_from) * a.scale64 - (far ? 0.0 : (double)c + (double)from * (double)a.scale);
-    };
     if (wave == WAVES) {
         lo2 = all2 = sum == 0.0 ? -INFINITY : log2(sum) + shift();
         if (tail) all2 = fmax(f.top2, lo2) + log2(1.0 + exp2(-fabs(f.top2 - lo2)));
-    } else if (tail) {
-        lo2 = sum == 0.0 ? -INFINITY : (double)__builtin_amdgcn_frexp_exp(sum) +
-                                           (double)__builtin_amdgcn_logf((float)__builtin_amdgcn_frexp_mant(sum)) + shift();
-        const float d = (float)(f.top2 - lo2), u = __builtin_amdgcn_exp2f(-fabsf(d)), inv = 1.0f / (1.0f + u);
-        factor = sum == 0.0 ? 0.0f : (float)(total * (double)(d > 0.0f ? u * inv : inv) - pt);  // (0: none of them has a q)
     }
-    if (!f.any) factor = 0.0f;
-    if (broken) factor = NAN;
     if (a.loss && wave == WAVES && lane == 0) {
         double loss = f.any ? f.terms + f.mass * (all2 * kLn2) : 0.0;
         if (f.any && pt > 0.0) loss += pt * (log(pt) + (all2 - lo2) * kLn2);
@@ -418,12 +418,12 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         // (2^64 of the powers and both constants' roundings out of them again)
         const float c64 = scalar(far ? 64.0f : (float)(64.0 - (double)from * a.scale));
         const double back = (double)c - (double)c64 + 64.0;
-        factor = scalar(factor == 0.0f ? 0.0f : (float)((double)factor / sum * by * __builtin_amdgcn_exp2f((float)back) * 0x1p-64));
+        const float each = scalar(factor == 0.0 ? 0.0f : (float)(factor / sum * by * __builtin_amdgcn_exp2f((float)back) * 0x1p-64));
         auto power = [&](v4i v, int i) { return __builtin_amdgcn_exp2f(__builtin_fmaf(act_of<TYPE>(v, i), a.scale, c64)); };
         auto write = [&](uint32_t p, v4i v) {
             float g[kP];
 #pragma unroll
-            for (int i = 0; i < kP; ++i) g[i] = factor == 0.0f ? 0.0f : factor * power(v, i);
+            for (int i = 0; i < kP; ++i) g[i] = each == 0.0f ? 0.0f : each * power(v, i);
             put(p, g);
         };
         if (VECS) {

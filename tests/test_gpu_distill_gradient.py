@@ -87,3 +87,40 @@ def test_a_mass_that_is_not_one(D, v, kind):  # noqa: F811
             close(grad, want[1], bounds[1][1], "gradient")
             # L moves all logits alike: a row's gradients sum to 0
             assert (grad.double().sum(1).abs() <= bounds[1][1].sum(1)).all()
+
+
+@pytest.mark.parametrize("v", [60, 1001, 20000, 33001, 60000, 150000])
+@pytest.mark.parametrize("near", [1e-2, 1e-4, -1e-5])
+def test_the_tail_of_student_and_teacher_alike(D, v, near):  # noqa: F811
+    """qt - pt far below both. The classes outside the entries have the logit 0,
+    so that their powers and the sum of these are exact in fp32, and what is
+    left of the arithmetic is that in 64 bits (1e-14 of qt, 1e-9 of the
+    factor) and four roundings to fp32 of a gradient: by, the factor, a
+    power's product and the entries' own (bounded by their terms)."""
+    torch.manual_seed(v)
+    T, k = 1.25, 8
+    logits = torch.zeros(4, v, device="cuda")
+    index = torch.stack([torch.randperm(v, device="cuda")[:k] for _ in range(4)])
+    top = T * torch.log(torch.tensor(v / k, device="cuda")) + torch.tensor([0.0, 1.0, -2.0, 3.0], device="cuda")[:, None]
+    logits.scatter_(1, index, (top + 0.5 * torch.randn(4, k, device="cuda")).clamp_min(0.01))
+    z = logits.double() / T
+    # the student's own masses, a constant below or above in the logarithm
+    inside = torch.softmax(z, 1).gather(1, index).sum(1)
+    lse = (torch.logsumexp(z, 1) - torch.log1p(-near * (1 - inside) / inside)).float()
+    teacher = logits.gather(1, index)
+    loss, grad = torch.empty(4, device="cuda"), torch.empty_like(logits)
+    D.loss_backward(logits, index, teacher, grad, None, loss, lse, None, T)
+    z = z.requires_grad_()
+    p = torch.exp(teacher.double() / T - lse.double()[:, None])
+    hit = torch.zeros_like(logits, dtype=torch.bool).scatter_(1, index, True)
+    share = (v - k) * torch.ones(4, dtype=torch.float64, device="cuda")
+    L = torch.logsumexp(z.detach(), 1)
+    factor = share / torch.exp(L) - (1 - p.sum(1))
+    want = torch.where(hit, torch.softmax(z.detach(), 1), (factor / share)[:, None])
+    want.scatter_add_(1, index, -p)
+    size = torch.where(hit, torch.softmax(z.detach(), 1), want.abs())
+    size.scatter_add_(1, index, p)
+    slack = 1e-14 / torch.exp(L)[:, None]
+    close(grad, want / T, (4 * R.EPS * size + slack) / T + R.TINY["f32"], "gradient")
+    # (that far apart, and what rounding lse moves sum p by)
+    assert (factor.abs() <= 1.02 * abs(near) * (1 - p.sum(1)) + 1.02 * R.EPS * lse.double().abs()).all()
