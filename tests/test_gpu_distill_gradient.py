@@ -124,3 +124,16 @@ def test_the_tail_of_student_and_teacher_alike(D, v, near):  # noqa: F811
     close(grad, want / T, (4 * R.EPS * size + slack) / T + R.TINY["f32"], "gradient")
     # (that far apart, and what rounding lse moves sum p by)
     assert (factor.abs() <= 1.02 * abs(near) * (1 - p.sum(1)) + 1.02 * R.EPS * lse.double().abs()).all()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("v", [700, 9001, 33001, 150000])
+@pytest.mark.parametrize("by", [1e-14, 1e-22, 1e-30, 1e30])
+def test_very_small_and_large_weights(D, v, tail, by):  # noqa: F811
+    """Gradients far from 1 in size are as exact as others while fp32 holds them."""
+    logits, index, teacher, lse, _ = inputs(4, v, 12, "f32", 5, tail)
+    dloss = torch.tensor([1.0, -0.3, 2.0, 0.7], device="cuda") * by
+    grad = torch.empty_like(logits)
+    D.loss_backward(logits, index, teacher, grad, dloss, None, lse, None, 1.25)
+    _, (want, bound) = R.distill(logits, index, teacher, lse, None, 1.25, dloss, "f32")
+    close(grad, want, bound, "gradient")
