@@ -782,7 +782,7 @@ entq_status entq_norm_block_backward(const entq_norm *n, const void *d_dout, uin
  *     over all its classes; the mass outside the entries, pt = max(0, 1 - sum
  *     p), is a class of its own (none where the entries cover every class):
  *     loss = sum_j p_j (log p_j - z_(index j) + L) + pt (log pt - Lt + L),
- *     Lt the log-sum of z over the classes that are no entry's
+ *     Lt the log-sum of z over the classes that are no entry's, qt = exp(Lt - L)
  * times the row's weight. An entry with a negative index is none; a row
  * without entries has loss and gradient 0, and so has one of weight 0,
  * whatever its logits hold. Entries of one class count each (their p add up).
@@ -792,9 +792,10 @@ entq_status entq_norm_block_backward(const entq_norm *n, const void *d_dout, uin
  * differences from the row's largest, whatever its size: a mask may be of the
  * type's lowest value or -infinity, and a row of the lowest value alone is
  * uniform (one of -infinity alone NaN). Where the student gives a class that p
- * has no mass at all, the loss is infinite. The entries' terms and the
- * logarithms are in 64 bits, the sums over classes in fp32 for each of a row's
- * threads. */
+ * has no mass at all, the loss is infinite. The entries' terms, the logarithms
+ * and qt - pt are in 64 bits; the classes' exponentials in fp32, from a factor
+ * log2(e) / T rounded to fp32 (up to 2^-24 E_q |z - max| of L), and their sums in
+ * fp32 for each of a row's threads. */
 #define ENTQ_DISTILL_MAX_TOP 256u
 #define ENTQ_DISTILL_MAX_CLASSES 262144u
 

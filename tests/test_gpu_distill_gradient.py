@@ -137,3 +137,32 @@ def test_very_small_and_large_weights(D, v, tail, by):  # noqa: F811
     D.loss_backward(logits, index, teacher, grad, dloss, None, lse, None, 1.25)
     _, (want, bound) = R.distill(logits, index, teacher, lse, None, 1.25, dloss, "f32")
     close(grad, want, bound, "gradient")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("v", [500, 9000, 33001, 150000, 262144])
+@pytest.mark.parametrize("power", [-3, 0, 2])
+def test_small_losses_at_the_stated_error(D, v, power, kind):  # noqa: F811
+    """A loss of 1e-4 to 0.7 against the bound of the exponents' rounded factor
+    alone, |scale / (log2(e) / T) - 1| E_q |z - max|, and the result's rounding:
+    T is log2(e) times a power of two and the logits multiples of it, so that
+    every exponent is a whole number, every power and sum exact in fp32."""
+    T = float(torch.tensor(1.44269504088896340736 * 2.0 ** power, dtype=torch.float32))
+    scale64 = 1.44269504088896340736 / T
+    scale = float(torch.tensor(scale64, dtype=torch.float32))
+    assert scale == 2.0 ** -power
+    m = 4
+    steps = torch.tensor([22, 21, 20, 18], device="cuda")   # (a thread's sum with the largest: within 2^-23 .. 2^9)
+    logits = (-steps[:, None] * 2.0 ** power).repeat(1, v).to(TYPES[kind])
+    index = torch.tensor([[3], [v - 1], [v // 2], [7]], device="cuda")
+    logits.scatter_(1, index, 0.0)
+    loss, alone, grad = torch.empty(m, device="cuda"), torch.empty(m, device="cuda"), torch.empty_like(logits)
+    D.loss(logits, index, torch.zeros(m, 1, device="cuda"), alone, temperature=T)
+    D.loss_backward(logits, index, torch.zeros(m, 1, device="cuda"), grad, None, loss, temperature=T)
+    z = logits.double() / T
+    rest = (v - 1) * torch.exp(z.min(1).values)             # the sum is 1 + this
+    want = torch.log1p(rest)
+    slope = abs(scale / scale64 - 1) * (rest / (1 + rest)) * z.min(1).values.abs()
+    bound = 1.001 * slope + R.EPS * want + 1e-12 * want
+    close(loss, want, bound, "loss beside the gradient")
+    close(alone, want, bound, "loss")
