@@ -132,12 +132,12 @@ def workspace_bytes(x, router, gate, gate_scales, up, up_scales, down, down_scal
 
 class MixtureOfExperts(DecodedCodes):
     """p: a plan of Int8 tensors, for each expert gate [F, D], up [F, D] and
-    down [N, F], the experts one after the other (equal steps between their
-    codes and between their scales); scales: device float32 with the plan's row
-    scales; router: bfloat16, float16 or float32 [E, D]. ``decode`` fills the
-    code buffer (``codes``: device int8, at least out_elems; None: the layer's
-    own), which ``forward`` then uses. Streams and the buffer are as in
-    ``feed_forward.FeedForward``."""
+    down [N, F], the experts one after the other (equal steps upwards between
+    their codes and between their scales, of which each expert has its own);
+    scales: device float32 with the plan's row scales; router: bfloat16,
+    float16 or float32 [E, D]. ``decode`` fills the code buffer (``codes``:
+    device int8, at least out_elems; None: the layer's own), which ``forward``
+    then uses. Streams and the buffer are as in ``feed_forward.FeedForward``."""
 
     def __init__(self, p: Plan, scales, router, top_k, activation="silu", normalize=True,
                  codes=None):
@@ -156,13 +156,16 @@ class MixtureOfExperts(DecodedCodes):
         steps = [a[3] - a[0] if n > 1 else 0 for a in at]
         if any(a[i] != a[i % 3] + i // 3 * s for a, s in zip(at, steps) for i in range(3 * n)):
             raise EntqError(EINVAL, "the experts' tensors do not lie at equal steps")
+        if n > 1 and min(steps) <= 0:
+            raise EntqError(EINVAL, "the experts' tensors lie backwards or share their scales: each "
+                                    "expert is to have its own, after those of the one before")
         super().__init__(p, scales, codes)
         flat, rows = self.codes.view(-1), self.scales.view(-1)
         self._w = []
         for i, (r, c) in enumerate(shapes[:3]):
-            self._w += [flat.as_strided((n, r, c), (steps[0] or r * c, c, 1),
+            self._w += [flat.as_strided((n, r, c), (steps[0] if n > 1 else r * c, c, 1),
                                         flat.storage_offset() + at[0][i]),
-                        rows.as_strided((n, r), (steps[1] or r, 1),
+                        rows.as_strided((n, r), (steps[1] if n > 1 else r, 1),
                                         rows.storage_offset() + at[1][i])]
         self.router, self.top_k = router, top_k
         self.activation, self.normalize = activation, normalize
