@@ -103,6 +103,8 @@ struct OwnEntries {
     _Pragma("unroll") for (int i = 0; i < kOwn; ++i) if (const uint32_t j = i * 64 + lane; j < a.K)
 
 __device__ __forceinline__ void load_entries(const DistillArgs &a, uint64_t m, uint32_t lane, OwnEntries &o) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) o.at[i] = -1;  // (no way leaves it unset)
     ENTQ_OWN_ENTRIES(i, j) {
         const int64_t c = a.wide ? ((const int64_t *)a.index)[m * a.ldi + j] : ((const int32_t *)a.index)[m * a.ldi + j];
         o.at[i] = c < 0 ? -1 : c < (int64_t)a.V ? (int32_t)c : -2;
