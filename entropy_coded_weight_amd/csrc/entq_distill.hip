@@ -81,7 +81,7 @@ struct Entries {
     double terms;           // sum p (log p - z)
     double mass;            // sum p
     double top2;            // with a tail: log2 of the student's sum over the entries' classes,
-    double top;             // and the sum as the row's waves' sums count (an infinity beyond 64 bits)
+    double top;             // and the sum as the row's waves' sums count, 2^500 at most
     uint32_t distinct;      // of these classes
     bool any, bad, twice;   // an entry, an index beyond the classes, a class with two entries
 };
@@ -390,7 +390,10 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         __syncthreads();  // the largest logit
         refer();
         student_side(a, lane, all_from, own, entries, f);
-        if (tail) f.top = exp2(f.top2 - shift());
+        if (tail) {
+            f.top = exp2(f.top2 - shift());
+            f.top = f.top > 0x1p500 ? 0x1p500 : f.top;  // (qt is 0 as well; a NaN stays one)
+        }
         if (lane == 0) found = f;
         __syncthreads();  // the sum
     }
@@ -402,11 +405,12 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     const double rest = 1.0 - f.mass, pt = !tail || f.distinct == a.V || rest < 0.0 ? 0.0 : rest;
     const double total = f.mass + pt;  // L's coefficient: a NaN of the teacher reaches every class
     const bool broken = f.bad || total != total;
-    // What a power in the gradient is multiplied by, times their sum. In 64 bits,
+    // What a power in the gradient is multiplied by: total / sum, and with a tail
+    // (total qt - pt) / sum, qt = sum / (sum + top), as one quotient. In 64 bits,
     // since qt - pt may be far below both.
-    double factor = total;
-    if (tail) factor = sum == 0.0 ? 0.0 : total * (sum / (sum + f.top)) - pt;  // (0: none of them has a q)
-    if (!f.any) factor = 0.0;
+    const double both = sum + f.top;
+    double factor = (tail ? total * sum - pt * both : total) / (tail ? sum * both : sum);
+    if (!f.any || (tail && sum == 0.0)) factor = 0.0;  // (none of them has a q)
     if (broken) factor = NAN;
     // log2 of the sums over the classes outside the entries (lo2; of all classes
     // without a tail) and over all (all2)
@@ -426,7 +430,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         // (2^64 of the powers and both constants' roundings out of them again. A
         // factor that 2^-64 would take out of fp32's normal numbers leaves the powers
         // as they are: what the hardware flushes then is below 2^-126 2^-40.)
-        const double one = factor / sum * by;
+        const double one = factor * by;
         const float up = scalar(fabs(one) < 0x1p-40 ? 0.0f : 64.0f);
         const float c64 = scalar(far ? up : (float)(up - (double)from * a.scale));
         const double back = (double)c - (double)c64 + up;
