@@ -80,8 +80,8 @@ __device__ __forceinline__ void remove(v4i &v, int i) {
 struct Entries {
     double terms;           // sum p (log p - z)
     double mass;            // sum p
-    double top2;            // with a tail: log2 of the student's sum over the entries' classes,
-    double top;             // and the sum as the row's waves' sums count, 2^500 at most
+    double top;             // with a tail: the student's sum over the entries' classes, from all's largest
+    double back;            // and what takes the row's waves' sum there
     uint32_t distinct;      // of these classes
     bool any, bad, twice;   // an entry, an index beyond the classes, a class with two entries
 };
@@ -171,21 +171,19 @@ __device__ __forceinline__ Entries teacher_side(const DistillArgs &a, uint64_t m
 // ... then the student's, its logits counted from `from`.
 __device__ __forceinline__ void student_side(const DistillArgs &a, uint32_t lane, double from, const OwnEntries &o,
                                              EntryTable &e, Entries &f) {
-    double peak = -INFINITY, s = 0.0;
+    double s = 0.0;
     ENTQ_OWN_ENTRIES(i, j) {
         const double z = o.at[i] >= 0 ? (o.logit[i] - from) * a.scale64 : -INFINITY;
         e.z2[j] = z;
-        peak = z > peak || z != z ? z : peak;
         if (o.at[i] >= 0 && !(o.p[i] == 0.0)) s += o.p[i] * z;
     }
     f.terms -= wave_sum(s) * kLn2;
     if (!a.lse) return;
-    peak = wave_max64(peak);
     s = 0.0;
     ENTQ_OWN_ENTRIES(i, j) {
-        if (o.first[i]) s += exp2((o.logit[i] - from) * a.scale64 - peak);
+        if (o.first[i]) s += exp2((o.logit[i] - from) * a.scale64);
     }
-    f.top2 = peak == -INFINITY ? peak : peak + log2(wave_sum(s));
+    f.top = wave_sum(s);
 }
 
 // One workgroup per token: WAVES waves for the row, and one for the entries,
@@ -210,9 +208,10 @@ __device__ __forceinline__ void student_side(const DistillArgs &a, uint32_t lane
 // there, to 1e-6 of their values (without the 64 where the weight is so small
 // that they would not be there anyway).
 //
-// Bound by memory: 4096 x 32000 bf16 in 46.6 us (5.6 TB/s read), with the
-// gradient 108 us (4.9 TB/s; a copy reaches 5.1), 515 x 50021 f16 with it in
-// 24.8 us. What carries that are waves: a workgroup has a multiple of 4 (with
+// Bound by memory where rows fill their variant: 4096 x 32000 bf16 in 46.7 us
+// (5.6 TB/s of reads, part of them from the last-level cache: 32768 rows 382 us, 5.5 TB/s),
+// with the gradient 108.5 us (4.8 TB/s; a copy reaches 5.1; 32768 rows 814 us), 515 x 50021
+// f16 with it in 25.3 us. What carries that are waves: a workgroup has a multiple of 4 (with
 // 9, one SIMD's three decide, and the first took 107 us), the entries have a
 // wave to themselves (in a wave of the row their 64-bit registers come on top
 // of the row's: 54.7 and 127.4 us), and the registers are held to 80 and 64
@@ -390,10 +389,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
         __syncthreads();  // the largest logit
         refer();
         student_side(a, lane, all_from, own, entries, f);
-        if (tail) {
-            f.top = exp2(f.top2 - shift());
-            f.top = f.top > 0x1p500 ? 0x1p500 : f.top;  // (qt is 0 as well; a NaN stays one)
-        }
+        if (tail) f.back = exp2(shift());
         if (lane == 0) found = f;
         __syncthreads();  // the sum
     }
@@ -406,18 +402,18 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     const double total = f.mass + pt;  // L's coefficient: a NaN of the teacher reaches every class
     const bool broken = f.bad || total != total;
     // What a power in the gradient is multiplied by: total / sum, and with a tail
-    // (total qt - pt) / sum, qt = sum / (sum + top), as one quotient. In 64 bits,
-    // since qt - pt may be far below both.
-    const double both = sum + f.top;
-    double factor = (tail ? total * sum - pt * both : total) / (tail ? sum * both : sum);
-    if (!f.any || (tail && sum == 0.0)) factor = 0.0;  // (none of them has a q)
+    // (total qt - pt) / sum, qt = out / (out + top), as one quotient. In 64 bits,
+    // since qt - pt may be far below both. (A sum of 0 is no class's.)
+    const double out = tail && sum != 0.0 ? sum * f.back : 0.0, both = out + f.top;
+    double factor = (tail ? total * out - pt * both : total) / (tail ? sum * both : sum);
+    if (!f.any || (tail && sum == 0.0)) factor = 0.0;
     if (broken) factor = NAN;
     // log2 of the sums over the classes outside the entries (lo2; of all classes
     // without a tail) and over all (all2)
     double lo2, all2;
     if (wave == WAVES) {
         lo2 = all2 = sum == 0.0 ? -INFINITY : log2(sum) + shift();
-        if (tail) all2 = fmax(f.top2, lo2) + log2(1.0 + exp2(-fabs(f.top2 - lo2)));
+        if (tail) all2 = log2(both);
     }
     if (a.loss && wave == WAVES && lane == 0) {
         double loss = f.any ? f.terms + f.mass * (all2 * kLn2) : 0.0;
@@ -478,6 +474,19 @@ int launch_rows(const DistillArgs &a, hipStream_t s) {
     return hipGetLastError() == hipSuccess ? ENTQ_OK : ENTQ_EHIP;
 }
 
+// The fewest waves and pieces that hold a row: each of these variants was slower
+// than the smaller ones at every size that both take, because unused pieces cost
+// what used ones do. 131 million bf16 logits with gradient, us, this choice and the next
+// larger one's: 768 pieces 144 and 411, 900 350 and 670, 2000 173 and 277, 4032
+// 109 and 143, 5000 127 and 197, 6720 113 and 173, 8000 156 and 188, 8640 157 and
+// 189, 10000 178 and (the row read again, VECS 0) 203, 16320 137 and 187; the
+// losses alone 768 pieces 96 and 300, 4032 63 and 102, 6720 67 and 111, 8640 97 and
+// 136, 16320 85 and 107. Rows of 1024 fp32 logits with a bf16 gradient: 8000 pieces 64
+// and 73, 16320 110 and 170. 96 rows: 768 pieces 12.3 and 14.6, 16320 28.3 and
+// 36.7. Rows far shorter than their variant pay for it (900 pieces 3.4 times their
+// bytes' time, 128 pieces, a workgroup for each 1024 classes, 7 times: 735), and rows
+// beyond 16320 pieces for two readings of the loss and three with the gradient
+// (16384: 186).
 template <int TYPE, int GRAD>
 int launch_distill(const DistillArgs &a, hipStream_t s) {
     const uint32_t pieces = (a.V + kPer<TYPE> - 1) / kPer<TYPE>;

@@ -643,6 +643,10 @@ uint32_t splits_of(uint32_t results, uint32_t most) {
 }
 
 // Columns of a job: as many as the experts have tokens on average, times two.
+// With 16, 32 and 64 of them, us: 8 tokens an expert (32 tokens, 2 of 8, 4096 x
+// 8192) 180, 197, 219; 16 (64 tokens) 245, 217, 236; 32 (64 tokens, 2 of 4) 205,
+// 174, 156; between the steps the choice is 5 % off at most (24 an expert, 48
+// tokens, 2 of 4, 4096 x 4096: 104, 87, 91).
 uint32_t columns_of(uint32_t tokens, uint32_t top_k, uint32_t experts) {
     const uint32_t average = tokens * top_k / experts;
     return tokens <= 16 || average <= 8 ? 16 : tokens <= 32 || average <= 16 ? 32 : 64;
