@@ -400,11 +400,12 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     const Entries f = found;
     const double rest = 1.0 - f.mass, pt = !tail || f.distinct == a.V || rest < 0.0 ? 0.0 : rest;
     const double total = f.mass + pt;  // L's coefficient: a NaN of the teacher reaches every class
-    const bool broken = f.bad || total != total;
     // What a power in the gradient is multiplied by: total / sum, and with a tail
     // (total qt - pt) / sum, qt = out / (out + top), as one quotient. In 64 bits,
     // since qt - pt may be far below both. (A sum of 0 is no class's.)
     const double out = tail && sum != 0.0 ? sum * f.back : 0.0, both = out + f.top;
+    // (both 0: all of the row is -infinity, and no softmax)
+    const bool broken = f.bad || total != total || (tail && f.any && both == 0.0);
     double factor = (tail ? total * out - pt * both : total) / (tail ? sum * both : sum);
     if (!f.any || (tail && sum == 0.0)) factor = 0.0;
     if (broken) factor = NAN;

@@ -166,3 +166,18 @@ def test_small_losses_at_the_stated_error(D, v, power, kind):  # noqa: F811
     bound = 1.001 * slope + R.EPS * want + 1e-12 * want
     close(loss, want, bound, "loss beside the gradient")
     close(alone, want, bound, "loss")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("v", [40, 5000, 33000, 150000])
+@pytest.mark.parametrize("tail", [False, True])
+def test_a_row_of_minus_infinity_alone(D, v, tail, kind):  # noqa: F811
+    """There is no softmax of it: NaN, and not 0 for the classes outside."""
+    logits, index, teacher, lse, _ = inputs(4, v, 8, kind, 4, tail)
+    logits[1:3] = -float("inf")
+    index[2] = -1
+    loss, grad = torch.empty(4, device="cuda"), torch.empty_like(logits)
+    D.loss_backward(logits, index, teacher, grad, None, loss, lse, None, 1.25)
+    assert loss.isnan().tolist() == [False, True, False, False]
+    assert grad[1].isnan().all() and torch.isfinite(grad[[0, 3]]).all()
+    assert loss[2] == 0 and not grad[2].any()
