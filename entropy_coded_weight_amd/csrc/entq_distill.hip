@@ -208,10 +208,10 @@ __device__ __forceinline__ void student_side(const DistillArgs &a, uint32_t lane
 // there, to 1e-6 of their values (without the 64 where the weight is so small
 // that they would not be there anyway).
 //
-// Bound by memory where rows fill their variant: 4096 x 32000 bf16 in 46.7 us
-// (5.6 TB/s of reads, part of them from the last-level cache: 32768 rows 382 us, 5.5 TB/s),
-// with the gradient 108.5 us (4.8 TB/s; a copy reaches 5.1; 32768 rows 814 us), 515 x 50021
-// f16 with it in 25.3 us. What carries that are waves: a workgroup has a multiple of 4 (with
+// Bound by memory where rows fill their variant: 4096 x 32000 bf16 in 46.6 us
+// (5.6 TB/s of reads, part of them from the last-level cache: 32768 rows 383 us, 5.5 TB/s),
+// with the gradient 107.6 us (4.9 TB/s; a copy reaches 5.1; 32768 rows 806 us), 515 x 50021
+// f16 with it in 24.7 us. What carries that are waves: a workgroup has a multiple of 4 (with
 // 9, one SIMD's three decide, and the first took 107 us), the entries have a
 // wave to themselves (in a wave of the row their 64-bit registers come on top
 // of the row's: 54.7 and 127.4 us), and the registers are held to 80 and 64
@@ -400,15 +400,20 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     const Entries f = found;
     const double rest = 1.0 - f.mass, pt = !tail || f.distinct == a.V || rest < 0.0 ? 0.0 : rest;
     const double total = f.mass + pt;  // L's coefficient: a NaN of the teacher reaches every class
-    // What a power in the gradient is multiplied by: total / sum, and with a tail
-    // (total qt - pt) / sum, qt = out / (out + top), as one quotient. In 64 bits,
-    // since qt - pt may be far below both. (A sum of 0 is no class's.)
+    // with a tail, the sums outside the entries and of all classes, from all's
+    // largest (a sum of 0 is no class's; both 0: all of the row is -infinity, and
+    // no softmax)
     const double out = tail && sum != 0.0 ? sum * f.back : 0.0, both = out + f.top;
-    // (both 0: all of the row is -infinity, and no softmax)
     const bool broken = f.bad || total != total || (tail && f.any && both == 0.0);
-    double factor = (tail ? total * out - pt * both : total) / (tail ? sum * both : sum);
-    if (!f.any || (tail && sum == 0.0)) factor = 0.0;
-    if (broken) factor = NAN;
+    // What a power in the gradient is multiplied by: total / sum, and with a tail
+    // (total qt - pt) / sum, qt = out / both, as one quotient. In 64 bits, since qt -
+    // pt may be far below both.
+    double factor = 0.0;
+    if (a.dlogits) {
+        factor = (tail ? total * out - pt * both : total) / (tail ? sum * both : sum);
+        if (!f.any || (tail && sum == 0.0)) factor = 0.0;
+        if (broken) factor = NAN;
+    }
     // log2 of the sums over the classes outside the entries (lo2; of all classes
     // without a tail) and over all (all2)
     double lo2, all2;
