@@ -17,7 +17,8 @@ import torch
 
 from . import EINVAL, KIND_INT8, EntqError, Experts, Plan, Rows, lib
 from .feed_forward import DecodedCodes
-from .int8 import (_BF16, _F16, _F32, MAX_COLS, _activation, _enqueue, _gpu, _matrix, _no_graph)
+from .int8 import (_BF16, _F16, _F32, MAX_COLS, _activation, _check_activations, _enqueue, _gpu,
+                   _matrix, _no_graph)
 
 MAX_TOKENS = 64
 MAX_EXPERTS = 256
@@ -179,9 +180,7 @@ class MixtureOfExperts(DecodedCodes):
         MAX_TOKENS run in groups of that many, each of which reads its experts'
         codes again."""
         index = self.plan.device.index
-        _matrix("x", x, index, _FLOATS, (x.shape[0], self.width) if x.dim() == 2 else None)
-        _no_graph("x", x)
-        m = x.shape[0]
+        m = _check_activations("x", x, index, self.width)
         _matrix("y", y, index, _FLOATS, (m, self.out))
         _choice("experts", experts, torch.int32, index, (m, self.top_k))
         _choice("weights", weights, torch.float32, index, (m, self.top_k))

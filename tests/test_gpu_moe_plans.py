@@ -49,3 +49,19 @@ def test_gaps_between_experts(E, M):  # noqa: F811
     mix.decode(blob)
     mix.forward(x, y)
     assert torch.equal(y, want)
+
+
+def test_what_is_no_activation_is_refused(E, M):  # noqa: F811
+    b, p, blob, scales, w = plan_of(E, 2, 64, 32, 48)
+    mix = M.MixtureOfExperts(p, scales, torch.zeros(2, 64, device="cuda"), 1)
+    y = torch.zeros(3, 48, device="cuda")
+    for x in (None, 3.0, [[0.0] * 64], torch.zeros(3, 64), torch.zeros(64, device="cuda"), torch.zeros(3, 63, device="cuda"),
+              torch.zeros(3, 64, dtype=torch.int8, device="cuda"), torch.zeros(1, 3, 64, device="cuda")):
+        with pytest.raises(E.EntqError) as ei:
+            mix.forward(x, y)
+        assert ei.value.status == E.EINVAL
+    x = torch.zeros(3, 64, device="cuda")
+    for bad in (dict(y=None), dict(experts=[1]), dict(weights=3)):
+        with pytest.raises(E.EntqError) as ei:
+            mix.forward(x, **{"y": y, **bad})
+        assert ei.value.status == E.EINVAL
