@@ -12,7 +12,9 @@ p is the softmax of teacher[m] / T over the token's entries, or, with
 ``teacher_lse`` (the logsumexp of all the teacher's logits / T), exp(teacher /
 T - lse), and the mass outside the entries is compared with the student's mass
 there as one more class. An index below 0 is no entry; a row of weight 0 may
-hold anything. Masks may be the type's lowest value or -infinity.
+hold anything. Masks may be the type's lowest value or -infinity. A NaN in a
+token's logits, entries or log-sum, or an index beyond the classes, makes all of
+its loss and gradient NaN.
 
 logits: bfloat16, float16 or float32 [M, V]; index: int32 or int64 [M, K], K
 up to MAX_TOP; teacher: any of the logits' types [M, K] (unit stride along the
