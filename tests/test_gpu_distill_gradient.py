@@ -181,3 +181,23 @@ def test_a_row_of_minus_infinity_alone(D, v, tail, kind):  # noqa: F811
     assert loss.isnan().tolist() == [False, True, False, False]
     assert grad[1].isnan().all() and torch.isfinite(grad[[0, 3]]).all()
     assert loss[2] == 0 and not grad[2].any()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("v", [40, 5000, 33000, 150000])
+@pytest.mark.parametrize("tail", [False, True])
+def test_no_number_among_the_students_logits(D, v, tail, kind):  # noqa: F811
+    """A NaN or an infinity at an entry's class and at another: no softmax of the
+    row, whatever the entry's mass is."""
+    logits, index, teacher, lse, _ = inputs(6, v, 8, kind, 4, tail)
+    other = next(c for c in range(v) if c not in index[1:5].flatten().tolist())
+    logits[1, int(index[1, 0])] = float("nan")
+    logits[2, other] = float("nan")
+    logits[3, int(index[3, 0])] = float("inf")
+    logits[4, other] = float("inf")
+    logits[5, int(index[5, 2])] = float("nan")
+    teacher[5, 2] = -float("inf")
+    loss, grad = torch.empty(6, device="cuda"), torch.empty_like(logits)
+    D.loss_backward(logits, index, teacher, grad, None, loss, lse, None, 1.25)
+    assert loss.isnan().tolist() == [False] + [True] * 5
+    assert grad[1:].isnan().all() and torch.isfinite(grad[0]).all()
