@@ -87,7 +87,7 @@ struct Entries {
 };
 struct EntryTable {
     int32_t where[kMaxTop]; // an entry's class, -1: none
-    float mass[kMaxTop];    // the teacher's p of it
+    double mass[kMaxTop];   // the teacher's p of it
     double z2[kMaxTop];     // the student's exponent of it
     bool later[kMaxTop];    // an earlier entry has its class
 };
@@ -159,7 +159,7 @@ __device__ __forceinline__ Entries teacher_side(const DistillArgs &a, uint64_t m
         if (o.at[i] < 0) continue;
         const double logp = o.teacher[i] * a.inv_t - lse;
         o.p[i] = exp(logp);
-        e.mass[j] = (float)o.p[i];
+        e.mass[j] = o.p[i];
         f.mass += o.p[i];
         if (!(o.p[i] == 0.0)) f.terms += o.p[i] * logp;
     }
@@ -458,12 +458,12 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     __syncthreads();
     for (uint32_t j = lane; j < a.K; j += 64) {
         if (entries.where[j] < 0 || entries.later[j]) continue;
-        float p = entries.mass[j];
+        double p = entries.mass[j];
         if (f.twice) {
             for (uint32_t i = j + 1; i < a.K; ++i)
                 if (entries.where[i] == entries.where[j]) p += entries.mass[i];
         }
-        const float g = broken ? NAN : (float)by * ((float)(total * exp2(entries.z2[j] - all2)) - p);
+        const float g = broken ? NAN : (float)(by * (total * exp2(entries.z2[j] - all2) - p));
         if (GRAD == ENTQ_F32)
             ((float *)grad)[entries.where[j]] = g;
         else

@@ -95,8 +95,8 @@ def test_the_tail_of_student_and_teacher_alike(D, v, near):  # noqa: F811
     """qt - pt far below both. The classes outside the entries have the logit 0,
     so that their powers and the sum of these are exact in fp32, and what is
     left of the arithmetic is that in 64 bits (1e-14 of qt, 1e-9 of the
-    factor) and four roundings to fp32 of a gradient: by, the factor, a
-    power's product and the entries' own (bounded by their terms)."""
+    factor) and roundings to fp32: of a gradient outside the factor's and the
+    product's, of the entries' the result's; four are allowed."""
     torch.manual_seed(v)
     T, k = 1.25, 8
     logits = torch.zeros(4, v, device="cuda")
@@ -105,20 +105,21 @@ def test_the_tail_of_student_and_teacher_alike(D, v, near):  # noqa: F811
     logits.scatter_(1, index, (top + 0.5 * torch.randn(4, k, device="cuda")).clamp_min(0.01))
     z = logits.double() / T
     # the student's own masses, a constant below or above in the logarithm
-    inside = torch.softmax(z, 1).gather(1, index).sum(1)
-    lse = (torch.logsumexp(z, 1) - torch.log1p(-near * (1 - inside) / inside)).float()
+    L = torch.logsumexp(z, 1)
+    inside = torch.exp(z - L[:, None]).gather(1, index).sum(1)
+    lse = (L - torch.log1p(-near * (1 - inside) / inside)).float()
     teacher = logits.gather(1, index)
     loss, grad = torch.empty(4, device="cuda"), torch.empty_like(logits)
     D.loss_backward(logits, index, teacher, grad, None, loss, lse, None, T)
-    z = z.requires_grad_()
     p = torch.exp(teacher.double() / T - lse.double()[:, None])
     hit = torch.zeros_like(logits, dtype=torch.bool).scatter_(1, index, True)
     share = (v - k) * torch.ones(4, dtype=torch.float64, device="cuda")
-    L = torch.logsumexp(z.detach(), 1)
+    # (torch's softmax of 64 bits is off by 5e-7 of its values on this GPU)
+    q = torch.exp(z - L[:, None])
     factor = share / torch.exp(L) - (1 - p.sum(1))
-    want = torch.where(hit, torch.softmax(z.detach(), 1), (factor / share)[:, None])
+    want = torch.where(hit, q, (factor / share)[:, None])
     want.scatter_add_(1, index, -p)
-    size = torch.where(hit, torch.softmax(z.detach(), 1), want.abs())
+    size = torch.where(hit, q, want.abs())
     size.scatter_add_(1, index, p)
     slack = 1e-14 / torch.exp(L)[:, None]
     close(grad, want / T, (4 * R.EPS * size + slack) / T + R.TINY["f32"], "gradient")
@@ -201,3 +202,20 @@ def test_no_number_among_the_students_logits(D, v, tail, kind):  # noqa: F811
     D.loss_backward(logits, index, teacher, grad, None, loss, lse, None, 1.25)
     assert loss.isnan().tolist() == [False] + [True] * 5
     assert grad[1:].isnan().all() and torch.isfinite(grad[0]).all()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("v", [300, 9000, 150000])
+def test_entries_of_masses_below_fp32(D, v, tail):  # noqa: F811
+    """Masses below fp32's smallest number, times a weight that brings them back."""
+    logits, index, teacher, lse, _ = inputs(3, v, 8, "f32", 6, tail)
+    at = index[:, 5:].long()
+    low = logits.amax(1, keepdim=True) - 1.25 * torch.tensor([[106.0, 112.0, 118.0]], device="cuda")
+    logits.scatter_(1, at, low)
+    teacher[:, 5:] = teacher[:, :1] - 1.25 * torch.tensor([[107.0, 111.5, 119.0]], device="cuda")
+    dloss = torch.tensor([1e30, -3e28, 2e32], device="cuda")
+    grad = torch.empty_like(logits)
+    D.loss_backward(logits, index, teacher, grad, dloss, None, lse, None, 1.25)
+    _, (want, bound) = R.distill(logits, index, teacher, lse, None, 1.25, dloss, "f32")
+    assert bool((want.gather(1, at) != 0).all())
+    close(grad, want, bound, "gradient")
