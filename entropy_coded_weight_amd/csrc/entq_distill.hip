@@ -208,10 +208,10 @@ __device__ __forceinline__ void student_side(const DistillArgs &a, uint32_t lane
 // there, to 1e-6 of their values (without the 64 where the weight is so small
 // that they would not be there anyway).
 //
-// Bound by memory where rows fill their variant: 4096 x 32000 bf16 in 46.6 us
+// Bound by memory where rows fill their variant: 4096 x 32000 bf16 in 46.7 us
 // (5.6 TB/s of reads, part of them from the last-level cache: 32768 rows 383 us, 5.5 TB/s),
 // with the gradient 107.6 us (4.9 TB/s; a copy reaches 5.1; 32768 rows 806 us), 515 x 50021
-// f16 with it in 24.7 us. What carries that are waves: a workgroup has a multiple of 4 (with
+// f16 with it in 24.9 us. What carries that are waves: a workgroup has a multiple of 4 (with
 // 9, one SIMD's three decide, and the first took 107 us), the entries have a
 // wave to themselves (in a wave of the row their 64-bit registers come on top
 // of the row's: 54.7 and 127.4 us), and the registers are held to 80 and 64
@@ -420,6 +420,7 @@ __global__ __launch_bounds__(64 * WAVES + 64, (kResident<VECS, WAVES>)) void dis
     if (wave == WAVES) {
         lo2 = all2 = sum == 0.0 ? -INFINITY : log2(sum) + shift();
         if (tail) all2 = log2(both);
+        all2 = scalar(all2);  // (28 bytes of scratch without, where registers are held to 64, and 20 with it)
     }
     if (a.loss && wave == WAVES && lane == 0) {
         double loss = f.any ? f.terms + f.mass * (all2 * kLn2) : 0.0;
